@@ -23,6 +23,17 @@ An fp8 (e4m3) cache (``include/mla_fp8.h``) holds half the bytes per token:
 
     kv8 = quantize_cache_fp8(kv_cache)                       # mla_cache_quantize_fp8
     o_latent, lse = decode_fp8(p, q_latent, q_rope, kv8, block_table)   # mla_decode_fp8
+
+A speculative step over trees of drafted tokens (``include/mla_tree.h``; ragged
+token arrays, each function with an _fp8 twin for an fp8 cache):
+
+    q_latent, q_rope, st = query(q_nope, q_pe, w_uk, positions)         # mla_query
+    st = cache_append(kv_latent, k_pe, gamma, kv_cache, block_table, seq_lens,
+                      token_offsets, positions=positions)               # mla_cache_append
+    p = tree_plan(seq_lens, token_offsets, masks, max_pages_per_seq=maxp)   # mla_tree_plan
+    o_latent, lse = tree_decode(p, q_latent, q_rope, kv_cache, block_table)  # mla_tree_decode
+    new_seq_lens, st = cache_commit(kv_cache, block_table, seq_lens, token_offsets,
+                                    paths, path_lens)                   # mla_cache_commit
 """
 
 from ._binding import (D_V, HIDDEN, DEFAULT_ROPE_BASE, DEFAULT_RMS_EPS, DEFAULT_SCALE, D_LATENT, D_NOPE, D_ROPE, LIB_PATH, NUM_HEADS, PAGE_SIZE,
@@ -31,6 +42,9 @@ from ._binding import (D_V, HIDDEN, DEFAULT_ROPE_BASE, DEFAULT_RMS_EPS, DEFAULT_
                        decode_diag, decode_fp8, decode_noalloc, epilog_oproj, epilog_uv, quantize_cache_fp8,
                        load_library, num_units, parse_plan, plan, prolog, rope_table,
                        plan_device_bytes, plan_host, plan_layout, workspace_size)
+from ._binding import (MLA_DEV_BAD_OFFSETS, MLA_DEV_BAD_PATH, TREE_MAX_NODES, TreePlan, cache_append, cache_append_fp8,
+                       cache_commit, cache_commit_fp8, query, tree_decode, tree_decode_fp8, tree_plan,
+                       tree_plan_device, tree_plan_host, tree_workspace_size)
 
 __all__ = ["D_V", "HIDDEN", "epilog_oproj", "epilog_uv",
            "quantize_cache_fp8",
@@ -39,4 +53,7 @@ __all__ = ["D_V", "HIDDEN", "epilog_oproj", "epilog_uv",
            "MLAError", "MLA_FLAG_POW2_MAX", "MLA_INJECT_WITHHOLD_K_LOAD", "NOALLOC_SCRATCH_BYTES", "Plan", "check", "decode",
            "decode_diag", "decode_fp8", "decode_noalloc",
            "load_library", "num_units", "parse_plan",
-           "plan", "plan_device_bytes", "prolog", "rope_table", "plan_host", "plan_layout", "workspace_size"]
+           "plan", "plan_device_bytes", "prolog", "rope_table", "plan_host", "plan_layout", "workspace_size",
+           "MLA_DEV_BAD_OFFSETS", "MLA_DEV_BAD_PATH", "TREE_MAX_NODES", "TreePlan", "cache_append", "cache_append_fp8",
+           "cache_commit", "cache_commit_fp8", "query", "tree_decode", "tree_decode_fp8", "tree_plan",
+           "tree_plan_device", "tree_plan_host", "tree_workspace_size"]

@@ -9,6 +9,7 @@ no CPU path: if the library is missing, every call raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -46,7 +47,14 @@ class _Problem(ctypes.Structure):
                 ("max_pages_per_seq", ctypes.c_int32), ("flags", ctypes.c_int32)]
 
 
+class _Ragged(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("tokens", ctypes.c_int32),
+                ("num_heads", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("max_pages_per_seq", ctypes.c_int32), ("flags", ctypes.c_int32)]
+
+
 _P = ctypes.POINTER(_Problem)
+_R = ctypes.POINTER(_Ragged)
 _vp = ctypes.c_void_p
 _SIGS = {
     "mla_decode_workspace_size": (ctypes.c_int, [_P, ctypes.POINTER(ctypes.c_size_t)]),
@@ -73,7 +81,21 @@ _SIGS = {
     "mla_epilog_uv": (ctypes.c_int, [_P, _vp, _vp, _vp, _vp, _vp]),
     "mla_cache_quantize_fp8": (ctypes.c_int, [_vp, ctypes.c_int64, _vp, _vp]),
     "mla_epilog_oproj": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, _vp, _vp, _vp, _vp, _vp]),
+    "mla_query": (ctypes.c_int, [ctypes.c_int32, _vp, ctypes.c_int64, ctypes.c_int64, _vp, ctypes.c_int64,
+                                 ctypes.c_int64, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "mla_cache_append": (ctypes.c_int, [_R, _vp, ctypes.c_int64, _vp, ctypes.c_int64, _vp, ctypes.c_float, _vp, _vp,
+                                        _vp, ctypes.c_int64, _vp, _vp, _vp, _vp, _vp]),
+    "mla_tree_workspace_size": (ctypes.c_int, [_R, ctypes.POINTER(ctypes.c_size_t)]),
+    "mla_tree_plan": (ctypes.c_int, [_R, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "mla_tree_decode": (ctypes.c_int, [_R, _vp, _vp, _vp, ctypes.c_int64, _vp, ctypes.c_float, _vp, _vp, _vp,
+                                       ctypes.c_size_t, _vp]),
+    "mla_tree_plan_bytes": (ctypes.c_size_t, [_R, ctypes.c_int32]),
+    "mla_tree_plan_host": (ctypes.c_int, [_R, _vp, _vp, _vp, ctypes.c_int32, _vp, ctypes.c_size_t]),
+    "mla_cache_commit": (ctypes.c_int, [_R, _vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int64, _vp,
+                                        _vp, _vp, _vp, ctypes.c_int32, _vp, _vp, _vp, _vp]),
 }
+for _name in ("mla_cache_append", "mla_tree_decode"):   # the fp8 entry points take the same arguments
+    _SIGS[_name + "_fp8"] = _SIGS[_name]
 
 
 def load_library(path: str | None = None) -> ctypes.CDLL:
@@ -472,8 +494,325 @@ def quantize_cache_fp8(kv_cache, *, out=None, stream=None):
     return out
 
 
-def check(p: Plan, stream=None) -> int:
-    """Synchronise and return the device status bits (0 = no input error seen)."""
+# ----------------------------------------------------------------------------- trees of drafted tokens
+
+TREE_MAX_NODES = 64
+MLA_DEV_BAD_OFFSETS = 0x10
+MLA_DEV_BAD_PATH = 0x20
+
+
+def _launch_on(dev, stream):
+    """Context of a call: its device, and its stream as the current one, so that what the call
+    allocates or clears belongs to that stream too."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream must be one of {dev}, the tensors' device")
+    return torch.cuda.stream(stream)
+
+
+def _ragged(batch: int, tokens: int, max_pages: int, flags: int = 0) -> _Ragged:
+    return _Ragged(int(batch), int(tokens), NUM_HEADS, PAGE_SIZE, int(max_pages), int(flags))
+
+
+def _req_index(t, name, dtype, shape, device):
+    """An index array: contiguous, of one dtype and shape (None: any extent), on the device."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device.type != "cuda" or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be on {device or 'a CUDA device'}")
+    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _strides(t, name, shape, device):
+    """A bf16 input whose last dim is contiguous -> its other dims' strides in elements.
+
+    The others may be strided (a view of a larger projection): positive multiples of 8.
+    """
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.device.type != "cuda" or (device is not None and t.device != device):
+        raise ValueError(f"{name} must be on {device or 'a CUDA device'}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.data_ptr() % 16:
+        raise ValueError(f"{name} must be 16-byte aligned")
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    # the stride of a dimension of one element is never used: any legal value does
+    st = [8 if n == 1 else v for n, v in zip(shape[:-1], st)]
+    if any(v < 1 or v % 8 or v >= 1 << 31 for v in st):
+        raise ValueError(f"{name}'s strides must be positive multiples of 8")
+    return st
+
+
+def _req_out(t, name, dtype, shape, device):
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _req(t, name, dtype, shape, device)
+    return t
+
+
+def _req_status(status, device):
+    import torch
+    if status is None:
+        return torch.zeros(1, dtype=torch.int32, device=device)
+    _req_index(status, "status", torch.int32, (1,), device)
+    return status
+
+
+def _rope_table_for(table, rope_base, dev, stream, what):
+    """The caller's table, or the one of rope_base, built once per device and kept."""
+    import torch
+    if table is None:
+        key = (dev.index, float(rope_base))
+        table = _rope_tables.get(key)
+        if table is None:
+            # the kept table must hold its values for every later call on any stream
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError(f"{what}: build the rotary table with rope_table() before "
+                                   "capturing a CUDA graph, and pass it as table=")
+            table = rope_table(rope_base, dev, stream)
+            (stream if stream is not None else torch.cuda.current_stream()).synchronize()
+            _rope_tables[key] = table
+    _req_index(table, "table", torch.float32, (ROPE_TABLE_FLOATS,), dev)
+    return table
+
+
+def query(q_nope, q_pe, w_uk, positions, *, rope_base: float = DEFAULT_ROPE_BASE, table=None, q_latent=None,
+          q_rope=None, status=None, stream=None):
+    """Absorbed and rotated queries at explicit positions (``mla_query``).
+
+    q_nope [T][128][128] and q_pe [T][128][64] bf16 (last dim contiguous, otherwise strided:
+    both may be views of one projection's output), w_uk [128][128][512] bf16, positions [T]
+    int32; a negative position leaves the token's output rows as they were.  table: a
+    rope_table() tensor; without one, the table of rope_base is built once per device and
+    kept.  Returns (q_latent [T][128][512], q_rope [T][128][64], status): status is a
+    one-element int32 device tensor of MLA_DEV_* bits.
+    """
+    import torch
+    if q_nope.dim() != 3 or q_nope.shape[0] < 1:
+        raise ValueError("q_nope must be [tokens][heads][128]")
+    T, dev = q_nope.shape[0], q_nope.device
+    ns = _strides(q_nope, "q_nope", (T, NUM_HEADS, D_NOPE), None)
+    ps = _strides(q_pe, "q_pe", (T, NUM_HEADS, D_ROPE), dev)
+    _req(w_uk, "w_uk", torch.bfloat16, (NUM_HEADS, D_NOPE, D_LATENT), dev)
+    _req_index(positions, "positions", torch.int32, (T,), dev)
+    with _launch_on(dev, stream):
+        table = _rope_table_for(table, rope_base, dev, stream, "query")
+        q_latent = _req_out(q_latent, "q_latent", torch.bfloat16, (T, NUM_HEADS, D_LATENT), dev)
+        q_rope = _req_out(q_rope, "q_rope", torch.bfloat16, (T, NUM_HEADS, D_ROPE), dev)
+        status = _req_status(status, dev)
+        _check(load_library().mla_query(
+            T, q_nope.data_ptr(), ns[0], ns[1], q_pe.data_ptr(), ps[0], ps[1], w_uk.data_ptr(), table.data_ptr(),
+            positions.data_ptr(), q_latent.data_ptr(), q_rope.data_ptr(), status.data_ptr(),
+            _stream_handle(None)), "mla_query")
+    return q_latent, q_rope, status
+
+
+def cache_append(kv_latent, k_pe, kv_norm_weight, kv_cache, block_table, seq_lens, token_offsets, *, positions=None,
+                 rope_base: float = DEFAULT_ROPE_BASE, rms_eps: float = DEFAULT_RMS_EPS, table=None, status=None,
+                 stream=None):
+    """Append ragged tokens to the paged cache (``mla_cache_append``) -> status.
+
+    kv_latent [T][512] (before RMSNorm) and k_pe [T][64] (before RoPE) bf16, last dim contiguous,
+    rows strided at will; kv_norm_weight [512] bf16; kv_cache [pages][64][576] bf16, updated in
+    place; block_table [B][max_pages], seq_lens [B] (these tokens counted) and token_offsets
+    [B + 1] int32: request b's tokens are rows token_offsets[b] .. token_offsets[b + 1] - 1 and
+    go to its last slots.  positions [T] int32: RoPE positions (default: the slots); a negative
+    one leaves the token out.  table, status as in ``query``.
+    """
+    return _append(kv_latent, k_pe, kv_norm_weight, kv_cache, block_table, seq_lens, token_offsets, positions,
+                   rope_base, rms_eps, table, status, stream, False)
+
+
+def cache_append_fp8(kv_latent, k_pe, kv_norm_weight, kv_cache_fp8, block_table, seq_lens, token_offsets, *,
+                     positions=None, rope_base: float = DEFAULT_ROPE_BASE, rms_eps: float = DEFAULT_RMS_EPS,
+                     table=None, status=None, stream=None):
+    """``cache_append`` into an fp8 cache (``mla_cache_append_fp8``; uint8 [pages][64][656])."""
+    return _append(kv_latent, k_pe, kv_norm_weight, kv_cache_fp8, block_table, seq_lens, token_offsets, positions,
+                   rope_base, rms_eps, table, status, stream, True)
+
+
+def _append(kv_latent, k_pe, kv_norm_weight, kv_cache, block_table, seq_lens, token_offsets, positions, rope_base,
+            rms_eps, table, status, stream, fp8):
+    import torch
+    if kv_latent.dim() != 2 or kv_latent.shape[0] < 1:
+        raise ValueError("kv_latent must be [tokens][512]")
+    T, dev = kv_latent.shape[0], kv_latent.device
+    ls = _strides(kv_latent, "kv_latent", (T, D_LATENT), None)
+    ks = _strides(k_pe, "k_pe", (T, D_ROPE), dev)
+    _req(kv_norm_weight, "kv_norm_weight", torch.bfloat16, (D_LATENT,), dev)
+    _req_cache(kv_cache, dev, fp8)
+    _req_index(block_table, "block_table", torch.int32, (None, None), dev)
+    B = block_table.shape[0]
+    _req_index(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    _req_index(token_offsets, "token_offsets", torch.int32, (B + 1,), dev)
+    if positions is not None:
+        _req_index(positions, "positions", torch.int32, (T,), dev)
+    name = "mla_cache_append_fp8" if fp8 else "mla_cache_append"
+    with _launch_on(dev, stream):
+        table = _rope_table_for(table, rope_base, dev, stream, "cache_append")
+        status = _req_status(status, dev)
+        prob = _ragged(B, T, block_table.shape[1])
+        _check(getattr(load_library(), name)(
+            ctypes.byref(prob), kv_latent.data_ptr(), ls[0], k_pe.data_ptr(), ks[0], kv_norm_weight.data_ptr(),
+            float(rms_eps), table.data_ptr(), positions.data_ptr() if positions is not None else None,
+            kv_cache.data_ptr(), kv_cache.shape[0], block_table.data_ptr(), seq_lens.data_ptr(),
+            token_offsets.data_ptr(), status.data_ptr(), _stream_handle(None)), name)
+    return status
+
+
+def _req_cache(kv_cache, dev, fp8, layers=False):
+    import torch
+    name = "kv_cache_fp8" if fp8 else "kv_cache"
+    _req(kv_cache, name, torch.uint8 if fp8 else torch.bfloat16, None, dev)
+    row = FP8_ROW_BYTES if fp8 else D_LATENT + D_ROPE
+    if kv_cache.dim() not in ((3, 4) if layers else (3,)) or tuple(kv_cache.shape[-2:]) != (PAGE_SIZE, row):
+        raise ValueError(f"{name} must be {'([layers])' if layers else ''}[num_pages][64][{row}]")
+
+
+@dataclass
+class TreePlan:
+    """A split-KV schedule of a batch of trees in a device workspace (one step's lengths, offsets and masks)."""
+    batch: int
+    tokens: int
+    max_pages: int
+    workspace: object   # torch.uint8 CUDA tensor, owned by this TreePlan
+
+    def problem(self, flags: int = 0) -> _Ragged:
+        return _ragged(self.batch, self.tokens, self.max_pages, flags)
+
+
+def tree_workspace_size(batch: int, tokens: int, max_pages: int) -> int:
+    n = ctypes.c_size_t(0)
+    prob = _ragged(batch, tokens, max_pages)
+    _check(load_library().mla_tree_workspace_size(ctypes.byref(prob), ctypes.byref(n)), "mla_tree_workspace_size")
+    return n.value
+
+
+def tree_plan(seq_lens, token_offsets, masks, *, max_pages_per_seq: int, workspace=None, stream=None) -> TreePlan:
+    """Build the schedule of a batch of drafted trees on the device (``mla_tree_plan``).
+
+    seq_lens [B] int32 (cached keys, the trees' nodes included), token_offsets [B + 1] int32 (request
+    b's nodes are rows token_offsets[b] .. token_offsets[b + 1] - 1 of the token arrays; at most
+    64 each), masks [T] int64: bit j of a node's mask is set if it sees node j of its tree.  T may
+    exceed token_offsets[B] (padding).  The plan serves every layer of the step; calls that share
+    it must be ordered.
+    """
+    import torch
+    _req_index(seq_lens, "seq_lens", torch.int32, (None,), None)
+    B, dev = seq_lens.shape[0], seq_lens.device
+    _req_index(token_offsets, "token_offsets", torch.int32, (B + 1,), dev)
+    _req_index(masks, "masks", torch.int64, (None,), dev)
+    T = masks.shape[0]
+    with _launch_on(dev, stream):
+        if workspace is None:
+            workspace = torch.empty(tree_workspace_size(B, T, max_pages_per_seq), dtype=torch.uint8, device=dev)
+        _req(workspace, "workspace", torch.uint8, None, dev)
+        prob = _ragged(B, T, max_pages_per_seq)
+        _check(load_library().mla_tree_plan(ctypes.byref(prob), seq_lens.data_ptr(), token_offsets.data_ptr(),
+                                            masks.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                            _stream_handle(None)), "mla_tree_plan")
+    return TreePlan(B, T, int(max_pages_per_seq), workspace)
+
+
+def tree_decode(p: TreePlan, q_latent, q_rope, kv_cache, block_table, *, scale: float = DEFAULT_SCALE, out=None,
+                lse=None, stream=None, pow2_max: bool = False):
+    """Attention of drafted trees over the paged cache (``mla_tree_decode``) -> (o_latent bf16, lse fp32).
+
+    q_latent [T][128][512], q_rope [T][128][64] bf16; outputs [T][128][512] and [T][128].  A node
+    that sees no key gives o = 0 and lse = -inf; rows behind the last request are not written.
+    ``check(p)`` reads the status bits.  pow2_max as in ``decode``.
+    """
+    return _tree_decode(p, q_latent, q_rope, kv_cache, block_table, scale, out, lse, stream, pow2_max, False)
+
+
+def tree_decode_fp8(p: TreePlan, q_latent, q_rope, kv_cache_fp8, block_table, *, scale: float = DEFAULT_SCALE,
+                    out=None, lse=None, stream=None, pow2_max: bool = False):
+    """``tree_decode`` over an fp8 cache (``mla_tree_decode_fp8``; uint8 [pages][64][656])."""
+    return _tree_decode(p, q_latent, q_rope, kv_cache_fp8, block_table, scale, out, lse, stream, pow2_max, True)
+
+
+def _tree_decode(p, q_latent, q_rope, kv_cache, block_table, scale, out, lse, stream, pow2_max, fp8):
+    import torch
+    dev, T = p.workspace.device, p.tokens
+    _req(q_latent, "q_latent", torch.bfloat16, (T, NUM_HEADS, D_LATENT), dev)
+    _req(q_rope, "q_rope", torch.bfloat16, (T, NUM_HEADS, D_ROPE), dev)
+    _req_cache(kv_cache, dev, fp8)
+    _req_index(block_table, "block_table", torch.int32, (p.batch, p.max_pages), dev)
+    name = "mla_tree_decode_fp8" if fp8 else "mla_tree_decode"
+    with _launch_on(dev, stream):
+        out = _req_out(out, "out", torch.bfloat16, (T, NUM_HEADS, D_LATENT), dev)
+        lse = _req_out(lse, "lse", torch.float32, (T, NUM_HEADS), dev)
+        prob = p.problem(MLA_FLAG_POW2_MAX if pow2_max else 0)
+        _check(getattr(load_library(), name)(
+            ctypes.byref(prob), q_latent.data_ptr(), q_rope.data_ptr(), kv_cache.data_ptr(), kv_cache.shape[0],
+            block_table.data_ptr(), float(scale), out.data_ptr(), lse.data_ptr(), p.workspace.data_ptr(),
+            p.workspace.numel(), _stream_handle(None)), name)
+    return out, lse
+
+
+def cache_commit(kv_cache, block_table, seq_lens, token_offsets, paths, path_lens, *, new_seq_lens=None, status=None,
+                 stream=None):
+    """Move the accepted nodes' rows to the front of their trees' slots (``mla_cache_commit``).
+
+    kv_cache [pages][64][576] or [layers][pages][64][576] bf16, updated in place in every layer;
+    paths [B][max_path] int32 (strictly increasing node indices, max_path <= 64), path_lens [B]
+    int32; block_table, seq_lens and token_offsets as in ``cache_append``.  Returns
+    (new_seq_lens [B] int32, status).
+    """
+    return _commit(kv_cache, block_table, seq_lens, token_offsets, paths, path_lens, new_seq_lens, status, stream,
+                   False)
+
+
+def cache_commit_fp8(kv_cache_fp8, block_table, seq_lens, token_offsets, paths, path_lens, *, new_seq_lens=None,
+                     status=None, stream=None):
+    """``cache_commit`` for fp8 caches (uint8 [pages][64][656] or [layers][pages][64][656])."""
+    return _commit(kv_cache_fp8, block_table, seq_lens, token_offsets, paths, path_lens, new_seq_lens, status, stream,
+                   True)
+
+
+def _commit(kv_cache, block_table, seq_lens, token_offsets, paths, path_lens, new_seq_lens, status, stream, fp8):
+    import torch
+    _req_index(block_table, "block_table", torch.int32, (None, None), None)
+    B, dev = block_table.shape[0], block_table.device
+    _req_cache(kv_cache, dev, fp8, layers=True)
+    _req_index(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    _req_index(token_offsets, "token_offsets", torch.int32, (B + 1,), dev)
+    _req_index(paths, "paths", torch.int32, (B, None), dev)
+    _req_index(path_lens, "path_lens", torch.int32, (B,), dev)
+    row = FP8_ROW_BYTES if fp8 else 2 * (D_LATENT + D_ROPE)
+    layers, pages = (kv_cache.shape[0] if kv_cache.dim() == 4 else 1), kv_cache.shape[-3]
+    with _launch_on(dev, stream):
+        if new_seq_lens is None:
+            new_seq_lens = torch.empty(B, dtype=torch.int32, device=dev)
+        _req_index(new_seq_lens, "new_seq_lens", torch.int32, (B,), dev)
+        status = _req_status(status, dev)
+        # the tokens bound the offsets; here the trees' own sizes do
+        prob = _ragged(B, (1 << 24) - 1, block_table.shape[1])
+        _check(load_library().mla_cache_commit(
+            ctypes.byref(prob), kv_cache.data_ptr(), layers, pages * PAGE_SIZE * row, row, pages,
+            block_table.data_ptr(), seq_lens.data_ptr(), token_offsets.data_ptr(), paths.data_ptr(), paths.shape[1],
+            path_lens.data_ptr(), new_seq_lens.data_ptr(), status.data_ptr(), _stream_handle(None)),
+            "mla_cache_commit")
+    return new_seq_lens, status
+
+
+def check(p, stream=None) -> int:
+    """Synchronise and return the device status bits of a Plan or TreePlan (0 = no input error seen)."""
     import torch
     v = ctypes.c_int32(0)
     with torch.cuda.device(p.workspace.device):
@@ -490,8 +829,11 @@ def _align(x: int, a: int) -> int:
     return (x + a - 1) // a * a
 
 
-def plan_layout(batch: int, s_q: int, units: int) -> dict:
-    """Byte offsets of the schedule regions (mirrors plan_layout in csrc/mla_internal.h)."""
+def plan_layout(batch: int, s_q: int, units: int, tree: bool = False) -> dict:
+    """Byte offsets of the schedule regions (mirrors make_layout in csrc/mla_internal.h).
+
+    A tree schedule has one row per token: batch * s_q is then the number of tokens.
+    """
     rows = batch * s_q
     max_items = rows + units
     off = 64
@@ -510,6 +852,10 @@ def plan_layout(batch: int, s_q: int, units: int) -> dict:
     off = _align(off, 8)
     L["row_pos"] = off
     off += 8 * rows
+    if tree:
+        off = _align(off, 16)
+        L["tree_rows"] = off
+        off += 16 * rows
     L["plan_end"] = off
     return L
 
@@ -521,15 +867,20 @@ _HDR = np.dtype([("magic", "<u4"), ("batch", "<i4"), ("s_q", "<i4"), ("max_pages
                  ("target", "<i8")])
 
 
-def parse_plan(buf, batch: int, s_q: int, units: int) -> dict:
+_TREE_ROW = np.dtype([("mask", "<u8"), ("context", "<i4"), ("req", "<i4")])
+
+
+def parse_plan(buf, batch: int, s_q: int, units: int, tree: bool = False) -> dict:
     """Decode schedule bytes (host copy of a workspace prefix) into numpy arrays."""
     b = np.frombuffer(bytes(buf), dtype=np.uint8)
-    L = plan_layout(batch, s_q, units)
+    L = plan_layout(batch, s_q, units, tree)
     hdr = b[:64].view(_HDR)[0]
     n = int(hdr["num_items"])
     R = L["num_rows"]
     items = b[L["items"]:L["items"] + 16 * n].view("<i4").reshape(n, 4)
+    more = {"tree_rows": b[L["tree_rows"]:L["tree_rows"] + 16 * R].view(_TREE_ROW).copy()} if tree else {}
     return {
+        **more,
         "header": {k: int(hdr[k]) for k in _HDR.names},
         "items": items.copy(),   # columns: row, kv_begin, kv_end, part
         "item_unit": b[L["item_unit"]:L["item_unit"] + 4 * n].view("<i4").copy(),
@@ -561,3 +912,23 @@ def plan_device_bytes(p: Plan) -> bytes:
     """Host copy of a device schedule (for tests)."""
     L = plan_layout(p.batch, p.s_q, num_units())
     return p.workspace[:L["plan_end"]].cpu().numpy().tobytes()
+
+
+def tree_plan_host(seq_lens, token_offsets, masks, *, max_pages_per_seq: int, num_units: int) -> dict:
+    """Run the tree planner's algorithm on the CPU (``mla_tree_plan_host``) and parse it."""
+    lib = load_library()
+    sl, off = np.ascontiguousarray(seq_lens, np.int32), np.ascontiguousarray(token_offsets, np.int32)
+    m = np.ascontiguousarray(masks, np.uint64)
+    prob = _ragged(sl.shape[0], m.shape[0], max_pages_per_seq)
+    nbytes = lib.mla_tree_plan_bytes(ctypes.byref(prob), int(num_units))
+    buf = np.zeros(max(nbytes, 1), dtype=np.uint8)
+    _check(lib.mla_tree_plan_host(ctypes.byref(prob), sl.ctypes.data, off.ctypes.data, m.ctypes.data, int(num_units),
+                                  buf.ctypes.data, nbytes), "mla_tree_plan_host")
+    return parse_plan(buf.tobytes(), 1, m.shape[0], num_units, tree=True)
+
+
+def tree_plan_device(p: TreePlan) -> dict:
+    """Host copy of a device schedule of trees, parsed (for tests)."""
+    units = num_units()
+    end = plan_layout(1, p.tokens, units, tree=True)["plan_end"]
+    return parse_plan(p.workspace[:end].cpu().numpy().tobytes(), 1, p.tokens, units, tree=True)

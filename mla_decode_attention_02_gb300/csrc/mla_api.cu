@@ -9,6 +9,7 @@
 #include <cstring>
 
 #include "mla_internal.h"
+#include "mla_tree.h"
 
 namespace mla {
 mla_status plan_host(const mla_problem *prob, const int32_t *seq_lens, int32_t num_units,
@@ -16,14 +17,19 @@ mla_status plan_host(const mla_problem *prob, const int32_t *seq_lens, int32_t n
 cudaError_t launch_plan(const int32_t *seq_lens, void *ws, int32_t batch, int32_t s_q,
                         int32_t max_pages, int32_t num_units, cudaStream_t stream);
 cudaError_t launch_combine(const void *ws, void *o_latent, float *lse, int32_t batch, int32_t s_q,
-                           int32_t num_units, cudaStream_t stream);
+                           int32_t num_units, bool tree, cudaStream_t stream);
 cudaError_t main_units(int32_t *units);
 bool plan_fits(int32_t rows, int32_t units);
 cudaError_t launch_main(const void *q_latent, const void *q_rope, const void *kv,
                         int64_t num_pages, const int32_t *block_table, float scale, void *ws,
                         void *o_latent, float *lse, int32_t batch, int32_t s_q, int32_t max_pages,
                         int32_t num_units, uint64_t wait_limit_ns, uint32_t test_flags,
-                        uint32_t flags, bool fp8, cudaStream_t stream);
+                        uint32_t flags, bool fp8, bool tree, cudaStream_t stream);
+mla_status tree_plan_host(const mla_ragged *prob, const int32_t *seq_lens, const int32_t *offsets,
+                          const uint64_t *masks, int32_t num_units, uint8_t *ws);
+cudaError_t launch_tree_plan(const int32_t *seq_lens, const int32_t *offsets, const uint64_t *masks, void *ws,
+                             int32_t batch, int32_t tokens, int32_t max_pages, int32_t num_units,
+                             cudaStream_t stream);
 constexpr uint64_t kDefaultWaitLimitNs = 2000000000ull;  // a bounded device wait gives up after 2 s
 }  // namespace mla
 
@@ -172,9 +178,9 @@ static mla_status decode_impl(const mla_problem *prob, const void *q_latent, con
     cudaError_t e = mla::launch_main(q_latent, q_rope, kv_cache, num_pages, block_table, scale,
                                      workspace, o_latent, lse, prob->batch, prob->s_q,
                                      prob->max_pages_per_seq, units, wait_limit_ns, test_flags,
-                                     (uint32_t)prob->flags, fp8, s);
+                                     (uint32_t)prob->flags, fp8, false, s);
     if (e != cudaSuccess || !mark(1)) return MLA_ERR_CUDA;
-    e = mla::launch_combine(workspace, o_latent, lse, prob->batch, prob->s_q, units, s);
+    e = mla::launch_combine(workspace, o_latent, lse, prob->batch, prob->s_q, units, false, s);
     if (e != cudaSuccess || !mark(2)) return MLA_ERR_CUDA;
     return MLA_OK;
 }
@@ -228,6 +234,95 @@ mla_status mla_decode_check(const void *workspace, int32_t *device_status, mla_s
     *device_status = v;
     if (v == 0) return MLA_OK;
     return (v & MLA_DEV_TIMEOUT) ? MLA_ERR_TIMEOUT : MLA_ERR_DEVICE_CHECK;
+}
+
+// ---------------------------------------------------------------- trees of drafted tokens
+
+mla_status mla_tree_workspace_size(const mla_ragged *prob, size_t *bytes) {
+    mla_status st = mla::check_ragged(prob, MLA_FLAG_POW2_MAX);
+    if (st != MLA_OK) return st;
+    if (!bytes) return MLA_ERR_INVALID_ARG;
+    int32_t units = 0;
+    if (mla::main_units(&units) != cudaSuccess) return MLA_ERR_CUDA;
+    if (!mla::plan_fits(prob->tokens, units)) return MLA_ERR_UNSUPPORTED;
+    *bytes = mla::make_layout(prob->tokens, units, true).total;
+    return MLA_OK;
+}
+
+size_t mla_tree_plan_bytes(const mla_ragged *prob, int32_t num_units) {
+    if (mla::check_ragged(prob, MLA_FLAG_POW2_MAX) != MLA_OK || num_units < 1) return 0;
+    return mla::make_layout(prob->tokens, num_units, true).plan_end;
+}
+
+mla_status mla_tree_plan_host(const mla_ragged *prob, const int32_t *seq_lens_host, const int32_t *token_offsets_host,
+                              const uint64_t *masks_host, int32_t num_units, void *plan_host, size_t plan_bytes) {
+    mla_status st = mla::check_ragged(prob, MLA_FLAG_POW2_MAX);
+    if (st != MLA_OK) return st;
+    if (!seq_lens_host || !token_offsets_host || !masks_host || !plan_host || num_units < 1) return MLA_ERR_INVALID_ARG;
+    if (plan_bytes < mla::make_layout(prob->tokens, num_units, true).plan_end) return MLA_ERR_WORKSPACE;
+    return mla::tree_plan_host(prob, seq_lens_host, token_offsets_host, masks_host, num_units,
+                               static_cast<uint8_t *>(plan_host));
+}
+
+mla_status mla_tree_plan(const mla_ragged *prob, const int32_t *seq_lens, const int32_t *token_offsets,
+                         const uint64_t *masks, void *workspace, size_t workspace_bytes, mla_stream_t stream) {
+    mla::NvtxRange nvtx_range("mla_tree_plan");
+    mla_status st = mla::check_ragged(prob, MLA_FLAG_POW2_MAX);
+    if (st != MLA_OK) return st;
+    if (!seq_lens || (reinterpret_cast<uintptr_t>(seq_lens) & 3u) || !token_offsets ||
+        (reinterpret_cast<uintptr_t>(token_offsets) & 3u) || !masks || (reinterpret_cast<uintptr_t>(masks) & 7u) ||
+        !workspace || !aligned16(workspace))
+        return MLA_ERR_INVALID_ARG;
+    if (workspace_bytes < mla::make_layout(prob->tokens, 1, true).total) return MLA_ERR_WORKSPACE;
+    int32_t units = 0;
+    if (mla::main_units(&units) != cudaSuccess) return MLA_ERR_CUDA;
+    if (!mla::plan_fits(prob->tokens, units)) return MLA_ERR_UNSUPPORTED;
+    if (workspace_bytes < mla::make_layout(prob->tokens, units, true).total) return MLA_ERR_WORKSPACE;
+    const cudaError_t e = mla::launch_tree_plan(seq_lens, token_offsets, masks, workspace, prob->batch, prob->tokens,
+                                                prob->max_pages_per_seq, units, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+static mla_status tree_impl(const mla_ragged *prob, const void *q_latent, const void *q_rope, const void *kv_cache,
+                            int64_t num_pages, const int32_t *block_table, float scale, void *o_latent, float *lse,
+                            void *workspace, size_t workspace_bytes, bool fp8, mla_stream_t stream) {
+    mla_status st = mla::check_ragged(prob, MLA_FLAG_POW2_MAX);
+    if (st != MLA_OK) return st;
+    const void *ptrs[] = {q_latent, q_rope, kv_cache, o_latent, lse, workspace};
+    for (const void *p : ptrs)
+        if (!p || !aligned16(p)) return MLA_ERR_INVALID_ARG;
+    if (!block_table || (reinterpret_cast<uintptr_t>(block_table) & 3u)) return MLA_ERR_INVALID_ARG;
+    if (num_pages < 1 || num_pages > ((int64_t)1 << 31) - 1) return MLA_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || !(scale > 0.f)) return MLA_ERR_INVALID_ARG;
+    if (workspace_bytes < mla::make_layout(prob->tokens, 1, true).total) return MLA_ERR_WORKSPACE;
+    int32_t units = 0;
+    if (mla::main_units(&units) != cudaSuccess) return MLA_ERR_CUDA;
+    if (!mla::plan_fits(prob->tokens, units)) return MLA_ERR_UNSUPPORTED;
+    if (workspace_bytes < mla::make_layout(prob->tokens, units, true).total) return MLA_ERR_WORKSPACE;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = mla::launch_main(q_latent, q_rope, kv_cache, num_pages, block_table, scale, workspace, o_latent,
+                                     lse, prob->batch, prob->tokens, prob->max_pages_per_seq, units,
+                                     mla::kDefaultWaitLimitNs, 0, (uint32_t)prob->flags, fp8, true, s);
+    if (e != cudaSuccess) return MLA_ERR_CUDA;
+    e = mla::launch_combine(workspace, o_latent, lse, prob->batch, prob->tokens, units, true, s);
+    return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+mla_status mla_tree_decode(const mla_ragged *prob, const void *q_latent, const void *q_rope, const void *kv_cache,
+                           int64_t num_pages, const int32_t *block_table, float scale, void *o_latent, float *lse,
+                           void *workspace, size_t workspace_bytes, mla_stream_t stream) {
+    mla::NvtxRange nvtx_range("mla_tree_decode");
+    return tree_impl(prob, q_latent, q_rope, kv_cache, num_pages, block_table, scale, o_latent, lse, workspace,
+                     workspace_bytes, false, stream);
+}
+
+mla_status mla_tree_decode_fp8(const mla_ragged *prob, const void *q_latent, const void *q_rope,
+                               const void *kv_cache_fp8, int64_t num_pages, const int32_t *block_table, float scale,
+                               void *o_latent, float *lse, void *workspace, size_t workspace_bytes,
+                               mla_stream_t stream) {
+    mla::NvtxRange nvtx_range("mla_tree_decode_fp8");
+    return tree_impl(prob, q_latent, q_rope, kv_cache_fp8, num_pages, block_table, scale, o_latent, lse, workspace,
+                     workspace_bytes, true, stream);
 }
 
 }  // extern "C"

@@ -135,6 +135,9 @@ __device__ __forceinline__ void merge_task_cta(int32_t r, int32_t h, int32_t n, 
     __syncthreads();   // red / red_m are reused by the next task
 }
 
+// kTree: s_q is the number of tokens (rows); rows that see no key are written
+// here, rows behind the last request are not written at all.
+template <bool kTree>
 __global__ void __launch_bounds__(32 * kCombineWarps, 3)
 mla_combine_kernel(const uint8_t *__restrict__ ws, __nv_bfloat16 *__restrict__ o_latent,
                    float *__restrict__ lse_out, int32_t batch, int32_t s_q, int32_t num_units) {
@@ -145,8 +148,14 @@ mla_combine_kernel(const uint8_t *__restrict__ ws, __nv_bfloat16 *__restrict__ o
     // nothing to merge when no row was split and every row was valid: the main
     // kernel wrote every output itself
     const PlanHeader *hdr = reinterpret_cast<const PlanHeader *>(ws);
-    if (hdr->num_parts == 0 && (hdr->status & MLA_DEV_BAD_SEQ_LEN) == 0) return;
-    const PlanLayout L = plan_layout(batch, s_q, num_units);
+    if constexpr (kTree) {
+        // (a workspace that holds another schedule was flagged by the main kernel)
+        if (hdr->magic != kTreeMagic || hdr->batch != batch || hdr->s_q != s_q || hdr->num_units != num_units) return;
+        if (hdr->num_parts == 0 && (hdr->split & 2) == 0) return;
+    } else {
+        if (hdr->num_parts == 0 && (hdr->status & MLA_DEV_BAD_SEQ_LEN) == 0) return;
+    }
+    const PlanLayout L = make_layout(kTree ? s_q : batch * s_q, num_units, kTree);
     const int32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t tasks = (int64_t)L.num_rows * kHeads;
     const int32_t *row_nparts = reinterpret_cast<const int32_t *>(ws + L.row_nparts);
@@ -162,7 +171,13 @@ mla_combine_kernel(const uint8_t *__restrict__ ws, __nv_bfloat16 *__restrict__ o
         const int32_t h = (int32_t)(task % kHeads);
         const int32_t n = row_nparts[r];
         if (n == 1 || n > kWarpParts) continue;  // written by the main kernel / merged below
+        if (kTree && n == kRowUnused) continue;
         __nv_bfloat16 *orow = o_latent + ((size_t)r * kHeads + h) * kDl;
+        if (kTree && n == kRowEmpty) {
+            for (int d = lane; d < kDl; d += 32) orow[d] = __float2bfloat16(0.f);
+            if (lane == 0) lse_out[(size_t)r * kHeads + h] = -INFINITY;
+            continue;
+        }
         if (n == 0) {          // invalid row (bad seq_len): NaN, flagged in the status word
             const __nv_bfloat16 nan = __float2bfloat16(__int_as_float(0x7fc00000));
             for (int d = lane; d < kDl; d += 32) orow[d] = nan;
@@ -229,8 +244,8 @@ mla_combine_kernel(const uint8_t *__restrict__ ws, __nv_bfloat16 *__restrict__ o
 }  // namespace
 
 cudaError_t launch_combine(const void *ws, void *o_latent, float *lse, int32_t batch, int32_t s_q,
-                           int32_t num_units, cudaStream_t stream) {
-    const int64_t tasks = (int64_t)batch * s_q * kHeads;
+                           int32_t num_units, bool tree, cudaStream_t stream) {
+    const int64_t tasks = (int64_t)(tree ? 1 : batch) * s_q * kHeads;
     const int grid = (int)(tasks < kCombineGrid ? tasks : kCombineGrid);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
@@ -241,8 +256,9 @@ cudaError_t launch_combine(const void *ws, void *o_latent, float *lse, int32_t b
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mla_combine_kernel, static_cast<const uint8_t *>(ws),
-                              static_cast<__nv_bfloat16 *>(o_latent), lse, batch, s_q, num_units);
+    return cudaLaunchKernelEx(&cfg, tree ? mla_combine_kernel<true> : mla_combine_kernel<false>,
+                              static_cast<const uint8_t *>(ws), static_cast<__nv_bfloat16 *>(o_latent), lse, batch,
+                              s_q, num_units);
 }
 
 }  // namespace mla

@@ -10,6 +10,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "mla_decode.h"
+#include "mla_tree.h"
 
 #if defined(__CUDACC__)
 #define MLA_HD __host__ __device__ __forceinline__
@@ -35,6 +36,7 @@ constexpr int kDr = MLA_D_ROPE;          // k_rope values per cached row
 constexpr int kDrow = kDl + kDr;         // 576 values per cached row
 constexpr int kPage = MLA_PAGE_SIZE;     // tokens per cache page
 constexpr uint32_t kPlanMagic = 0x31414c4du;  // "MLA1"
+constexpr uint32_t kTreeMagic = 0x54414c4du;  // "MLAT": the schedule of a batch of trees
 
 // Planner tuning, in units of one cache page of work (about 1.1 us of an SM
 // pair on this part): the fixed cost of a work item (query load, pipeline
@@ -55,34 +57,50 @@ struct PlanHeader {  // 64 bytes at workspace offset 0
     uint32_t magic;
     int32_t batch, s_q, max_pages;
     int32_t num_units, num_rows, max_items, num_items;
-    int32_t num_parts, status, split, min_split;  // split: rows may be cut (1) or not (0)
+    // split: bit 0, rows may be cut; bit 1 (tree schedules), the merge writes rows of its own
+    int32_t num_parts, status, split, min_split;
     int64_t total_cost, target;
 };
 static_assert(sizeof(PlanHeader) == 64, "header layout");
 
 // One contiguous key range of one (request, query token) row.
 struct WorkItem {
-    int32_t row;       // b * s_q + t
+    int32_t row;       // b * s_q + t; of a tree schedule: the token
     int32_t kv_begin;  // first key (a multiple of the page size)
     int32_t kv_end;    // one past the last key
     int32_t part;      // partial slot, or -1: this item is the whole row
 };
 static_assert(sizeof(WorkItem) == 16, "item layout");
 
-// Byte offsets of every region of the workspace.
+// A node of a tree schedule: the tree slots it sees (bits below its tree's
+// size), its request's context length and its request.
+struct TreeRow {
+    uint64_t mask;
+    int32_t context;
+    int32_t req;
+};
+static_assert(sizeof(TreeRow) == 16, "tree row layout");
+
+// row_nparts of rows without work items in a tree schedule (0: invalid, NaN).
+constexpr int32_t kRowEmpty = -1;    // sees no key: o = 0, lse = -infinity
+constexpr int32_t kRowUnused = -2;   // behind the last request: left as it is
+
+// Byte offsets of every region of the workspace (tree_rows: tree schedules only).
 struct PlanLayout {
-    size_t items, item_unit, unit_begin, row_nparts, row_part0, row_item0, row_pos, plan_end;
+    size_t items, item_unit, unit_begin, row_nparts, row_part0, row_item0, row_pos, tree_rows, plan_end;
     size_t lse_part, o_part, total;
     int32_t num_rows, max_items, max_parts;
 };
 
 MLA_HD size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-MLA_HD PlanLayout plan_layout(int32_t batch, int32_t s_q, int32_t num_units) {
+MLA_HD PlanLayout make_layout(int32_t num_rows, int32_t num_units, bool tree) {
     PlanLayout L;
-    L.num_rows = batch * s_q;
+    L.num_rows = num_rows;
     L.max_items = L.num_rows + num_units;
-    L.max_parts = L.max_items;
+    // a boundary between two units cuts at most one row, so cut rows come to at most
+    // 2 (num_units - 1) pieces; a batch of trees has many rows, and a partial is 256 KB
+    L.max_parts = tree && 2 * num_units < L.max_items ? 2 * num_units : L.max_items;
     size_t off = sizeof(PlanHeader);
     L.items = off;
     off += sizeof(WorkItem) * (size_t)L.max_items;
@@ -99,6 +117,12 @@ MLA_HD PlanLayout plan_layout(int32_t batch, int32_t s_q, int32_t num_units) {
     off = align_up(off, 8);
     L.row_pos = off;
     off += sizeof(int64_t) * (size_t)L.num_rows;
+    L.tree_rows = 0;
+    if (tree) {
+        off = align_up(off, 16);
+        L.tree_rows = off;
+        off += sizeof(TreeRow) * (size_t)L.num_rows;
+    }
     L.plan_end = off;
     off = align_up(off, 256);
     L.lse_part = off;
@@ -108,6 +132,27 @@ MLA_HD PlanLayout plan_layout(int32_t batch, int32_t s_q, int32_t num_units) {
     off += sizeof(float) * (size_t)L.max_parts * kHeads * kDl;
     L.total = align_up(off, 256);
     return L;
+}
+
+MLA_HD PlanLayout plan_layout(int32_t batch, int32_t s_q, int32_t num_units) {
+    return make_layout(batch * s_q, num_units, false);
+}
+
+// A node's keys: one past its last visible one (0: it sees none), given its
+// request's context length and its mask.  The keys in between may be masked.
+MLA_HD int32_t tree_end(int32_t context, uint64_t mask) {
+    int32_t bits = 0;
+    for (int32_t s = 32; s > 0; s >>= 1)
+        if (mask >> (bits + s - 1) >> 1) bits += s;
+    return mask ? context + bits + 1 : context;
+}
+
+// Bit j: whether token first + j of a page is visible.
+MLA_HD uint64_t tree_page_mask(int32_t context, uint64_t mask, int32_t first) {
+    const int32_t d = context - first;   // leading tokens that are context
+    if (d >= kPage) return ~0ull;
+    if (d > 0) return (mask << d) | ((1ull << d) - 1);
+    return -d < 64 ? mask >> -d : 0;
 }
 
 // Pages row r = (b, t) must read, or -1 when its seq_len is invalid.
@@ -167,6 +212,9 @@ MLA_HD int64_t mid_unit(int64_t x0, int64_t cost, int64_t target, int32_t num_un
 struct NoEmit {
     MLA_HD void operator()(int32_t, int32_t, int32_t, int32_t) const {}
 };
+
+// Checks of a ragged problem that make no CUDA call (flags: those allowed).
+mla_status check_ragged(const mla_ragged *p, int32_t flags);
 
 // Host-side argument checks of a decode call that make no CUDA call
 // (mla_api.cu); shared by mla_decode and the allocation-free entry point.

@@ -71,6 +71,15 @@
 // rings, which sets this variant's page rate (about twice the bf16 cache's
 // time per page, measured): the fp8 cache halves the bytes held per token,
 // not the time.
+//
+// Trees of drafted tokens (kTree): the same kernel over a schedule with one row
+// per node (mla_tree_plan).  All 128 heads of a node see the same keys, so the
+// mask of a page is one 64-bit word for the whole CTA: full pages of the context
+// take the unmasked path, and only the one or two pages that hold the tree's own
+// slots (64 at most) mask scores and zero the V rows that the node does not see
+// (their weights are zero, but a row may hold NaN).  Every item's first page holds a
+// visible key: a row of more than one page begins with context, and a piece of a
+// cut row is at least four pages long.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -319,6 +328,17 @@ __device__ __forceinline__ float fast_exp2(float x) {
     return y;
 }
 
+// Zero the latent rows of a landed V stage whose bit in `seen` is clear, one warp
+// (lane: 16-byte chunk lane % 8 of dim block lane / 8), then make the stores
+// visible to the tensor cores.
+__device__ __noinline__ void zero_v_unseen(uint8_t *vst, uint64_t seen, int lane) {
+    uint8_t *mine = vst + (lane >> 3) * kVBlk + (lane & 7) * 16;
+    for (uint64_t z = ~seen; z; z &= z - 1)
+        *reinterpret_cast<uint4 *>(mine + (__ffsll((long long)z) - 1) * 128) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
 // Byte offset of 16-byte chunk cc (8 tokens) of head h's row in a P half
 // tile (64-byte rows, 64-byte swizzle: chunk cc of row h sits at
 // cc ^ ((h >> 1) & 3)).
@@ -520,7 +540,8 @@ __device__ __noinline__ void convert_codes(uint8_t *stage, int t, int bar_id, in
     }
 }
 
-template <bool kFp8>
+// kTree: P.s_q is the number of tokens (rows).
+template <bool kFp8, bool kTree>
 __global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
 mla_main_tc_kernel(const __grid_constant__ Params P) {
     extern __shared__ uint8_t smem_raw[];
@@ -605,12 +626,15 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
     pdl_wait_prior();
     pdl_launch_dependents();
 
-    const PlanLayout L = plan_layout(P.batch, P.s_q, P.num_units);
+    const PlanLayout L = make_layout(kTree ? P.s_q : P.batch * P.s_q, P.num_units, kTree);
+    const TreeRow *tree_rows = reinterpret_cast<const TreeRow *>(P.ws + L.tree_rows);
+    // request of an item's row
+    auto request = [&](int32_t row) { return kTree ? tree_rows[row].req : row / P.s_q; };
     const WorkItem *items = reinterpret_cast<const WorkItem *>(P.ws + L.items);
     const int32_t *unit_begin = reinterpret_cast<const int32_t *>(P.ws + L.unit_begin);
     float *lse_part = reinterpret_cast<float *>(P.ws + L.lse_part);
     float *o_part = reinterpret_cast<float *>(P.ws + L.o_part);
-    const bool plan_ok = hdr->magic == kPlanMagic && hdr->batch == P.batch &&
+    const bool plan_ok = hdr->magic == (kTree ? kTreeMagic : kPlanMagic) && hdr->batch == P.batch &&
                          hdr->s_q == P.s_q && hdr->num_units == P.num_units &&
                          hdr->max_pages == P.max_pages && (int)unit < P.num_units;
     int i_begin = 0, i_end = 0;
@@ -638,7 +662,7 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
         bool ok = true;
         for (int i = i_begin; i < i_end && ok; ++i) {
             const WorkItem it = items[i];
-            const int b = it.row / P.s_q;
+            const int b = request(it.row);
             const int p0 = it.kv_begin / kPage;
             const int n = (it.kv_end - it.kv_begin + kPage - 1) / kPage;
             const uint32_t ii = (uint32_t)(i - i_begin);
@@ -782,6 +806,12 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
             const WorkItem it = items[i];
             const int n = (it.kv_end - it.kv_begin + kPage - 1) / kPage;
             const uint32_t ii = (uint32_t)(i - i_begin);
+            int32_t context = 0;
+            uint64_t mask = 0;
+            if (kTree && !qk) {
+                context = tree_rows[it.row].context;
+                mask = tree_rows[it.row].mask;
+            }
             if (qk && (!wait_warp(ctl, bar(ctl, B_Q_FULL), ii & 1) || !wait_warp(ctl, bar(ctl, B_QTILE), ii & 1)))
                 break;
             for (int k = 0; k < n && ok; ++k, ++g) {
@@ -830,7 +860,12 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
                     }
                     // the masked tail's latent rows in the V stage become zeros, so that
                     // 0 * garbage stays 0 in PV (the stage has landed: waited above)
-                    if (k == n - 1) {
+                    if constexpr (kTree) {
+                        if (k >= n - 2) {   // a tree's slots lie in its row's last two pages
+                            const uint64_t seen = tree_page_mask(context, mask, it.kv_begin + k * kPage);
+                            if (~seen) zero_v_unseen(smem + kOffV + p * kVStageBytes, seen, lane);
+                        }
+                    } else if (k == n - 1) {
                         const int valid_last = it.kv_end - (it.kv_begin + (n - 1) * kPage);
                         if (valid_last < kPage) zero_v_tail(smem + kOffV + p * kVStageBytes, valid_last, lane);
                     }
@@ -882,6 +917,12 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
             const int n = (it.kv_end - it.kv_begin + kPage - 1) / kPage;
             const int valid_last = it.kv_end - (it.kv_begin + (n - 1) * kPage);
             const uint32_t ii = (uint32_t)(i - i_begin);
+            int32_t context = 0;
+            uint64_t mask = 0;
+            if constexpr (kTree) {
+                context = tree_rows[it.row].context;
+                mask = tree_rows[it.row].mask;
+            }
 
             // q of this head -> TMEM: dims 0-319 from the staged blocks (the
             // staging was issued after the previous item's score MMAs were done, into
@@ -947,8 +988,14 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(ctl, B_SEMPTY + sp));
 
+                // visible ones of this CTA's 32 tokens: a prefix (v_own of them), or a tree's bits
                 const int valid = (k == n - 1) ? valid_last : kPage;
                 const int v_own = min(max(valid - tok_own, 0), kHalfTok);
+                uint32_t seen = 0xffffffffu;
+                if constexpr (kTree) {
+                    if (k >= n - 2) seen = (uint32_t)(tree_page_mask(context, mask, it.kv_begin + k * kPage) >> tok_own);
+                }
+                const bool all = kTree ? seen == 0xffffffffu : v_own == kHalfTok;
                 // fp8 cache: the score MMAs contracted q with the codes and k_rope / s, so
                 // each token's raw score is multiplied by its scale s (> 0)
                 const float *tsc = reinterpret_cast<const float *>(smem + kOffScale + (g % kScaleSlots) * kScaleStage);
@@ -961,13 +1008,13 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
                 // are -inf
                 const float sc = P.scale_log2;
                 float rmax = NEG_INF;
-                if (v_own == kHalfTok) {
+                if (all) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) rmax = fmaxf(rmax, __uint_as_float(r[j]));
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
-                        if (j >= v_own) r[j] = __float_as_uint(NEG_INF);
+                        if (kTree ? !(seen >> j & 1) : j >= v_own) r[j] = __float_as_uint(NEG_INF);
                         rmax = fmaxf(rmax, __uint_as_float(r[j]));
                     }
                 }
@@ -989,8 +1036,9 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
                     if constexpr (kFp8) {
                         // PV contracts with the codes: each weight carries its token's
                         // scale (masked tokens stay 0 whatever their scale slot holds)
-                        pk[j] = pack_bf16(2 * j < v_own ? e0 * tsc[8 * j] : 0.f,
-                                          2 * j + 1 < v_own ? e1 * tsc[8 * j + 4] : 0.f);
+                        const bool s0 = kTree ? seen >> (2 * j) & 1 : 2 * j < v_own;
+                        const bool s1 = kTree ? seen >> (2 * j + 1) & 1 : 2 * j + 1 < v_own;
+                        pk[j] = pack_bf16(s0 ? e0 * tsc[8 * j] : 0.f, s1 ? e1 * tsc[8 * j + 4] : 0.f);
                     } else {
                         pk[j] = pack_bf16(e0, e1);
                     }
@@ -1043,7 +1091,7 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
             total_pages += (uint32_t)((items[i].kv_end - items[i].kv_begin + kPage - 1) / kPage);
         for (int i = i_begin; i < i_end && ok; ++i) {
             const WorkItem it = items[i];
-            const int b = it.row / P.s_q;
+            const int b = request(it.row);
             const int p0 = it.kv_begin / kPage;
             const int n = (it.kv_end - it.kv_begin + kPage - 1) / kPage;
             const uint32_t ii = (uint32_t)(i - i_begin);
@@ -1078,7 +1126,7 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
                 uint8_t *pst = smem + kOffP + ps * kPSlotBytes;
                 const float2 h0 = *reinterpret_cast<const float2 *>(pst + kPHalf + h * 8);
                 const float2 h1 = *reinterpret_cast<const float2 *>(pst + kPPart + kPHalf + h * 8);
-                const float nref = fmaxf(m_ref, fmaxf(h0.x, h1.x));   // finite: token 0 is valid
+                const float nref = fmaxf(m_ref, fmaxf(h0.x, h1.x));   // finite: the item's first page has a visible key
                 if (h0.x != NEG_INF && h0.x < nref) scale_p_row(pst, h, rescale(h0.x - nref, pow2));
                 if (h1.x != NEG_INF && h1.x < nref) scale_p_row(pst + kPPart, h, rescale(h1.x - nref, pow2));
                 // O is rescaled (rarely) once the previous PV is done
@@ -1219,7 +1267,7 @@ bool encode(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims,
 struct DeviceInfo {
     int units = 0;
     bool attr_set = false;
-    int fp8 = 0;   // the fp8 variant: 0 not checked, 1 runs on the same units, -1 does not
+    int variant[4] = {};   // the other variants: 0 not checked, 1 runs on the same units, -1 does not
 };
 std::mutex g_dev_mutex;
 DeviceInfo g_dev[64];
@@ -1229,7 +1277,7 @@ cudaError_t prepare(int dev, int *units) {
     std::lock_guard<std::mutex> lock(g_dev_mutex);
     DeviceInfo &d = g_dev[dev];
     if (!d.attr_set) {
-        cudaError_t e = cudaFuncSetAttribute(mla_main_tc_kernel<false>,
+        cudaError_t e = cudaFuncSetAttribute(mla_main_tc_kernel<false, false>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)kSmemBytes);
         if (e != cudaSuccess) return e;
@@ -1248,7 +1296,7 @@ cudaError_t prepare(int dev, int *units) {
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
         int n = 0;
-        e = cudaOccupancyMaxActiveClusters(&n, mla_main_tc_kernel<false>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&n, mla_main_tc_kernel<false, false>, &cfg);
         if (e != cudaSuccess) return e;
         if (n < 1) return cudaErrorInvalidConfiguration;
         d.units = n;
@@ -1258,19 +1306,29 @@ cudaError_t prepare(int dev, int *units) {
     return cudaSuccess;
 }
 
-// The fp8 variant runs the same schedule, so it must fit as many units.
-cudaError_t prepare_fp8(int dev, int units) {
+using MainKernel = void (*)(Params);
+
+// The kernel of a variant, its block and its shared memory.
+MainKernel main_kernel(bool fp8, bool tree) {
+    if (tree) return fp8 ? mla_main_tc_kernel<true, true> : mla_main_tc_kernel<false, true>;
+    return fp8 ? mla_main_tc_kernel<true, false> : mla_main_tc_kernel<false, false>;
+}
+
+// Every other variant runs schedules of as many units, so it must fit them.
+cudaError_t prepare_variant(int dev, int units, bool fp8, bool tree) {
+    const int v = (fp8 ? 1 : 0) + (tree ? 2 : 0);
+    if (v == 0) return cudaSuccess;
     std::lock_guard<std::mutex> lock(g_dev_mutex);
     DeviceInfo &d = g_dev[dev];
-    if (d.fp8 == 0) {
-        cudaError_t e = cudaFuncSetAttribute(mla_main_tc_kernel<true>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)kSmemBytesFp8);
+    if (d.variant[v] == 0) {
+        const MainKernel kernel = main_kernel(fp8, tree);
+        const int smem = (int)(fp8 ? kSmemBytesFp8 : kSmemBytes);
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(kClusterSize * units);
-        cfg.blockDim = dim3(kThreadsFp8);
-        cfg.dynamicSmemBytes = kSmemBytesFp8;
+        cfg.blockDim = dim3(fp8 ? kThreadsFp8 : kThreads);
+        cfg.dynamicSmemBytes = smem;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
         attr.val.clusterDim.x = kClusterSize;
@@ -1279,11 +1337,11 @@ cudaError_t prepare_fp8(int dev, int units) {
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
         int n = 0;
-        e = cudaOccupancyMaxActiveClusters(&n, mla_main_tc_kernel<true>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
         if (e != cudaSuccess) return e;
-        d.fp8 = n >= units ? 1 : -1;
+        d.variant[v] = n >= units ? 1 : -1;
     }
-    return d.fp8 == 1 ? cudaSuccess : cudaErrorInvalidConfiguration;
+    return d.variant[v] == 1 ? cudaSuccess : cudaErrorInvalidConfiguration;
 }
 
 }  // namespace
@@ -1303,16 +1361,16 @@ cudaError_t launch_main(const void *q_latent, const void *q_rope, const void *kv
                         int64_t num_pages, const int32_t *block_table, float scale, void *ws,
                         void *o_latent, float *lse, int32_t batch, int32_t s_q, int32_t max_pages,
                         int32_t num_units, uint64_t wait_limit_ns, uint32_t test_flags, uint32_t flags,
-                        bool fp8, cudaStream_t stream) {
-    if (fp8) {
+                        bool fp8, bool tree, cudaStream_t stream) {
+    if (fp8 || tree) {
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return e;
-        e = prepare_fp8(dev, num_units);
+        e = prepare_variant(dev, num_units, fp8, tree);
         if (e != cudaSuccess) return e;
     }
     Params p;
-    const cuuint64_t qrows = (cuuint64_t)batch * s_q * kHeads;
+    const cuuint64_t qrows = (cuuint64_t)(tree ? 1 : batch) * s_q * kHeads;   // tree: s_q tokens in all
     {
         cuuint64_t dims[2] = {(cuuint64_t)kDl, qrows};
         cuuint64_t strides[1] = {(cuuint64_t)kDl * 2};
@@ -1390,8 +1448,7 @@ cudaError_t launch_main(const void *q_latent, const void *q_rope, const void *kv
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return fp8 ? cudaLaunchKernelEx(&cfg, mla_main_tc_kernel<true>, p)
-               : cudaLaunchKernelEx(&cfg, mla_main_tc_kernel<false>, p);
+    return cudaLaunchKernelEx(&cfg, main_kernel(fp8, tree), p);
 }
 
 }  // namespace mla

@@ -53,6 +53,7 @@
 
 #include "mla_internal.h"
 #include "mla_prolog.h"
+#include "mla_rope.cuh"
 #include "sm103_ptx.cuh"
 
 namespace mla {
@@ -66,7 +67,6 @@ constexpr int kBM = 128;                  // tokens per tile (MMA M)
 constexpr int kBN = 128;                  // latent columns per CTA (MMA N)
 constexpr int kNParts = kDl / kBN;        // CTAs per (head, token tile)
 constexpr int kThreadsP = 128;
-constexpr int kPairs = kDr / 2;           // RoPE pairs per 64-dim vector
 constexpr int kPartPairs = kPairs / kNParts;              // pairs each quarter rotates
 constexpr uint32_t kABlk = kBM * 128;     // one 64-dim block of the A tile: 128 rows x 128 B
 constexpr uint32_t kABytes = (kDn / 64) * kABlk;          // 32 KB (a full 128-token tile)
@@ -95,6 +95,8 @@ struct PrologParams {
     const int32_t *block_table;
     const int32_t *seq_lens;
     const float *rope_table;   // g_hi[32], then g_lo[32] (mla_prolog_rope_table)
+    const int32_t *positions;  // mla_query: the tokens' positions (negative: left out)
+    int64_t pe_token, pe_head; // mla_query: q_pe strides in elements
     __nv_bfloat16 *q_latent;
     __nv_bfloat16 *q_rope;
     __nv_bfloat16 *kv_cache;
@@ -120,39 +122,11 @@ __device__ __forceinline__ bool bounded_wait(uint32_t bar, uint32_t parity, int3
     return true;
 }
 
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t *>(&v);
-}
-
-// sin and cos of the angle pos * 2 pi (g_hi + g_lo), 0 <= pos < 2^31 (see the file notes).
-__device__ __forceinline__ void rope_sincos(int32_t pos, float g_hi, float g_lo, float &s, float &c) {
-    const float ph = (float)(pos >> 16), pl = (float)(pos & 0xffff);   // both exact
-    const float gh16 = g_hi * 65536.f, gl16 = g_lo * 65536.f;          // exact scalings
-    const float a1 = ph * gh16, e1 = fmaf(ph, gh16, -a1);             // ph * gh16 = a1 + e1 exactly
-    const float a2 = pl * g_hi, e2 = fmaf(pl, g_hi, -a2);
-    float r = (a1 - rintf(a1)) + (a2 - rintf(a2));                      // fractions of the big terms
-    r += e1 + e2 + fmaf(ph, gl16, pl * g_lo);
-    r -= rintf(r);
-    __sincosf(r * 6.28318530717958648f, &s, &c);
-}
-
-// Rotate the four pairs held by eight consecutive bf16 values, pairs p0 .. p0 + 3.
-__device__ __forceinline__ uint4 rope8(uint4 v, int32_t pos, int p0, const float *g_hi,
-                                       const float *g_lo) {
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float s, c;
-        rope_sincos(pos, g_hi[p0 + j], g_lo[p0 + j], s, c);
-        const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j]));
-        w[j] = pack_bf16x2(x.x * c - x.y * s, x.x * s + x.y * c);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Position of token tok, or -1 when it has no slot in its request's table.
+// Position of token tok, or -1 when it has no slot in its request's table
+// (mla_query: when it is left out).
+template <bool kAppend>
 __device__ __forceinline__ int32_t token_pos(const PrologParams &P, int tok) {
+    if constexpr (!kAppend) return P.positions[tok];
     const int b = tok / P.s_q, t = tok % P.s_q;
     const int64_t pos = (int64_t)P.seq_lens[b] - P.s_q + t;
     return pos < 0 || pos >= (int64_t)P.max_pages * kPage ? -1 : (int32_t)pos;
@@ -199,6 +173,9 @@ __device__ __forceinline__ void append_token(const PrologParams &P, int tok, int
     if (c < kDr / 8) reinterpret_cast<uint4 *>(dst + kDl)[c] = rope8(k, pos, c * 4, g_hi, g_lo);
 }
 
+// kAppend = false (mla_query): positions are given, q may be strided, nothing is
+// appended and the rows of a token with a negative position are not written.
+template <bool kAppend>
 __global__ void __launch_bounds__(kThreadsP, 4) mla_prolog_kernel(const __grid_constant__ PrologParams P) {
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[2];   // 0: operands landed, 1: MMAs done
@@ -275,15 +252,18 @@ __global__ void __launch_bounds__(kThreadsP, 4) mla_prolog_kernel(const __grid_c
             const int i = tid + 96 * k;
             if (i < 2 * kBM && tok0 + i / 2 < P.tokens)
                 v[k] = *reinterpret_cast<const uint4 *>(
-                    P.q_pe + ((size_t)(tok0 + i / 2) * kHeads + h) * kDr + np * 16 + (i & 1) * 8);
+                    P.q_pe +
+                    (kAppend ? ((size_t)(tok0 + i / 2) * kHeads + h) * kDr
+                             : (size_t)((tok0 + i / 2) * P.pe_token + h * P.pe_head)) +
+                    np * 16 + (i & 1) * 8);
         }
         float th = 0.f, tl = 0.f;
         if (warp == 1) {
             th = P.rope_table[tid];
             tl = P.rope_table[kPairs + tid];
         }
-        const int32_t p0 = tid < kBM && tok0 + tid < P.tokens ? token_pos(P, tok0 + tid) : -1;
-        const int32_t p1 = tid + 96 < kBM && tok0 + tid + 96 < P.tokens ? token_pos(P, tok0 + tid + 96) : -1;
+        const int32_t p0 = tid < kBM && tok0 + tid < P.tokens ? token_pos<kAppend>(P, tok0 + tid) : -1;
+        const int32_t p1 = tid + 96 < kBM && tok0 + tid + 96 < P.tokens ? token_pos<kAppend>(P, tok0 + tid + 96) : -1;
         if (warp == 1) {
             g_hi[tid] = th;
             g_lo[tid] = tl;
@@ -291,13 +271,14 @@ __global__ void __launch_bounds__(kThreadsP, 4) mla_prolog_kernel(const __grid_c
         pos_s[tid] = p0;
         if (tid + 96 < kBM) pos_s[tid + 96] = p1;
         named_sync(1, 96);
-        if (np == 0 && warp >= 2 && tok0 + h < P.tokens)
+        if (kAppend && np == 0 && warp >= 2 && tok0 + h < P.tokens)
             append_token(P, tok0 + h, pos_s[h], tid - 32, g_hi, g_lo, red);
 #pragma unroll
         for (int k = 0; k < kQIters; ++k) {
             const int i = tid + 96 * k;
             if (i < 2 * kBM && tok0 + i / 2 < P.tokens) {
                 const int32_t pos = pos_s[i / 2];
+                if (!kAppend && pos < 0) continue;
                 *reinterpret_cast<uint4 *>(P.q_rope + ((size_t)(tok0 + i / 2) * kHeads + h) * kDr +
                                            np * 16 + (i & 1) * 8) =
                     pos < 0 ? make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u)
@@ -347,7 +328,7 @@ __global__ void __launch_bounds__(kThreadsP, 4) mla_prolog_kernel(const __grid_c
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                          : "r"(s_b + b * kOBlk + r * 128 + ((j ^ (r & 7)) * 16)));
-            if (tok < P.tokens)
+            if (tok < P.tokens && (kAppend || P.positions[tok] >= 0))
                 *reinterpret_cast<uint4 *>(P.q_latent + ((size_t)tok * kHeads + h) * kDl + np * kBN +
                                            j16 * 8) = v;
         }
@@ -363,7 +344,42 @@ __global__ void __launch_bounds__(kThreadsP, 4) mla_prolog_kernel(const __grid_c
 // ---------------------------------------------------------------- host side
 
 std::mutex g_prolog_mutex;
-bool g_prolog_attr[64];
+bool g_prolog_attr[64];   // both variants
+
+cudaError_t prepare_prolog() {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(g_prolog_mutex);
+    if (!g_prolog_attr[dev]) {
+        e = cudaFuncSetAttribute(mla_prolog_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemP);
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(mla_prolog_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemP);
+        if (e != cudaSuccess) return e;
+        g_prolog_attr[dev] = true;
+    }
+    return cudaSuccess;
+}
+
+// Shared memory of a CTA whose A tile holds a_rows token rows.
+uint32_t prolog_smem(int32_t a_rows) {
+    return std::max<uint32_t>(kSmemMinP, ((2u * a_rows * 128 + 1023u) & ~1023u) + kBBytes + 1024);
+}
+
+cudaError_t launch_prolog(const PrologParams &p, bool append, unsigned ctas, mla_stream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreadsP);
+    cfg.dynamicSmemBytes = prolog_smem(p.a_rows);
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, append ? mla_prolog_kernel<true> : mla_prolog_kernel<false>, p);
+}
 
 bool aligned16(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -416,20 +432,9 @@ extern "C" mla_status mla_prolog(const mla_problem *prob, const void *q_nope, co
         return MLA_ERR_INVALID_ARG;
     if (num_pages < 1 || !std::isfinite(rms_eps) || rms_eps < 0.f) return MLA_ERR_INVALID_ARG;
 
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MLA_ERR_CUDA;
-    {
-        std::lock_guard<std::mutex> lock(g_prolog_mutex);
-        if (!g_prolog_attr[dev]) {
-            if (cudaFuncSetAttribute(mla_prolog_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)kSmemP) != cudaSuccess)
-                return MLA_ERR_CUDA;
-            g_prolog_attr[dev] = true;
-        }
-    }
+    if (prepare_prolog() != cudaSuccess) return MLA_ERR_CUDA;
     PrologParams p{};
     p.a_rows = tokens >= kBM ? kBM : (int32_t)((tokens + 7) / 8 * 8);
-    const uint32_t smem = std::max<uint32_t>(kSmemMinP, ((2u * p.a_rows * 128 + 1023u) & ~1023u) + kBBytes + 1024);
     const cuuint64_t H = kHeads, T = (cuuint64_t)tokens;
     // q_nope (dims, tokens, dim blocks, heads); W_UK (cols, dims, col blocks, heads)
     if (!encode_bf16_4d(&p.tm_a, q_nope, T, kDn / 64, H, H * kDn * 2, 128, kDn * 2, (cuuint32_t)p.a_rows, kDn / 64) ||
@@ -451,15 +456,40 @@ extern "C" mla_status mla_prolog(const mla_problem *prob, const void *q_nope, co
     p.tokens = (int32_t)tokens;
     p.s_q = prob->s_q;
     p.max_pages = prob->max_pages_per_seq;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(kThreadsP);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mla_prolog_kernel, p) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+    return launch_prolog(p, true, (unsigned)ctas, stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+extern "C" mla_status mla_query(int32_t tokens, const void *q_nope, int64_t nope_token_stride,
+                                int64_t nope_head_stride, const void *q_pe, int64_t pe_token_stride,
+                                int64_t pe_head_stride, const void *w_uk, const float *rope_table,
+                                const int32_t *positions, void *q_latent, void *q_rope, int32_t *device_status,
+                                mla_stream_t stream) {
+    mla::NvtxRange nvtx_range("mla_query");
+    using namespace mla;
+    if (tokens < 1) return MLA_ERR_INVALID_ARG;
+    const int64_t ctas = ((int64_t)tokens + kBM - 1) / kBM * kHeads * kNParts;
+    if ((int64_t)tokens * kHeads >= (int64_t)1 << 31 || ctas >= (int64_t)1 << 31) return MLA_ERR_UNSUPPORTED;
+    if (!aligned16(q_nope) || !aligned16(q_pe) || !aligned16(w_uk) || !aligned16(q_latent) || !aligned16(q_rope) ||
+        !rope_table || !positions || !device_status || (reinterpret_cast<uintptr_t>(rope_table) & 3u) ||
+        (reinterpret_cast<uintptr_t>(positions) & 3u) || (reinterpret_cast<uintptr_t>(device_status) & 3u))
+        return MLA_ERR_INVALID_ARG;
+    for (const int64_t s : {nope_token_stride, nope_head_stride, pe_token_stride, pe_head_stride})
+        if (s < 1 || s % 8 || s >= (int64_t)1 << 31) return MLA_ERR_INVALID_ARG;
+    if (prepare_prolog() != cudaSuccess) return MLA_ERR_CUDA;
+    PrologParams p{};
+    p.a_rows = tokens >= kBM ? kBM : (tokens + 7) / 8 * 8;
+    if (!encode_bf16_4d(&p.tm_a, q_nope, (cuuint64_t)tokens, kDn / 64, kHeads, (cuuint64_t)nope_token_stride * 2, 128,
+                        (cuuint64_t)nope_head_stride * 2, (cuuint32_t)p.a_rows, kDn / 64) ||
+        !encode_bf16_4d(&p.tm_b, w_uk, kDn, kDl / 64, kHeads, kDl * 2, 128, (cuuint64_t)kDn * kDl * 2, kDn, kBN / 64))
+        return MLA_ERR_CUDA;
+    p.q_pe = static_cast<const __nv_bfloat16 *>(q_pe);
+    p.pe_token = pe_token_stride;
+    p.pe_head = pe_head_stride;
+    p.positions = positions;
+    p.rope_table = rope_table;
+    p.q_latent = static_cast<__nv_bfloat16 *>(q_latent);
+    p.q_rope = static_cast<__nv_bfloat16 *>(q_rope);
+    p.status = device_status;
+    p.tokens = tokens;
+    return launch_prolog(p, false, (unsigned)ctas, stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }

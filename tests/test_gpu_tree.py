@@ -397,6 +397,7 @@ def test_a_speculative_step(fp8):
     """Query, append, attention, value projection, commit, then the next step's tokens: in one graph, against fp64."""
     counts, lens = [7, 12, 1], [90, 400, 64]
     c = TU.case(counts, lens, "tree", seed=61, spare=6)
+    c["block_table"][2, 1] = c["order"][-1]                        # the next step's token needs a second page
     T = c["T"]
     _, _, cache = TU.tensors(c, seed=62, poison=False)
     g = torch.Generator().manual_seed(63)

@@ -501,94 +501,137 @@ MLA_DEV_BAD_OFFSETS = 0x10
 MLA_DEV_BAD_PATH = 0x20
 
 
-def _launch_on(dev, stream):
+def _launch_on(index, stream):
     """Context of a call: its device, and its stream as the current one, so that what the call
     allocates or clears belongs to that stream too."""
     import torch
     if stream is None:
-        return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-    if stream.device != dev:
-        raise ValueError(f"stream must be one of {dev}, the tensors' device")
+        return _HERE_ALREADY if torch.cuda.current_device() == index else torch.cuda.device(index)
+    if stream.device.index != index:
+        raise ValueError(f"stream must be one of cuda:{index}, the tensors' device")
     return torch.cuda.stream(stream)
+
+
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _current_stream(index) -> int:
+    """Handle of the current stream of a device (a few times cheaper than a torch.cuda.Stream object: a
+    small operator's launch takes a few microseconds in all)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _ragged(batch: int, tokens: int, max_pages: int, flags: int = 0) -> _Ragged:
     return _Ragged(int(batch), int(tokens), NUM_HEADS, PAGE_SIZE, int(max_pages), int(flags))
 
 
-def _req_index(t, name, dtype, shape, device):
-    """An index array: contiguous, of one dtype and shape (None: any extent), on the device."""
+def _refuse(t, name, dtype, shape, index, strided=False):
+    """Raise what is wrong with an argument that _dense or _strided did not take."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device.type != "cuda" or (device is not None and t.device != device):
-        raise ValueError(f"{name} must be on {device or 'a CUDA device'}")
-    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
-        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    if not t.is_contiguous():
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not strided and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be 16-byte aligned")
 
 
-def _strides(t, name, shape, device):
-    """A bf16 input whose last dim is contiguous -> its other dims' strides in elements.
+def _dense(t, name, dtype, shape, index) -> int:
+    """Address of a dense array of this dtype and shape on device `index` (16-byte aligned unless integers)."""
+    import torch
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
+            and index >= 0 and t.is_contiguous()):
+        ptr = t.data_ptr()
+        if not ptr & 15 or dtype is torch.int32 or dtype is torch.int64:
+            return ptr
+    _refuse(t, name, dtype, shape, index)
+
+
+def _strided(t, name, shape, index):
+    """Address and strides (in elements) of a bf16 input whose last dim is contiguous.
 
     The others may be strided (a view of a larger projection): positive multiples of 8.
     """
     import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.device.type != "cuda" or (device is not None and t.device != device):
-        raise ValueError(f"{name} must be on {device or 'a CUDA device'}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.data_ptr() % 16:
-        raise ValueError(f"{name} must be 16-byte aligned")
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.shape == shape
+            and t.get_device() == index and index >= 0 and not t.data_ptr() & 15):
+        _refuse(t, name, torch.bfloat16, shape, index, strided=True)
     st = t.stride()
     if st[-1] != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
     # the stride of a dimension of one element is never used: any legal value does
-    st = [8 if n == 1 else v for n, v in zip(shape[:-1], st)]
-    if any(v < 1 or v % 8 or v >= 1 << 31 for v in st):
-        raise ValueError(f"{name}'s strides must be positive multiples of 8")
-    return st
+    if shape[0] == 1:
+        st = (8,) + st[1:]
+    for v in st[:-1]:
+        if v < 1 or v % 8 or v >= 1 << 31:
+            raise ValueError(f"{name}'s strides must be positive multiples of 8")
+    return (t.data_ptr(), *st[:-1])
 
 
-def _req_out(t, name, dtype, shape, device):
+def _index_of(t, name, dim) -> int:
+    """Device index of the argument that fixes the device, with its dimension count."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != dim or 0 in t.shape:
+        raise ValueError(f"{name} must have {dim} non-empty dimensions, got {tuple(t.shape)}")
+    return t.get_device()
+
+
+def _out(t, name, dtype, shape, index):
+    """The caller's output, or a new one on the current stream."""
     import torch
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _req(t, name, dtype, shape, device)
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
+    _dense(t, name, dtype, shape, index)
     return t
 
 
-def _req_status(status, device):
+def _status_word(status, index):
     import torch
     if status is None:
-        return torch.zeros(1, dtype=torch.int32, device=device)
-    _req_index(status, "status", torch.int32, (1,), device)
+        return torch.zeros(1, dtype=torch.int32, device=torch.device("cuda", index))
+    _dense(status, "status", torch.int32, (1,), index)
     return status
 
 
-def _rope_table_for(table, rope_base, dev, stream, what):
-    """The caller's table, or the one of rope_base, built once per device and kept."""
+def _table_of(table, rope_base, index, what) -> int:
+    """Address of the caller's table, or of rope_base's, built once per device and kept (call on the launch's stream)."""
     import torch
     if table is None:
-        key = (dev.index, float(rope_base))
+        key = (index, float(rope_base))
         table = _rope_tables.get(key)
         if table is None:
             # the kept table must hold its values for every later call on any stream
             if torch.cuda.is_current_stream_capturing():
                 raise RuntimeError(f"{what}: build the rotary table with rope_table() before "
                                    "capturing a CUDA graph, and pass it as table=")
-            table = rope_table(rope_base, dev, stream)
-            (stream if stream is not None else torch.cuda.current_stream()).synchronize()
+            table = rope_table(rope_base, torch.device("cuda", index))
+            torch.cuda.current_stream().synchronize()
             _rope_tables[key] = table
-    _req_index(table, "table", torch.float32, (ROPE_TABLE_FLOATS,), dev)
-    return table
+    return _dense(table, "table", torch.float32, (ROPE_TABLE_FLOATS,), index)
+
+
+def _cache_ptr(kv_cache, fp8, index, layers=False) -> int:
+    import torch
+    name = "kv_cache_fp8" if fp8 else "kv_cache"
+    row = FP8_ROW_BYTES if fp8 else D_LATENT + D_ROPE
+    if not isinstance(kv_cache, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    shape = kv_cache.shape
+    if len(shape) not in ((3, 4) if layers else (3,)) or shape[-2] != PAGE_SIZE or shape[-1] != row or 0 in shape:
+        if kv_cache.dtype != (torch.uint8 if fp8 else torch.bfloat16):
+            raise TypeError(f"{name} must be {torch.uint8 if fp8 else torch.bfloat16}, got {kv_cache.dtype}")
+        raise ValueError(f"{name} must be {'([layers])' if layers else ''}[num_pages][64][{row}]")
+    return _dense(kv_cache, name, torch.uint8 if fp8 else torch.bfloat16, shape, index)
 
 
 def query(q_nope, q_pe, w_uk, positions, *, rope_base: float = DEFAULT_ROPE_BASE, table=None, q_latent=None,
@@ -603,22 +646,18 @@ def query(q_nope, q_pe, w_uk, positions, *, rope_base: float = DEFAULT_ROPE_BASE
     one-element int32 device tensor of MLA_DEV_* bits.
     """
     import torch
-    if q_nope.dim() != 3 or q_nope.shape[0] < 1:
-        raise ValueError("q_nope must be [tokens][heads][128]")
-    T, dev = q_nope.shape[0], q_nope.device
-    ns = _strides(q_nope, "q_nope", (T, NUM_HEADS, D_NOPE), None)
-    ps = _strides(q_pe, "q_pe", (T, NUM_HEADS, D_ROPE), dev)
-    _req(w_uk, "w_uk", torch.bfloat16, (NUM_HEADS, D_NOPE, D_LATENT), dev)
-    _req_index(positions, "positions", torch.int32, (T,), dev)
-    with _launch_on(dev, stream):
-        table = _rope_table_for(table, rope_base, dev, stream, "query")
-        q_latent = _req_out(q_latent, "q_latent", torch.bfloat16, (T, NUM_HEADS, D_LATENT), dev)
-        q_rope = _req_out(q_rope, "q_rope", torch.bfloat16, (T, NUM_HEADS, D_ROPE), dev)
-        status = _req_status(status, dev)
-        _check(load_library().mla_query(
-            T, q_nope.data_ptr(), ns[0], ns[1], q_pe.data_ptr(), ps[0], ps[1], w_uk.data_ptr(), table.data_ptr(),
-            positions.data_ptr(), q_latent.data_ptr(), q_rope.data_ptr(), status.data_ptr(),
-            _stream_handle(None)), "mla_query")
+    index = _index_of(q_nope, "q_nope", 3)
+    T = q_nope.shape[0]
+    args = (*_strided(q_nope, "q_nope", (T, NUM_HEADS, D_NOPE), index), *_strided(q_pe, "q_pe", (T, NUM_HEADS, D_ROPE), index),
+            _dense(w_uk, "w_uk", torch.bfloat16, (NUM_HEADS, D_NOPE, D_LATENT), index))
+    pos = _dense(positions, "positions", torch.int32, (T,), index)
+    with _launch_on(index, stream):
+        tab = _table_of(table, rope_base, index, "query")
+        q_latent = _out(q_latent, "q_latent", torch.bfloat16, (T, NUM_HEADS, D_LATENT), index)
+        q_rope = _out(q_rope, "q_rope", torch.bfloat16, (T, NUM_HEADS, D_ROPE), index)
+        status = _status_word(status, index)
+        _check(load_library().mla_query(T, *args, tab, pos, q_latent.data_ptr(), q_rope.data_ptr(), status.data_ptr(),
+                                        _current_stream(index)), "mla_query")
     return q_latent, q_rope, status
 
 
@@ -649,39 +688,28 @@ def cache_append_fp8(kv_latent, k_pe, kv_norm_weight, kv_cache_fp8, block_table,
 def _append(kv_latent, k_pe, kv_norm_weight, kv_cache, block_table, seq_lens, token_offsets, positions, rope_base,
             rms_eps, table, status, stream, fp8):
     import torch
-    if kv_latent.dim() != 2 or kv_latent.shape[0] < 1:
-        raise ValueError("kv_latent must be [tokens][512]")
-    T, dev = kv_latent.shape[0], kv_latent.device
-    ls = _strides(kv_latent, "kv_latent", (T, D_LATENT), None)
-    ks = _strides(k_pe, "k_pe", (T, D_ROPE), dev)
-    _req(kv_norm_weight, "kv_norm_weight", torch.bfloat16, (D_LATENT,), dev)
-    _req_cache(kv_cache, dev, fp8)
-    _req_index(block_table, "block_table", torch.int32, (None, None), dev)
-    B = block_table.shape[0]
-    _req_index(seq_lens, "seq_lens", torch.int32, (B,), dev)
-    _req_index(token_offsets, "token_offsets", torch.int32, (B + 1,), dev)
-    if positions is not None:
-        _req_index(positions, "positions", torch.int32, (T,), dev)
-    name = "mla_cache_append_fp8" if fp8 else "mla_cache_append"
-    with _launch_on(dev, stream):
-        table = _rope_table_for(table, rope_base, dev, stream, "cache_append")
-        status = _req_status(status, dev)
-        prob = _ragged(B, T, block_table.shape[1])
-        _check(getattr(load_library(), name)(
-            ctypes.byref(prob), kv_latent.data_ptr(), ls[0], k_pe.data_ptr(), ks[0], kv_norm_weight.data_ptr(),
-            float(rms_eps), table.data_ptr(), positions.data_ptr() if positions is not None else None,
-            kv_cache.data_ptr(), kv_cache.shape[0], block_table.data_ptr(), seq_lens.data_ptr(),
-            token_offsets.data_ptr(), status.data_ptr(), _stream_handle(None)), name)
+    index = _index_of(kv_latent, "kv_latent", 2)
+    T = kv_latent.shape[0]
+    lat = _strided(kv_latent, "kv_latent", (T, D_LATENT), index)
+    pe = _strided(k_pe, "k_pe", (T, D_ROPE), index)
+    gamma = _dense(kv_norm_weight, "kv_norm_weight", torch.bfloat16, (D_LATENT,), index)
+    cache = _cache_ptr(kv_cache, fp8, index)
+    _index_of(block_table, "block_table", 2)
+    B, width = block_table.shape
+    bt = _dense(block_table, "block_table", torch.int32, (B, width), index)
+    sl = _dense(seq_lens, "seq_lens", torch.int32, (B,), index)
+    off = _dense(token_offsets, "token_offsets", torch.int32, (B + 1,), index)
+    pos = None if positions is None else _dense(positions, "positions", torch.int32, (T,), index)
+    lib = load_library()
+    with _launch_on(index, stream):
+        tab = _table_of(table, rope_base, index, "cache_append")
+        status = _status_word(status, index)
+        prob = _Ragged(B, T, NUM_HEADS, PAGE_SIZE, width, 0)
+        f = lib.mla_cache_append_fp8 if fp8 else lib.mla_cache_append
+        _check(f(ctypes.byref(prob), *lat, *pe, gamma, rms_eps, tab, pos, cache, kv_cache.shape[0], bt, sl, off,
+                 status.data_ptr(), _current_stream(index)),
+               "mla_cache_append_fp8" if fp8 else "mla_cache_append")
     return status
-
-
-def _req_cache(kv_cache, dev, fp8, layers=False):
-    import torch
-    name = "kv_cache_fp8" if fp8 else "kv_cache"
-    _req(kv_cache, name, torch.uint8 if fp8 else torch.bfloat16, None, dev)
-    row = FP8_ROW_BYTES if fp8 else D_LATENT + D_ROPE
-    if kv_cache.dim() not in ((3, 4) if layers else (3,)) or tuple(kv_cache.shape[-2:]) != (PAGE_SIZE, row):
-        raise ValueError(f"{name} must be {'([layers])' if layers else ''}[num_pages][64][{row}]")
 
 
 @dataclass
@@ -713,19 +741,23 @@ def tree_plan(seq_lens, token_offsets, masks, *, max_pages_per_seq: int, workspa
     it must be ordered.
     """
     import torch
-    _req_index(seq_lens, "seq_lens", torch.int32, (None,), None)
-    B, dev = seq_lens.shape[0], seq_lens.device
-    _req_index(token_offsets, "token_offsets", torch.int32, (B + 1,), dev)
-    _req_index(masks, "masks", torch.int64, (None,), dev)
+    index = _index_of(seq_lens, "seq_lens", 1)
+    B = seq_lens.shape[0]
+    sl = _dense(seq_lens, "seq_lens", torch.int32, (B,), index)
+    off = _dense(token_offsets, "token_offsets", torch.int32, (B + 1,), index)
+    _index_of(masks, "masks", 1)
     T = masks.shape[0]
-    with _launch_on(dev, stream):
+    m = _dense(masks, "masks", torch.int64, (T,), index)
+    lib = load_library()
+    with _launch_on(index, stream):
+        prob = _Ragged(B, T, NUM_HEADS, PAGE_SIZE, max_pages_per_seq, 0)
         if workspace is None:
-            workspace = torch.empty(tree_workspace_size(B, T, max_pages_per_seq), dtype=torch.uint8, device=dev)
-        _req(workspace, "workspace", torch.uint8, None, dev)
-        prob = _ragged(B, T, max_pages_per_seq)
-        _check(load_library().mla_tree_plan(ctypes.byref(prob), seq_lens.data_ptr(), token_offsets.data_ptr(),
-                                            masks.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                            _stream_handle(None)), "mla_tree_plan")
+            n = ctypes.c_size_t(0)
+            _check(lib.mla_tree_workspace_size(ctypes.byref(prob), ctypes.byref(n)), "mla_tree_workspace_size")
+            workspace = torch.empty(n.value, dtype=torch.uint8, device=seq_lens.device)
+        nbytes = workspace.numel()
+        ws = _dense(workspace, "workspace", torch.uint8, (nbytes,), index)
+        _check(lib.mla_tree_plan(ctypes.byref(prob), sl, off, m, ws, nbytes, _current_stream(index)), "mla_tree_plan")
     return TreePlan(B, T, int(max_pages_per_seq), workspace)
 
 
@@ -748,20 +780,20 @@ def tree_decode_fp8(p: TreePlan, q_latent, q_rope, kv_cache_fp8, block_table, *,
 
 def _tree_decode(p, q_latent, q_rope, kv_cache, block_table, scale, out, lse, stream, pow2_max, fp8):
     import torch
-    dev, T = p.workspace.device, p.tokens
-    _req(q_latent, "q_latent", torch.bfloat16, (T, NUM_HEADS, D_LATENT), dev)
-    _req(q_rope, "q_rope", torch.bfloat16, (T, NUM_HEADS, D_ROPE), dev)
-    _req_cache(kv_cache, dev, fp8)
-    _req_index(block_table, "block_table", torch.int32, (p.batch, p.max_pages), dev)
-    name = "mla_tree_decode_fp8" if fp8 else "mla_tree_decode"
-    with _launch_on(dev, stream):
-        out = _req_out(out, "out", torch.bfloat16, (T, NUM_HEADS, D_LATENT), dev)
-        lse = _req_out(lse, "lse", torch.float32, (T, NUM_HEADS), dev)
-        prob = p.problem(MLA_FLAG_POW2_MAX if pow2_max else 0)
-        _check(getattr(load_library(), name)(
-            ctypes.byref(prob), q_latent.data_ptr(), q_rope.data_ptr(), kv_cache.data_ptr(), kv_cache.shape[0],
-            block_table.data_ptr(), float(scale), out.data_ptr(), lse.data_ptr(), p.workspace.data_ptr(),
-            p.workspace.numel(), _stream_handle(None)), name)
+    T, ws = p.tokens, p.workspace
+    index = ws.get_device()
+    ql = _dense(q_latent, "q_latent", torch.bfloat16, (T, NUM_HEADS, D_LATENT), index)
+    qr = _dense(q_rope, "q_rope", torch.bfloat16, (T, NUM_HEADS, D_ROPE), index)
+    cache = _cache_ptr(kv_cache, fp8, index)
+    bt = _dense(block_table, "block_table", torch.int32, (p.batch, p.max_pages), index)
+    lib = load_library()
+    with _launch_on(index, stream):
+        out = _out(out, "out", torch.bfloat16, (T, NUM_HEADS, D_LATENT), index)
+        lse = _out(lse, "lse", torch.float32, (T, NUM_HEADS), index)
+        prob = _Ragged(p.batch, T, NUM_HEADS, PAGE_SIZE, p.max_pages, MLA_FLAG_POW2_MAX if pow2_max else 0)
+        f = lib.mla_tree_decode_fp8 if fp8 else lib.mla_tree_decode
+        _check(f(ctypes.byref(prob), ql, qr, cache, kv_cache.shape[0], bt, scale, out.data_ptr(), lse.data_ptr(),
+                 ws.data_ptr(), ws.numel(), _current_stream(index)), "mla_tree_decode_fp8" if fp8 else "mla_tree_decode")
     return out, lse
 
 
@@ -787,27 +819,27 @@ def cache_commit_fp8(kv_cache_fp8, block_table, seq_lens, token_offsets, paths, 
 
 def _commit(kv_cache, block_table, seq_lens, token_offsets, paths, path_lens, new_seq_lens, status, stream, fp8):
     import torch
-    _req_index(block_table, "block_table", torch.int32, (None, None), None)
-    B, dev = block_table.shape[0], block_table.device
-    _req_cache(kv_cache, dev, fp8, layers=True)
-    _req_index(seq_lens, "seq_lens", torch.int32, (B,), dev)
-    _req_index(token_offsets, "token_offsets", torch.int32, (B + 1,), dev)
-    _req_index(paths, "paths", torch.int32, (B, None), dev)
-    _req_index(path_lens, "path_lens", torch.int32, (B,), dev)
+    index = _index_of(block_table, "block_table", 2)
+    B, width = block_table.shape
+    bt = _dense(block_table, "block_table", torch.int32, (B, width), index)
+    cache = _cache_ptr(kv_cache, fp8, index, layers=True)
+    sl = _dense(seq_lens, "seq_lens", torch.int32, (B,), index)
+    off = _dense(token_offsets, "token_offsets", torch.int32, (B + 1,), index)
+    _index_of(paths, "paths", 2)
+    most = paths.shape[1]
+    way = _dense(paths, "paths", torch.int32, (B, most), index)
+    lens = _dense(path_lens, "path_lens", torch.int32, (B,), index)
     row = FP8_ROW_BYTES if fp8 else 2 * (D_LATENT + D_ROPE)
-    layers, pages = (kv_cache.shape[0] if kv_cache.dim() == 4 else 1), kv_cache.shape[-3]
-    with _launch_on(dev, stream):
-        if new_seq_lens is None:
-            new_seq_lens = torch.empty(B, dtype=torch.int32, device=dev)
-        _req_index(new_seq_lens, "new_seq_lens", torch.int32, (B,), dev)
-        status = _req_status(status, dev)
-        # the tokens bound the offsets; here the trees' own sizes do
-        prob = _ragged(B, (1 << 24) - 1, block_table.shape[1])
+    shape = kv_cache.shape
+    layers, pages = (shape[0] if len(shape) == 4 else 1), shape[-3]
+    with _launch_on(index, stream):
+        new_seq_lens = _out(new_seq_lens, "new_seq_lens", torch.int32, (B,), index)
+        status = _status_word(status, index)
+        # the offsets alone say how many nodes there are: any bound on them will do
+        prob = _Ragged(B, (1 << 24) - 1, NUM_HEADS, PAGE_SIZE, width, 0)
         _check(load_library().mla_cache_commit(
-            ctypes.byref(prob), kv_cache.data_ptr(), layers, pages * PAGE_SIZE * row, row, pages,
-            block_table.data_ptr(), seq_lens.data_ptr(), token_offsets.data_ptr(), paths.data_ptr(), paths.shape[1],
-            path_lens.data_ptr(), new_seq_lens.data_ptr(), status.data_ptr(), _stream_handle(None)),
-            "mla_cache_commit")
+            ctypes.byref(prob), cache, layers, pages * PAGE_SIZE * row, row, pages, bt, sl, off, way, most, lens,
+            new_seq_lens.data_ptr(), status.data_ptr(), _current_stream(index)), "mla_cache_commit")
     return new_seq_lens, status
 
 

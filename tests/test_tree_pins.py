@@ -243,10 +243,12 @@ def test_binding_refuses_wrong_tensors():
         mla.query(cpu[..., :128], cpu[..., 128:], None, None)
     with pytest.raises(TypeError, match="bfloat16"):
         mla.query(cpu.float()[..., :128], cpu[..., 128:], None, None)
-    with pytest.raises(ValueError, match="tokens"):
+    with pytest.raises(ValueError, match="q_nope"):
         mla.query(cpu[:0, :, :128], cpu[:0, :, 128:], None, None)
-    with pytest.raises(ValueError, match="tokens"):
+    with pytest.raises(ValueError, match="kv_latent"):
         mla.cache_append(cpu, cpu, None, None, None, None, None)
+    with pytest.raises(TypeError, match="kv_latent"):
+        mla.cache_append(None, cpu, None, None, None, None, None)
     with pytest.raises(TypeError, match="int32"):
         mla.tree_plan(torch.zeros(2), None, None, max_pages_per_seq=1)
     with pytest.raises(ValueError, match="CUDA"):

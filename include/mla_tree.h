@@ -145,8 +145,19 @@ mla_status mla_tree_decode(const mla_ragged *prob, const void *q_latent, const v
                            void *workspace, size_t workspace_bytes, mla_stream_t stream);
 mla_status mla_tree_decode_fp8(const mla_ragged *prob, const void *q_latent, const void *q_rope,
                                const void *kv_cache_fp8, int64_t num_pages, const int32_t *block_table, float scale,
-                               void *o_latent, float *lse, void *workspace, size_t workspace_bytes,
-                               mla_stream_t stream);
+                               void *o_latent, float *lse, void *workspace, size_t workspace_bytes, void *scratch,
+                               size_t scratch_bytes, mla_stream_t stream);
+
+/*
+ * Bytes of the optional scratch of mla_tree_decode_fp8: room for every table
+ * entry's page as bf16 rows (batch * max_pages_per_seq * 73,984).  With scratch
+ * (16-byte aligned, at least this size) each page that the trees read is
+ * expanded once per call and the nodes share it; without (NULL) each node expands
+ * the pages again as it reads them, which costs about twice the time from a few
+ * nodes per request on.  The results are equal bit for bit.  Concurrent calls need a
+ * scratch each.  Batches of more than 65,535 cannot use one (MLA_ERR_CUDA).
+ */
+mla_status mla_tree_scratch_size(const mla_ragged *prob, size_t *bytes);
 
 /*
  * The planner's algorithm on the host, for tests and tooling: the schedule

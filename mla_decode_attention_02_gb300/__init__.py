@@ -42,7 +42,7 @@ from ._binding import (D_V, HIDDEN, DEFAULT_ROPE_BASE, DEFAULT_RMS_EPS, DEFAULT_
                        decode_diag, decode_fp8, decode_noalloc, epilog_oproj, epilog_uv, quantize_cache_fp8,
                        load_library, num_units, parse_plan, plan, prolog, rope_table,
                        plan_device_bytes, plan_host, plan_layout, workspace_size)
-from ._binding import (MLA_DEV_BAD_OFFSETS, MLA_DEV_BAD_PATH, TREE_MAX_NODES, TreePlan, cache_append, cache_append_fp8,
+from ._binding import (MLA_DEV_BAD_OFFSETS, MLA_DEV_BAD_PATH, EXPANDED_PAGE_BYTES, EXPAND_LIMIT_BYTES, TREE_MAX_NODES, TreePlan, cache_append, cache_append_fp8,
                        cache_commit, cache_commit_fp8, query, tree_decode, tree_decode_fp8, tree_plan,
                        tree_plan_device, tree_plan_host, tree_workspace_size)
 
@@ -54,6 +54,6 @@ __all__ = ["D_V", "HIDDEN", "epilog_oproj", "epilog_uv",
            "decode_diag", "decode_fp8", "decode_noalloc",
            "load_library", "num_units", "parse_plan",
            "plan", "plan_device_bytes", "prolog", "rope_table", "plan_host", "plan_layout", "workspace_size",
-           "MLA_DEV_BAD_OFFSETS", "MLA_DEV_BAD_PATH", "TREE_MAX_NODES", "TreePlan", "cache_append", "cache_append_fp8",
+           "MLA_DEV_BAD_OFFSETS", "MLA_DEV_BAD_PATH", "EXPANDED_PAGE_BYTES", "EXPAND_LIMIT_BYTES", "TREE_MAX_NODES", "TreePlan", "cache_append", "cache_append_fp8",
            "cache_commit", "cache_commit_fp8", "query", "tree_decode", "tree_decode_fp8", "tree_plan",
            "tree_plan_device", "tree_plan_host", "tree_workspace_size"]

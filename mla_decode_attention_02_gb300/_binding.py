@@ -89,13 +89,15 @@ _SIGS = {
     "mla_tree_plan": (ctypes.c_int, [_R, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
     "mla_tree_decode": (ctypes.c_int, [_R, _vp, _vp, _vp, ctypes.c_int64, _vp, ctypes.c_float, _vp, _vp, _vp,
                                        ctypes.c_size_t, _vp]),
+    "mla_tree_decode_fp8": (ctypes.c_int, [_R, _vp, _vp, _vp, ctypes.c_int64, _vp, ctypes.c_float, _vp, _vp, _vp,
+                                           ctypes.c_size_t, _vp, ctypes.c_size_t, _vp]),
+    "mla_tree_scratch_size": (ctypes.c_int, [_R, ctypes.POINTER(ctypes.c_size_t)]),
     "mla_tree_plan_bytes": (ctypes.c_size_t, [_R, ctypes.c_int32]),
     "mla_tree_plan_host": (ctypes.c_int, [_R, _vp, _vp, _vp, ctypes.c_int32, _vp, ctypes.c_size_t]),
     "mla_cache_commit": (ctypes.c_int, [_R, _vp, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int64, _vp,
                                         _vp, _vp, _vp, ctypes.c_int32, _vp, _vp, _vp, _vp]),
 }
-for _name in ("mla_cache_append", "mla_tree_decode"):   # the fp8 entry points take the same arguments
-    _SIGS[_name + "_fp8"] = _SIGS[_name]
+_SIGS["mla_cache_append_fp8"] = _SIGS["mla_cache_append"]
 
 
 def load_library(path: str | None = None) -> ctypes.CDLL:
@@ -541,29 +543,37 @@ def _refuse(t, name, dtype, shape, index, strided=False):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not strided and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    raise ValueError(f"{name} must be 16-byte aligned")
+    raise ValueError(f"{name} must be 16-byte aligned (integers: to their size)")
 
 
-def _dense(t, name, dtype, shape, index) -> int:
-    """Address of a dense array of this dtype and shape on device `index` (16-byte aligned unless integers)."""
-    import torch
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
-            and index >= 0 and t.is_contiguous()):
-        ptr = t.data_ptr()
-        if not ptr & 15 or dtype is torch.int32 or dtype is torch.int64:
-            return ptr
+def _dense(t, name, dtype, shape, index, align=16) -> int:
+    """Address of a dense array of this dtype and shape on device `index`.
+
+    A call of a small operator takes a few microseconds on the GPU, so what is not needed to
+    accept an argument is left to _refuse.
+    """
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            ptr = t.data_ptr()
+            if not ptr % align:
+                return ptr
+    except AttributeError:
+        pass
     _refuse(t, name, dtype, shape, index)
 
 
-def _strided(t, name, shape, index):
-    """Address and strides (in elements) of a bf16 input whose last dim is contiguous.
+def _strided(t, name, dtype, shape, index):
+    """Address and strides (in elements) of an input whose last dim is contiguous.
 
     The others may be strided (a view of a larger projection): positive multiples of 8.
     """
-    import torch
-    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.shape == shape
-            and t.get_device() == index and index >= 0 and not t.data_ptr() & 15):
-        _refuse(t, name, torch.bfloat16, shape, index, strided=True)
+    try:
+        ptr = t.data_ptr()
+        taken = t.dtype is dtype and t.shape == shape and t.get_device() == index and not ptr % 16
+    except AttributeError:
+        taken = False
+    if not taken:
+        _refuse(t, name, dtype, shape, index, strided=True)
     st = t.stride()
     if st[-1] != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
@@ -573,17 +583,21 @@ def _strided(t, name, shape, index):
     for v in st[:-1]:
         if v < 1 or v % 8 or v >= 1 << 31:
             raise ValueError(f"{name}'s strides must be positive multiples of 8")
-    return (t.data_ptr(), *st[:-1])
+    return (ptr, *st[:-1])
 
 
-def _index_of(t, name, dim) -> int:
-    """Device index of the argument that fixes the device, with its dimension count."""
+def _index_of(t, name, dim, dtype) -> int:
+    """Device index of the argument that fixes the device and a size, with its dimension count."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != dim or 0 in t.shape:
-        raise ValueError(f"{name} must have {dim} non-empty dimensions, got {tuple(t.shape)}")
-    return t.get_device()
+    shape = t.shape
+    if len(shape) != dim or 0 in shape:
+        raise ValueError(f"{name} must have {dim} non-empty dimensions, got {tuple(shape)}")
+    index = t.get_device()
+    if index < 0:
+        _refuse(t, name, dtype, shape, index)
+    return index
 
 
 def _out(t, name, dtype, shape, index):
@@ -591,7 +605,7 @@ def _out(t, name, dtype, shape, index):
     import torch
     if t is None:
         return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
-    _dense(t, name, dtype, shape, index)
+    _dense(t, name, dtype, shape, index, 4 if dtype is torch.int32 else 16)
     return t
 
 
@@ -599,7 +613,7 @@ def _status_word(status, index):
     import torch
     if status is None:
         return torch.zeros(1, dtype=torch.int32, device=torch.device("cuda", index))
-    _dense(status, "status", torch.int32, (1,), index)
+    _dense(status, "status", torch.int32, (1,), index, 4)
     return status
 
 
@@ -617,21 +631,21 @@ def _table_of(table, rope_base, index, what) -> int:
             table = rope_table(rope_base, torch.device("cuda", index))
             torch.cuda.current_stream().synchronize()
             _rope_tables[key] = table
-    return _dense(table, "table", torch.float32, (ROPE_TABLE_FLOATS,), index)
+    return _dense(table, "table", torch.float32, (ROPE_TABLE_FLOATS,), index, 4)
 
 
 def _cache_ptr(kv_cache, fp8, index, layers=False) -> int:
     import torch
-    name = "kv_cache_fp8" if fp8 else "kv_cache"
-    row = FP8_ROW_BYTES if fp8 else D_LATENT + D_ROPE
+    name, dtype, row = (("kv_cache_fp8", torch.uint8, FP8_ROW_BYTES) if fp8 else
+                        ("kv_cache", torch.bfloat16, D_LATENT + D_ROPE))
     if not isinstance(kv_cache, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     shape = kv_cache.shape
-    if len(shape) not in ((3, 4) if layers else (3,)) or shape[-2] != PAGE_SIZE or shape[-1] != row or 0 in shape:
-        if kv_cache.dtype != (torch.uint8 if fp8 else torch.bfloat16):
-            raise TypeError(f"{name} must be {torch.uint8 if fp8 else torch.bfloat16}, got {kv_cache.dtype}")
+    if shape[-2:] != (PAGE_SIZE, row) or not (len(shape) == 3 or (layers and len(shape) == 4)) or 0 in shape:
+        if kv_cache.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {kv_cache.dtype}")
         raise ValueError(f"{name} must be {'([layers])' if layers else ''}[num_pages][64][{row}]")
-    return _dense(kv_cache, name, torch.uint8 if fp8 else torch.bfloat16, shape, index)
+    return _dense(kv_cache, name, dtype, shape, index)
 
 
 def query(q_nope, q_pe, w_uk, positions, *, rope_base: float = DEFAULT_ROPE_BASE, table=None, q_latent=None,
@@ -646,11 +660,11 @@ def query(q_nope, q_pe, w_uk, positions, *, rope_base: float = DEFAULT_ROPE_BASE
     one-element int32 device tensor of MLA_DEV_* bits.
     """
     import torch
-    index = _index_of(q_nope, "q_nope", 3)
+    index = _index_of(q_nope, "q_nope", 3, torch.bfloat16)
     T = q_nope.shape[0]
-    args = (*_strided(q_nope, "q_nope", (T, NUM_HEADS, D_NOPE), index), *_strided(q_pe, "q_pe", (T, NUM_HEADS, D_ROPE), index),
+    args = (*_strided(q_nope, "q_nope", torch.bfloat16, (T, NUM_HEADS, D_NOPE), index), *_strided(q_pe, "q_pe", torch.bfloat16, (T, NUM_HEADS, D_ROPE), index),
             _dense(w_uk, "w_uk", torch.bfloat16, (NUM_HEADS, D_NOPE, D_LATENT), index))
-    pos = _dense(positions, "positions", torch.int32, (T,), index)
+    pos = _dense(positions, "positions", torch.int32, (T,), index, 4)
     with _launch_on(index, stream):
         tab = _table_of(table, rope_base, index, "query")
         q_latent = _out(q_latent, "q_latent", torch.bfloat16, (T, NUM_HEADS, D_LATENT), index)
@@ -688,18 +702,18 @@ def cache_append_fp8(kv_latent, k_pe, kv_norm_weight, kv_cache_fp8, block_table,
 def _append(kv_latent, k_pe, kv_norm_weight, kv_cache, block_table, seq_lens, token_offsets, positions, rope_base,
             rms_eps, table, status, stream, fp8):
     import torch
-    index = _index_of(kv_latent, "kv_latent", 2)
+    index = _index_of(kv_latent, "kv_latent", 2, torch.bfloat16)
     T = kv_latent.shape[0]
-    lat = _strided(kv_latent, "kv_latent", (T, D_LATENT), index)
-    pe = _strided(k_pe, "k_pe", (T, D_ROPE), index)
+    lat = _strided(kv_latent, "kv_latent", torch.bfloat16, (T, D_LATENT), index)
+    pe = _strided(k_pe, "k_pe", torch.bfloat16, (T, D_ROPE), index)
     gamma = _dense(kv_norm_weight, "kv_norm_weight", torch.bfloat16, (D_LATENT,), index)
     cache = _cache_ptr(kv_cache, fp8, index)
-    _index_of(block_table, "block_table", 2)
+    _index_of(block_table, "block_table", 2, torch.int32)
     B, width = block_table.shape
-    bt = _dense(block_table, "block_table", torch.int32, (B, width), index)
-    sl = _dense(seq_lens, "seq_lens", torch.int32, (B,), index)
-    off = _dense(token_offsets, "token_offsets", torch.int32, (B + 1,), index)
-    pos = None if positions is None else _dense(positions, "positions", torch.int32, (T,), index)
+    bt = _dense(block_table, "block_table", torch.int32, (B, width), index, 4)
+    sl = _dense(seq_lens, "seq_lens", torch.int32, (B,), index, 4)
+    off = _dense(token_offsets, "token_offsets", torch.int32, (B + 1,), index, 4)
+    pos = None if positions is None else _dense(positions, "positions", torch.int32, (T,), index, 4)
     lib = load_library()
     with _launch_on(index, stream):
         tab = _table_of(table, rope_base, index, "cache_append")
@@ -741,13 +755,13 @@ def tree_plan(seq_lens, token_offsets, masks, *, max_pages_per_seq: int, workspa
     it must be ordered.
     """
     import torch
-    index = _index_of(seq_lens, "seq_lens", 1)
+    index = _index_of(seq_lens, "seq_lens", 1, torch.int32)
     B = seq_lens.shape[0]
-    sl = _dense(seq_lens, "seq_lens", torch.int32, (B,), index)
-    off = _dense(token_offsets, "token_offsets", torch.int32, (B + 1,), index)
-    _index_of(masks, "masks", 1)
+    sl = _dense(seq_lens, "seq_lens", torch.int32, (B,), index, 4)
+    off = _dense(token_offsets, "token_offsets", torch.int32, (B + 1,), index, 4)
+    _index_of(masks, "masks", 1, torch.int64)
     T = masks.shape[0]
-    m = _dense(masks, "masks", torch.int64, (T,), index)
+    m = _dense(masks, "masks", torch.int64, (T,), index, 8)
     lib = load_library()
     with _launch_on(index, stream):
         prob = _Ragged(B, T, NUM_HEADS, PAGE_SIZE, max_pages_per_seq, 0)
@@ -773,27 +787,51 @@ def tree_decode(p: TreePlan, q_latent, q_rope, kv_cache, block_table, *, scale: 
 
 
 def tree_decode_fp8(p: TreePlan, q_latent, q_rope, kv_cache_fp8, block_table, *, scale: float = DEFAULT_SCALE,
-                    out=None, lse=None, stream=None, pow2_max: bool = False):
-    """``tree_decode`` over an fp8 cache (``mla_tree_decode_fp8``; uint8 [pages][64][656])."""
-    return _tree_decode(p, q_latent, q_rope, kv_cache_fp8, block_table, scale, out, lse, stream, pow2_max, True)
+                    out=None, lse=None, stream=None, pow2_max: bool = False, scratch=None):
+    """``tree_decode`` over an fp8 cache (``mla_tree_decode_fp8``; uint8 [pages][64][656]).
+
+    scratch: where each page is expanded once for all nodes, a uint8 tensor of at least
+    batch * max_pages * EXPANDED_PAGE_BYTES bytes, or False for none.  By default one is allocated
+    for the call if the trees average two nodes or more and it takes no more than
+    EXPAND_LIMIT_BYTES.  The results are the same bit for bit.
+    """
+    return _tree_decode(p, q_latent, q_rope, kv_cache_fp8, block_table, scale, out, lse, stream, pow2_max, True,
+                        scratch)
 
 
-def _tree_decode(p, q_latent, q_rope, kv_cache, block_table, scale, out, lse, stream, pow2_max, fp8):
+EXPANDED_PAGE_BYTES = PAGE_SIZE * (2 * (D_LATENT + D_ROPE) + 4)
+EXPAND_LIMIT_BYTES = 8 << 30
+
+
+def _tree_decode(p, q_latent, q_rope, kv_cache, block_table, scale, out, lse, stream, pow2_max, fp8, scratch=False):
     import torch
     T, ws = p.tokens, p.workspace
     index = ws.get_device()
     ql = _dense(q_latent, "q_latent", torch.bfloat16, (T, NUM_HEADS, D_LATENT), index)
     qr = _dense(q_rope, "q_rope", torch.bfloat16, (T, NUM_HEADS, D_ROPE), index)
     cache = _cache_ptr(kv_cache, fp8, index)
-    bt = _dense(block_table, "block_table", torch.int32, (p.batch, p.max_pages), index)
+    bt = _dense(block_table, "block_table", torch.int32, (p.batch, p.max_pages), index, 4)
     lib = load_library()
     with _launch_on(index, stream):
         out = _out(out, "out", torch.bfloat16, (T, NUM_HEADS, D_LATENT), index)
         lse = _out(lse, "lse", torch.float32, (T, NUM_HEADS), index)
         prob = _Ragged(p.batch, T, NUM_HEADS, PAGE_SIZE, p.max_pages, MLA_FLAG_POW2_MAX if pow2_max else 0)
-        f = lib.mla_tree_decode_fp8 if fp8 else lib.mla_tree_decode
-        _check(f(ctypes.byref(prob), ql, qr, cache, kv_cache.shape[0], bt, scale, out.data_ptr(), lse.data_ptr(),
-                 ws.data_ptr(), ws.numel(), _current_stream(index)), "mla_tree_decode_fp8" if fp8 else "mla_tree_decode")
+        args = (ctypes.byref(prob), ql, qr, cache, kv_cache.shape[0], bt, scale, out.data_ptr(), lse.data_ptr(),
+                ws.data_ptr(), ws.numel())
+        if not fp8:
+            _check(lib.mla_tree_decode(*args, _current_stream(index)), "mla_tree_decode")
+            return out, lse
+        if scratch is None:
+            need = p.batch * p.max_pages * EXPANDED_PAGE_BYTES
+            if T >= 2 * p.batch and need <= EXPAND_LIMIT_BYTES and p.batch <= 65535:
+                scratch = torch.empty(need, dtype=torch.uint8, device=ws.device)
+            else:
+                scratch = False
+        room = (None, 0)
+        if scratch is not False:
+            n = scratch.numel()
+            room = (_dense(scratch, "scratch", torch.uint8, (n,), index), n)
+        _check(lib.mla_tree_decode_fp8(*args, *room, _current_stream(index)), "mla_tree_decode_fp8")
     return out, lse
 
 
@@ -819,16 +857,16 @@ def cache_commit_fp8(kv_cache_fp8, block_table, seq_lens, token_offsets, paths, 
 
 def _commit(kv_cache, block_table, seq_lens, token_offsets, paths, path_lens, new_seq_lens, status, stream, fp8):
     import torch
-    index = _index_of(block_table, "block_table", 2)
+    index = _index_of(block_table, "block_table", 2, torch.int32)
     B, width = block_table.shape
-    bt = _dense(block_table, "block_table", torch.int32, (B, width), index)
+    bt = _dense(block_table, "block_table", torch.int32, (B, width), index, 4)
     cache = _cache_ptr(kv_cache, fp8, index, layers=True)
-    sl = _dense(seq_lens, "seq_lens", torch.int32, (B,), index)
-    off = _dense(token_offsets, "token_offsets", torch.int32, (B + 1,), index)
-    _index_of(paths, "paths", 2)
+    sl = _dense(seq_lens, "seq_lens", torch.int32, (B,), index, 4)
+    off = _dense(token_offsets, "token_offsets", torch.int32, (B + 1,), index, 4)
+    _index_of(paths, "paths", 2, torch.int32)
     most = paths.shape[1]
-    way = _dense(paths, "paths", torch.int32, (B, most), index)
-    lens = _dense(path_lens, "path_lens", torch.int32, (B,), index)
+    way = _dense(paths, "paths", torch.int32, (B, most), index, 4)
+    lens = _dense(path_lens, "path_lens", torch.int32, (B,), index, 4)
     row = FP8_ROW_BYTES if fp8 else 2 * (D_LATENT + D_ROPE)
     shape = kv_cache.shape
     layers, pages = (shape[0] if len(shape) == 4 else 1), shape[-3]
@@ -861,10 +899,10 @@ def _align(x: int, a: int) -> int:
     return (x + a - 1) // a * a
 
 
-def plan_layout(batch: int, s_q: int, units: int, tree: bool = False) -> dict:
+def plan_layout(batch: int, s_q: int, units: int, trees: int = 0) -> dict:
     """Byte offsets of the schedule regions (mirrors make_layout in csrc/mla_internal.h).
 
-    A tree schedule has one row per token: batch * s_q is then the number of tokens.
+    A tree schedule has one row per token: batch * s_q is then the number of tokens, and trees its batch.
     """
     rows = batch * s_q
     max_items = rows + units
@@ -884,10 +922,12 @@ def plan_layout(batch: int, s_q: int, units: int, tree: bool = False) -> dict:
     off = _align(off, 8)
     L["row_pos"] = off
     off += 8 * rows
-    if tree:
+    if trees:
         off = _align(off, 16)
         L["tree_rows"] = off
         off += 16 * rows
+        L["tree_pages"] = off
+        off += 4 * trees
     L["plan_end"] = off
     return L
 
@@ -902,15 +942,16 @@ _HDR = np.dtype([("magic", "<u4"), ("batch", "<i4"), ("s_q", "<i4"), ("max_pages
 _TREE_ROW = np.dtype([("mask", "<u8"), ("context", "<i4"), ("req", "<i4")])
 
 
-def parse_plan(buf, batch: int, s_q: int, units: int, tree: bool = False) -> dict:
+def parse_plan(buf, batch: int, s_q: int, units: int, trees: int = 0) -> dict:
     """Decode schedule bytes (host copy of a workspace prefix) into numpy arrays."""
     b = np.frombuffer(bytes(buf), dtype=np.uint8)
-    L = plan_layout(batch, s_q, units, tree)
+    L = plan_layout(batch, s_q, units, trees)
     hdr = b[:64].view(_HDR)[0]
     n = int(hdr["num_items"])
     R = L["num_rows"]
     items = b[L["items"]:L["items"] + 16 * n].view("<i4").reshape(n, 4)
-    more = {"tree_rows": b[L["tree_rows"]:L["tree_rows"] + 16 * R].view(_TREE_ROW).copy()} if tree else {}
+    more = {"tree_rows": b[L["tree_rows"]:L["tree_rows"] + 16 * R].view(_TREE_ROW).copy(),
+            "tree_pages": b[L["tree_pages"]:L["tree_pages"] + 4 * trees].view("<i4").copy()} if trees else {}
     return {
         **more,
         "header": {k: int(hdr[k]) for k in _HDR.names},
@@ -956,11 +997,11 @@ def tree_plan_host(seq_lens, token_offsets, masks, *, max_pages_per_seq: int, nu
     buf = np.zeros(max(nbytes, 1), dtype=np.uint8)
     _check(lib.mla_tree_plan_host(ctypes.byref(prob), sl.ctypes.data, off.ctypes.data, m.ctypes.data, int(num_units),
                                   buf.ctypes.data, nbytes), "mla_tree_plan_host")
-    return parse_plan(buf.tobytes(), 1, m.shape[0], num_units, tree=True)
+    return parse_plan(buf.tobytes(), 1, m.shape[0], num_units, trees=sl.shape[0])
 
 
 def tree_plan_device(p: TreePlan) -> dict:
     """Host copy of a device schedule of trees, parsed (for tests)."""
     units = num_units()
-    end = plan_layout(1, p.tokens, units, tree=True)["plan_end"]
-    return parse_plan(p.workspace[:end].cpu().numpy().tobytes(), 1, p.tokens, units, tree=True)
+    end = plan_layout(1, p.tokens, units, trees=p.batch)["plan_end"]
+    return parse_plan(p.workspace[:end].cpu().numpy().tobytes(), 1, p.tokens, units, trees=p.batch)

@@ -24,7 +24,10 @@ cudaError_t launch_main(const void *q_latent, const void *q_rope, const void *kv
                         int64_t num_pages, const int32_t *block_table, float scale, void *ws,
                         void *o_latent, float *lse, int32_t batch, int32_t s_q, int32_t max_pages,
                         int32_t num_units, uint64_t wait_limit_ns, uint32_t test_flags,
-                        uint32_t flags, bool fp8, bool tree, cudaStream_t stream);
+                        uint32_t flags, bool fp8, bool tree, const void *expanded, cudaStream_t stream);
+cudaError_t launch_expand(const void *ws, const void *kv_cache_fp8, int64_t num_pages, const int32_t *block_table,
+                          void *expanded, int32_t batch, int32_t tokens, int32_t max_pages, int32_t num_units,
+                          cudaStream_t stream);
 mla_status tree_plan_host(const mla_ragged *prob, const int32_t *seq_lens, const int32_t *offsets,
                           const uint64_t *masks, int32_t num_units, uint8_t *ws);
 cudaError_t launch_tree_plan(const int32_t *seq_lens, const int32_t *offsets, const uint64_t *masks, void *ws,
@@ -178,7 +181,7 @@ static mla_status decode_impl(const mla_problem *prob, const void *q_latent, con
     cudaError_t e = mla::launch_main(q_latent, q_rope, kv_cache, num_pages, block_table, scale,
                                      workspace, o_latent, lse, prob->batch, prob->s_q,
                                      prob->max_pages_per_seq, units, wait_limit_ns, test_flags,
-                                     (uint32_t)prob->flags, fp8, false, s);
+                                     (uint32_t)prob->flags, fp8, false, nullptr, s);
     if (e != cudaSuccess || !mark(1)) return MLA_ERR_CUDA;
     e = mla::launch_combine(workspace, o_latent, lse, prob->batch, prob->s_q, units, false, s);
     if (e != cudaSuccess || !mark(2)) return MLA_ERR_CUDA;
@@ -245,13 +248,13 @@ mla_status mla_tree_workspace_size(const mla_ragged *prob, size_t *bytes) {
     int32_t units = 0;
     if (mla::main_units(&units) != cudaSuccess) return MLA_ERR_CUDA;
     if (!mla::plan_fits(prob->tokens, units)) return MLA_ERR_UNSUPPORTED;
-    *bytes = mla::make_layout(prob->tokens, units, true).total;
+    *bytes = mla::make_layout(prob->tokens, units, prob->batch).total;
     return MLA_OK;
 }
 
 size_t mla_tree_plan_bytes(const mla_ragged *prob, int32_t num_units) {
     if (mla::check_ragged(prob, MLA_FLAG_POW2_MAX) != MLA_OK || num_units < 1) return 0;
-    return mla::make_layout(prob->tokens, num_units, true).plan_end;
+    return mla::make_layout(prob->tokens, num_units, prob->batch).plan_end;
 }
 
 mla_status mla_tree_plan_host(const mla_ragged *prob, const int32_t *seq_lens_host, const int32_t *token_offsets_host,
@@ -259,7 +262,7 @@ mla_status mla_tree_plan_host(const mla_ragged *prob, const int32_t *seq_lens_ho
     mla_status st = mla::check_ragged(prob, MLA_FLAG_POW2_MAX);
     if (st != MLA_OK) return st;
     if (!seq_lens_host || !token_offsets_host || !masks_host || !plan_host || num_units < 1) return MLA_ERR_INVALID_ARG;
-    if (plan_bytes < mla::make_layout(prob->tokens, num_units, true).plan_end) return MLA_ERR_WORKSPACE;
+    if (plan_bytes < mla::make_layout(prob->tokens, num_units, prob->batch).plan_end) return MLA_ERR_WORKSPACE;
     return mla::tree_plan_host(prob, seq_lens_host, token_offsets_host, masks_host, num_units,
                                static_cast<uint8_t *>(plan_host));
 }
@@ -273,11 +276,11 @@ mla_status mla_tree_plan(const mla_ragged *prob, const int32_t *seq_lens, const 
         (reinterpret_cast<uintptr_t>(token_offsets) & 3u) || !masks || (reinterpret_cast<uintptr_t>(masks) & 7u) ||
         !workspace || !aligned16(workspace))
         return MLA_ERR_INVALID_ARG;
-    if (workspace_bytes < mla::make_layout(prob->tokens, 1, true).total) return MLA_ERR_WORKSPACE;
+    if (workspace_bytes < mla::make_layout(prob->tokens, 1, prob->batch).total) return MLA_ERR_WORKSPACE;
     int32_t units = 0;
     if (mla::main_units(&units) != cudaSuccess) return MLA_ERR_CUDA;
     if (!mla::plan_fits(prob->tokens, units)) return MLA_ERR_UNSUPPORTED;
-    if (workspace_bytes < mla::make_layout(prob->tokens, units, true).total) return MLA_ERR_WORKSPACE;
+    if (workspace_bytes < mla::make_layout(prob->tokens, units, prob->batch).total) return MLA_ERR_WORKSPACE;
     const cudaError_t e = mla::launch_tree_plan(seq_lens, token_offsets, masks, workspace, prob->batch, prob->tokens,
                                                 prob->max_pages_per_seq, units, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
@@ -285,7 +288,8 @@ mla_status mla_tree_plan(const mla_ragged *prob, const int32_t *seq_lens, const 
 
 static mla_status tree_impl(const mla_ragged *prob, const void *q_latent, const void *q_rope, const void *kv_cache,
                             int64_t num_pages, const int32_t *block_table, float scale, void *o_latent, float *lse,
-                            void *workspace, size_t workspace_bytes, bool fp8, mla_stream_t stream) {
+                            void *workspace, size_t workspace_bytes, bool fp8, void *scratch, size_t scratch_bytes,
+                            mla_stream_t stream) {
     mla_status st = mla::check_ragged(prob, MLA_FLAG_POW2_MAX);
     if (st != MLA_OK) return st;
     const void *ptrs[] = {q_latent, q_rope, kv_cache, o_latent, lse, workspace};
@@ -294,15 +298,22 @@ static mla_status tree_impl(const mla_ragged *prob, const void *q_latent, const 
     if (!block_table || (reinterpret_cast<uintptr_t>(block_table) & 3u)) return MLA_ERR_INVALID_ARG;
     if (num_pages < 1 || num_pages > ((int64_t)1 << 31) - 1) return MLA_ERR_INVALID_ARG;
     if (!std::isfinite(scale) || !(scale > 0.f)) return MLA_ERR_INVALID_ARG;
-    if (workspace_bytes < mla::make_layout(prob->tokens, 1, true).total) return MLA_ERR_WORKSPACE;
+    if (scratch && !aligned16(scratch)) return MLA_ERR_INVALID_ARG;
+    if (scratch && scratch_bytes < mla::expanded_bytes(prob->batch, prob->max_pages_per_seq)) return MLA_ERR_WORKSPACE;
+    if (workspace_bytes < mla::make_layout(prob->tokens, 1, prob->batch).total) return MLA_ERR_WORKSPACE;
     int32_t units = 0;
     if (mla::main_units(&units) != cudaSuccess) return MLA_ERR_CUDA;
     if (!mla::plan_fits(prob->tokens, units)) return MLA_ERR_UNSUPPORTED;
-    if (workspace_bytes < mla::make_layout(prob->tokens, units, true).total) return MLA_ERR_WORKSPACE;
+    if (workspace_bytes < mla::make_layout(prob->tokens, units, prob->batch).total) return MLA_ERR_WORKSPACE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = mla::launch_main(q_latent, q_rope, kv_cache, num_pages, block_table, scale, workspace, o_latent,
-                                     lse, prob->batch, prob->tokens, prob->max_pages_per_seq, units,
-                                     mla::kDefaultWaitLimitNs, 0, (uint32_t)prob->flags, fp8, true, s);
+    cudaError_t e = cudaSuccess;
+    if (scratch)
+        e = mla::launch_expand(workspace, kv_cache, num_pages, block_table, scratch, prob->batch, prob->tokens,
+                               prob->max_pages_per_seq, units, s);
+    if (e != cudaSuccess) return MLA_ERR_CUDA;
+    e = mla::launch_main(q_latent, q_rope, kv_cache, num_pages, block_table, scale, workspace, o_latent, lse,
+                         prob->batch, prob->tokens, prob->max_pages_per_seq, units, mla::kDefaultWaitLimitNs, 0,
+                         (uint32_t)prob->flags, fp8, true, scratch, s);
     if (e != cudaSuccess) return MLA_ERR_CUDA;
     e = mla::launch_combine(workspace, o_latent, lse, prob->batch, prob->tokens, units, true, s);
     return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
@@ -313,16 +324,24 @@ mla_status mla_tree_decode(const mla_ragged *prob, const void *q_latent, const v
                            void *workspace, size_t workspace_bytes, mla_stream_t stream) {
     mla::NvtxRange nvtx_range("mla_tree_decode");
     return tree_impl(prob, q_latent, q_rope, kv_cache, num_pages, block_table, scale, o_latent, lse, workspace,
-                     workspace_bytes, false, stream);
+                     workspace_bytes, false, nullptr, 0, stream);
 }
 
 mla_status mla_tree_decode_fp8(const mla_ragged *prob, const void *q_latent, const void *q_rope,
                                const void *kv_cache_fp8, int64_t num_pages, const int32_t *block_table, float scale,
-                               void *o_latent, float *lse, void *workspace, size_t workspace_bytes,
-                               mla_stream_t stream) {
+                               void *o_latent, float *lse, void *workspace, size_t workspace_bytes, void *scratch,
+                               size_t scratch_bytes, mla_stream_t stream) {
     mla::NvtxRange nvtx_range("mla_tree_decode_fp8");
     return tree_impl(prob, q_latent, q_rope, kv_cache_fp8, num_pages, block_table, scale, o_latent, lse, workspace,
-                     workspace_bytes, true, stream);
+                     workspace_bytes, true, scratch, scratch_bytes, stream);
+}
+
+mla_status mla_tree_scratch_size(const mla_ragged *prob, size_t *bytes) {
+    const mla_status st = mla::check_ragged(prob, MLA_FLAG_POW2_MAX);
+    if (st != MLA_OK) return st;
+    if (!bytes) return MLA_ERR_INVALID_ARG;
+    *bytes = mla::expanded_bytes(prob->batch, prob->max_pages_per_seq);
+    return MLA_OK;
 }
 
 }  // extern "C"

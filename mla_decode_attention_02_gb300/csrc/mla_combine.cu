@@ -155,7 +155,7 @@ mla_combine_kernel(const uint8_t *__restrict__ ws, __nv_bfloat16 *__restrict__ o
     } else {
         if (hdr->num_parts == 0 && (hdr->status & MLA_DEV_BAD_SEQ_LEN) == 0) return;
     }
-    const PlanLayout L = make_layout(kTree ? s_q : batch * s_q, num_units, kTree);
+    const PlanLayout L = make_layout(kTree ? s_q : batch * s_q, num_units, kTree ? batch : 0);
     const int32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t tasks = (int64_t)L.num_rows * kHeads;
     const int32_t *row_nparts = reinterpret_cast<const int32_t *>(ws + L.row_nparts);

@@ -85,17 +85,20 @@ static_assert(sizeof(TreeRow) == 16, "tree row layout");
 constexpr int32_t kRowEmpty = -1;    // sees no key: o = 0, lse = -infinity
 constexpr int32_t kRowUnused = -2;   // behind the last request: left as it is
 
-// Byte offsets of every region of the workspace (tree_rows: tree schedules only).
+// Byte offsets of every region of the workspace (tree_rows, and tree_pages, the pages
+// each request's rows read: tree schedules only).
 struct PlanLayout {
-    size_t items, item_unit, unit_begin, row_nparts, row_part0, row_item0, row_pos, tree_rows, plan_end;
+    size_t items, item_unit, unit_begin, row_nparts, row_part0, row_item0, row_pos, tree_rows, tree_pages, plan_end;
     size_t lse_part, o_part, total;
     int32_t num_rows, max_items, max_parts;
 };
 
 MLA_HD size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
-MLA_HD PlanLayout make_layout(int32_t num_rows, int32_t num_units, bool tree) {
+// trees: the batch of a tree schedule, 0 otherwise.
+MLA_HD PlanLayout make_layout(int32_t num_rows, int32_t num_units, int32_t trees) {
     PlanLayout L;
+    const bool tree = trees > 0;
     L.num_rows = num_rows;
     L.max_items = L.num_rows + num_units;
     // a boundary between two units cuts at most one row, so cut rows come to at most
@@ -117,11 +120,13 @@ MLA_HD PlanLayout make_layout(int32_t num_rows, int32_t num_units, bool tree) {
     off = align_up(off, 8);
     L.row_pos = off;
     off += sizeof(int64_t) * (size_t)L.num_rows;
-    L.tree_rows = 0;
+    L.tree_rows = L.tree_pages = 0;
     if (tree) {
         off = align_up(off, 16);
         L.tree_rows = off;
         off += sizeof(TreeRow) * (size_t)L.num_rows;
+        L.tree_pages = off;
+        off += sizeof(int32_t) * (size_t)trees;
     }
     L.plan_end = off;
     off = align_up(off, 256);
@@ -135,7 +140,15 @@ MLA_HD PlanLayout make_layout(int32_t num_rows, int32_t num_units, bool tree) {
 }
 
 MLA_HD PlanLayout plan_layout(int32_t batch, int32_t s_q, int32_t num_units) {
-    return make_layout(batch * s_q, num_units, false);
+    return make_layout(batch * s_q, num_units, 0);
+}
+
+// The expanded form of an fp8 cache that a batch of trees reads (mla_expand.cu): per
+// request and table entry 64 rows of 576 bf16 values, then every row's scale (fp32).
+constexpr size_t kExpandedPage = (size_t)kPage * kDrow * 2;
+MLA_HD size_t expanded_scales(int32_t batch, int32_t max_pages) { return (size_t)batch * max_pages * kExpandedPage; }
+MLA_HD size_t expanded_bytes(int32_t batch, int32_t max_pages) {
+    return (size_t)batch * max_pages * (kExpandedPage + kPage * sizeof(float));
 }
 
 // A node's keys: one past its last visible one (0: it sees none), given its

@@ -197,6 +197,7 @@ struct Params {
     // [block][token][64 dims], the layout the MMAs read
     CUtensorMap tm_k;       // box 64 x 32 x 9 x 1: a token half, all 576 dims
     CUtensorMap tm_v;       // box 64 x 64 x 4 x 1: all 64 tokens, one CTA's 256 output dims
+    // (expanded fp8 rows: tm_k / tm_v view those, tm_ks their scales, (64 floats, pages), box 32 x 1)
     // fp8 cache: tm_k / tm_v are views of the e4m3 codes (128 codes, 64 tokens, 4 blocks,
     // pages; box 128 x 32 x 4 x 1 and 128 x 64 x 2 x 1), and
     CUtensorMap tm_kr;      // k_rope / s: (64 values, 64 tokens, pages), box 64 x 32 x 1, bf16
@@ -541,9 +542,12 @@ __device__ __noinline__ void convert_codes(uint8_t *stage, int t, int bar_id, in
 }
 
 // kTree: P.s_q is the number of tokens (rows).
-template <bool kFp8, bool kTree>
-__global__ void __launch_bounds__(kFp8 ? kThreadsFp8 : kThreads, 1)
+// kExpanded (with kFp8): the codes come as bf16 rows, expanded ahead (mla_expand.cu).
+template <bool kFp8, bool kTree, bool kExpanded>
+__global__ void __launch_bounds__(kFp8 && !kExpanded ? kThreadsFp8 : kThreads, 1)
 mla_main_tc_kernel(const __grid_constant__ Params P) {
+    constexpr bool kConv = kFp8 && !kExpanded;      // converter warps expand the stages
+    constexpr int kScaleStep = kExpanded ? 1 : 4;   // floats from one token's scale to the next
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
@@ -626,7 +630,7 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
     pdl_wait_prior();
     pdl_launch_dependents();
 
-    const PlanLayout L = make_layout(kTree ? P.s_q : P.batch * P.s_q, P.num_units, kTree);
+    const PlanLayout L = make_layout(kTree ? P.s_q : P.batch * P.s_q, P.num_units, kTree ? P.batch : 0);
     const TreeRow *tree_rows = reinterpret_cast<const TreeRow *>(P.ws + L.tree_rows);
     // request of an item's row
     auto request = [&](int32_t row) { return kTree ? tree_rows[row].req : row / P.s_q; };
@@ -672,8 +676,9 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
                 const int ahead = k0 + lane + kPrefetch < n ? bt[k0 + lane + kPrefetch] : 0;
                 const int cnt = min(32, n - k0);
                 for (int kk = 0; kk < cnt; ++kk, ++g) {
-                    const int page = __shfl_sync(0xffffffffu, mine, kk);
-                    const int page_ahead = __shfl_sync(0xffffffffu, ahead, kk);
+                    // expanded rows stand in table order
+                    const int page = kExpanded ? b * P.max_pages + p0 + k0 + kk : __shfl_sync(0xffffffffu, mine, kk);
+                    const int page_ahead = kExpanded ? page + kPrefetch : __shfl_sync(0xffffffffu, ahead, kk);
                     const uint32_t p = g & 1;
                     if (kring) {
                         if (k0 + kk == 0) {
@@ -709,7 +714,12 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
                             // one 36 KB box: an SM ingests a few large TMA copies much
                             // faster than many 4 KB ones
                             const uint32_t fa = bar(ctl, B_KFULL + p);
-                            if constexpr (kFp8) {
+                            if constexpr (kExpanded) {
+                                mbar_arrive_expect_tx(fa, kKStageBytes + kHalfTok * 4);
+                                tma_load_4d(s_k + p * kKStageBytes, &P.tm_k, 0, tok_own, 0, page, fa);
+                                tma_load_2d(s_base + kOffScale + (g % kScaleSlots) * kScaleStage, &P.tm_ks, tok_own,
+                                            page, fa);
+                            } else if constexpr (kFp8) {
                                 // the codes (16 KB) into the upper half of the stage's latent
                                 // blocks, k_rope / s (4 KB) into its place (the converter
                                 // warps expand the codes downward), the tokens' scales into
@@ -759,7 +769,7 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
                         }
                         if (lane == 0) {
                             const uint32_t fv = bar(ctl, B_VFULL + p);
-                            if constexpr (kFp8) {
+                            if constexpr (kConv) {
                                 // the codes of this CTA's 256 output dims (16 KB) into the upper
                                 // half of the stage (the scales came with the page's K load)
                                 mbar_arrive_expect_tx(fv, kVStageBytes / 2);
@@ -822,7 +832,7 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
                     const uint32_t ko = p * kKStageBytes;
                     const uint32_t tSp = tS + kHalfTok * p;
                     // (fp8: the stage is read once the converter warps turned its codes into bf16)
-                    if (!wait_warp(ctl, bar(ctl, (kFp8 ? B_KCONV : B_KFULL) + p), (g >> 1) & 1)) { ok = false; break; }
+                    if (!wait_warp(ctl, bar(ctl, (kConv ? B_KCONV : B_KFULL) + p), (g >> 1) & 1)) { ok = false; break; }
                     if (g >= 2 && !wait_warp(ctl, bar(ctl, B_SEMPTY + p), ((g >> 1) - 1) & 1)) {
                         ok = false;
                         break;
@@ -849,7 +859,7 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
                     // warps released the P slot
                     const uint32_t ps = g % kPSlots, pu = g / kPSlots;
                     const uint32_t vo = p * kVStageBytes, po = ps * kPSlotBytes;
-                    if (!wait_warp(ctl, bar(ctl, (kFp8 ? B_VCONV : B_VFULL) + p), (g >> 1) & 1) ||
+                    if (!wait_warp(ctl, bar(ctl, (kConv ? B_VCONV : B_VFULL) + p), (g >> 1) & 1) ||
                         !wait_warp(ctl, bar(ctl, B_PREADY + ps), pu & 1)) {
                         ok = false;
                         break;
@@ -1001,7 +1011,7 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
                 const float *tsc = reinterpret_cast<const float *>(smem + kOffScale + (g % kScaleSlots) * kScaleStage);
                 if constexpr (kFp8) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * tsc[4 * j]);
+                    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * tsc[kScaleStep * j]);
                 }
                 // scores in log2 units are r * scale_log2 (scale > 0, so the max of
                 // the raw scores gives the max); masked tokens (ragged last page)
@@ -1038,7 +1048,8 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
                         // scale (masked tokens stay 0 whatever their scale slot holds)
                         const bool s0 = kTree ? seen >> (2 * j) & 1 : 2 * j < v_own;
                         const bool s1 = kTree ? seen >> (2 * j + 1) & 1 : 2 * j + 1 < v_own;
-                        pk[j] = pack_bf16(s0 ? e0 * tsc[8 * j] : 0.f, s1 ? e1 * tsc[8 * j + 4] : 0.f);
+                        pk[j] = pack_bf16(s0 ? e0 * tsc[kScaleStep * 2 * j] : 0.f,
+                                          s1 ? e1 * tsc[kScaleStep * (2 * j + 1)] : 0.f);
                     } else {
                         pk[j] = pack_bf16(e0, e1);
                     }
@@ -1198,7 +1209,7 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
             }
             __syncwarp();
         }
-    } else if constexpr (kFp8) {
+    } else if constexpr (kConv) {
         // ------------------------------------------------------------ fp8 -> bf16 converters
         // Warps 12-13 expand each landed K stage, warps 14-15 each V stage, in place:
         // the codes sit in the upper half of the stage's latent blocks; every thread
@@ -1267,7 +1278,7 @@ bool encode(CUtensorMap *m, const void *base, int rank, const cuuint64_t *dims,
 struct DeviceInfo {
     int units = 0;
     bool attr_set = false;
-    int variant[4] = {};   // the other variants: 0 not checked, 1 runs on the same units, -1 does not
+    int variant[6] = {};   // the other variants: 0 not checked, 1 runs on the same units, -1 does not
 };
 std::mutex g_dev_mutex;
 DeviceInfo g_dev[64];
@@ -1277,7 +1288,7 @@ cudaError_t prepare(int dev, int *units) {
     std::lock_guard<std::mutex> lock(g_dev_mutex);
     DeviceInfo &d = g_dev[dev];
     if (!d.attr_set) {
-        cudaError_t e = cudaFuncSetAttribute(mla_main_tc_kernel<false, false>,
+        cudaError_t e = cudaFuncSetAttribute(mla_main_tc_kernel<false, false, false>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)kSmemBytes);
         if (e != cudaSuccess) return e;
@@ -1296,7 +1307,7 @@ cudaError_t prepare(int dev, int *units) {
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
         int n = 0;
-        e = cudaOccupancyMaxActiveClusters(&n, mla_main_tc_kernel<false, false>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&n, mla_main_tc_kernel<false, false, false>, &cfg);
         if (e != cudaSuccess) return e;
         if (n < 1) return cudaErrorInvalidConfiguration;
         d.units = n;
@@ -1308,26 +1319,28 @@ cudaError_t prepare(int dev, int *units) {
 
 using MainKernel = void (*)(Params);
 
-// The kernel of a variant, its block and its shared memory.
-MainKernel main_kernel(bool fp8, bool tree) {
-    if (tree) return fp8 ? mla_main_tc_kernel<true, true> : mla_main_tc_kernel<false, true>;
-    return fp8 ? mla_main_tc_kernel<true, false> : mla_main_tc_kernel<false, false>;
+// A variant of the kernel and its block (expanded: of an fp8 cache and trees).
+MainKernel main_kernel(bool fp8, bool tree, bool expanded) {
+    if (expanded) return mla_main_tc_kernel<true, true, true>;
+    if (tree) return fp8 ? mla_main_tc_kernel<true, true, false> : mla_main_tc_kernel<false, true, false>;
+    return fp8 ? mla_main_tc_kernel<true, false, false> : mla_main_tc_kernel<false, false, false>;
 }
+int main_threads(bool fp8, bool expanded) { return fp8 && !expanded ? kThreadsFp8 : kThreads; }
 
 // Every other variant runs schedules of as many units, so it must fit them.
-cudaError_t prepare_variant(int dev, int units, bool fp8, bool tree) {
-    const int v = (fp8 ? 1 : 0) + (tree ? 2 : 0);
+cudaError_t prepare_variant(int dev, int units, bool fp8, bool tree, bool expanded) {
+    const int v = (fp8 ? 1 : 0) + (tree ? 2 : 0) + (expanded ? 2 : 0);
     if (v == 0) return cudaSuccess;
     std::lock_guard<std::mutex> lock(g_dev_mutex);
     DeviceInfo &d = g_dev[dev];
     if (d.variant[v] == 0) {
-        const MainKernel kernel = main_kernel(fp8, tree);
+        const MainKernel kernel = main_kernel(fp8, tree, expanded);
         const int smem = (int)(fp8 ? kSmemBytesFp8 : kSmemBytes);
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(kClusterSize * units);
-        cfg.blockDim = dim3(fp8 ? kThreadsFp8 : kThreads);
+        cfg.blockDim = dim3(main_threads(fp8, expanded));
         cfg.dynamicSmemBytes = smem;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
@@ -1361,15 +1374,16 @@ cudaError_t launch_main(const void *q_latent, const void *q_rope, const void *kv
                         int64_t num_pages, const int32_t *block_table, float scale, void *ws,
                         void *o_latent, float *lse, int32_t batch, int32_t s_q, int32_t max_pages,
                         int32_t num_units, uint64_t wait_limit_ns, uint32_t test_flags, uint32_t flags,
-                        bool fp8, bool tree, cudaStream_t stream) {
+                        bool fp8, bool tree, const void *expanded, cudaStream_t stream) {
     if (fp8 || tree) {
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
         if (e != cudaSuccess) return e;
-        e = prepare_variant(dev, num_units, fp8, tree);
+        e = prepare_variant(dev, num_units, fp8, tree, expanded != nullptr);
         if (e != cudaSuccess) return e;
     }
     Params p;
+    int64_t num_kv_pages = num_pages;
     const cuuint64_t qrows = (cuuint64_t)(tree ? 1 : batch) * s_q * kHeads;   // tree: s_q tokens in all
     {
         cuuint64_t dims[2] = {(cuuint64_t)kDl, qrows};
@@ -1385,7 +1399,18 @@ cudaError_t launch_main(const void *q_latent, const void *q_rope, const void *kv
         if (!encode(&p.tm_q_rope, q_rope, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
     }
-    if (fp8) {
+    if (expanded) {
+        // bf16 rows in table order (the views of a bf16 cache), then the rows' scales
+        kv = expanded;
+        num_kv_pages = (int64_t)batch * max_pages;
+        cuuint64_t sdims[2] = {(cuuint64_t)kPage, (cuuint64_t)num_kv_pages};
+        cuuint64_t sstrides[1] = {kPage * sizeof(float)};
+        cuuint32_t sbox[2] = {(cuuint32_t)kHalfTok, 1};
+        if (!encode(&p.tm_ks, static_cast<const uint8_t *>(expanded) + expanded_scales(batch, max_pages), 2, sdims,
+                    sstrides, sbox, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_DATA_TYPE_FLOAT32))
+            return cudaErrorInvalidValue;
+    }
+    if (fp8 && !expanded) {
         // 656-byte rows: the codes as (128 codes, token, 128-code block, page), the
         // block stride (128 bytes) below the row stride; k_rope / s (bf16) at byte 512
         // and the scale (fp32) at byte 640 of each row
@@ -1411,7 +1436,7 @@ cudaError_t launch_main(const void *q_latent, const void *q_rope, const void *kv
     } else {
         // (dim within block, token, dim block, page); the block stride (128 bytes) is
         // below the token stride, so a box lands block-major in shared memory
-        cuuint64_t dims[4] = {64, (cuuint64_t)kPage, (cuuint64_t)(kDrow / 64), (cuuint64_t)num_pages};
+        cuuint64_t dims[4] = {64, (cuuint64_t)kPage, (cuuint64_t)(kDrow / 64), (cuuint64_t)num_kv_pages};
         cuuint64_t strides[3] = {(cuuint64_t)kDrow * 2, 128, (cuuint64_t)kDrow * 2 * kPage};
         cuuint32_t box_k[4] = {64, (cuuint32_t)kHalfTok, (cuuint32_t)(kDrow / 64), 1};
         cuuint32_t box_v[4] = {64, (cuuint32_t)kPage, 4, 1};
@@ -1436,7 +1461,7 @@ cudaError_t launch_main(const void *q_latent, const void *q_rope, const void *kv
 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kClusterSize * num_units);
-    cfg.blockDim = dim3(fp8 ? kThreadsFp8 : kThreads);
+    cfg.blockDim = dim3(main_threads(fp8, expanded != nullptr));
     cfg.dynamicSmemBytes = fp8 ? kSmemBytesFp8 : kSmemBytes;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -1448,7 +1473,7 @@ cudaError_t launch_main(const void *q_latent, const void *q_rope, const void *kv
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, main_kernel(fp8, tree), p);
+    return cudaLaunchKernelEx(&cfg, main_kernel(fp8, tree, expanded != nullptr), p);
 }
 
 }  // namespace mla

@@ -113,7 +113,7 @@ mla_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__restrict_
     __shared__ int64_t carry, carry_parts, max_load;
     __shared__ int32_t bad, special;
     extern __shared__ int64_t plan_smem[];
-    const PlanLayout L = make_layout(kTree ? s_q : batch * s_q, num_units, kTree);
+    const PlanLayout L = make_layout(kTree ? s_q : batch * s_q, num_units, kTree ? batch : 0);
     const int32_t R = L.num_rows;
     TreeRow *tree_rows = reinterpret_cast<TreeRow *>(ws + L.tree_rows);
     // row at position k of the cost line
@@ -153,7 +153,10 @@ mla_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__restrict_
         for (int32_t r = threadIdx.x; r < R; r += kPlanThreads) s_pages[r] = wrong ? kNoneBad : kNoneUnused;
         __syncthreads();
         // one warp per request: lane i has its nodes i and i + 32
+        int32_t *tree_pages = reinterpret_cast<int32_t *>(ws + L.tree_pages);
+        for (int32_t b = threadIdx.x; b < batch && wrong; b += kPlanThreads) tree_pages[b] = 0;
         for (int32_t b = threadIdx.x / 32; b < batch && !wrong; b += kPlanThreads / 32) {
+            int32_t most = 0;
             const int32_t o0 = offsets[b], nodes = offsets[b + 1] - o0;
             const int32_t len = seq_lens[b];
             for (int32_t i = threadIdx.x & 31; i < nodes; i += 32) {
@@ -161,9 +164,12 @@ mla_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__restrict_
                 const int32_t p = tree_row(len, nodes, b, masks[o0 + i], max_pages, &row);
                 tree_rows[o0 + i] = row;
                 s_pages[o0 + i] = p;
+                most = max(most, p);
                 if (p == kNoneBad) bad = MLA_DEV_BAD_SEQ_LEN;
                 if (p < 0) special = 1;
             }
+            most = __reduce_max_sync(0xffffffffu, most);
+            if ((threadIdx.x & 31) == 0) tree_pages[b] = most;
         }
         if (wrong && threadIdx.x == 0) {
             bad = MLA_DEV_BAD_OFFSETS;
@@ -397,13 +403,14 @@ mla_status plan_host(const mla_problem *prob, const int32_t *seq_lens, int32_t n
 mla_status tree_plan_host(const mla_ragged *prob, const int32_t *seq_lens, const int32_t *offsets,
                           const uint64_t *masks, int32_t num_units, uint8_t *ws) {
     const int32_t batch = prob->batch, T = prob->tokens;
-    const PlanLayout L = make_layout(T, num_units, true);
+    const PlanLayout L = make_layout(T, num_units, batch);
     TreeRow *rows = reinterpret_cast<TreeRow *>(ws + L.tree_rows);
     PlanHeader h = {};
     h.magic = kTreeMagic;
     h.batch = batch;
     h.s_q = T;
     h.max_pages = prob->max_pages_per_seq;
+    int32_t *tree_pages = reinterpret_cast<int32_t *>(ws + L.tree_pages);
     // each row's pages, kept in row_nparts until the row is planned
     int32_t *pages = reinterpret_cast<int32_t *>(ws + L.row_nparts);
     bool wrong = false;
@@ -412,12 +419,15 @@ mla_status tree_plan_host(const mla_ragged *prob, const int32_t *seq_lens, const
         h.status = MLA_DEV_BAD_OFFSETS;
         h.split = 2;
     }
+    for (int32_t b = 0; b < batch && wrong; ++b) tree_pages[b] = 0;
     for (int32_t r = 0; r < T; ++r) pages[r] = wrong ? kNoneBad : kNoneUnused;
     for (int32_t b = 0; b < batch && !wrong; ++b) {
         const int32_t nodes = offsets[b + 1] - offsets[b];
+        tree_pages[b] = 0;
         for (int32_t i = 0; i < nodes; ++i) {
             const int32_t r = offsets[b] + i;
             pages[r] = tree_row(seq_lens[b], nodes, b, masks[r], h.max_pages, &rows[r]);
+            if (pages[r] > tree_pages[b]) tree_pages[b] = pages[r];
             if (pages[r] == kNoneBad) h.status = MLA_DEV_BAD_SEQ_LEN;
             if (pages[r] < 0) h.split = 2;
         }

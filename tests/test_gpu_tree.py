@@ -99,6 +99,26 @@ def test_tree_decode_parity(counts, lens, kind, fp8):
     assert (f64(out)[:n][empty] == 0).all()
 
 
+def test_tree_fp8_scratch_changes_no_bit():
+    c = TU.case([7, 0, 64, 16, 3], [40, 9, 700, 129, 3], ["tree", "tree", "bits", "self", "chain"], seed=13, pad=2)
+    ql, qr, cache = TU.tensors(c, seed=14)
+    cache = fp8_of(cache)
+    out, lse, status, p = run_tree(c, ql, qr, cache, True, scratch=False)
+    n = len(c["counts"]) * c["block_table"].shape[1] * mla.EXPANDED_PAGE_BYTES
+    room = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")       # NaN in whatever is not expanded
+    for s in (room, None):
+        o2, l2, st2, _ = run_tree(c, ql, qr, cache, True, scratch=s)
+        assert status == st2 == 0
+        assert torch.equal(out, o2) and torch.equal(lse, l2)
+    c["block_table"][3, 1] = c["pages"]                                  # a bad page: the same rows, the same flag
+    a = run_tree(c, ql, qr, cache, True, scratch=False)
+    b = run_tree(c, ql, qr, cache, True, scratch=room)
+    assert a[2] == b[2] == mla.MLA_DEV_BAD_PAGE
+    assert torch.equal(torch.nan_to_num(a[0], nan=9.0), torch.nan_to_num(b[0], nan=9.0))
+    with pytest.raises(mla.MLAError, match="workspace"):
+        run_tree(c, ql, qr, cache, True, scratch=room[:-16])
+
+
 def test_tree_decode_pow2():
     c = TU.case([9, 12], [300, 2000], "tree", seed=21)
     ql, qr, cache = TU.tensors(c, seed=22)
@@ -167,7 +187,7 @@ def test_tree_plan_matches_the_host():
                                   num_units=mla.num_units())
         assert got["header"] == want["header"]
         n = int(c["offsets"][-1])
-        for k in ("items", "item_unit", "unit_begin", "row_nparts", "row_part0", "row_item0", "row_pos"):
+        for k in ("items", "item_unit", "unit_begin", "row_nparts", "row_part0", "row_item0", "row_pos", "tree_pages"):
             assert np.array_equal(got[k], want[k]), k
         assert np.array_equal(got["tree_rows"][:n], want["tree_rows"][:n])
 

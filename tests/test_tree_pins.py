@@ -111,6 +111,7 @@ def _check_plan(c, units, max_pages=None):
             assert len(mine) == 0 and p["row_nparts"][t] == -1
             continue
         assert p["row_nparts"][t] == len(mine)
+        assert p["tree_pages"][b] >= (seen[-1] + 64) // 64
         at = 0
         for i, (_, k0, k1, part) in enumerate(mine):
             assert k0 == at and k1 > k0 and (k0 % 64 == 0)
@@ -185,8 +186,9 @@ def test_entry_points_refuse_before_any_cuda_call():
         return lib.mla_tree_plan(_ref(prob), sl, off, m, ws, n, None)
 
     def decode(prob=_ragged(), ql=A, qr=A, kv=A, pages=8, bt=A, scale=0.07, o=A, lse=A, ws=A, n=1 << 30,
-               name="mla_tree_decode"):
-        return getattr(lib, name)(_ref(prob), ql, qr, kv, pages, bt, scale, o, lse, ws, n, None)
+               scratch=None, room=0, name="mla_tree_decode"):
+        more = (scratch, room) if name == "mla_tree_decode_fp8" else ()
+        return getattr(lib, name)(_ref(prob), ql, qr, kv, pages, bt, scale, o, lse, ws, n, *more, None)
 
     def commit(prob=_ragged(), kv=A, layers=2, stride=8 * 64 * 1152, row=1152, pages=8, bt=A, sl=A, off=A, paths=A,
                mp=4, pl=A, new=A + 64, st=A):
@@ -232,7 +234,11 @@ def test_entry_points_refuse_before_any_cuda_call():
     assert commit(layers=0) == 1 and commit(row=1024) == 1 and commit(pages=0) == 1
     assert commit(mp=0) == 1 and commit(mp=65) == 1
     assert commit(stride=8 * 64 * 1152 + 8) == 1 and commit(stride=8 * 64 * 1152 - 16) == 1
+    assert decode(scratch=A + 8, room=1 << 30, name="mla_tree_decode_fp8") == 1
+    assert decode(scratch=A, room=2 * 4 * mla.EXPANDED_PAGE_BYTES - 1, name="mla_tree_decode_fp8") == 3
     n = ctypes.c_size_t(0)
+    assert lib.mla_tree_scratch_size(_ref(_ragged()), ctypes.byref(n)) == 0 and n.value == 8 * mla.EXPANDED_PAGE_BYTES
+    assert lib.mla_tree_scratch_size(_ref(_ragged()), None) == 1 and lib.mla_tree_scratch_size(None, ctypes.byref(n)) == 1
     assert lib.mla_tree_workspace_size(None, ctypes.byref(n)) == 1
     assert lib.mla_tree_workspace_size(_ref(_ragged()), None) == 1
 

@@ -459,22 +459,14 @@ extern "C" mla_status mla_prolog(const mla_problem *prob, const void *q_nope, co
     return launch_prolog(p, true, (unsigned)ctas, stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
-extern "C" mla_status mla_query(int32_t tokens, const void *q_nope, int64_t nope_token_stride,
-                                int64_t nope_head_stride, const void *q_pe, int64_t pe_token_stride,
-                                int64_t pe_head_stride, const void *w_uk, const float *rope_table,
-                                const int32_t *positions, void *q_latent, void *q_rope, int32_t *device_status,
-                                mla_stream_t stream) {
-    mla::NvtxRange nvtx_range("mla_query");
-    using namespace mla;
-    if (tokens < 1) return MLA_ERR_INVALID_ARG;
+namespace mla {
+
+// mla_query for few tokens (its arguments are checked): one CTA per (head, token tile, column quarter).
+mla_status launch_query_small(int32_t tokens, const void *q_nope, int64_t nope_token_stride, int64_t nope_head_stride,
+                              const void *q_pe, int64_t pe_token_stride, int64_t pe_head_stride, const void *w_uk,
+                              const float *rope_table, const int32_t *positions, void *q_latent, void *q_rope,
+                              int32_t *device_status, mla_stream_t stream) {
     const int64_t ctas = ((int64_t)tokens + kBM - 1) / kBM * kHeads * kNParts;
-    if ((int64_t)tokens * kHeads >= (int64_t)1 << 31 || ctas >= (int64_t)1 << 31) return MLA_ERR_UNSUPPORTED;
-    if (!aligned16(q_nope) || !aligned16(q_pe) || !aligned16(w_uk) || !aligned16(q_latent) || !aligned16(q_rope) ||
-        !rope_table || !positions || !device_status || (reinterpret_cast<uintptr_t>(rope_table) & 3u) ||
-        (reinterpret_cast<uintptr_t>(positions) & 3u) || (reinterpret_cast<uintptr_t>(device_status) & 3u))
-        return MLA_ERR_INVALID_ARG;
-    for (const int64_t s : {nope_token_stride, nope_head_stride, pe_token_stride, pe_head_stride})
-        if (s < 1 || s % 8 || s >= (int64_t)1 << 31) return MLA_ERR_INVALID_ARG;
     if (prepare_prolog() != cudaSuccess) return MLA_ERR_CUDA;
     PrologParams p{};
     p.a_rows = tokens >= kBM ? kBM : (tokens + 7) / 8 * 8;
@@ -493,3 +485,5 @@ extern "C" mla_status mla_query(int32_t tokens, const void *q_nope, int64_t nope
     p.tokens = tokens;
     return launch_prolog(p, false, (unsigned)ctas, stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
+
+}  // namespace mla

@@ -124,7 +124,7 @@ mla_status mla_tree_workspace_size(const mla_ragged *prob, size_t *bytes);
  * copied into the workspace; bits at or past the tree's size are ignored.  The
  * schedule stays valid for every later mla_tree_decode with the same problem,
  * lengths, offsets and masks (every layer of a step).  Also clears the status
- * word.  Up to about 12,000 tokens (MLA_ERR_UNSUPPORTED beyond: the planner's
+ * word.  Up to 10,000 tokens (MLA_ERR_UNSUPPORTED beyond: the planner's
  * working set is held on one SM).
  * Rows of a request whose seq_len is below its node count or beyond
  * max_pages_per_seq pages: MLA_DEV_BAD_SEQ_LEN, and NaN outputs.  Bad offsets:

@@ -28,6 +28,7 @@ cudaError_t launch_main(const void *q_latent, const void *q_rope, const void *kv
 cudaError_t launch_expand(const void *ws, const void *kv_cache_fp8, int64_t num_pages, const int32_t *block_table,
                           void *expanded, int32_t batch, int32_t tokens, int32_t max_pages, int32_t num_units,
                           cudaStream_t stream);
+bool tree_plan_fits(int32_t rows, int32_t units);
 mla_status tree_plan_host(const mla_ragged *prob, const int32_t *seq_lens, const int32_t *offsets,
                           const uint64_t *masks, int32_t num_units, uint8_t *ws);
 cudaError_t launch_tree_plan(const int32_t *seq_lens, const int32_t *offsets, const uint64_t *masks, void *ws,
@@ -247,7 +248,7 @@ mla_status mla_tree_workspace_size(const mla_ragged *prob, size_t *bytes) {
     if (!bytes) return MLA_ERR_INVALID_ARG;
     int32_t units = 0;
     if (mla::main_units(&units) != cudaSuccess) return MLA_ERR_CUDA;
-    if (!mla::plan_fits(prob->tokens, units)) return MLA_ERR_UNSUPPORTED;
+    if (!mla::tree_plan_fits(prob->tokens, units)) return MLA_ERR_UNSUPPORTED;
     *bytes = mla::make_layout(prob->tokens, units, prob->batch).total;
     return MLA_OK;
 }
@@ -263,8 +264,12 @@ mla_status mla_tree_plan_host(const mla_ragged *prob, const int32_t *seq_lens_ho
     if (st != MLA_OK) return st;
     if (!seq_lens_host || !token_offsets_host || !masks_host || !plan_host || num_units < 1) return MLA_ERR_INVALID_ARG;
     if (plan_bytes < mla::make_layout(prob->tokens, num_units, prob->batch).plan_end) return MLA_ERR_WORKSPACE;
-    return mla::tree_plan_host(prob, seq_lens_host, token_offsets_host, masks_host, num_units,
-                               static_cast<uint8_t *>(plan_host));
+    try {
+        return mla::tree_plan_host(prob, seq_lens_host, token_offsets_host, masks_host, num_units,
+                                   static_cast<uint8_t *>(plan_host));
+    } catch (...) {   // out of host memory: nothing is thrown across the C boundary
+        return MLA_ERR_WORKSPACE;
+    }
 }
 
 mla_status mla_tree_plan(const mla_ragged *prob, const int32_t *seq_lens, const int32_t *token_offsets,
@@ -279,7 +284,7 @@ mla_status mla_tree_plan(const mla_ragged *prob, const int32_t *seq_lens, const 
     if (workspace_bytes < mla::make_layout(prob->tokens, 1, prob->batch).total) return MLA_ERR_WORKSPACE;
     int32_t units = 0;
     if (mla::main_units(&units) != cudaSuccess) return MLA_ERR_CUDA;
-    if (!mla::plan_fits(prob->tokens, units)) return MLA_ERR_UNSUPPORTED;
+    if (!mla::tree_plan_fits(prob->tokens, units)) return MLA_ERR_UNSUPPORTED;
     if (workspace_bytes < mla::make_layout(prob->tokens, units, prob->batch).total) return MLA_ERR_WORKSPACE;
     const cudaError_t e = mla::launch_tree_plan(seq_lens, token_offsets, masks, workspace, prob->batch, prob->tokens,
                                                 prob->max_pages_per_seq, units, reinterpret_cast<cudaStream_t>(stream));
@@ -303,7 +308,7 @@ static mla_status tree_impl(const mla_ragged *prob, const void *q_latent, const 
     if (workspace_bytes < mla::make_layout(prob->tokens, 1, prob->batch).total) return MLA_ERR_WORKSPACE;
     int32_t units = 0;
     if (mla::main_units(&units) != cudaSuccess) return MLA_ERR_CUDA;
-    if (!mla::plan_fits(prob->tokens, units)) return MLA_ERR_UNSUPPORTED;
+    if (!mla::tree_plan_fits(prob->tokens, units)) return MLA_ERR_UNSUPPORTED;
     if (workspace_bytes < mla::make_layout(prob->tokens, units, prob->batch).total) return MLA_ERR_WORKSPACE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;

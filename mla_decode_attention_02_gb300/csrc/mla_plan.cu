@@ -20,11 +20,6 @@
 // every item follows from prefix sums alone: no atomics, no sorting, and
 // the same bytes on every run.  The host twin below runs the identical
 // integer arithmetic sequentially.
-//
-// Trees of drafted tokens (kTree) bring one row per node, in token order, with
-// their keys from the offsets and masks of include/mla_tree.h: a row's work ends
-// at its last visible key.  The schedule then holds each row's context length,
-// mask and request, so that the main kernel needs none of the arrays.
 #include <cuda_runtime.h>
 
 #include <cstring>
@@ -50,27 +45,6 @@ MLA_HD int32_t line_row(int32_t k, int32_t batch, int32_t s_q) {
     return (k % batch) * s_q + k / batch;
 }
 
-// Pages of a tree's rows that have no work items (their row_nparts follow).
-constexpr int32_t kNoneUnused = 0, kNoneBad = -1, kNoneEmpty = -2;
-MLA_HD int32_t none_parts(int32_t pages) {
-    return pages == kNoneBad ? 0 : pages == kNoneEmpty ? kRowEmpty : kRowUnused;
-}
-
-// A node's row and its pages: pages to read, or one of the kNone codes.
-MLA_HD int32_t tree_row(int32_t seq_len, int32_t nodes, int32_t req, uint64_t mask, int32_t max_pages, TreeRow *row) {
-    const bool ok = seq_len >= nodes && seq_len <= (int64_t)max_pages * kPage;
-    row->mask = ok ? (nodes < 64 ? mask & ((1ull << nodes) - 1) : mask) : 0;
-    row->context = ok ? seq_len - nodes : 0;
-    row->req = req;
-    if (!ok) return kNoneBad;
-    const int32_t end = tree_end(row->context, row->mask);
-    return end > 0 ? (end + kPage - 1) / kPage : kNoneEmpty;
-}
-
-// Whether request b's stretch of the token array is sound.
-MLA_HD bool tree_offsets_ok(int32_t o0, int32_t o1, int32_t b, int32_t tokens) {
-    return o0 >= 0 && o0 <= o1 && o1 <= tokens && (b > 0 || o0 == 0) && (int64_t)o1 - o0 <= MLA_TREE_MAX_NODES;
-}
 
 // Inclusive block-wide sum of one int64 per thread (kPlanThreads threads, at
 // most 32 warps).
@@ -103,21 +77,15 @@ size_t plan_smem_bytes(int32_t R, int32_t U) {
     return sizeof(int64_t) * ((size_t)R + U) + sizeof(int32_t) * (2 * (size_t)R + U);
 }
 
-// kTree: s_q is the number of tokens (rows), offsets and masks are read.
-template <bool kTree>
 __global__ void __launch_bounds__(kPlanThreads, 1)
-mla_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__restrict__ offsets,
-                const uint64_t *__restrict__ masks, uint8_t *__restrict__ ws, int32_t batch,
+mla_plan_kernel(const int32_t *__restrict__ seq_lens, uint8_t *__restrict__ ws, int32_t batch,
                 int32_t s_q, int32_t max_pages, int32_t num_units) {
     __shared__ int64_t warp_sums[32];
     __shared__ int64_t carry, carry_parts, max_load;
-    __shared__ int32_t bad, special;
+    __shared__ int32_t bad;
     extern __shared__ int64_t plan_smem[];
-    const PlanLayout L = make_layout(kTree ? s_q : batch * s_q, num_units, kTree ? batch : 0);
+    const PlanLayout L = plan_layout(batch, s_q, num_units);
     const int32_t R = L.num_rows;
-    TreeRow *tree_rows = reinterpret_cast<TreeRow *>(ws + L.tree_rows);
-    // row at position k of the cost line
-    auto line = [&](int32_t k) { return kTree ? k : line_row(k, batch, s_q); };
     int64_t *s_pos = plan_smem;                                        // [R] cost-line start
     int64_t *first_pos = s_pos + R;                                    // [U] (no-split runs)
     int32_t *s_pages = reinterpret_cast<int32_t *>(first_pos + num_units);  // [R]
@@ -131,7 +99,6 @@ mla_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__restrict_
     int32_t *row_item0 = reinterpret_cast<int32_t *>(ws + L.row_item0);
     int64_t *row_pos = reinterpret_cast<int64_t *>(ws + L.row_pos);
 
-    if (kTree) ptx::pdl_wait_prior();
     // The main kernel may start its prologue now; it waits for this grid before
     // reading the schedule.
     ptx::pdl_launch_dependents();
@@ -141,53 +108,17 @@ mla_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__restrict_
         carry_parts = 0;
         max_load = 0;
         bad = 0;
-        special = 0;
     }
     __syncthreads();
-    if constexpr (kTree) {
-        // every request's rows; with bad offsets no row belongs to any (all NaN)
-        bool wrong = false;
-        for (int32_t b = threadIdx.x; b < batch; b += kPlanThreads)
-            wrong |= !tree_offsets_ok(offsets[b], offsets[b + 1], b, s_q);
-        wrong = __syncthreads_or(wrong) != 0;
-        for (int32_t r = threadIdx.x; r < R; r += kPlanThreads) s_pages[r] = wrong ? kNoneBad : kNoneUnused;
-        __syncthreads();
-        // one warp per request: lane i has its nodes i and i + 32
-        int32_t *tree_pages = reinterpret_cast<int32_t *>(ws + L.tree_pages);
-        for (int32_t b = threadIdx.x; b < batch && wrong; b += kPlanThreads) tree_pages[b] = 0;
-        for (int32_t b = threadIdx.x / 32; b < batch && !wrong; b += kPlanThreads / 32) {
-            int32_t most = 0;
-            const int32_t o0 = offsets[b], nodes = offsets[b + 1] - o0;
-            const int32_t len = seq_lens[b];
-            for (int32_t i = threadIdx.x & 31; i < nodes; i += 32) {
-                TreeRow row;
-                const int32_t p = tree_row(len, nodes, b, masks[o0 + i], max_pages, &row);
-                tree_rows[o0 + i] = row;
-                s_pages[o0 + i] = p;
-                most = max(most, p);
-                if (p == kNoneBad) bad = MLA_DEV_BAD_SEQ_LEN;
-                if (p < 0) special = 1;
-            }
-            most = __reduce_max_sync(0xffffffffu, most);
-            if ((threadIdx.x & 31) == 0) tree_pages[b] = most;
-        }
-        if (wrong && threadIdx.x == 0) {
-            bad = MLA_DEV_BAD_OFFSETS;
-            special = 1;
-        }
-        __syncthreads();
-    }
     for (int32_t base = 0; base < R; base += kPlanThreads) {
         const int32_t k = base + threadIdx.x;
-        const int32_t r = k < R ? line(k) : R;
+        const int32_t r = k < R ? line_row(k, batch, s_q) : R;
         int64_t c = 0;
         if (r < R) {
-            if constexpr (!kTree) {
-                const int32_t p = row_pages(seq_lens[r / s_q], s_q, r % s_q, max_pages);
-                if (p < 0) bad = MLA_DEV_BAD_SEQ_LEN;
-                s_pages[r] = p;
-            }
-            c = row_cost(s_pages[r]);
+            const int32_t p = row_pages(seq_lens[r / s_q], s_q, r % s_q, max_pages);
+            if (p < 0) bad = 1;
+            s_pages[r] = p;
+            c = row_cost(p);
         }
         const int64_t incl = block_inclusive_sum(c, warp_sums);
         if (r < R) {
@@ -204,9 +135,9 @@ mla_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__restrict_
 
     // Pass 1b: largest unit load if no row is cut (rows on their midpoint units).
     for (int32_t k = threadIdx.x; k < R; k += kPlanThreads) {
-        const int32_t r = line(k);
+        const int32_t r = line_row(k, batch, s_q);
         const int64_t u = mid_unit(s_pos[r], row_cost(s_pages[r]), target, num_units);
-        const int32_t rp = k > 0 ? line(k - 1) : 0;
+        const int32_t rp = k > 0 ? line_row(k - 1, batch, s_q) : 0;
         if (k == 0 || mid_unit(s_pos[rp], row_cost(s_pages[rp]), target, num_units) != u)
             first_pos[u] = s_pos[r];
     }
@@ -214,10 +145,10 @@ mla_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__restrict_
     {
         int64_t my_max = 0;
         for (int32_t k = threadIdx.x; k < R; k += kPlanThreads) {
-            const int32_t r = line(k);
+            const int32_t r = line_row(k, batch, s_q);
             const int64_t c = row_cost(s_pages[r]);
             const int64_t u = mid_unit(s_pos[r], c, target, num_units);
-            const int32_t rn = k < R - 1 ? line(k + 1) : 0;
+            const int32_t rn = k < R - 1 ? line_row(k + 1, batch, s_q) : 0;
             if (k == R - 1 || mid_unit(s_pos[rn], row_cost(s_pages[rn]), target, num_units) != u) {
                 const int64_t load = s_pos[r] + c - first_pos[u];
                 my_max = load > my_max ? load : my_max;
@@ -233,7 +164,7 @@ mla_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__restrict_
     // Pass 2: pieces per row -> first item and first partial slot; emit the items.
     for (int32_t base = 0; base < R; base += kPlanThreads) {
         const int32_t k = base + threadIdx.x;
-        const int32_t r = k < R ? line(k) : R;
+        const int32_t r = k < R ? line_row(k, batch, s_q) : R;
         int64_t n = 0, np = 0;
         if (r < R) {
             n = cut_row(s_pos[r], s_pages[r], target, num_units, split, NoEmit{});
@@ -246,12 +177,9 @@ mla_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__restrict_
             const int32_t part0 = n > 1 ? (int32_t)(carry_parts + incl_p - np) : -1;
             row_item0[r] = first;
             row_part0[r] = part0;
-            row_nparts[r] = kTree && n == 0 ? none_parts(s_pages[r]) : (int32_t)n;
-            int32_t vis = 0;
-            if (s_pages[r] > 0) {
-                if constexpr (kTree) vis = tree_end(tree_rows[r].context, tree_rows[r].mask);
-                else vis = seq_lens[r / s_q] - s_q + 1 + r % s_q;
-            }
+            row_nparts[r] = (int32_t)n;
+            const int32_t t = r % s_q;
+            const int32_t vis = s_pages[r] > 0 ? seq_lens[r / s_q] - s_q + 1 + t : 0;
             cut_row(s_pos[r], s_pages[r], target, num_units, split,
                     [&](int32_t i, int32_t pg0, int32_t pg1, int32_t unit) {
                         WorkItem it;
@@ -288,7 +216,7 @@ mla_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__restrict_
 
     if (threadIdx.x == 0) {
         PlanHeader h;
-        h.magic = kTree ? kTreeMagic : kPlanMagic;
+        h.magic = kPlanMagic;
         h.batch = batch;
         h.s_q = s_q;
         h.max_pages = max_pages;
@@ -297,8 +225,8 @@ mla_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__restrict_
         h.max_items = L.max_items;
         h.num_items = num_items;
         h.num_parts = num_parts;
-        h.status = bad;
-        h.split = (split ? 1 : 0) | (kTree && special ? 2 : 0);
+        h.status = bad ? MLA_DEV_BAD_SEQ_LEN : 0;
+        h.split = split ? 1 : 0;
         h.min_split = kMinSplitPages;
         h.total_cost = total;
         h.target = target;
@@ -308,13 +236,12 @@ mla_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__restrict_
 
 }  // namespace
 
-// Host twin of mla_plan_kernel (same integer arithmetic, sequential), over the
-// rows' pages and keys in cost-line order: row(k) gives the row at position k,
-// pages(r) and end(r) its pages (<= 0: none) and its last key's end, none(r) the
-// row_nparts of a row without pages.
-template <typename Row, typename Pages, typename End, typename None>
-static void plan_rows(const PlanLayout &L, int32_t num_units, uint8_t *ws, PlanHeader h, Row row, Pages pages, End end,
-                      None none) {
+// Host twin of mla_plan_kernel (same integer arithmetic, sequential).
+mla_status plan_host(const mla_problem *prob, const int32_t *seq_lens, int32_t num_units,
+                     uint8_t *ws) {
+    const int32_t batch = prob->batch, s_q = prob->s_q, max_pages = prob->max_pages_per_seq;
+    const PlanLayout L = plan_layout(batch, s_q, num_units);
+    PlanHeader *hdr = reinterpret_cast<PlanHeader *>(ws);
     WorkItem *items = reinterpret_cast<WorkItem *>(ws + L.items);
     int32_t *item_unit = reinterpret_cast<int32_t *>(ws + L.item_unit);
     int32_t *unit_begin = reinterpret_cast<int32_t *>(ws + L.unit_begin);
@@ -323,18 +250,21 @@ static void plan_rows(const PlanLayout &L, int32_t num_units, uint8_t *ws, PlanH
     int32_t *row_item0 = reinterpret_cast<int32_t *>(ws + L.row_item0);
     int64_t *row_pos = reinterpret_cast<int64_t *>(ws + L.row_pos);
     const int32_t R = L.num_rows;
+    int bad = 0;
     int64_t total = 0;
     for (int32_t k = 0; k < R; ++k) {
-        const int32_t r = row(k);
+        const int32_t r = line_row(k, batch, s_q);
+        int32_t p = row_pages(seq_lens[r / s_q], s_q, r % s_q, max_pages);
+        if (p < 0) bad = 1;
         row_pos[r] = total;
-        total += row_cost(pages(r));
+        total += row_cost(p);
     }
     const int64_t target = total > 0 ? (total + num_units - 1) / num_units : 1;
     // largest unit load if no row is cut (rows on their midpoint units)
     int64_t max_load = 0, run_first = 0, run_unit = -1;
     for (int32_t k = 0; k < R; ++k) {
-        const int32_t r = row(k);
-        const int64_t c = row_cost(pages(r));
+        const int32_t r = line_row(k, batch, s_q);
+        const int64_t c = row_cost(row_pages(seq_lens[r / s_q], s_q, r % s_q, max_pages));
         const int64_t u = mid_unit(row_pos[r], c, target, num_units);
         if (u != run_unit) {
             run_unit = u;
@@ -346,11 +276,12 @@ static void plan_rows(const PlanLayout &L, int32_t num_units, uint8_t *ws, PlanH
     const bool split = target + kItemCost + kSplitPenalty < max_load;
     int32_t n_items = 0, n_parts = 0, last_unit = -1;
     for (int32_t k = 0; k < R; ++k) {
-        const int32_t r = row(k);
-        const int32_t p = pages(r);
+        const int32_t r = line_row(k, batch, s_q);
+        const int32_t b = r / s_q, t = r % s_q;
+        const int32_t p = row_pages(seq_lens[b], s_q, t, max_pages);
         const int32_t n = cut_row(row_pos[r], p, target, num_units, split, NoEmit{});
         const int32_t part0 = n > 1 ? n_parts : -1;
-        const int32_t vis = p > 0 ? end(r) : 0;
+        const int32_t vis = p > 0 ? seq_lens[b] - s_q + 1 + t : 0;
         cut_row(row_pos[r], p, target, num_units, split,
                 [&](int32_t i, int32_t pg0, int32_t pg1, int32_t unit) {
                     WorkItem it;
@@ -363,79 +294,29 @@ static void plan_rows(const PlanLayout &L, int32_t num_units, uint8_t *ws, PlanH
                     for (int32_t v = last_unit + 1; v <= unit; ++v) unit_begin[v] = n_items + i;
                     if (unit > last_unit) last_unit = unit;
                 });
-        row_nparts[r] = n > 0 ? n : none(r);
+        row_nparts[r] = n;
         row_part0[r] = part0;
         row_item0[r] = n_items;
         n_items += n;
         if (n > 1) n_parts += n;
     }
     for (int32_t v = last_unit + 1; v <= num_units; ++v) unit_begin[v] = n_items;
+    PlanHeader h;
+    h.magic = kPlanMagic;
+    h.batch = batch;
+    h.s_q = s_q;
+    h.max_pages = max_pages;
     h.num_units = num_units;
     h.num_rows = R;
     h.max_items = L.max_items;
     h.num_items = n_items;
     h.num_parts = n_parts;
-    h.split |= split ? 1 : 0;
+    h.status = bad ? MLA_DEV_BAD_SEQ_LEN : 0;
+    h.split = split ? 1 : 0;
     h.min_split = kMinSplitPages;
     h.total_cost = total;
     h.target = target;
-    *reinterpret_cast<PlanHeader *>(ws) = h;
-}
-
-mla_status plan_host(const mla_problem *prob, const int32_t *seq_lens, int32_t num_units,
-                     uint8_t *ws) {
-    const int32_t batch = prob->batch, s_q = prob->s_q, max_pages = prob->max_pages_per_seq;
-    auto pages = [&](int32_t r) { return row_pages(seq_lens[r / s_q], s_q, r % s_q, max_pages); };
-    PlanHeader h = {};
-    h.magic = kPlanMagic;
-    h.batch = batch;
-    h.s_q = s_q;
-    h.max_pages = max_pages;
-    for (int32_t r = 0; r < batch * s_q; ++r)
-        if (pages(r) < 0) h.status = MLA_DEV_BAD_SEQ_LEN;
-    plan_rows(
-        plan_layout(batch, s_q, num_units), num_units, ws, h,
-        [&](int32_t k) { return line_row(k, batch, s_q); }, pages,
-        [&](int32_t r) { return seq_lens[r / s_q] - s_q + 1 + r % s_q; }, [](int32_t) { return 0; });
-    return MLA_OK;
-}
-
-mla_status tree_plan_host(const mla_ragged *prob, const int32_t *seq_lens, const int32_t *offsets,
-                          const uint64_t *masks, int32_t num_units, uint8_t *ws) {
-    const int32_t batch = prob->batch, T = prob->tokens;
-    const PlanLayout L = make_layout(T, num_units, batch);
-    TreeRow *rows = reinterpret_cast<TreeRow *>(ws + L.tree_rows);
-    PlanHeader h = {};
-    h.magic = kTreeMagic;
-    h.batch = batch;
-    h.s_q = T;
-    h.max_pages = prob->max_pages_per_seq;
-    int32_t *tree_pages = reinterpret_cast<int32_t *>(ws + L.tree_pages);
-    // each row's pages, kept in row_nparts until the row is planned
-    int32_t *pages = reinterpret_cast<int32_t *>(ws + L.row_nparts);
-    bool wrong = false;
-    for (int32_t b = 0; b < batch; ++b) wrong |= !tree_offsets_ok(offsets[b], offsets[b + 1], b, T);
-    if (wrong) {
-        h.status = MLA_DEV_BAD_OFFSETS;
-        h.split = 2;
-    }
-    for (int32_t b = 0; b < batch && wrong; ++b) tree_pages[b] = 0;
-    for (int32_t r = 0; r < T; ++r) pages[r] = wrong ? kNoneBad : kNoneUnused;
-    for (int32_t b = 0; b < batch && !wrong; ++b) {
-        const int32_t nodes = offsets[b + 1] - offsets[b];
-        tree_pages[b] = 0;
-        for (int32_t i = 0; i < nodes; ++i) {
-            const int32_t r = offsets[b] + i;
-            pages[r] = tree_row(seq_lens[b], nodes, b, masks[r], h.max_pages, &rows[r]);
-            if (pages[r] > tree_pages[b]) tree_pages[b] = pages[r];
-            if (pages[r] == kNoneBad) h.status = MLA_DEV_BAD_SEQ_LEN;
-            if (pages[r] < 0) h.split = 2;
-        }
-    }
-    plan_rows(
-        L, num_units, ws, h, [](int32_t k) { return k; }, [&](int32_t r) { return pages[r]; },
-        [&](int32_t r) { return tree_end(rows[r].context, rows[r].mask); },
-        [&](int32_t r) { return none_parts(pages[r]); });
+    *hdr = h;
     return MLA_OK;
 }
 
@@ -446,48 +327,13 @@ cudaError_t launch_plan(const int32_t *seq_lens, void *ws, int32_t batch, int32_
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(mla_plan_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        attr_err = cudaFuncSetAttribute(mla_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         (int)kMaxPlanSmem);
     });
     if (attr_err != cudaSuccess) return attr_err;
-    mla_plan_kernel<false><<<1, kPlanThreads, smem, stream>>>(seq_lens, nullptr, nullptr, static_cast<uint8_t *>(ws),
-                                                              batch, s_q, max_pages, num_units);
+    mla_plan_kernel<<<1, kPlanThreads, smem, stream>>>(seq_lens, static_cast<uint8_t *>(ws), batch,
+                                                       s_q, max_pages, num_units);
     return cudaGetLastError();
-}
-
-cudaError_t launch_tree_plan(const int32_t *seq_lens, const int32_t *offsets, const uint64_t *masks, void *ws,
-                             int32_t batch, int32_t tokens, int32_t max_pages, int32_t num_units,
-                             cudaStream_t stream) {
-    const size_t smem = plan_smem_bytes(tokens, num_units);
-    if (smem > kMaxPlanSmem) return cudaErrorInvalidValue;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    // the attribute belongs to the device: set once on each
-    static std::mutex mutex;
-    static bool set[64];
-    {
-        std::lock_guard<std::mutex> lock(mutex);
-        if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-        if (!set[dev]) {
-            e = cudaFuncSetAttribute(mla_plan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)kMaxPlanSmem);
-            if (e != cudaSuccess) return e;
-            set[dev] = true;
-        }
-    }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(1);
-    cfg.blockDim = dim3(kPlanThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mla_plan_kernel<true>, seq_lens, offsets, masks, static_cast<uint8_t *>(ws), batch,
-                              tokens, max_pages, num_units);
 }
 
 bool plan_fits(int32_t rows, int32_t units) { return plan_smem_bytes(rows, units) <= kMaxPlanSmem; }

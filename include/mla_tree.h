@@ -96,7 +96,7 @@ mla_status mla_query(int32_t tokens, const void *q_nope, int64_t nope_token_stri
  *             depth past the context, whatever its slot); a negative one marks a token to leave out
  *   kv_cache  [num_pages][64][576] bf16, or for mla_cache_append_fp8 [num_pages][64][656] bytes
  *             (mla_fp8.h); only the tokens' rows are written.  Distinct tokens must have distinct rows.
- * The fp8 row is quantised from the fp32 values (one rounding), s = max |c_kv| / 448 of them.
+ * The fp8 row is quantised from the unrounded values, s = max |c_kv| / 448 of them (1 for a zero row).
  * A token whose slot is out of range (MLA_DEV_BAD_SEQ_LEN) or whose page is (MLA_DEV_BAD_PAGE) is
  * not written.  With bad offsets (MLA_DEV_BAD_OFFSETS) which tokens are written is unspecified, but
  * nothing outside the pool is.  MLA_TREE_MAX_NODES does not bound n_b here.

@@ -60,11 +60,13 @@ __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
     }
 }
 
-__device__ __forceinline__ uint2 codes8(const float (&f)[8], float s) {
+// Codes of 448 f / amax.
+__device__ __forceinline__ uint2 codes8(const float (&f)[8], float amax) {
     uint32_t c[2] = {0, 0};
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        c[j / 4] |= (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(f[j], s), __NV_SATFINITE, __NV_E4M3) << (8 * (j % 4));
+        c[j / 4] |= (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(f[j] * 448.f, amax), __NV_SATFINITE, __NV_E4M3)
+                    << (8 * (j % 4));
     return make_uint2(c[0], c[1]);
 }
 
@@ -131,9 +133,9 @@ __global__ void __launch_bounds__(32 * kAppendWarps) mla_cache_append_kernel(con
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         const float inv = rsqrtf(ss * (1.0f / kDl) + P.eps);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            a[j] *= inv * ga[j];
-            c[j] *= inv * gb[j];
+        for (int j = 0; j < 8; ++j) {   // x * gamma: exact, a product of two bf16 values has 16 bits
+            a[j] *= ga[j];
+            c[j] *= gb[j];
         }
         float sn, cs;
         rope_sincos(P.positions ? given : (int32_t)slot, g_hi, g_lo, sn, cs);
@@ -146,13 +148,23 @@ __global__ void __launch_bounds__(32 * kAppendWarps) mla_cache_append_kernel(con
             for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fmaxf(fabsf(a[j]), fabsf(c[j])));
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            const float s = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+            // The norm's factor cancels in c / s = 448 (x gamma) / max |x gamma|: both sides of the
+            // division are exact, so each code is the correctly rounded quotient's.  (s is 0 only if
+            // the norm overflowed: a zero row, as in bf16.)
+            float s = __fdiv_rn(amax * inv, 448.f);
+            const bool zero = !(s > 0.f);
+            if (zero) s = 1.f;
             uint8_t *dst = P.cache + row * MLA_FP8_ROW_BYTES;
-            reinterpret_cast<uint2 *>(dst)[lane] = codes8(a, s);
-            reinterpret_cast<uint2 *>(dst)[lane + 32] = codes8(c, s);
+            reinterpret_cast<uint2 *>(dst)[lane] = zero ? make_uint2(0, 0) : codes8(a, amax);
+            reinterpret_cast<uint2 *>(dst)[lane + 32] = zero ? make_uint2(0, 0) : codes8(c, amax);
             reinterpret_cast<uint32_t *>(dst + kDl)[lane] = pack_bf16x2(__fdiv_rn(k0, s), __fdiv_rn(k1, s));
             if (lane < 4) reinterpret_cast<uint32_t *>(dst + kDl + 2 * kDr)[lane] = lane == 0 ? __float_as_uint(s) : 0u;
         } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                a[j] *= inv;
+                c[j] *= inv;
+            }
             uint8_t *dst = P.cache + row * (kDrow * 2);
             reinterpret_cast<uint4 *>(dst)[lane] = make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]),
                                                               pack_bf16x2(a[4], a[5]), pack_bf16x2(a[6], a[7]));

@@ -503,14 +503,18 @@ MLA_DEV_BAD_OFFSETS = 0x10
 MLA_DEV_BAD_PATH = 0x20
 
 
-def _launch_on(index, stream):
+def _launch_on(index, stream, *tensors):
     """Context of a call: its device, and its stream as the current one, so that what the call
-    allocates or clears belongs to that stream too."""
+    allocates or clears belongs to that stream too.  On a stream of the caller's choice the
+    tensors are marked as in use there, so that freeing one does not hand its memory out early."""
     import torch
     if stream is None:
         return _HERE_ALREADY if torch.cuda.current_device() == index else torch.cuda.device(index)
     if stream.device.index != index:
         raise ValueError(f"stream must be one of cuda:{index}, the tensors' device")
+    for t in tensors:
+        if t is not None and t is not False:
+            t.record_stream(stream)
     return torch.cuda.stream(stream)
 
 
@@ -665,7 +669,7 @@ def query(q_nope, q_pe, w_uk, positions, *, rope_base: float = DEFAULT_ROPE_BASE
     args = (*_strided(q_nope, "q_nope", torch.bfloat16, (T, NUM_HEADS, D_NOPE), index), *_strided(q_pe, "q_pe", torch.bfloat16, (T, NUM_HEADS, D_ROPE), index),
             _dense(w_uk, "w_uk", torch.bfloat16, (NUM_HEADS, D_NOPE, D_LATENT), index))
     pos = _dense(positions, "positions", torch.int32, (T,), index, 4)
-    with _launch_on(index, stream):
+    with _launch_on(index, stream, q_nope, q_pe, w_uk, positions, table, q_latent, q_rope, status):
         tab = _table_of(table, rope_base, index, "query")
         q_latent = _out(q_latent, "q_latent", torch.bfloat16, (T, NUM_HEADS, D_LATENT), index)
         q_rope = _out(q_rope, "q_rope", torch.bfloat16, (T, NUM_HEADS, D_ROPE), index)
@@ -715,7 +719,8 @@ def _append(kv_latent, k_pe, kv_norm_weight, kv_cache, block_table, seq_lens, to
     off = _dense(token_offsets, "token_offsets", torch.int32, (B + 1,), index, 4)
     pos = None if positions is None else _dense(positions, "positions", torch.int32, (T,), index, 4)
     lib = load_library()
-    with _launch_on(index, stream):
+    with _launch_on(index, stream, kv_latent, k_pe, kv_norm_weight, kv_cache, block_table, seq_lens, token_offsets,
+                    positions, table, status):
         tab = _table_of(table, rope_base, index, "cache_append")
         status = _status_word(status, index)
         prob = _Ragged(B, T, NUM_HEADS, PAGE_SIZE, width, 0)
@@ -763,7 +768,7 @@ def tree_plan(seq_lens, token_offsets, masks, *, max_pages_per_seq: int, workspa
     T = masks.shape[0]
     m = _dense(masks, "masks", torch.int64, (T,), index, 8)
     lib = load_library()
-    with _launch_on(index, stream):
+    with _launch_on(index, stream, seq_lens, token_offsets, masks, workspace):
         prob = _Ragged(B, T, NUM_HEADS, PAGE_SIZE, max_pages_per_seq, 0)
         if workspace is None:
             n = ctypes.c_size_t(0)
@@ -787,8 +792,13 @@ def tree_decode(p: TreePlan, q_latent, q_rope, kv_cache, block_table, *, scale: 
 
 
 def tree_decode_fp8(p: TreePlan, q_latent, q_rope, kv_cache_fp8, block_table, *, scale: float = DEFAULT_SCALE,
-                    out=None, lse=None, stream=None, pow2_max: bool = False, scratch=None):
+                    out=None, lse=None, stream=None, pow2_max: bool = True, scratch=None):
     """``tree_decode`` over an fp8 cache (``mla_tree_decode_fp8``; uint8 [pages][64][656]).
+
+    pow2_max is on here: a weight times its token's scale is never exactly 1, so the exact
+    running maximum gains nothing, and rescaling a page half to the pair's maximum by a power
+    of two does not round its weights a second time (error of o over 100-200 keys 2.45e-3 ->
+    2.32e-3 of its norm, 1.66e-3 being its own rounding to bf16).
 
     scratch: where each page is expanded once for all nodes, a uint8 tensor of at least
     batch * max_pages * EXPANDED_PAGE_BYTES bytes, or False for none.  By default one is allocated
@@ -811,8 +821,10 @@ def _tree_decode(p, q_latent, q_rope, kv_cache, block_table, scale, out, lse, st
     qr = _dense(q_rope, "q_rope", torch.bfloat16, (T, NUM_HEADS, D_ROPE), index)
     cache = _cache_ptr(kv_cache, fp8, index)
     bt = _dense(block_table, "block_table", torch.int32, (p.batch, p.max_pages), index, 4)
+    if scratch is not None and scratch is not False and not isinstance(scratch, torch.Tensor):
+        raise TypeError("scratch must be a torch.Tensor, False or None")
     lib = load_library()
-    with _launch_on(index, stream):
+    with _launch_on(index, stream, ws, q_latent, q_rope, kv_cache, block_table, out, lse, scratch):
         out = _out(out, "out", torch.bfloat16, (T, NUM_HEADS, D_LATENT), index)
         lse = _out(lse, "lse", torch.float32, (T, NUM_HEADS), index)
         prob = _Ragged(p.batch, T, NUM_HEADS, PAGE_SIZE, p.max_pages, MLA_FLAG_POW2_MAX if pow2_max else 0)
@@ -870,7 +882,8 @@ def _commit(kv_cache, block_table, seq_lens, token_offsets, paths, path_lens, ne
     row = FP8_ROW_BYTES if fp8 else 2 * (D_LATENT + D_ROPE)
     shape = kv_cache.shape
     layers, pages = (shape[0] if len(shape) == 4 else 1), shape[-3]
-    with _launch_on(index, stream):
+    with _launch_on(index, stream, kv_cache, block_table, seq_lens, token_offsets, paths, path_lens, new_seq_lens,
+                    status):
         new_seq_lens = _out(new_seq_lens, "new_seq_lens", torch.int32, (B,), index)
         status = _status_word(status, index)
         # the offsets alone say how many nodes there are: any bound on them will do

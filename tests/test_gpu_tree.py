@@ -110,6 +110,12 @@ def test_tree_fp8_scratch_changes_no_bit():
         o2, l2, st2, _ = run_tree(c, ql, qr, cache, True, scratch=s)
         assert status == st2 == 0
         assert torch.equal(out, o2) and torch.equal(lse, l2)
+    a = run_tree(c, ql, qr, cache, True, scratch=False, pow2_max=False)
+    b = run_tree(c, ql, qr, cache, True, scratch=room, pow2_max=False)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    ref = OT.tree_decode(ql, qr, OF.dequantize_cache(cache.numpy()), c["block_table"], c["seq_lens"], c["offsets"],
+                         c["masks"], scale=SCALE)
+    check_rows(a[0], a[1], ref, slice(0, int(c["offsets"][-1])))
     c["block_table"][3, 1] = c["pages"]                                  # a bad page: the same rows, the same flag
     a = run_tree(c, ql, qr, cache, True, scratch=False)
     b = run_tree(c, ql, qr, cache, True, scratch=room)
@@ -158,6 +164,14 @@ def test_tree_of_a_chain_is_the_two_token_decode():
     ref = OT.tree_decode(ql, qr, cache, c["block_table"], c["seq_lens"], c["offsets"], c["masks"], scale=SCALE)
     check_rows(out, lse, ref, slice(None))
     check_rows(o2.view(10, 128, 512), l2.view(10, 128), ref, slice(None))
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_tree_batch_without_requests(fp8):
+    c = TU.case([0, 0, 0], [0, 7, -3], "tree", seed=29, pad=5, width=2)
+    ql, qr, cache = TU.tensors(c, seed=30)
+    out, lse, status, _ = run_tree(c, ql, qr, fp8_of(cache) if fp8 else cache, fp8)
+    assert status == 0 and (out == 7).all() and (lse == 7).all()
 
 
 def test_tree_bad_inputs_are_flagged():
@@ -243,6 +257,9 @@ def test_tree_refuses_wrong_arguments():
     with pytest.raises(mla.MLAError):
         mla.tree_plan(d["seq_lens"], d["offsets"], d["masks"], max_pages_per_seq=2,
                       workspace=torch.empty(4096, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(TypeError, match="scratch"):
+        mla.tree_decode_fp8(p, ql, qr, torch.zeros(9, 64, 656, dtype=torch.uint8, device="cuda"), d["block_table"],
+                            scratch=True)
     big = torch.zeros(20000, dtype=torch.int64, device="cuda")
     with pytest.raises(mla.MLAError, match="unsupported"):
         mla.tree_plan(d["seq_lens"], d["offsets"], big, max_pages_per_seq=2)

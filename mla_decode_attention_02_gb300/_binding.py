@@ -503,6 +503,45 @@ MLA_DEV_BAD_OFFSETS = 0x10
 MLA_DEV_BAD_PATH = 0x20
 
 
+_host = None
+_HOST_ENTRIES = ("mla_query", "mla_cache_append", "mla_cache_append_fp8", "mla_tree_workspace_size", "mla_tree_plan",
+                 "mla_tree_decode", "mla_tree_decode_fp8", "mla_cache_commit")
+
+
+def _native():
+    """The marshalling of the tree step's calls in C++ (csrc/host/mla_host.cpp).
+
+    Its functions take the plain case, dense CUDA tensors on the current device and stream, and
+    return None for any other; the Python below then does the call or says what is wrong with it.
+    """
+    global _host
+    if _host is None:
+        lib = load_library()
+        if not os.path.exists(os.path.join(_HERE, "_mla_host.so")):
+            raise RuntimeError("_mla_host.so is missing: build the library first "
+                               "(python -m mla_decode_attention_02_gb300.build)")
+        import torch  # noqa: F401  (its libraries are what the module links to)
+
+        from . import _mla_host
+        _mla_host.bind(*[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _HOST_ENTRIES])
+        _host = _mla_host
+    return _host
+
+
+def _made(r, what):
+    """The outputs of a native call, or the error of one that the C ABI refused."""
+    if type(r) is int:
+        raise MLAError(r, what)
+    return r
+
+
+def _kept_table(table, t, rope_base):
+    """The caller's table, or the kept one of rope_base if there is one."""
+    if table is not None:
+        return table
+    return _rope_tables.get((t.get_device(), float(rope_base))) if hasattr(t, "get_device") else None
+
+
 def _launch_on(index, stream, *tensors):
     """Context of a call: its device, and its stream as the current one, so that what the call
     allocates or clears belongs to that stream too.  On a stream of the caller's choice the
@@ -663,6 +702,11 @@ def query(q_nope, q_pe, w_uk, positions, *, rope_base: float = DEFAULT_ROPE_BASE
     kept.  Returns (q_latent [T][128][512], q_rope [T][128][64], status): status is a
     one-element int32 device tensor of MLA_DEV_* bits.
     """
+    if stream is None:
+        r = (_host or _native()).query(q_nope, q_pe, w_uk, positions, _kept_table(table, q_nope, rope_base), q_latent,
+                                       q_rope, status)
+        if r is not None:
+            return _made(r, "mla_query")
     import torch
     index = _index_of(q_nope, "q_nope", 3, torch.bfloat16)
     T = q_nope.shape[0]
@@ -705,6 +749,12 @@ def cache_append_fp8(kv_latent, k_pe, kv_norm_weight, kv_cache_fp8, block_table,
 
 def _append(kv_latent, k_pe, kv_norm_weight, kv_cache, block_table, seq_lens, token_offsets, positions, rope_base,
             rms_eps, table, status, stream, fp8):
+    if stream is None:
+        r = (_host or _native()).append(fp8, kv_latent, k_pe, kv_norm_weight, kv_cache, block_table, seq_lens,
+                                        token_offsets, positions, rms_eps, _kept_table(table, kv_latent, rope_base),
+                                        status)
+        if r is not None:
+            return _made(r, "mla_cache_append_fp8" if fp8 else "mla_cache_append")
     import torch
     index = _index_of(kv_latent, "kv_latent", 2, torch.bfloat16)
     T = kv_latent.shape[0]
@@ -759,6 +809,10 @@ def tree_plan(seq_lens, token_offsets, masks, *, max_pages_per_seq: int, workspa
     exceed token_offsets[B] (padding).  The plan serves every layer of the step; calls that share
     it must be ordered.
     """
+    if stream is None:
+        r = (_host or _native()).tree_plan(seq_lens, token_offsets, masks, max_pages_per_seq, workspace)
+        if r is not None:
+            return TreePlan(seq_lens.shape[0], masks.shape[0], max_pages_per_seq, _made(r, "mla_tree_plan"))
     import torch
     index = _index_of(seq_lens, "seq_lens", 1, torch.int32)
     B = seq_lens.shape[0]
@@ -814,17 +868,27 @@ EXPAND_LIMIT_BYTES = 8 << 30
 
 
 def _tree_decode(p, q_latent, q_rope, kv_cache, block_table, scale, out, lse, stream, pow2_max, fp8, scratch=False):
-    import torch
     T, ws = p.tokens, p.workspace
+    if fp8 and scratch is None:
+        need = p.batch * p.max_pages * EXPANDED_PAGE_BYTES
+        scratch = need if T >= 2 * p.batch and need <= EXPAND_LIMIT_BYTES and p.batch <= 65535 else False
+    if stream is None and scratch is not True:
+        r = (_host or _native()).tree_decode(p.batch, T, p.max_pages, ws, q_latent, q_rope, kv_cache, block_table, scale,
+                                             out, lse, MLA_FLAG_POW2_MAX if pow2_max else 0, fp8,
+                                             None if scratch is False else scratch)
+        if r is not None:
+            return _made(r, "mla_tree_decode_fp8" if fp8 else "mla_tree_decode")
+    import torch
     index = ws.get_device()
     ql = _dense(q_latent, "q_latent", torch.bfloat16, (T, NUM_HEADS, D_LATENT), index)
     qr = _dense(q_rope, "q_rope", torch.bfloat16, (T, NUM_HEADS, D_ROPE), index)
     cache = _cache_ptr(kv_cache, fp8, index)
     bt = _dense(block_table, "block_table", torch.int32, (p.batch, p.max_pages), index, 4)
-    if scratch is not None and scratch is not False and not isinstance(scratch, torch.Tensor):
+    if scratch is not False and (scratch is True or not isinstance(scratch, (int, torch.Tensor))):
         raise TypeError("scratch must be a torch.Tensor, False or None")
     lib = load_library()
-    with _launch_on(index, stream, ws, q_latent, q_rope, kv_cache, block_table, out, lse, scratch):
+    with _launch_on(index, stream, ws, q_latent, q_rope, kv_cache, block_table, out, lse,
+                    None if isinstance(scratch, int) else scratch):
         out = _out(out, "out", torch.bfloat16, (T, NUM_HEADS, D_LATENT), index)
         lse = _out(lse, "lse", torch.float32, (T, NUM_HEADS), index)
         prob = _Ragged(p.batch, T, NUM_HEADS, PAGE_SIZE, p.max_pages, MLA_FLAG_POW2_MAX if pow2_max else 0)
@@ -833,12 +897,8 @@ def _tree_decode(p, q_latent, q_rope, kv_cache, block_table, scale, out, lse, st
         if not fp8:
             _check(lib.mla_tree_decode(*args, _current_stream(index)), "mla_tree_decode")
             return out, lse
-        if scratch is None:
-            need = p.batch * p.max_pages * EXPANDED_PAGE_BYTES
-            if T >= 2 * p.batch and need <= EXPAND_LIMIT_BYTES and p.batch <= 65535:
-                scratch = torch.empty(need, dtype=torch.uint8, device=ws.device)
-            else:
-                scratch = False
+        if scratch is not False and isinstance(scratch, int):
+            scratch = torch.empty(scratch, dtype=torch.uint8, device=ws.device)
         room = (None, 0)
         if scratch is not False:
             n = scratch.numel()
@@ -868,6 +928,11 @@ def cache_commit_fp8(kv_cache_fp8, block_table, seq_lens, token_offsets, paths, 
 
 
 def _commit(kv_cache, block_table, seq_lens, token_offsets, paths, path_lens, new_seq_lens, status, stream, fp8):
+    if stream is None:
+        r = (_host or _native()).commit(fp8, kv_cache, block_table, seq_lens, token_offsets, paths, path_lens,
+                                        new_seq_lens, status)
+        if r is not None:
+            return _made(r, "mla_cache_commit")
     import torch
     index = _index_of(block_table, "block_table", 2, torch.int32)
     B, width = block_table.shape

@@ -1,4 +1,6 @@
-"""Build the CUDA library libmla_decode.so in-tree with nvcc (sm_103a only).
+"""Build the CUDA library libmla_decode.so in-tree with nvcc (sm_103a only), and
+beside it _mla_host.so, the argument marshalling of the tree step's calls on
+torch's tensor objects (host C++, against the installed torch's headers).
 
 All translation units compile in parallel and link with -shared; the CUDA
 runtime links statically and the driver API is reached through
@@ -18,6 +20,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libmla_decode.so")
+HOST_SRC = os.path.join(CSRC, "host", "mla_host.cpp")
+HOST_PATH = os.path.join(HERE, "_mla_host.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -36,14 +40,33 @@ def _deps() -> list[str]:
     files = sources()
     files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
     files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
-    return files
+    return files + [HOST_SRC]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(HOST_PATH):
         return False
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(HOST_PATH))
     return all(os.path.getmtime(f) <= t for f in _deps())
+
+
+def _build_host() -> None:
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
+    inc = [INCLUDE, os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], cuda]
+    tmp = HOST_PATH + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *[x for d in inc for x in ("-isystem" if d != INCLUDE else "-I", d)], HOST_SRC, "-o", tmp,
+           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {HOST_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, HOST_PATH)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: tuple = ()) -> str:
@@ -67,7 +90,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags: tuple = ()) -
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        host = ex.submit(_build_host)
         objs = list(ex.map(compile_one, sources()))
+        host.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc, ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -259,3 +259,19 @@ def test_binding_refuses_wrong_tensors():
         mla.tree_plan(torch.zeros(2), None, None, max_pages_per_seq=1)
     with pytest.raises(ValueError, match="CUDA"):
         mla.cache_commit(None, torch.zeros(1, 1, dtype=torch.int32), None, None, None, None)
+
+
+def test_native_marshalling_leaves_what_is_not_plain():
+    """The C++ marshalling takes CUDA tensors only; anything else is the Python checks' to name."""
+    h = binding._native()
+    t = torch.zeros(1, dtype=torch.int32)
+    assert h.query(*[t] * 8) is None and h.query() is None
+    assert h.append(False, *[t] * 11) is None
+    assert h.append(False, *[None] * 11) is None
+    assert h.tree_plan(t, t, t, 1, None) is None
+    assert h.tree_decode(1, 1, 1, t, t, t, t, t, 1.0, None, None, 0, False, None) is None
+    assert h.commit(False, *[t] * 8) is None and h.commit(*[object()] * 9) is None
+    with pytest.raises(TypeError):
+        h.bind(1)
+    with pytest.raises(ValueError):
+        h.bind(*[0] * len(binding._HOST_ENTRIES))

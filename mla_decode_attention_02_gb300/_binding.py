@@ -1004,6 +1004,8 @@ def plan_layout(batch: int, s_q: int, units: int, trees: int = 0) -> dict:
         off = _align(off, 16)
         L["tree_rows"] = off
         off += 16 * rows
+        L["tree_items"] = off
+        off += 16 * max_items
         L["tree_pages"] = off
         off += 4 * trees
     L["plan_end"] = off
@@ -1029,6 +1031,7 @@ def parse_plan(buf, batch: int, s_q: int, units: int, trees: int = 0) -> dict:
     R = L["num_rows"]
     items = b[L["items"]:L["items"] + 16 * n].view("<i4").reshape(n, 4)
     more = {"tree_rows": b[L["tree_rows"]:L["tree_rows"] + 16 * R].view(_TREE_ROW).copy(),
+            "tree_items": b[L["tree_items"]:L["tree_items"] + 16 * n].view(_TREE_ROW).copy(),
             "tree_pages": b[L["tree_pages"]:L["tree_pages"] + 4 * trees].view("<i4").copy()} if trees else {}
     return {
         **more,

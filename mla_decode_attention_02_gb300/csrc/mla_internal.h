@@ -85,10 +85,12 @@ static_assert(sizeof(TreeRow) == 16, "tree row layout");
 constexpr int32_t kRowEmpty = -1;    // sees no key: o = 0, lse = -infinity
 constexpr int32_t kRowUnused = -2;   // behind the last request: left as it is
 
-// Byte offsets of every region of the workspace (tree_rows, and tree_pages, the pages
-// each request's rows read: tree schedules only).
+// Byte offsets of every region of the workspace.  Tree schedules only: tree_rows (the
+// nodes, by token), tree_items (the same by item, read beside it) and tree_pages (the
+// pages each request's rows read).
 struct PlanLayout {
-    size_t items, item_unit, unit_begin, row_nparts, row_part0, row_item0, row_pos, tree_rows, tree_pages, plan_end;
+    size_t items, item_unit, unit_begin, row_nparts, row_part0, row_item0, row_pos;
+    size_t tree_rows, tree_items, tree_pages, plan_end;
     size_t lse_part, o_part, total;
     int32_t num_rows, max_items, max_parts;
 };
@@ -120,11 +122,13 @@ MLA_HD PlanLayout make_layout(int32_t num_rows, int32_t num_units, int32_t trees
     off = align_up(off, 8);
     L.row_pos = off;
     off += sizeof(int64_t) * (size_t)L.num_rows;
-    L.tree_rows = L.tree_pages = 0;
+    L.tree_rows = L.tree_items = L.tree_pages = 0;
     if (tree) {
         off = align_up(off, 16);
         L.tree_rows = off;
         off += sizeof(TreeRow) * (size_t)L.num_rows;
+        L.tree_items = off;
+        off += sizeof(TreeRow) * (size_t)L.max_items;
         L.tree_pages = off;
         off += sizeof(int32_t) * (size_t)trees;
     }

@@ -77,9 +77,10 @@
 // mask of a page is one 64-bit word for the whole CTA: full pages of the context
 // take the unmasked path, and only the one or two pages that hold the tree's own
 // slots (64 at most) mask scores and zero the V rows that the node does not see
-// (their weights are zero, but a row may hold NaN).  Every item's first page holds a
-// visible key: a row of more than one page begins with context, and a piece of a
-// cut row is at least four pages long.
+// (their weights are zero, but a row may hold NaN).  Every page of a row holds a visible
+// key, so every item's first page gives a finite maximum: a row ends with its last
+// visible key, and a page before its last one starts with context (at most 64 slots
+// lie between the context and the row's end).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -631,9 +632,9 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
     pdl_launch_dependents();
 
     const PlanLayout L = make_layout(kTree ? P.s_q : P.batch * P.s_q, P.num_units, kTree ? P.batch : 0);
-    const TreeRow *tree_rows = reinterpret_cast<const TreeRow *>(P.ws + L.tree_rows);
-    // request of an item's row
-    auto request = [&](int32_t row) { return kTree ? tree_rows[row].req : row / P.s_q; };
+    const TreeRow *tree_items = reinterpret_cast<const TreeRow *>(P.ws + L.tree_items);
+    // request of an item
+    auto request = [&](int i, int32_t row) { return kTree ? tree_items[i].req : row / P.s_q; };
     const WorkItem *items = reinterpret_cast<const WorkItem *>(P.ws + L.items);
     const int32_t *unit_begin = reinterpret_cast<const int32_t *>(P.ws + L.unit_begin);
     float *lse_part = reinterpret_cast<float *>(P.ws + L.lse_part);
@@ -666,7 +667,7 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
         bool ok = true;
         for (int i = i_begin; i < i_end && ok; ++i) {
             const WorkItem it = items[i];
-            const int b = request(it.row);
+            const int b = request(i, it.row);
             const int p0 = it.kv_begin / kPage;
             const int n = (it.kv_end - it.kv_begin + kPage - 1) / kPage;
             const uint32_t ii = (uint32_t)(i - i_begin);
@@ -691,6 +692,12 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
                             if (ii > 0 && !wait_warp(ctl, bar(ctl, B_Q_EMPTY), (ii - 1) & 1)) {
                                 ok = false;
                                 break;
+                            }
+                            // (trees: the unit's first q tile starts on its way to L2 too)
+                            if (kTree && ii == 0 && lane == 0) {
+                                for (int b = kQTDims / 64; b < kDl / 64; ++b)
+                                    tma_prefetch_2d(&P.tm_q_lat, 64 * b, it.row * kHeads);
+                                tma_prefetch_2d(&P.tm_q_rope, 0, it.row * kHeads);
                             }
                             if (lane == 0) {
                                 const uint32_t fq = bar(ctl, B_QSTAGE);
@@ -819,8 +826,8 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
             int32_t context = 0;
             uint64_t mask = 0;
             if (kTree && !qk) {
-                context = tree_rows[it.row].context;
-                mask = tree_rows[it.row].mask;
+                context = tree_items[i].context;
+                mask = tree_items[i].mask;
             }
             if (qk && (!wait_warp(ctl, bar(ctl, B_Q_FULL), ii & 1) || !wait_warp(ctl, bar(ctl, B_QTILE), ii & 1)))
                 break;
@@ -930,8 +937,8 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
             int32_t context = 0;
             uint64_t mask = 0;
             if constexpr (kTree) {
-                context = tree_rows[it.row].context;
-                mask = tree_rows[it.row].mask;
+                context = tree_items[i].context;
+                mask = tree_items[i].mask;
             }
 
             // q of this head -> TMEM: dims 0-319 from the staged blocks (the
@@ -1102,7 +1109,7 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
             total_pages += (uint32_t)((items[i].kv_end - items[i].kv_begin + kPage - 1) / kPage);
         for (int i = i_begin; i < i_end && ok; ++i) {
             const WorkItem it = items[i];
-            const int b = request(it.row);
+            const int b = request(i, it.row);
             const int p0 = it.kv_begin / kPage;
             const int n = (it.kv_end - it.kv_begin + kPage - 1) / kPage;
             const uint32_t ii = (uint32_t)(i - i_begin);

@@ -11,13 +11,17 @@
 //    longest row to the unit with the least work so far (ranks by counting,
 //    ties to the lower index).  Taken when its largest load is within 1/32 of
 //    what cutting would give.
+//  - Even pieces: with no more rows than units, every row in pieces of one size (two
+//    pages at least), as small as one piece per unit allows.  Taken by the same measure.
 //  - Cut rows: the rows lie on a cost line, every units-th row together (in token
 //    order when there are no more rows than units), and the line is cut into equal
 //    stretches as in mla_plan.cu (cut_row); a unit then runs its pieces in token order.
 //
 // Measured (decode alone) against the line in token order: 64 requests of 16
 // nodes over 4096 keys 1001 -> 957 us (whole rows), 268 nodes of 80 keys 52 -> 44,
-// 138 nodes of mixed lengths 118 -> 114 (cut rows).
+// 138 nodes of mixed lengths 118 -> 114 (cut rows).  Even pieces against cut rows (at least
+// four pages each): 8 nodes of 700 keys 21.3 -> 19.3, 16 of 1500 28.4 -> 25.3, one of 8192
+// 22.9 -> 20.8; 24 of 131072 697 against 683, which the measure leaves to cut rows.
 //
 // One CTA; every choice is a function of the inputs alone, and the host twin
 // below makes the same ones.
@@ -81,6 +85,16 @@ MLA_HD bool keep_whole(int64_t max_load, int64_t target) {
     return max_load <= target + kItemCost + kSplitPenalty + target / 32;
 }
 
+// Pieces of a row when pieces have `cap` pages at most, and the first page of piece i of k.
+constexpr int32_t kEvenPages = 2;
+MLA_HD int32_t even_pieces(int32_t pages, int32_t cap) { return pages > 0 ? (pages - 1) / cap + 1 : 0; }
+// The largest cap that even pieces are taken with (keep_whole of a unit's piece and its item cost).
+MLA_HD int32_t even_most(int64_t longest, int64_t target) {
+    const int64_t cap = target + kSplitPenalty + target / 32;
+    return (int32_t)(cap < longest ? cap : longest);
+}
+MLA_HD int32_t even_page(int32_t pages, int32_t i, int32_t k) { return (int32_t)((int64_t)pages * i / k); }
+
 size_t tree_plan_smem(int32_t R, int32_t U) {
     return 8 * (size_t)R + 4 * (3 * (size_t)R + 2 * (size_t)U) + 4 * (3 * (size_t)U + 2);
 }
@@ -142,6 +156,7 @@ mla_tree_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__rest
     int32_t *row_part0 = reinterpret_cast<int32_t *>(ws + L.row_part0);
     int32_t *row_item0 = reinterpret_cast<int32_t *>(ws + L.row_item0);
     TreeRow *tree_rows = reinterpret_cast<TreeRow *>(ws + L.tree_rows);
+    TreeRow *tree_items = reinterpret_cast<TreeRow *>(ws + L.tree_items);
     int32_t *tree_pages = reinterpret_cast<int32_t *>(ws + L.tree_pages);
 
     if (tid == 0) {
@@ -226,10 +241,13 @@ mla_tree_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__rest
         }
     }
     __syncthreads();
-    int64_t total = 0, longest = 0;
-    for (int w = 0; w < kTreeThreads / 32; ++w) {
-        total += warp_sums[w];
-        longest = warp_most[w] > longest ? warp_most[w] : longest;
+    static_assert(kTreeThreads == 512, "16 warps' sums, twice over a warp");
+    int64_t total = warp_sums[lane & 15], longest = warp_most[lane & 15];
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+        const int64_t m = __shfl_xor_sync(0xffffffffu, longest, o);
+        longest = m > longest ? m : longest;
     }
     __syncthreads();
     const int64_t target = total > 0 ? (total + U - 1) / U : 1;
@@ -273,6 +291,32 @@ mla_tree_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__rest
         whole = keep_whole(most >> 8, target);
     }
 
+    // ---- even pieces: the smallest cap under which every piece has a unit of its own
+    bool even = !whole && R <= U && total > 0;
+    int32_t cap = 0;
+    if (even) {
+        int32_t lo = kEvenPages, hi = even_most(longest, target);   // every warp the same search
+        auto fits = [&](int32_t c) {
+            int32_t pieces = 0;
+            for (int32_t r = lane; r < R; r += 32) pieces += even_pieces(pages(r), c);
+            return __reduce_add_sync(0xffffffffu, pieces) <= U;
+        };
+        even = hi >= lo && fits(hi);
+        while (even && lo < hi) {
+            const int32_t mid = lo + (hi - lo) / 2;
+            if (fits(mid)) hi = mid;
+            else lo = mid + 1;
+        }
+        cap = lo;
+    }
+
+    // an item's place in the schedule
+    auto put = [&](int32_t at, int32_t unit, int32_t r, int32_t pg0, int32_t pg1, int32_t end, int32_t part,
+                   const TreeRow &row) {
+        items[at] = WorkItem{r, pg0 * kPage, min(pg1 * kPage, end), part};
+        item_unit[at] = unit;
+        tree_items[at] = row;
+    };
     int32_t num_items = 0, num_parts = 0;
     if (whole) {
         if (tid < U) {
@@ -293,16 +337,37 @@ mla_tree_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__rest
             row_part0[r] = -1;
             const int32_t at = p > 0 ? s_begin[s_unit[r]] + s_row[r] : -1;
             row_item0[r] = at;
-            if (p > 0) {
-                WorkItem it;
-                it.row = r;
-                it.kv_begin = 0;
-                it.kv_end = s_end[r];
-                it.part = -1;
-                items[at] = it;
-                item_unit[at] = s_unit[r];
+            if (p > 0) put(at, s_unit[r], r, 0, p, s_end[r], -1, tree_rows[r]);
+        }
+    } else if (even) {
+        // ---- even pieces, one per unit, in token order
+        for (int32_t r = tid; r < R; r += kTreeThreads) s_row[r] = even_pieces(pages(r), cap);
+        __syncthreads();
+        for (int32_t r = tid; r < R; r += kTreeThreads) {
+            const int32_t p = pages(r), k = s_row[r];
+            TreeRow row = {};
+            if (p > 0) row = tree_rows[r];
+            int32_t first = 0, part0 = 0;
+#pragma unroll 8
+            for (int32_t j = 0; j < r; ++j) {
+                first += s_row[j];
+                part0 += s_row[j] > 1 ? s_row[j] : 0;
+            }
+            row_nparts[r] = p > 0 ? k : none_parts(p);
+            row_part0[r] = k > 1 ? part0 : -1;
+            row_item0[r] = p > 0 ? first : -1;
+            for (int32_t i = 0; i < k; ++i)
+                put(first + i, first + i, r, even_page(p, i, k), even_page(p, i + 1, k), s_end[r],
+                    k > 1 ? part0 + i : -1, row);
+            if (r == R - 1) {
+                carry = first + k;
+                carry_parts = part0 + (k > 1 ? k : 0);
             }
         }
+        __syncthreads();
+        num_items = (int32_t)carry;
+        num_parts = (int32_t)carry_parts;
+        for (int32_t v = tid; v <= U; v += kTreeThreads) unit_begin[v] = min(v, num_items);
     } else {
         // ---- cut rows: positions on the line
         for (int32_t base = 0; base < R; base += kTreeThreads) {
@@ -318,6 +383,7 @@ mla_tree_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__rest
         if (tid == 0) carry = 0;
         __syncthreads();
         // the pieces in line order: their units and rows, and each row's first partial
+        int32_t my_part0 = -1;   // of the thread's row, if it has one alone
         for (int32_t base = 0; base < R; base += kTreeThreads) {
             const int32_t k = base + tid;
             const int32_t r = k < R ? tree_line(k, R, U) : 0;
@@ -327,9 +393,10 @@ mla_tree_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__rest
             const int64_t incl = block_scan(both, warp_sums);
             if (k < R) {
                 const int32_t first = (int32_t)carry + (int32_t)(incl & 0xffffffff) - n;
+                my_part0 = n > 1 ? (int32_t)carry_parts + (int32_t)(incl >> 32) - n : -1;
                 row_item0[r] = n > 0 ? first : -1;
                 row_nparts[r] = n > 0 ? n : none_parts(pages(r));
-                row_part0[r] = n > 1 ? (int32_t)carry_parts + (int32_t)(incl >> 32) - n : -1;
+                row_part0[r] = my_part0;
                 cut_row(s_pos[r], pages(r), target, U, true, [&](int32_t i, int32_t, int32_t, int32_t unit) {
                     s_unit[first + i] = unit;
                     s_row[first + i] = r;
@@ -356,19 +423,15 @@ mla_tree_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__rest
         __syncthreads();
         for (int32_t v = tid; v <= U; v += kTreeThreads) unit_begin[v] = s_begin[v];
         // each unit's pieces in token order (a unit has one piece of a row at most)
-        for (int32_t r = tid; r < R; r += kTreeThreads) {
+        for (int32_t k = tid; k < R; k += kTreeThreads) {
+            const int32_t r = tree_line(k, R, U);
             if (pages(r) <= 0) continue;
-            const int32_t end = s_end[r], part0 = row_part0[r];
+            const TreeRow row = tree_rows[r];
+            const int32_t end = s_end[r], part0 = R <= kTreeThreads ? my_part0 : row_part0[r];
             cut_row(s_pos[r], pages(r), target, U, true, [&](int32_t i, int32_t pg0, int32_t pg1, int32_t unit) {
                 int32_t at = s_begin[unit];
                 for (int32_t j = s_begin[unit]; j < s_begin[unit + 1]; ++j) at += s_row[j] < r;
-                WorkItem it;
-                it.row = r;
-                it.kv_begin = pg0 * kPage;
-                it.kv_end = min(pg1 * kPage, end);
-                it.part = part0 >= 0 ? part0 + i : -1;
-                items[at] = it;
-                item_unit[at] = unit;
+                put(at, unit, r, pg0, pg1, end, part0 >= 0 ? part0 + i : -1, row);
             });
         }
     }
@@ -406,6 +469,7 @@ mla_status tree_plan_host(const mla_ragged *prob, const int32_t *seq_lens, const
     int32_t *row_part0 = reinterpret_cast<int32_t *>(ws + L.row_part0);
     int32_t *row_item0 = reinterpret_cast<int32_t *>(ws + L.row_item0);
     TreeRow *rows = reinterpret_cast<TreeRow *>(ws + L.tree_rows);
+    TreeRow *tree_items = reinterpret_cast<TreeRow *>(ws + L.tree_items);
     int32_t *tree_pages = reinterpret_cast<int32_t *>(ws + L.tree_pages);
     PlanHeader h = {};
     std::vector<int32_t> pages((size_t)R, kNoneUnused);
@@ -454,11 +518,44 @@ mla_status tree_plan_host(const mla_ragged *prob, const int32_t *seq_lens, const
         }
         whole = keep_whole(*std::max_element(load.begin(), load.end()), target);
     }
+    bool even = !whole && R <= U && total > 0;
+    int32_t cap = 0;
+    if (even) {
+        int32_t lo = kEvenPages, hi = even_most(longest, target);
+        auto fits = [&](int32_t c) {
+            int64_t pieces = 0;
+            for (int32_t p : pages) pieces += even_pieces(p, c);
+            return pieces <= U;
+        };
+        even = hi >= lo && fits(hi);
+        while (even && lo < hi) {
+            const int32_t mid = lo + (hi - lo) / 2;
+            if (fits(mid)) hi = mid;
+            else lo = mid + 1;
+        }
+        cap = lo;
+    }
     for (int32_t r = 0; r < R; ++r) {
         row_nparts[r] = pages[r] > 0 ? 1 : none_parts(pages[r]);
         row_part0[r] = row_item0[r] = -1;
     }
-    if (!whole) {
+    if (even) {
+        for (auto &l : lists) l.clear();
+        int32_t unit = 0;
+        for (int32_t r = 0; r < R; ++r) {
+            const int32_t p = pages[r], k = even_pieces(p, cap);
+            if (k > 0) row_item0[r] = unit;
+            if (k > 1) {
+                row_nparts[r] = k;
+                row_part0[r] = h.num_parts;
+                h.num_parts += k;
+            }
+            const int32_t end = p > 0 ? tree_end(rows[r].context, rows[r].mask) : 0;
+            for (int32_t i = 0; i < k; ++i)
+                lists[unit++].push_back({r, even_page(p, i, k) * kPage, std::min(even_page(p, i + 1, k) * kPage, end),
+                                         k > 1 ? row_part0[r] + i : -1});
+        }
+    } else if (!whole) {
         for (auto &l : lists) l.clear();
         int64_t at = 0;
         int32_t n_items = 0;
@@ -486,6 +583,7 @@ mla_status tree_plan_host(const mla_ragged *prob, const int32_t *seq_lens, const
         for (const WorkItem &it : lists[u]) {
             if (whole) row_item0[it.row] = h.num_items;
             items[h.num_items] = it;
+            tree_items[h.num_items] = rows[it.row];
             item_unit[h.num_items++] = u;
         }
     }

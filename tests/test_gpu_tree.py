@@ -193,6 +193,7 @@ def test_tree_bad_inputs_are_flagged():
 def test_tree_plan_matches_the_host():
     for seed, (counts, lens) in enumerate([([7, 0, 64, 1], [900, 5, 64, 9000]), ([16] * 30, list(range(20, 3020, 100))),
                                            ([3], [3]), ([2] * 9, [70] * 9), ([64] * 31 + [1, 17], [64 + 5 * i for i in range(33)]),
+                                           ([8], [700]), ([1, 0, 3], [8192, 1, 2500]), ([12, 12], [40000, 39000]),
                                            ([33] * 300, [33 + i % 900 for i in range(300)])]):
         c = TU.case(counts, lens, "tree", seed=seed, pad=seed)
         d = TU.index_tensors(c)
@@ -202,7 +203,7 @@ def test_tree_plan_matches_the_host():
                                   num_units=mla.num_units())
         assert got["header"] == want["header"]
         n = int(c["offsets"][-1])
-        for k in ("items", "item_unit", "unit_begin", "row_nparts", "row_part0", "row_item0", "tree_pages"):
+        for k in ("items", "item_unit", "unit_begin", "row_nparts", "row_part0", "row_item0", "tree_pages", "tree_items"):
             assert np.array_equal(got[k], want[k]), k
         assert np.array_equal(got["tree_rows"][:n], want["tree_rows"][:n])
 

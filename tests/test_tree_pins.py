@@ -111,6 +111,7 @@ def _check_plan(c, units, max_pages=None):
             assert len(mine) == 0 and p["row_nparts"][t] == -1
             continue
         assert p["row_nparts"][t] == len(mine)
+        assert (p["tree_items"][items[:, 0] == t] == row).all()
         assert p["tree_pages"][b] >= (seen[-1] + 64) // 64
         at = 0
         for i, (_, k0, k1, part) in enumerate(mine):

@@ -19,11 +19,11 @@
 #include <ATen/ops/zeros.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cstdint>
 #include <cstring>
-#include <exception>
 
 #include "mla_fp8.h"
 #include "mla_tree.h"
@@ -120,15 +120,12 @@ bool cache_shape(const at::Tensor *t, bool fp8, bool layers) {
            t->numel() > 0;
 }
 
-// Every function: no C++ exception leaves it.
+// Every function: no C++ exception leaves it (torch's become its Python ones, out of memory too).
 template <typename F>
 PyObject *guarded(F f) {
-    try {
-        return f();
-    } catch (const std::exception &e) {
-        if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
-        return nullptr;
-    }
+    HANDLE_TH_ERRORS
+    return f();
+    END_HANDLE_TH_ERRORS
 }
 #define MLA_NOT_PLAIN Py_RETURN_NONE
 

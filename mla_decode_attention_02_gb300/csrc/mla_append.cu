@@ -13,7 +13,7 @@
 // need no shared memory.  The token's request is found by a 32-way search of
 // token_offsets (two or three rounds of one load per lane) while the token's
 // values are already on their way.  Bound by memory: 1152 bytes in and 1152 or
-// 656 out per token (8731 tokens of six prompts in 4.5 us, 4.5 TB/s); small batches
+// 656 out per token (8780 tokens of six prompts in 4.5 us, 4.5 TB/s); small batches
 // by the chain of dependent loads (offsets, length and table, page) and the launch
 // (8 tokens 1.9 us, 1300 tokens into fp8 rows 3.1 us).
 #include <cuda_bf16.h>

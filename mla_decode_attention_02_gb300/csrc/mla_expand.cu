@@ -10,7 +10,7 @@
 // and its scale s goes to an array beside, for the softmax.  Values and roundings of
 // the result are those of the in-kernel expansion.  One warp per row: lane l turns
 // 16 codes into two 16-byte stores.  Bound by memory: 656 bytes in, 1156 out per row
-// (17 requests, 38,000 rows: about 12 us, most of it the first touch of the cache).
+// (17 requests, 43,600 rows: about 12 us, most of it the first touch of the cache).
 // With it a page of tree attention costs a bf16 page (1.0 us a unit instead of 1.9):
 // 64 requests of 4096 keys with 1, 2, 4, 8 nodes each took 143, 273, 509, 989 us with the
 // in-kernel expansion and 174, 246, 368, 612 with this one.

@@ -239,6 +239,75 @@ def test_tree_many_rows_and_repeats():
         assert torch.equal(og, out) and torch.equal(lg, lse)
 
 
+def test_trees_on_two_streams_at_once():
+    cases = [TU.case([9, 30, 5], [1500, 700, 3000], "tree", seed=71), TU.case([16] * 6, [900] * 6, "bits", seed=72)]
+    data = [TU.tensors(c, seed=73 + i) for i, c in enumerate(cases)]
+    alone = [run_tree(c, *t)[:2] for c, t in zip(cases, data)]
+    dev = [(TU.index_tensors(c), [x.cuda() for x in t]) for c, t in zip(cases, data)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(6):
+        for i, (d, t) in enumerate(dev):
+            p = mla.tree_plan(d["seq_lens"], d["offsets"], d["masks"], max_pages_per_seq=d["block_table"].shape[1],
+                              stream=streams[i])
+            got[i].append(mla.tree_decode(p, *t, d["block_table"], scale=SCALE, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        for o, l in got[i]:
+            assert torch.equal(o, alone[i][0]) and torch.equal(l, alone[i][1])
+
+
+def test_rows_past_32_bit_offsets():
+    """A pool whose last pages lie past 2^31 elements: append, attention and commit there."""
+    pages = 60000                                                 # 2.2e9 elements, 4.4 GB
+    pool = torch.zeros(pages, 64, 576, dtype=torch.bfloat16, device="cuda")
+    c = TU.case([5, 3], [70, 131], "tree", seed=75, spare=0)
+    c["block_table"] = np.where(c["block_table"] < 1 << 30, pages - 1 - c["block_table"], -1).astype(np.int32)
+    d = TU.index_tensors(c)
+    g = torch.Generator().manual_seed(76)
+    kv = torch.randn(201, 576, generator=g).to(torch.bfloat16).cuda()
+    gamma = torch.ones(512, dtype=torch.bfloat16, device="cuda")
+    st = mla.cache_append(kv[:, :512], kv[:, 512:], gamma, pool, d["block_table"], d["seq_lens"],
+                          torch.tensor([0, 70, 201], dtype=torch.int32, device="cuda"))
+    assert st.item() == 0
+    used = pool[pages - 8:].cpu()
+    small = TU.case([5, 3], [70, 131], "tree", seed=75, spare=0)
+    table = np.where(c["block_table"] >= 0, c["block_table"] - (pages - 8), 0)
+    slots = OT.token_slots(table, c["seq_lens"], [0, 70, 201])
+    lat, rope = OT.token_rows(f64(kv)[:, :512], f64(kv)[:, 512:], np.ones(512), [s for _, _, s in slots])
+    rows = f64(used.reshape(-1, 576))
+    at = [r for _, r, _ in slots]
+    assert (np.abs(rows[at][:, :512] - lat) <= (BF + 1e-5) * np.abs(lat)).all()
+    ql, qr, _ = TU.tensors(small, seed=77)
+    p = mla.tree_plan(d["seq_lens"], d["offsets"], d["masks"], max_pages_per_seq=d["block_table"].shape[1])
+    o, lse = mla.tree_decode(p, ql.cuda(), qr.cuda(), pool, d["block_table"], scale=SCALE)
+    assert mla.check(p) == 0
+    ref = OT.tree_decode(ql, qr, used, table, c["seq_lens"], c["offsets"], c["masks"], scale=SCALE)
+    check_rows(o, lse, ref, slice(None))
+    paths = np.array([[0, 3, 4], [1, 2, 0]], np.int32)
+    plens = np.array([3, 2], np.int32)
+    new, st = mla.cache_commit(pool, d["block_table"], d["seq_lens"], d["offsets"], torch.from_numpy(paths).cuda(),
+                               torch.from_numpy(plens).cuda())
+    want, lens = OT.commit(used.view(torch.int16).reshape(-1, 576).numpy(), table, c["seq_lens"], c["offsets"], paths, plens)
+    assert st.item() == 0 and new.cpu().tolist() == lens.tolist()
+    assert np.array_equal(pool[pages - 8:].cpu().view(torch.int16).reshape(-1, 576).numpy(), want)
+    assert not pool[:pages - 8].any()
+
+
+def test_query_past_32_bit_offsets():
+    T = 33000                                                     # 2.16e9 output values
+    g = torch.Generator(device="cuda").manual_seed(78)
+    q = torch.randn(T, 128, 192, generator=g, device="cuda", dtype=torch.bfloat16)
+    w = torch.randn(128, 128, 512, generator=g, device="cuda", dtype=torch.bfloat16) * 128 ** -0.5
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    ql, qr, st = mla.query(q[..., :128], q[..., 128:], w, pos)
+    assert st.item() == 0
+    for at in (0, T - 60):                                         # a small call's rows are the same
+        a, b, _ = mla.query(q[at:at + 60, :, :128], q[at:at + 60, :, 128:], w, pos[at:at + 60])
+        assert torch.equal(ql[at:at + 60], a) and torch.equal(qr[at:at + 60], b)
+
+
 def test_tree_refuses_wrong_arguments():
     c = TU.case([3], [100], "tree", seed=33)
     ql, qr, cache = TU.tensors(c, seed=34)
@@ -297,15 +366,16 @@ def test_query_parity(T, strided):
     assert (np.abs(f64(qr)[keep] - ref) <= BF * np.abs(ref) + 2e-5 * pair).all()
 
 
-def test_query_equals_the_prolog():
+@pytest.mark.parametrize("B", [3, 100], ids=["few", "many"])
+def test_query_equals_the_prolog(B):
     import workloads as W
-    t = W.prolog_tensors(3, 2, 5)
-    c = W.sparse_cache([700, 64, 9000], 2, 5)
+    t = W.prolog_tensors(B, 2, 5)
+    c = W.sparse_cache([700, 64, 9000][:B] + [65 + 31 * i for i in range(B - 3)], 2, 5)
     d = {k: v.cuda() for k, v in t.items() if isinstance(v, torch.Tensor)}
     ql, qr, _ = mla.prolog(d["q_nope"], d["q_pe"], d["kv_latent"], d["k_pe"], d["w_uk"], d["kv_norm_weight"],
                            c["kv_cache"].cuda(), c["block_table"].cuda(), c["seq_lens"].cuda())
     pos = (c["seq_lens"][:, None] - 2 + torch.arange(2)).to(torch.int32).view(-1).cuda()
-    a, b, _ = mla.query(d["q_nope"].view(6, 128, 128), d["q_pe"].view(6, 128, 64), d["w_uk"], pos)
+    a, b, _ = mla.query(d["q_nope"].view(2 * B, 128, 128), d["q_pe"].view(2 * B, 128, 64), d["w_uk"], pos)
     assert torch.equal(a.view_as(ql), ql) and torch.equal(b.view_as(qr), qr)
 
 

@@ -42,7 +42,7 @@ constexpr int kMaxUnits = 96;   // units at most that whole rows are dealt to
 // Ranks compare 32-bit keys of a load or cost and an index below 256, so the loads of
 // the dealt waves stay below 2^23 (a total far beyond what fits one step).
 constexpr int64_t kMaxDealt = (int64_t)1 << 23;
-static_assert(kMaxUnits <= 256 && 2 * kMaxUnits <= kTreeThreads && kMaxUnits % 4 == 0, "rank keys");
+static_assert(kMaxUnits <= 256 && 4 * kMaxUnits <= kTreeThreads && kMaxUnits % 32 == 0, "rank keys");
 constexpr size_t kMaxTreeSmem = 200 * 1024;      // working set of the planner kernel
 
 // Pages of rows that have no work items (their row_nparts follow).
@@ -110,22 +110,10 @@ __device__ int64_t block_scan(int64_t v, int64_t *warp_sums) {
     if (lane == 31) warp_sums[warp] = v;
     __syncthreads();
     int64_t before = 0;
-    for (int w = 0; w < warp; ++w) before += warp_sums[w];
+#pragma unroll
+    for (int w = 0; w < kTreeThreads / 32; ++w) before += w < warp ? warp_sums[w] : 0;
     __syncthreads();
     return v + before;
-}
-
-// How many keys are below (kAbove: above) `mine`.
-template <bool kAbove>
-__device__ __forceinline__ int32_t rank_of(const uint32_t *keys, uint32_t mine) {
-    int32_t rank = 0;
-#pragma unroll
-    for (int v = 0; v < kMaxUnits / 4; ++v) {
-        const uint4 k = reinterpret_cast<const uint4 *>(keys)[v];
-        rank += kAbove ? (k.x > mine) + (k.y > mine) + (k.z > mine) + (k.w > mine)
-                       : (k.x < mine) + (k.y < mine) + (k.z < mine) + (k.w < mine);
-    }
-    return rank;
 }
 
 __global__ void __launch_bounds__(kTreeThreads, 1)
@@ -134,8 +122,8 @@ mla_tree_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__rest
                      int32_t max_pages, int32_t num_units) {
     __shared__ int64_t warp_sums[kTreeThreads / 32], warp_most[kTreeThreads / 32];
     __shared__ int64_t carry, carry_parts;
-    __shared__ __align__(16) uint32_t unit_key[kMaxUnits], wave_key[kMaxUnits];
-    __shared__ int32_t bad, special;
+    __shared__ __align__(16) uint32_t unit_key[kMaxUnits];
+    __shared__ int32_t bad, special, even_cap;   // even_cap: 0 for no even pieces
     extern __shared__ int64_t smem[];
     const int32_t R = tokens, U = num_units, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const PlanLayout L = make_layout(R, U, batch);
@@ -161,7 +149,7 @@ mla_tree_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__rest
 
     if (tid == 0) {
         carry = carry_parts = 0;
-        bad = special = 0;
+        bad = special = even_cap = 0;
     }
     for (int32_t r = tid; r < R; r += kTreeThreads) s_end[r] = kNoneUnused;
     for (int32_t u = tid; u < U; u += kTreeThreads) s_count[u] = 0;
@@ -255,34 +243,46 @@ mla_tree_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__rest
     // ---- whole rows: deal them in waves (not tried when one row alone is too long for it)
     bool whole = try_whole(U, longest, total, target);
     if (whole) {
-        // keys: a unit's by load, a row's by cost; all distinct within a wave, padded with keys that no rank counts
-        auto row_key = [&](int32_t r0, int32_t i) {
-            return r0 + i < R && i < U ? (uint32_t)row_cost(pages(r0 + i)) << 8 | (uint32_t)(255 - i) : 0u;
-        };
-        if (tid < kMaxUnits) {
-            unit_key[tid] = tid < U ? (uint32_t)tid : 0xffffffffu;
-            wave_key[tid] = row_key(0, tid);
+        // keys: a unit's by load, a row's by cost; all distinct within a wave.  First every row's
+        // rank in its wave, the longest first (the keys in s_row, the ranks in s_unit).
+        for (int32_t r = tid; r < R; r += kTreeThreads)
+            s_row[r] = (int32_t)((uint32_t)row_cost(pages(r)) << 8 | (uint32_t)(255 - r % U));
+        if (tid < kMaxUnits) unit_key[tid] = tid < U ? (uint32_t)tid : 0xffffffffu;
+        __syncthreads();
+        for (int32_t r = tid; r < R; r += kTreeThreads) {
+            const int32_t r0 = r / U * U, n = min(U, R - r0);
+            const uint32_t mine = (uint32_t)s_row[r];
+            int32_t rank = 0;
+#pragma unroll 8
+            for (int32_t j = 0; j < n; ++j) rank += (uint32_t)s_row[r0 + j] > mine;
+            s_unit[r] = rank;
         }
         __syncthreads();
         for (int32_t r0 = 0; r0 < R; r0 += U) {
-            const int32_t n = min(U, R - r0), i = tid - kMaxUnits;
-            // ranks: the first threads' units by load, the next ones' rows by cost, the longest first
-            if (tid < U) {
-                s_rank[rank_of<false>(unit_key, unit_key[tid])] = tid;
-            } else if (i >= 0 && i < n) {
-                s_unit[r0 + i] = rank_of<true>(wave_key, wave_key[i]);
+            // units by load: four threads each count a quarter of the keys
+            if (tid < 4 * kMaxUnits) {
+                const int32_t u = tid >> 2;
+                const uint32_t mine = unit_key[u];
+                int32_t rank = 0;
+#pragma unroll
+                for (int v = 0; v < kMaxUnits / 16; ++v) {
+                    const uint4 k = reinterpret_cast<const uint4 *>(unit_key)[v * 4 + (tid & 3)];
+                    rank += (k.x < mine) + (k.y < mine) + (k.z < mine) + (k.w < mine);
+                }
+                rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+                rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+                if ((tid & 3) == 0 && u < U) s_rank[rank] = u;
             }
             __syncthreads();
-            if (i >= 0 && i < n) {
-                const int32_t r = r0 + i, u = s_rank[s_unit[r]];
+            const int32_t r = r0 + tid;
+            if (tid < U && r < R) {
+                const int32_t u = s_rank[s_unit[r]];
                 s_unit[r] = u;
                 if (pages(r) > 0) {
+                    unit_key[u] += (uint32_t)s_row[r] & ~255u;
                     s_row[r] = s_count[u]++;
-                    unit_key[u] += wave_key[i] & ~255u;
                 }
             }
-            __syncthreads();
-            if (tid < kMaxUnits) wave_key[tid] = row_key(r0 + U, tid);
             __syncthreads();
         }
         uint32_t most = 0;
@@ -292,23 +292,26 @@ mla_tree_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__rest
     }
 
     // ---- even pieces: the smallest cap under which every piece has a unit of its own
-    bool even = !whole && R <= U && total > 0;
-    int32_t cap = 0;
-    if (even) {
-        int32_t lo = kEvenPages, hi = even_most(longest, target);   // every warp the same search
-        auto fits = [&](int32_t c) {
-            int32_t pieces = 0;
-            for (int32_t r = lane; r < R; r += 32) pieces += even_pieces(pages(r), c);
-            return __reduce_add_sync(0xffffffffu, pieces) <= U;
-        };
-        even = hi >= lo && fits(hi);
-        while (even && lo < hi) {
-            const int32_t mid = lo + (hi - lo) / 2;
-            if (fits(mid)) hi = mid;
-            else lo = mid + 1;
+    if (!whole && R <= U && total > 0) {
+        if (warp == 0) {
+            int32_t lo = kEvenPages, hi = even_most(longest, target);
+            auto fits = [&](int32_t c) {
+                int32_t pieces = 0;
+                for (int32_t r = lane; r < R; r += 32) pieces += even_pieces(pages(r), c);
+                return __reduce_add_sync(0xffffffffu, pieces) <= U;
+            };
+            const bool ok = hi >= lo && fits(hi);
+            while (ok && lo < hi) {
+                const int32_t mid = lo + (hi - lo) / 2;
+                if (fits(mid)) hi = mid;
+                else lo = mid + 1;
+            }
+            if (lane == 0) even_cap = ok ? lo : 0;
         }
-        cap = lo;
+        __syncthreads();
     }
+    const int32_t cap = even_cap;
+    const bool even = cap > 0;
 
     // an item's place in the schedule
     auto put = [&](int32_t at, int32_t unit, int32_t r, int32_t pg0, int32_t pg1, int32_t end, int32_t part,

@@ -12,7 +12,8 @@
 //    ties to the lower index).  Taken when its largest load is within 1/32 of
 //    what cutting would give.
 //  - Even pieces: with no more rows than units, every row in pieces of one size (two
-//    pages at least), as small as one piece per unit allows.  Taken by the same measure.
+//    pages at least), as small as one piece per unit allows.  Taken up to 1/12 above the
+//    cut load.
 //  - Cut rows: the rows lie on a cost line, every units-th row together (in token
 //    order when there are no more rows than units), and the line is cut into equal
 //    stretches as in mla_plan.cu (cut_row); a unit then runs its pieces in token order.
@@ -21,7 +22,8 @@
 // nodes over 4096 keys 1001 -> 957 us (whole rows), 268 nodes of 80 keys 52 -> 44,
 // 138 nodes of mixed lengths 118 -> 114 (cut rows).  Even pieces against cut rows (at least
 // four pages each): 8 nodes of 700 keys 21.3 -> 19.3, 16 of 1500 28.4 -> 25.3, one of 8192
-// 22.9 -> 20.8; 24 of 131072 697 against 683, which the measure leaves to cut rows.
+// 22.9 -> 20.8; 24 of 131072 in three pieces each 697 against 683 in a short burst, but 735
+// against 760 in a run of seconds under the power cap (DRAM reads a twelfth).
 //
 // One CTA; every choice is a function of the inputs alone, and the host twin
 // below makes the same ones.
@@ -88,9 +90,10 @@ MLA_HD bool keep_whole(int64_t max_load, int64_t target) {
 // Pieces of a row when pieces have `cap` pages at most, and the first page of piece i of k.
 constexpr int32_t kEvenPages = 2;
 MLA_HD int32_t even_pieces(int32_t pages, int32_t cap) { return pages > 0 ? (pages - 1) / cap + 1 : 0; }
-// The largest cap that even pieces are taken with (keep_whole of a unit's piece and its item cost).
+// The largest cap that even pieces are taken with: up to 1/12 above the cut line's load, since a
+// request's nodes then read the same pages at the same time.
 MLA_HD int32_t even_most(int64_t longest, int64_t target) {
-    const int64_t cap = target + kSplitPenalty + target / 32;
+    const int64_t cap = target + kSplitPenalty + target / 12;
     return (int32_t)(cap < longest ? cap : longest);
 }
 MLA_HD int32_t even_page(int32_t pages, int32_t i, int32_t k) { return (int32_t)((int64_t)pages * i / k); }

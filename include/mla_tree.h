@@ -155,7 +155,7 @@ mla_status mla_tree_decode_fp8(const mla_ragged *prob, const void *q_latent, con
  * expanded once per call and the nodes share it; without (NULL) each node expands
  * the pages again as it reads them, which costs about twice the time from a few
  * nodes per request on.  The results are equal bit for bit.  Concurrent calls need a
- * scratch each.  Batches of more than 65,535 cannot use one (MLA_ERR_CUDA).
+ * scratch each.  Batches of more than 65,535 cannot use one (MLA_ERR_UNSUPPORTED).
  */
 mla_status mla_tree_scratch_size(const mla_ragged *prob, size_t *bytes);
 

@@ -710,7 +710,8 @@ def query(q_nope, q_pe, w_uk, positions, *, rope_base: float = DEFAULT_ROPE_BASE
     import torch
     index = _index_of(q_nope, "q_nope", 3, torch.bfloat16)
     T = q_nope.shape[0]
-    args = (*_strided(q_nope, "q_nope", torch.bfloat16, (T, NUM_HEADS, D_NOPE), index), *_strided(q_pe, "q_pe", torch.bfloat16, (T, NUM_HEADS, D_ROPE), index),
+    args = (*_strided(q_nope, "q_nope", torch.bfloat16, (T, NUM_HEADS, D_NOPE), index),
+            *_strided(q_pe, "q_pe", torch.bfloat16, (T, NUM_HEADS, D_ROPE), index),
             _dense(w_uk, "w_uk", torch.bfloat16, (NUM_HEADS, D_NOPE, D_LATENT), index))
     pos = _dense(positions, "positions", torch.int32, (T,), index, 4)
     with _launch_on(index, stream, q_nope, q_pe, w_uk, positions, table, q_latent, q_rope, status):
@@ -775,7 +776,7 @@ def _append(kv_latent, k_pe, kv_norm_weight, kv_cache, block_table, seq_lens, to
         status = _status_word(status, index)
         prob = _Ragged(B, T, NUM_HEADS, PAGE_SIZE, width, 0)
         f = lib.mla_cache_append_fp8 if fp8 else lib.mla_cache_append
-        _check(f(ctypes.byref(prob), *lat, *pe, gamma, rms_eps, tab, pos, cache, kv_cache.shape[0], bt, sl, off,
+        _check(f(ctypes.byref(prob), *lat, *pe, gamma, float(rms_eps), tab, pos, cache, kv_cache.shape[0], bt, sl, off,
                  status.data_ptr(), _current_stream(index)),
                "mla_cache_append_fp8" if fp8 else "mla_cache_append")
     return status
@@ -823,7 +824,7 @@ def tree_plan(seq_lens, token_offsets, masks, *, max_pages_per_seq: int, workspa
     m = _dense(masks, "masks", torch.int64, (T,), index, 8)
     lib = load_library()
     with _launch_on(index, stream, seq_lens, token_offsets, masks, workspace):
-        prob = _Ragged(B, T, NUM_HEADS, PAGE_SIZE, max_pages_per_seq, 0)
+        prob = _ragged(B, T, max_pages_per_seq)
         if workspace is None:
             n = ctypes.c_size_t(0)
             _check(lib.mla_tree_workspace_size(ctypes.byref(prob), ctypes.byref(n)), "mla_tree_workspace_size")
@@ -892,7 +893,7 @@ def _tree_decode(p, q_latent, q_rope, kv_cache, block_table, scale, out, lse, st
         out = _out(out, "out", torch.bfloat16, (T, NUM_HEADS, D_LATENT), index)
         lse = _out(lse, "lse", torch.float32, (T, NUM_HEADS), index)
         prob = _Ragged(p.batch, T, NUM_HEADS, PAGE_SIZE, p.max_pages, MLA_FLAG_POW2_MAX if pow2_max else 0)
-        args = (ctypes.byref(prob), ql, qr, cache, kv_cache.shape[0], bt, scale, out.data_ptr(), lse.data_ptr(),
+        args = (ctypes.byref(prob), ql, qr, cache, kv_cache.shape[0], bt, float(scale), out.data_ptr(), lse.data_ptr(),
                 ws.data_ptr(), ws.numel())
         if not fp8:
             _check(lib.mla_tree_decode(*args, _current_stream(index)), "mla_tree_decode")

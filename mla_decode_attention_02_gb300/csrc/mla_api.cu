@@ -304,6 +304,7 @@ static mla_status tree_impl(const mla_ragged *prob, const void *q_latent, const 
     if (num_pages < 1 || num_pages > ((int64_t)1 << 31) - 1) return MLA_ERR_INVALID_ARG;
     if (!std::isfinite(scale) || !(scale > 0.f)) return MLA_ERR_INVALID_ARG;
     if (scratch && !aligned16(scratch)) return MLA_ERR_INVALID_ARG;
+    if (scratch && prob->batch > 65535) return MLA_ERR_UNSUPPORTED;   // one grid row per request
     if (scratch && scratch_bytes < mla::expanded_bytes(prob->batch, prob->max_pages_per_seq)) return MLA_ERR_WORKSPACE;
     if (workspace_bytes < mla::make_layout(prob->tokens, 1, prob->batch).total) return MLA_ERR_WORKSPACE;
     int32_t units = 0;

@@ -79,9 +79,7 @@ mla_tree_expand_kernel(const uint8_t *__restrict__ ws, const uint8_t *__restrict
 cudaError_t launch_expand(const void *ws, const void *kv_cache_fp8, int64_t num_pages, const int32_t *block_table,
                           void *expanded, int32_t batch, int32_t tokens, int32_t max_pages, int32_t num_units,
                           cudaStream_t stream) {
-    // about eight CTAs per SM over the requests (a grid's y is at most 65535: more requests than that
-    // would not fit the planner either way, having no tokens)
-    if (batch > 65535) return cudaErrorInvalidValue;
+    // about eight CTAs per SM over the requests (65535 at most: the caller checks)
     int32_t x = 8 * 2 * num_units / batch;
     x = x < 1 ? 1 : x > max_pages ? max_pages : x;
     cudaLaunchConfig_t cfg = {};

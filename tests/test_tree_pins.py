@@ -237,6 +237,7 @@ def test_entry_points_refuse_before_any_cuda_call():
     assert commit(stride=8 * 64 * 1152 + 8) == 1 and commit(stride=8 * 64 * 1152 - 16) == 1
     assert decode(scratch=A + 8, room=1 << 30, name="mla_tree_decode_fp8") == 1
     assert decode(scratch=A, room=2 * 4 * mla.EXPANDED_PAGE_BYTES - 1, name="mla_tree_decode_fp8") == 3
+    assert decode(prob=_ragged(batch=65536), scratch=A, room=1 << 40, name="mla_tree_decode_fp8") == 2
     n = ctypes.c_size_t(0)
     assert lib.mla_tree_scratch_size(_ref(_ragged()), ctypes.byref(n)) == 0 and n.value == 8 * mla.EXPANDED_PAGE_BYTES
     assert lib.mla_tree_scratch_size(_ref(_ragged()), None) == 1 and lib.mla_tree_scratch_size(None, ctypes.byref(n)) == 1

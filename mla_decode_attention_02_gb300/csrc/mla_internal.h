@@ -233,11 +233,6 @@ struct NoEmit {
 // Checks of a ragged problem that make no CUDA call (flags: those allowed).
 mla_status check_ragged(const mla_ragged *p, int32_t flags);
 
-// mla_query: up to this many tokens one CTA per tile quarter, in one wave (four fit an SM); beyond, the
-// persistent kernel.  Measured, one CTA each against persistent: 64 tokens 5.7 / 6.6 us, 80 6.1 / 6.7,
-// 96 8.9 / 7.2 (three fit an SM), 128 10.7 / 8.3, 384 24.7 / 19.8, 1537 85.0 / 58.7.
-constexpr int32_t kQuerySmall = 80;
-
 // Host-side argument checks of a decode call that make no CUDA call
 // (mla_api.cu); shared by mla_decode and the allocation-free entry point.
 mla_status check_decode_args(const mla_problem *prob, const void *q_latent, const void *q_rope,

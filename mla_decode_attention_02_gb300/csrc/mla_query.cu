@@ -5,14 +5,15 @@
 // A persistent kernel for more than a few token tiles.  An item is one 128-token
 // tile of one head and one half (256) of the latent columns; each CTA (one per
 // SM) runs the tiles of one head-half after another, so W_UK's half (64 KB)
-// stays in shared memory over them.  Per item the tile's q_nope
+// stays in shared memory over them while the next one loads beside it (with one
+// buffer 129 tokens took 11.5 us instead of 10.5, 512 24.8 instead of 21.6).  Per item the tile's q_nope
 // (32 KB, two stages) comes by TMA, eight tcgen05.mma (M=128, N=256, K=16) fill one
 // of two TMEM accumulators, and the epilogue of the previous item runs meanwhile:
 //   warp 0      loads and MMAs (one elected lane)
-//   warps 1-8   TMEM -> bf16 -> the warp's own 8 KB of swizzled staging -> 256-byte row pieces
+//   warps 1-8   TMEM -> bf16 -> the warp's own 4 KB of swizzled staging -> 128-byte row pieces
 //   warps 9-12  q_pe, apart from the items: whole tokens, a quarter of the heads at a time
 // Bound by memory: 384 bytes in and 1152 out per token and head (the outputs are
-// three quarters), against 2 x 128 x 512 flops: 1537 tokens in 58.7 us, 5.4 TB/s.  q_pe by
+// three quarters), against 2 x 128 x 512 flops: 1537 tokens in 59.6 us, 5.4 TB/s.  q_pe by
 // items (each CTA its head's share, angles anew for every head) had taken 79.8.  The small-tile kernel of mla_prolog.cu
 // (one CTA per item of a quarter) does few tokens in one wave; from a few tiles on its
 // CTAs spend their time on latency: each loads, multiplies and stores once.
@@ -41,6 +42,10 @@ mla_status launch_query_small(int32_t tokens, const void *q_nope, int64_t nope_t
 namespace {
 using namespace ptx;
 
+// Up to this many tokens one CTA per tile quarter, in one wave (four fit an SM); beyond, the
+// persistent kernel.  Measured, one CTA each against persistent: 32 tokens 5.1 / 5.9 us, 80 6.0 / 6.2,
+// 96 8.9 / 6.6 (three fit an SM), 384 24.7 / 17.9, 1537 85.0 / 59.6.
+constexpr int32_t kQuerySmall = 80;
 constexpr int kTile = 128;                      // tokens per item (MMA M)
 constexpr int kCols = 256;                      // latent columns per item (MMA N)
 constexpr int kHalves = kDl / kCols;
@@ -51,8 +56,8 @@ constexpr uint32_t kWBlk = kDimN * 128;         // one 64-column block of W_UK: 
 constexpr uint32_t kWBytes = kCols / 64 * kWBlk;        // 64 KB
 constexpr uint32_t kABlk = kTile * 128;         // one 64-dim block of q_nope
 constexpr uint32_t kABytes = kDimN / 64 * kABlk;        // 32 KB
-constexpr uint32_t kStageBytes = 32 * 256;      // a warp's staging: 32 rows x 128 columns
-constexpr uint32_t kOffA = kWBytes, kOffStage = kOffA + 2 * kABytes;
+constexpr uint32_t kStageBytes = 32 * 128;      // a warp's staging: 32 rows x 64 columns
+constexpr uint32_t kOffA = 2 * kWBytes, kOffStage = kOffA + 2 * kABytes;
 constexpr uint32_t kQuerySmem = kOffStage + kEpiWarps * kStageBytes + 1024;
 constexpr uint64_t kQueryWaitNs = 2000000000ull;
 static_assert(kQuerySmem <= 232448 - 1024, "shared memory budget");
@@ -100,14 +105,14 @@ __device__ __noinline__ void query_landed(uint32_t bar, uint32_t parity, int32_t
 
 __global__ void __launch_bounds__(kQueryThreads, 1) mla_query_kernel(const __grid_constant__ QueryParams P) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[10];
+    __shared__ __align__(8) uint64_t bars[11];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const uint32_t s_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
-    // barriers (b: stage or accumulator): A landed, A read by the MMAs, accumulator full, accumulator read; W landed; drain
-    enum { B_AFULL = 0, B_AFREE = 2, B_CFULL = 4, B_CFREE = 6, B_W = 8, B_DRAIN = 9 };
+    // barriers (two each): A landed, A read by the MMAs, accumulator full, accumulator read, W landed; then drain
+    enum { B_AFULL = 0, B_AFREE = 2, B_CFULL = 4, B_CFREE = 6, B_W = 8, B_DRAIN = 10 };
     if (threadIdx.x == 0) {
         abort_flag = 0;
         for (int b = 0; b < 2; ++b) {
@@ -115,8 +120,8 @@ __global__ void __launch_bounds__(kQueryThreads, 1) mla_query_kernel(const __gri
             mbar_init(bar(B_AFREE + b), 1);
             mbar_init(bar(B_CFULL + b), 1);
             mbar_init(bar(B_CFREE + b), kEpiWarps);
+            mbar_init(bar(B_W + b), 1);
         }
-        mbar_init(bar(B_W), 1);
         mbar_init(bar(B_DRAIN), 1);
         fence_mbar_init();
     }
@@ -132,7 +137,7 @@ __global__ void __launch_bounds__(kQueryThreads, 1) mla_query_kernel(const __gri
     pdl_launch_dependents();
 
     // Items: CTA c takes head-half c over all tiles, so that the CTAs move along the tokens together
-    // and write neighbouring rows at the same time (1537 tokens: 69.5 -> 58.6 us against one contiguous
+    // and write neighbouring rows at the same time (1537 tokens: 58.6 us against 69.5 with one contiguous
     // run of (head, half, tile) per CTA), then a share of the other head-halves' items.
     const int64_t rest = ((int64_t)kHeads * kHalves - gridDim.x) * P.tiles;
     const int64_t r0 = rest * blockIdx.x / gridDim.x - P.tiles;
@@ -145,8 +150,18 @@ __global__ void __launch_bounds__(kQueryThreads, 1) mla_query_kernel(const __gri
             prefetch_tmap(&P.tm_a);
             prefetch_tmap(&P.tm_w);
             constexpr uint32_t idesc = idesc_bf16(kTile, kCols, 0, 1);
-            uint32_t w_loads = 0;
-            int loaded = 0, last = -1;
+            // W_UK's halves in the order of the items: each is loaded when the one before it comes
+            // into use, and the MMAs that read the one before that are done
+            int w_loads = 0, w_used = 0;
+            auto load_w = [&](int i) {   // the half of item i
+                const int hh = head_half(i);
+                const uint32_t full = bar(B_W + (w_loads & 1));
+                mbar_arrive_expect_tx(full, kWBytes);
+                tma_load_4d(s_base + (w_loads & 1) * kWBytes, &P.tm_w, 0, 0, hh % kHalves * (kCols / 64), hh / kHalves,
+                            full);
+                ++w_loads;
+            };
+            int loaded = 0, next_w = 0;   // next_w: the first item of the next half
             bool ok = true;
             auto load_a = [&](int i) {
                 const uint32_t full = bar(B_AFULL + (i & 1));
@@ -155,20 +170,22 @@ __global__ void __launch_bounds__(kQueryThreads, 1) mla_query_kernel(const __gri
                             head_half(i) / kHalves, full);
                 loaded = i + 1;
             };
-            if (n > 0) load_a(0);
+            if (n > 0) {
+                load_w(0);
+                load_a(0);
+            }
             for (int i = 0; i < n && ok; ++i) {
                 // the next item's tile, once the MMAs of the item before this one have read its stage
                 if (i >= 1) ok = query_wait(bar(B_AFREE + ((i - 1) & 1)), ((i - 1) >> 1) & 1, &abort_flag, P.status);
                 if (!ok) break;
                 if (i + 1 < n) load_a(i + 1);
-                const int hh = head_half(i);
-                if (hh != last) {   // (every MMA that read the other weights is done: waited above)
-                    mbar_arrive_expect_tx(bar(B_W), kWBytes);
-                    tma_load_4d(s_base, &P.tm_w, 0, 0, hh % kHalves * (kCols / 64), hh / kHalves, bar(B_W));
-                    ++w_loads;
-                    last = hh;
-                    ok = query_wait(bar(B_W), (w_loads - 1) & 1, &abort_flag, P.status);
+                if (i == next_w) {   // (every MMA of the items before is done: waited above)
+                    next_w = i + P.tiles - tile_of(i);
+                    if (next_w < n) load_w(next_w);
+                    ok = query_wait(bar(B_W + (w_used & 1)), (w_used >> 1) & 1, &abort_flag, P.status);
+                    ++w_used;
                 }
+                const uint32_t s_w = s_base + ((w_used - 1) & 1) * kWBytes;
                 ok = ok && query_wait(bar(B_AFULL + (i & 1)), (i >> 1) & 1, &abort_flag, P.status) &&
                      (i < 2 || query_wait(bar(B_CFREE + (i & 1)), ((i >> 1) - 1) & 1, &abort_flag, P.status));
                 if (!ok) break;
@@ -177,14 +194,15 @@ __global__ void __launch_bounds__(kQueryThreads, 1) mla_query_kernel(const __gri
                 for (int ks = 0; ks < kDimN / 16; ++ks)
                     mma_ss(tmem + (i & 1) * kCols,
                            smem_desc(s_base + kOffA + (i & 1) * kABytes + (ks / 4) * kABlk + (ks % 4) * 32, 16, 1024, 2),
-                           smem_desc(s_base + ks * 2048, kWBlk, 1024, 2), idesc, ks > 0 ? 1u : 0u);
+                           smem_desc(s_w + ks * 2048, kWBlk, 1024, 2), idesc, ks > 0 ? 1u : 0u);
                 mma_commit(bar(B_AFREE + (i & 1)));
                 mma_commit(bar(B_CFULL + (i & 1)));
             }
             // every copy has landed and every MMA is done before the CTA gives its memory up
             for (int i = loaded > 2 ? loaded - 2 : 0; i < loaded; ++i)
                 query_landed(bar(B_AFULL + (i & 1)), (i >> 1) & 1, P.status);
-            if (w_loads) query_landed(bar(B_W), (w_loads - 1) & 1, P.status);
+            for (int w = w_loads > 2 ? w_loads - 2 : 0; w < w_loads; ++w)
+                query_landed(bar(B_W + (w & 1)), (w >> 1) & 1, P.status);
             mma_commit(bar(B_DRAIN));
             query_landed(bar(B_DRAIN), 0, P.status);
         }
@@ -200,39 +218,42 @@ __global__ void __launch_bounds__(kQueryThreads, 1) mla_query_kernel(const __gri
             const unsigned wanted = __ballot_sync(0xffffffffu, pos >= 0);
             if (!__all_sync(0xffffffffu, query_wait(bar(B_CFULL + (i & 1)), (i >> 1) & 1, &abort_flag, P.status))) break;
             tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint32_t r[32];
-                tmem_ld32(acc + (i & 1) * kCols + c * 32, r);
-                tmem_wait_ld();
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint32_t at = stage + lane * 256 + (((c * 4 + q) ^ (lane & 15)) << 4);
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at),
-                                 "r"(pack_bf16x2(__uint_as_float(r[8 * q]), __uint_as_float(r[8 * q + 1]))),
-                                 "r"(pack_bf16x2(__uint_as_float(r[8 * q + 2]), __uint_as_float(r[8 * q + 3]))),
-                                 "r"(pack_bf16x2(__uint_as_float(r[8 * q + 4]), __uint_as_float(r[8 * q + 5]))),
-                                 "r"(pack_bf16x2(__uint_as_float(r[8 * q + 6]), __uint_as_float(r[8 * q + 7])))
-                                 : "memory");
-                }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_CFREE + (i & 1)));
-            const int j = lane & 15;
+            const int j = lane & 7;
             __nv_bfloat16 *out = P.q_latent + ((size_t)tok0 * kHeads + hh / kHalves) * kDl + hh % kHalves * kCols +
                                  part * 128 + j * 8;
-#pragma unroll 8
-            for (int k = 0; k < 16; ++k) {
-                const int row = 2 * k + (lane >> 4);
-                uint4 v;
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                             : "r"(stage + row * 256 + ((j ^ (row & 15)) << 4))
-                             : "memory");
-                if (wanted >> row & 1) *reinterpret_cast<uint4 *>(out + (size_t)row * kHeads * kDl) = v;
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {   // 64 columns at a time
+#pragma unroll
+                for (int d = 0; d < 2; ++d) {
+                    uint32_t r[32];
+                    tmem_ld32(acc + (i & 1) * kCols + c * 64 + d * 32, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t at = stage + lane * 128 + (((d * 4 + q) ^ (lane & 7)) << 4);
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at),
+                                     "r"(pack_bf16x2(__uint_as_float(r[8 * q]), __uint_as_float(r[8 * q + 1]))),
+                                     "r"(pack_bf16x2(__uint_as_float(r[8 * q + 2]), __uint_as_float(r[8 * q + 3]))),
+                                     "r"(pack_bf16x2(__uint_as_float(r[8 * q + 4]), __uint_as_float(r[8 * q + 5]))),
+                                     "r"(pack_bf16x2(__uint_as_float(r[8 * q + 6]), __uint_as_float(r[8 * q + 7])))
+                                     : "memory");
+                    }
+                }
+                if (c == 1) tc_fence_before();
+                __syncwarp();
+                if (c == 1 && lane == 0) mbar_arrive(bar(B_CFREE + (i & 1)));
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {   // four rows' 128 bytes at a time
+                    const int row = 4 * k + (lane >> 3);
+                    uint4 v;
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                 : "r"(stage + row * 128 + ((j ^ (row & 7)) << 4))
+                                 : "memory");
+                    if (wanted >> row & 1) *reinterpret_cast<uint4 *>(out + c * 64 + (size_t)row * kHeads * kDl) = v;
+                }
+                __syncwarp();   // the staging is read before the next rows go in
             }
-            __syncwarp();   // the staging is read before the next item's rows go in
         }
     } else {
         // ---- q_pe: a unit is a token's 32 heads [32 (u % 4), +32), a warp's units a contiguous run.

@@ -97,6 +97,8 @@ mla_status mla_query(int32_t tokens, const void *q_nope, int64_t nope_token_stri
  *   kv_cache  [num_pages][64][576] bf16, or for mla_cache_append_fp8 [num_pages][64][656] bytes
  *             (mla_fp8.h); only the tokens' rows are written.  Distinct tokens must have distinct rows.
  * The fp8 row is quantised from the unrounded values, s = max |c_kv| / 448 of them (1 for a zero row).
+ * A latent that is not finite (NaN or infinities in kv_latent or the weight; a zero one with rms_eps = 0)
+ * gives a row that is not: NaN where the arithmetic makes it in bf16, NaN codes and a NaN scale in fp8.
  * A token whose slot is out of range (MLA_DEV_BAD_SEQ_LEN) or whose page is (MLA_DEV_BAD_PAGE) is
  * not written.  With bad offsets (MLA_DEV_BAD_OFFSETS) which tokens are written is unspecified, but
  * nothing outside the pool is.  MLA_TREE_MAX_NODES does not bound n_b here.

@@ -144,20 +144,28 @@ __global__ void __launch_bounds__(32 * kAppendWarps) mla_cache_append_kernel(con
         const float k0 = k.x * cs - k.y * sn, k1 = k.x * sn + k.y * cs;
         const size_t row = (size_t)page * kPage + slot % kPage;
         if constexpr (kFp8) {
-            float amax = 0.f;
+            // the row's maximum by its bits: a NaN's are above every number's, so one NaN is kept
+            uint32_t top = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fmaxf(fabsf(a[j]), fabsf(c[j])));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            for (int j = 0; j < 8; ++j)
+                top = max(top, max(__float_as_uint(fabsf(a[j])), __float_as_uint(fabsf(c[j]))));
+            const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, top));
             // The norm's factor cancels in c / s = 448 (x gamma) / max |x gamma|: both sides of the
-            // division are exact, so each code is the correctly rounded quotient's.  (s is 0 only if
-            // the norm overflowed: a zero row, as in bf16.)
+            // division are exact, so each code is the correctly rounded quotient's.  s is 0 for a zero
+            // row (all of x gamma, or a norm past fp32's range, as in bf16).  It is no finite number if
+            // the latent is none (NaN or infinities in x or gamma; 0 / 0 without eps): the row then holds
+            // NaN codes and a NaN scale, and spoils what sees it as such a bf16 row does.
             float s = __fdiv_rn(amax * inv, 448.f);
-            const bool zero = !(s > 0.f);
+            const bool lost = !(s < INFINITY), zero = s == 0.f;
             if (zero) s = 1.f;
+            if (lost) s = __int_as_float(0x7fffffff);
+            auto codes = [&](const float (&f)[8]) {
+                if (lost) return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+                return zero ? make_uint2(0, 0) : codes8(f, amax);
+            };
             uint8_t *dst = P.cache + row * MLA_FP8_ROW_BYTES;
-            reinterpret_cast<uint2 *>(dst)[lane] = zero ? make_uint2(0, 0) : codes8(a, amax);
-            reinterpret_cast<uint2 *>(dst)[lane + 32] = zero ? make_uint2(0, 0) : codes8(c, amax);
+            reinterpret_cast<uint2 *>(dst)[lane] = codes(a);
+            reinterpret_cast<uint2 *>(dst)[lane + 32] = codes(c);
             reinterpret_cast<uint32_t *>(dst + kDl)[lane] = pack_bf16x2(__fdiv_rn(k0, s), __fdiv_rn(k1, s));
             if (lane < 4) reinterpret_cast<uint32_t *>(dst + kDl + 2 * kDr)[lane] = lane == 0 ? __float_as_uint(s) : 0u;
         } else {

@@ -1,0 +1,109 @@
+"""The tree step where it can go wrong silently: values that are not finite, memory that is short or shared
+between streams, and every row of long calls (bounds as in test_gpu_tree.py)."""
+
+import numpy as np
+import pytest
+import torch
+
+import mla_decode_attention_02_gb300 as mla
+import oracle.tree as OT
+import tree_util as TU
+from test_gpu_tree import SCALE, check_rows, f64
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+
+# ---------------------------------------------------------------- latents that are not finite
+
+def _append(fp8, kv, gamma, cache, d, **kw):
+    f = mla.cache_append_fp8 if fp8 else mla.cache_append
+    return f(kv[:, :512], kv[:, 512:], gamma, cache, d["block_table"], d["seq_lens"], d["offsets"], **kw)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("at", ["one", "all"])
+def test_append_keeps_what_is_not_finite(fp8, value, at):
+    """A token whose latent is not finite spoils its own row and the outputs of the nodes that see it, no other."""
+    c = TU.case([6, 3], [70, 20], "self", seed=81)                 # every node sees its context and itself
+    ql, qr, cache = TU.tensors(c, seed=82, quiet=True)
+    g = torch.Generator().manual_seed(83)
+    kv = torch.randn(c["T"], 576, generator=g).to(BF16)
+    bad = [1, 4]
+    for t in bad:
+        kv[t, (slice(0, 512) if at == "all" else 37 * t)] = value
+    gamma = (1 + 0.1 * torch.randn(512, generator=g)).to(BF16).cuda()
+    d = TU.index_tensors(c)
+    cc = mla.quantize_cache_fp8(cache.cuda()) if fp8 else cache.cuda()
+    assert _append(fp8, kv.cuda(), gamma, cc, d).item() == 0
+    slots = {t: r for t, r, _ in OT.token_slots(c["block_table"], c["seq_lens"], c["offsets"])}
+    flat = cc.view(-1, cc.shape[-1])
+    if fp8:
+        codes = flat[:, :512].view(torch.float8_e4m3fn).float().cpu()
+        scale = flat[:, 640:644].contiguous().view(torch.float32)[:, 0].cpu()
+        for t in range(c["T"]):
+            assert torch.isnan(codes[slots[t]]).all().item() is (t in bad), t
+            assert torch.isnan(scale[slots[t]]).item() is (t in bad), t
+    else:
+        for t in range(c["T"]):
+            assert torch.isnan(flat[slots[t], :512].float()).any().item() is (t in bad), t
+    p = mla.tree_plan(d["seq_lens"], d["offsets"], d["masks"], max_pages_per_seq=d["block_table"].shape[1])
+    good = [t for t in range(c["T"]) if t not in bad]
+    rows = _rows64(cc)
+    ref = OT.tree_decode(ql, qr, rows, c["block_table"], c["seq_lens"], c["offsets"], c["masks"], scale=SCALE)
+    for more in ({"scratch": False}, {"scratch": None}) if fp8 else ({},):
+        f = mla.tree_decode_fp8 if fp8 else mla.tree_decode
+        o, lse = f(p, ql.cuda(), qr.cuda(), cc, d["block_table"], scale=SCALE, **more)
+        assert mla.check(p) == 0
+        assert torch.isnan(o[bad].float()).any(-1).all() and torch.isnan(lse[bad]).all()
+        check_rows(o[good], lse[good], tuple(x[good] for x in ref), slice(None))
+
+
+def _rows64(cache):
+    """fp64 rows of a cache of either kind, as a tensor of its shape."""
+    if cache.dtype != torch.uint8:
+        return cache.double().cpu()
+    code, rope = cache[..., :512].view(torch.float8_e4m3fn), cache[..., 512:640].view(BF16)
+    s = cache[..., 640:644].contiguous().view(torch.float32)
+    return (torch.cat([code.float(), rope.float()], -1).double() * s.double()).cpu()
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_append_of_zero_latents(fp8):
+    """A zero latent is a zero row with any eps > 0; with eps = 0 it is 0 / 0 in either cache.  Zero weights: a zero row."""
+    c = TU.case([3], [9], "none", seed=84)
+    d = TU.index_tensors(c)
+    kv = torch.randn(3, 576, generator=torch.Generator().manual_seed(85)).to(BF16)
+    kv[1, :512] = 0
+    ones, zeros = torch.ones(512, dtype=BF16, device="cuda"), torch.zeros(512, dtype=BF16, device="cuda")
+    at = [r for _, r, _ in OT.token_slots(c["block_table"], c["seq_lens"], c["offsets"])]
+    empty = torch.zeros(c["pages"], 64, 656 if fp8 else 576, dtype=torch.uint8 if fp8 else BF16, device="cuda")
+
+    def rows(gamma, eps):
+        cache = empty.clone()
+        assert _append(fp8, kv.cuda(), gamma, cache, d, rms_eps=eps).item() == 0
+        if fp8:
+            assert (cache.view(-1, 656)[at][:, 644:] == 0).all()
+        return _rows64(cache).view(-1, 576)[at]
+
+    r = rows(ones, 1e-6)
+    assert (r[1, :512] == 0).all() and torch.isfinite(r).all() and (r[0, :512] != 0).any()
+    assert (r[:, 512:] != 0).all()                                # the rotary part stays
+    r = rows(ones, 0.0)
+    assert torch.isnan(r[1, :512]).all() and torch.isfinite(r[[0, 2]]).all()
+    r = rows(zeros, 1e-6)
+    assert (r[:, :512] == 0).all() and (r[:, 512:] != 0).all()
+
+
+def test_fp8_append_of_a_weight_that_is_not_a_number():
+    c = TU.case([2], [5], "none", seed=86)
+    d = TU.index_tensors(c)
+    kv = torch.randn(2, 576, generator=torch.Generator().manual_seed(87)).to(BF16).cuda()
+    for rest in (1.0, 0.0):
+        gamma = torch.full((512,), rest, dtype=BF16, device="cuda")
+        gamma[300] = float("nan")
+        cache = torch.zeros(c["pages"], 64, 656, dtype=torch.uint8, device="cuda")
+        _append(True, kv, gamma, cache, d)
+        at = [r for _, r, _ in OT.token_slots(c["block_table"], c["seq_lens"], c["offsets"])]
+        assert torch.isnan(_rows64(cache).view(-1, 576)[at][:, 300]).all()

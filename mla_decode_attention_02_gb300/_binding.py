@@ -183,13 +183,28 @@ class Plan:
     max_pages: int
     workspace: object   # torch.uint8 CUDA tensor, owned by this Plan
     seq_lens: object    # the device seq_lens it was built from
+    home: object = None  # handle of the stream that the workspace was allocated on, if known
 
     def problem(self, flags: int = 0) -> _Problem:
         return _problem(self.batch, self.s_q, self.max_pages, flags)
 
 
+def _used_on(workspace, home, stream):
+    """A plan's workspace is about to be used on `stream` (a torch stream).
+
+    The plan owns it and may be dropped while that work is still queued: unless its memory
+    belongs to that stream already, the allocator is told, and gives it out again only after.
+    """
+    if home is None or stream.cuda_stream != home:
+        workspace.record_stream(stream)
+
+
 def plan(seq_lens, *, s_q: int, max_pages_per_seq: int, workspace=None, stream=None) -> Plan:
-    """Build the split-KV schedule on the device (``mla_decode_plan``)."""
+    """Build the split-KV schedule on the device (``mla_decode_plan``).
+
+    decode may run on another stream than the plan, ordered after it by an event; the plan may
+    be dropped as soon as its last decode is enqueued.
+    """
     import torch
     _req(seq_lens, "seq_lens", torch.int32, None, None)
     if seq_lens.dim() != 1:
@@ -197,14 +212,19 @@ def plan(seq_lens, *, s_q: int, max_pages_per_seq: int, workspace=None, stream=N
     batch = seq_lens.shape[0]
     with torch.cuda.device(seq_lens.device):
         need = workspace_size(batch, s_q, max_pages_per_seq)
+        here = torch.cuda.current_stream()
+        home = None
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=seq_lens.device)
+            home = here.cuda_stream
         _req(workspace, "workspace", torch.uint8, None, seq_lens.device)
         prob = _problem(batch, s_q, max_pages_per_seq)
+        s = here if stream is None else stream
+        _used_on(workspace, home, s)
         _check(load_library().mla_decode_plan(ctypes.byref(prob), seq_lens.data_ptr(),
                                               workspace.data_ptr(), workspace.numel(),
-                                              _stream_handle(stream)), "mla_decode_plan")
-    return Plan(batch, s_q, max_pages_per_seq, workspace, seq_lens)
+                                              _stream_handle(s)), "mla_decode_plan")
+    return Plan(batch, s_q, max_pages_per_seq, workspace, seq_lens, home)
 
 
 def decode(p: Plan, q_latent, q_rope, kv_cache, block_table, *, scale: float = DEFAULT_SCALE,
@@ -268,9 +288,11 @@ def _decode(p, q_latent, q_rope, kv_cache, block_table, scale, out, lse, stream,
     _req(out, "out", torch.bfloat16, (B, S, NUM_HEADS, D_LATENT), dev)
     _req(lse, "lse", torch.float32, (B, S, NUM_HEADS), dev)
     prob = p.problem(flags)
+    s = torch.cuda.current_stream() if stream is None else stream
+    _used_on(p.workspace, p.home, s)
     args = [ctypes.byref(prob), q_latent.data_ptr(), q_rope.data_ptr(), kv_cache.data_ptr(),
             kv_cache.shape[0], block_table.data_ptr(), float(scale), out.data_ptr(),
-            lse.data_ptr(), p.workspace.data_ptr(), p.workspace.numel(), _stream_handle(stream)]
+            lse.data_ptr(), p.workspace.data_ptr(), p.workspace.numel(), _stream_handle(s)]
     handles = None
     if events is not None:
         if len(events) != 3:
@@ -808,7 +830,7 @@ def tree_plan(seq_lens, token_offsets, masks, *, max_pages_per_seq: int, workspa
     b's nodes are rows token_offsets[b] .. token_offsets[b + 1] - 1 of the token arrays; at most
     64 each), masks [T] int64: bit j of a node's mask is set if it sees node j of its tree.  T may
     exceed token_offsets[B] (padding).  The plan serves every layer of the step; calls that share
-    it must be ordered.
+    it must be ordered (by one stream, or events), and it may be dropped once the last is enqueued.
     """
     if stream is None:
         r = (_host or _native()).tree_plan(seq_lens, token_offsets, masks, max_pages_per_seq, workspace)
@@ -831,6 +853,7 @@ def tree_plan(seq_lens, token_offsets, masks, *, max_pages_per_seq: int, workspa
             workspace = torch.empty(n.value, dtype=torch.uint8, device=seq_lens.device)
         nbytes = workspace.numel()
         ws = _dense(workspace, "workspace", torch.uint8, (nbytes,), index)
+        _used_on(workspace, None, torch.cuda.current_stream())
         _check(lib.mla_tree_plan(ctypes.byref(prob), sl, off, m, ws, nbytes, _current_stream(index)), "mla_tree_plan")
     return TreePlan(B, T, int(max_pages_per_seq), workspace)
 
@@ -892,6 +915,7 @@ def _tree_decode(p, q_latent, q_rope, kv_cache, block_table, scale, out, lse, st
                     None if isinstance(scratch, int) else scratch):
         out = _out(out, "out", torch.bfloat16, (T, NUM_HEADS, D_LATENT), index)
         lse = _out(lse, "lse", torch.float32, (T, NUM_HEADS), index)
+        _used_on(ws, None, torch.cuda.current_stream())
         prob = _Ragged(p.batch, T, NUM_HEADS, PAGE_SIZE, p.max_pages, MLA_FLAG_POW2_MAX if pow2_max else 0)
         args = (ctypes.byref(prob), ql, qr, cache, kv_cache.shape[0], bt, float(scale), out.data_ptr(), lse.data_ptr(),
                 ws.data_ptr(), ws.numel())

@@ -17,6 +17,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/zeros.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -107,6 +108,14 @@ bool here(const at::Tensor *t) {
 
 mla_stream_t stream_of(int dev) {
     return reinterpret_cast<mla_stream_t>(c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream());
+}
+
+// The plan owns its workspace and may be dropped while calls on this stream are still queued, and
+// it may have been made on another stream: the allocator gives the memory out again only after them.
+// (Nothing is done if it was allocated on this stream, or not by the allocator.)
+void used_here(const at::Tensor &workspace, int dev) {
+    c10::cuda::CUDACachingAllocator::recordStream(workspace.storage().data_ptr(),
+                                                  c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev));
 }
 
 PyObject *wrap(const at::Tensor &t) { return THPVariable_Wrap(t); }
@@ -212,6 +221,7 @@ PyObject *py_tree_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
             const at::Tensor *given = tensor(a[4]);
             if (!given || !is(*given, at::kByte, given->sizes(), dev, 16)) MLA_NOT_PLAIN;
             ws = *given;
+            used_here(ws, dev);
         }
         const mla_status rc = g_entry.tree_plan(&prob, (const int32_t *)sl, (const int32_t *)off, (const uint64_t *)m,
                                                 ws.data_ptr(), (size_t)ws.numel(), stream_of(dev));
@@ -253,6 +263,7 @@ PyObject *py_tree_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
             if (!given || !is(*given, at::kByte, given->sizes(), dev, 16)) MLA_NOT_PLAIN;
             scratch = *given;
         }
+        used_here(*ws, dev);
         const mla_ragged prob = {(int32_t)B, (int32_t)T, (int32_t)kH, (int32_t)kP, (int32_t)pages, (int32_t)flags};
         const float scale = (float)PyFloat_AS_DOUBLE(a[8]);
         const mla_status rc =

@@ -107,3 +107,77 @@ def test_fp8_append_of_a_weight_that_is_not_a_number():
         _append(True, kv, gamma, cache, d)
         at = [r for _, r, _ in OT.token_slots(c["block_table"], c["seq_lens"], c["offsets"])]
         assert torch.isnan(_rows64(cache).view(-1, 576)[at][:, 300]).all()
+
+
+# ---------------------------------------------------------------- memory
+
+def _wait_ms(ms):
+    torch.cuda._sleep(int(ms * 2e6))
+
+
+@pytest.mark.parametrize("kind", ["tree", "tree_fp8", "plain", "plain_fp8"])
+@pytest.mark.parametrize("way", ["current", "given", "home"])
+def test_a_dropped_plan_outlives_its_calls(kind, way):
+    """A plan made on one stream and used on another ("current": the current one, "given": stream=) keeps its
+    memory from reuse until that work is done; on one stream alone ("home") it is free for the next call at once."""
+    c = TU.case([2, 2, 2], [90, 700, 64], "chain", seed=95)
+    ql, qr, cache = TU.tensors(c, seed=96, quiet=True)
+    d = TU.index_tensors(c)
+    tree, fp8 = kind.startswith("tree"), kind.endswith("fp8")
+    kv = mla.quantize_cache_fp8(cache.cuda()) if fp8 else cache.cuda()
+    ql, qr = ql.cuda(), qr.cuda()
+    table = torch.where(d["block_table"] == 1 << 30, -1, d["block_table"])
+    if tree:
+        plan = lambda **kw: mla.tree_plan(d["seq_lens"], d["offsets"], d["masks"], max_pages_per_seq=table.shape[1], **kw)  # noqa: E731
+        f = mla.tree_decode_fp8 if fp8 else mla.tree_decode
+        run = lambda p, **kw: f(p, ql, qr, kv, table, scale=SCALE, **kw)  # noqa: E731
+    else:
+        plan = lambda **kw: mla.plan(d["seq_lens"], s_q=2, max_pages_per_seq=table.shape[1], **kw)  # noqa: E731
+        f = mla.decode_fp8 if fp8 else mla.decode
+        run = lambda p, **kw: f(p, ql.view(3, 2, 128, 512), qr.view(3, 2, 128, 64), kv, table, scale=SCALE, **kw)  # noqa: E731
+    want = [x.clone() for x in run(plan())]
+    here, there = torch.cuda.current_stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    if way == "current":            # made where `there` is current, used here
+        home, user, kw = there, here, {}
+    elif way == "given":            # made here, used on a stream that the call names
+        home, user, kw = here, there, {"stream": there}
+    else:
+        home, user, kw = here, here, {}
+    user.wait_stream(home)
+    with torch.cuda.stream(user):
+        _wait_ms(50)
+    with torch.cuda.stream(home):
+        p = plan()
+    user.wait_stream(home)
+    run(p, out=out, lse=lse, **kw)
+    at, n = p.workspace.data_ptr(), p.workspace.numel()
+    del p
+    assert not user.query()                                        # the call still waits
+    with torch.cuda.stream(home):
+        got = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    again = [t.data_ptr() for t in got]
+    assert not user.query()
+    torch.cuda.synchronize()
+    assert (at in again) is (way == "home")
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_a_decode_plan_made_on_a_given_stream():
+    """plan(stream=s): the workspace comes from the current stream's memory and is written on s."""
+    c = TU.case([2], [400], "chain", seed=97)
+    d = TU.index_tensors(c)
+    mla.plan(d["seq_lens"], s_q=2, max_pages_per_seq=d["block_table"].shape[1])
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        _wait_ms(50)
+    p = mla.plan(d["seq_lens"], s_q=2, max_pages_per_seq=d["block_table"].shape[1], stream=s)
+    at, n = p.workspace.data_ptr(), p.workspace.numel()
+    del p
+    got = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    assert not s.query() and at not in [t.data_ptr() for t in got]
+    torch.cuda.synchronize()

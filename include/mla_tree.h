@@ -155,9 +155,10 @@ mla_status mla_tree_decode_fp8(const mla_ragged *prob, const void *q_latent, con
  * entry's page as bf16 rows (batch * max_pages_per_seq * 73,984).  With scratch
  * (16-byte aligned, at least this size) each page that the trees read is
  * expanded once per call and the nodes share it; without (NULL) each node expands
- * the pages again as it reads them, which costs about twice the time from a few
- * nodes per request on.  The results are equal bit for bit.  Concurrent calls need a
- * scratch each.  Batches of more than 65,535 cannot use one (MLA_ERR_UNSUPPORTED).
+ * the pages again as it reads them: 64 requests of 4096 keys take 0.8 times as long
+ * with 1 node each, and 1.1, 1.4 and 1.6 times with 2, 4 and 8.  The results are equal
+ * bit for bit.  Concurrent calls need a scratch each.  Batches of more than 65,535
+ * cannot use one (MLA_ERR_UNSUPPORTED).
  */
 mla_status mla_tree_scratch_size(const mla_ragged *prob, size_t *bytes);
 

@@ -811,6 +811,7 @@ class TreePlan:
     tokens: int
     max_pages: int
     workspace: object   # torch.uint8 CUDA tensor, owned by this TreePlan
+    scratch_fits: bool = True   # until a tree_decode_fp8 finds no memory for its own scratch
 
     def problem(self, flags: int = 0) -> _Ragged:
         return _ragged(self.batch, self.tokens, self.max_pages, flags)
@@ -881,7 +882,8 @@ def tree_decode_fp8(p: TreePlan, q_latent, q_rope, kv_cache_fp8, block_table, *,
     scratch: where each page is expanded once for all nodes, a uint8 tensor of at least
     batch * max_pages * EXPANDED_PAGE_BYTES bytes, or False for none.  By default one is allocated
     for the call if the trees average two nodes or more and it takes no more than
-    EXPAND_LIMIT_BYTES.  The results are the same bit for bit.
+    EXPAND_LIMIT_BYTES; where there is no memory for it, this and the plan's later calls go
+    without.  The results are the same bit for bit.
     """
     return _tree_decode(p, q_latent, q_rope, kv_cache_fp8, block_table, scale, out, lse, stream, pow2_max, True,
                         scratch)
@@ -895,11 +897,16 @@ def _tree_decode(p, q_latent, q_rope, kv_cache, block_table, scale, out, lse, st
     T, ws = p.tokens, p.workspace
     if fp8 and scratch is None:
         need = p.batch * p.max_pages * EXPANDED_PAGE_BYTES
-        scratch = need if T >= 2 * p.batch and need <= EXPAND_LIMIT_BYTES and p.batch <= 65535 else False
+        wanted = p.scratch_fits and T >= 2 * p.batch and need <= EXPAND_LIMIT_BYTES and p.batch <= 65535
+        scratch = need if wanted else False
     if stream is None and scratch is not True:
-        r = (_host or _native()).tree_decode(p.batch, T, p.max_pages, ws, q_latent, q_rope, kv_cache, block_table, scale,
-                                             out, lse, MLA_FLAG_POW2_MAX if pow2_max else 0, fp8,
-                                             None if scratch is False else scratch)
+        call = (_host or _native()).tree_decode
+        args = (p.batch, T, p.max_pages, ws, q_latent, q_rope, kv_cache, block_table, scale, out, lse,
+                MLA_FLAG_POW2_MAX if pow2_max else 0, fp8)
+        r = call(*args, None if scratch is False else scratch)
+        if r is False:      # no memory for the scratch
+            p.scratch_fits = scratch = False
+            r = call(*args, None)
         if r is not None:
             return _made(r, "mla_tree_decode_fp8" if fp8 else "mla_tree_decode")
     import torch
@@ -923,7 +930,10 @@ def _tree_decode(p, q_latent, q_rope, kv_cache, block_table, scale, out, lse, st
             _check(lib.mla_tree_decode(*args, _current_stream(index)), "mla_tree_decode")
             return out, lse
         if scratch is not False and isinstance(scratch, int):
-            scratch = torch.empty(scratch, dtype=torch.uint8, device=ws.device)
+            try:
+                scratch = torch.empty(scratch, dtype=torch.uint8, device=ws.device)
+            except torch.OutOfMemoryError:
+                p.scratch_fits = scratch = False
         room = (None, 0)
         if scratch is not False:
             n = scratch.numel()

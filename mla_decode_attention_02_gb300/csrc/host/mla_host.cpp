@@ -231,7 +231,7 @@ PyObject *py_tree_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
 }
 
 // batch, tokens, max_pages, workspace, q_latent, q_rope, cache, block_table, scale, out, lse, flags, fp8, scratch
-// (None: none; a positive int: so many bytes are made) -> (out, lse)
+// (None: none; a positive int: so many bytes are made) -> (out, lse), or False, nothing done, if they could not be
 PyObject *py_tree_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
         const at::Tensor *ws = n == 14 ? tensor(a[3]) : nullptr;
@@ -257,7 +257,11 @@ PyObject *py_tree_decode(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (!output(a[9], at::kBFloat16, {T, kH, kL}, dev, &out) || !output(a[10], at::kFloat, {T, kH}, dev, &lse))
             MLA_NOT_PLAIN;
         if (PyLong_Check(a[13])) {
-            scratch = make({room}, at::kByte, dev);
+            try {
+                scratch = make({room}, at::kByte, dev);
+            } catch (const c10::OutOfMemoryError &) {
+                Py_RETURN_FALSE;
+            }
         } else if (a[13] != Py_None) {
             const at::Tensor *given = tensor(a[13]);
             if (!given || !is(*given, at::kByte, given->sizes(), dev, 16)) MLA_NOT_PLAIN;

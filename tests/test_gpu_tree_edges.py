@@ -181,3 +181,57 @@ def test_a_decode_plan_made_on_a_given_stream():
     got = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(3)]
     assert not s.query() and at not in [t.data_ptr() for t in got]
     torch.cuda.synchronize()
+
+@pytest.mark.parametrize("how", ["plain", "stream", "graph"])
+def test_fp8_trees_run_where_memory_has_no_room_for_their_scratch(how):
+    """A block table far wider than its requests asks for more scratch than there is: the same bits without it."""
+    c = TU.case([5, 9, 16, 2], [70, 300, 129, 64], "tree", seed=91, width=8192)
+    ql, qr, cache = TU.tensors(c, seed=92, quiet=True)
+    d = TU.index_tensors(c)
+    ql, qr, kv = ql.cuda(), qr.cuda(), mla.quantize_cache_fp8(cache.cuda())
+    plan = lambda: mla.tree_plan(d["seq_lens"], d["offsets"], d["masks"], max_pages_per_seq=8192)  # noqa: E731
+    p = plan()
+    want = mla.tree_decode_fp8(p, ql, qr, kv, d["block_table"], scale=SCALE, scratch=False)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    need = p.batch * p.max_pages * mla.EXPANDED_PAGE_BYTES
+    room = torch.cuda.memory_reserved() + (256 << 20)
+    assert (1 << 30) < need <= mla.EXPAND_LIMIT_BYTES
+    torch.cuda.set_per_process_memory_fraction(room / torch.cuda.get_device_properties(0).total_memory)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            torch.empty(need, dtype=torch.uint8, device="cuda")
+        s = torch.cuda.Stream() if how == "stream" else None
+        if s is not None:
+            s.wait_stream(torch.cuda.current_stream())
+        call = lambda p: mla.tree_decode_fp8(p, ql, qr, kv, d["block_table"], scale=SCALE, stream=s)  # noqa: E731
+        if how == "graph":
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                got = [call(plan()) for _ in range(2)]
+            graph.replay()
+        else:
+            got = [call(p) for _ in range(3)]
+        torch.cuda.synchronize()
+        for o, lse in got:
+            assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        if how != "graph":
+            assert mla.check(p) == 0
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    o, lse = mla.tree_decode_fp8(plan(), ql, qr, kv, d["block_table"], scale=SCALE)       # and with it
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_fp8_trees_behind_a_wide_table_with_scratch():
+    c = TU.case([3, 12], [200, 90], "tree", seed=93, width=300)
+    ql, qr, cache = TU.tensors(c, seed=94, quiet=True)
+    d = TU.index_tensors(c)
+    kv = mla.quantize_cache_fp8(cache.cuda())
+    p = mla.tree_plan(d["seq_lens"], d["offsets"], d["masks"], max_pages_per_seq=300)
+    room = torch.full((2 * 300 * mla.EXPANDED_PAGE_BYTES,), 0xFF, dtype=torch.uint8, device="cuda")
+    ref = OT.tree_decode(ql, qr, _rows64(kv), c["block_table"], c["seq_lens"], c["offsets"], c["masks"], scale=SCALE)
+    for scratch in (False, None, room):
+        o, lse = mla.tree_decode_fp8(p, ql.cuda(), qr.cuda(), kv, d["block_table"], scale=SCALE, scratch=scratch)
+        assert mla.check(p) == 0
+        check_rows(o, lse, ref, slice(None))

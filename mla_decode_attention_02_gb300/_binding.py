@@ -13,6 +13,7 @@ import contextlib
 import ctypes
 import os
 import threading
+import warnings
 from dataclasses import dataclass
 
 import numpy as np
@@ -530,21 +531,31 @@ _HOST_ENTRIES = ("mla_query", "mla_cache_append", "mla_cache_append_fp8", "mla_t
                  "mla_tree_decode", "mla_tree_decode_fp8", "mla_cache_commit")
 
 
+class _PythonOnly:
+    """Stands for the native marshalling where there is none: no call is the plain case."""
+
+    query = append = tree_plan = tree_decode = commit = staticmethod(lambda *a: None)
+
+
 def _native():
     """The marshalling of the tree step's calls in C++ (csrc/host/mla_host.cpp).
 
     Its functions take the plain case, dense CUDA tensors on the current device and stream, and
     return None for any other; the Python below then does the call or says what is wrong with it.
+    Without the module the Python does every call, 10-25 us slower each.
     """
     global _host
     if _host is None:
         lib = load_library()
-        if not os.path.exists(os.path.join(_HERE, "_mla_host.so")):
-            raise RuntimeError("_mla_host.so is missing: build the library first "
-                               "(python -m mla_decode_attention_02_gb300.build)")
         import torch  # noqa: F401  (its libraries are what the module links to)
 
-        from . import _mla_host
+        try:
+            from . import _mla_host
+        except ImportError as e:
+            warnings.warn(f"_mla_host.so does not load, calls are marshalled in Python: {e} "
+                          "(python -m mla_decode_attention_02_gb300.build)", stacklevel=3)
+            _host = _PythonOnly
+            return _host
         _mla_host.bind(*[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _HOST_ENTRIES])
         _host = _mla_host
     return _host

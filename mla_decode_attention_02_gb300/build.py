@@ -2,6 +2,9 @@
 beside it _mla_host.so, the argument marshalling of the tree step's calls on
 torch's tensor objects (host C++, against the installed torch's headers).
 
+The library needs neither torch nor Python's headers.  Where _mla_host.so cannot
+be built, a warning says why and the binding marshals those calls in Python.
+
 All translation units compile in parallel and link with -shared; the CUDA
 runtime links statically and the driver API is reached through
 cudaGetDriverEntryPoint.  At load time the library needs nothing but libc and
@@ -11,9 +14,11 @@ the NVIDIA driver: every kernel is this library's own.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -36,18 +41,25 @@ def sources() -> list[str]:
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
-def _deps() -> list[str]:
-    files = sources()
-    files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
-    files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
-    return files + [HOST_SRC]
+def _headers() -> list[str]:
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
+    return files + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
+
+
+def _newer(built: str, files: list[str]) -> bool:
+    return os.path.exists(built) and all(os.path.getmtime(f) <= os.path.getmtime(built) for f in files)
+
+
+def _library_up_to_date() -> bool:
+    return _newer(LIB_PATH, sources() + _headers())
+
+
+def _host_up_to_date() -> bool:
+    return importlib.util.find_spec("torch") is None or _newer(HOST_PATH, [HOST_SRC] + _headers())
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(HOST_PATH):
-        return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(HOST_PATH))
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    return _library_up_to_date() and _host_up_to_date()
 
 
 def _build_host() -> None:
@@ -69,9 +81,7 @@ def _build_host() -> None:
     os.replace(tmp, HOST_PATH)
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags: tuple = ()) -> str:
-    if not force and up_to_date():
-        return LIB_PATH
+def _build_library(ex: cf.Executor, verbose: bool, extra_flags: tuple) -> None:
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
     common = [nvcc, ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -89,16 +99,26 @@ def build(force: bool = False, verbose: bool = False, extra_flags: tuple = ()) -
             print(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
-        host = ex.submit(_build_host)
-        objs = list(ex.map(compile_one, sources()))
-        host.result()
+    objs = list(ex.map(compile_one, sources()))
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc, ARCH, "-shared", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+
+
+def build(force: bool = False, verbose: bool = False, extra_flags: tuple = ()) -> str:
+    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        torch_here = importlib.util.find_spec("torch") is not None
+        host = ex.submit(_build_host) if torch_here and (force or not _host_up_to_date()) else None
+        if force or not _library_up_to_date():
+            _build_library(ex, verbose, extra_flags)
+        if host is not None:
+            try:
+                host.result()
+            except Exception as e:
+                warnings.warn(f"_mla_host.so was not built (calls are marshalled in Python): {e}", stacklevel=2)
     return LIB_PATH
 
 

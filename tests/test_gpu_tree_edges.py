@@ -235,3 +235,42 @@ def test_fp8_trees_behind_a_wide_table_with_scratch():
         o, lse = mla.tree_decode_fp8(p, ql.cuda(), qr.cuda(), kv, d["block_table"], scale=SCALE, scratch=scratch)
         assert mla.check(p) == 0
         check_rows(o, lse, ref, slice(None))
+
+
+# ---------------------------------------------------------------- marshalling
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_calls_marshalled_in_python_are_the_same(fp8, monkeypatch):
+    import mla_decode_attention_02_gb300._binding as binding
+    c = TU.case([4, 7, 0, 9], [70, 200, 5, 64], "tree", seed=98, pad=1)
+    _, _, cache = TU.tensors(c, seed=99, quiet=True)
+    d = TU.index_tensors(c)
+    g = torch.Generator().manual_seed(100)
+    q = torch.randn(c["T"], 128, 192, generator=g).to(BF16).cuda()
+    kv = torch.randn(c["T"], 576, generator=g).to(BF16).cuda()
+    w = (torch.randn(128, 128, 512, generator=g) * 128 ** -0.5).to(BF16).cuda()
+    pos = torch.arange(c["T"], dtype=torch.int32, device="cuda")
+    paths = torch.tensor([[0, 3], [2, 5], [0, 0], [1, 8]], dtype=torch.int32, device="cuda")
+    plens = torch.tensor([2, 2, 0, 2], dtype=torch.int32, device="cuda")
+    start = mla.quantize_cache_fp8(cache.cuda()) if fp8 else cache.cuda()
+    decode = mla.tree_decode_fp8 if fp8 else mla.tree_decode
+    commit = mla.cache_commit_fp8 if fp8 else mla.cache_commit
+
+    def step():
+        cc = start.clone()
+        ql, qr, s0 = mla.query(q[..., :128], q[..., 128:], w, pos)
+        s1 = _append(fp8, kv, torch.ones(512, dtype=BF16, device="cuda"), cc, d, positions=pos)
+        p = mla.tree_plan(d["seq_lens"], d["offsets"], d["masks"], max_pages_per_seq=d["block_table"].shape[1])
+        n = int(c["offsets"][-1])
+        o, lse = (x[:n] for x in decode(p, ql, qr, cc, d["block_table"], scale=SCALE))
+        held = cc.clone()
+        new, s2 = commit(cc, d["block_table"], d["seq_lens"], d["offsets"], paths, plens)
+        assert mla.check(p) == 0
+        return ql, qr, o, lse, held, cc, new, s0, s1, s2
+
+    assert type(binding._native()) is not type                    # the native module, not its stand-in
+    native = step()
+    monkeypatch.setattr(binding, "_host", binding._PythonOnly)
+    for a, b in zip(native, step()):
+        assert a.dtype == b.dtype and torch.equal(a.view(torch.uint8) if a.is_contiguous() else a, b.view(torch.uint8) if b.is_contiguous() else b)
+    assert all(s.item() == 0 for s in native[-3:])

@@ -547,18 +547,35 @@ def _native():
     global _host
     if _host is None:
         lib = load_library()
-        import torch  # noqa: F401  (its libraries are what the module links to)
-
         try:
-            from . import _mla_host
+            module = _load_host()
         except ImportError as e:
-            warnings.warn(f"_mla_host.so does not load, calls are marshalled in Python: {e} "
-                          "(python -m mla_decode_attention_02_gb300.build)", stacklevel=3)
+            warnings.warn(f"calls are marshalled in Python: {e} (python -m mla_decode_attention_02_gb300.build)",
+                          stacklevel=3)
             _host = _PythonOnly
             return _host
-        _mla_host.bind(*[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _HOST_ENTRIES])
-        _host = _mla_host
+        module.bind(*[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _HOST_ENTRIES])
+        _host = module
     return _host
+
+
+def _load_host():
+    """The host module built for this Python and this torch; ImportError if there is none."""
+    import importlib.machinery
+    import importlib.util
+
+    import torch  # noqa: F401  (its libraries are what the module links to)
+
+    from .build import host_path
+    path = host_path()
+    if not os.path.exists(path):
+        raise ImportError(f"{os.path.basename(path)} is missing")
+    name = __package__ + "._mla_host"
+    spec = importlib.util.spec_from_file_location(name, path,
+                                                  loader=importlib.machinery.ExtensionFileLoader(name, path))
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
 
 
 def _made(r, what):

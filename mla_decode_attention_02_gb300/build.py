@@ -1,8 +1,9 @@
 """Build the CUDA library libmla_decode.so in-tree with nvcc (sm_103a only), and
-beside it _mla_host.so, the argument marshalling of the tree step's calls on
-torch's tensor objects (host C++, against the installed torch's headers).
+beside it _mla_host.<tag>.so, the argument marshalling of the tree step's calls
+on torch's tensor objects (host C++, against the installed torch's headers; the
+tag names the Python ABI and the torch that it fits, and no other loads it).
 
-The library needs neither torch nor Python's headers.  Where _mla_host.so cannot
+The library needs neither torch nor Python's headers.  Where the host module cannot
 be built, a warning says why and the binding marshals those calls in Python.
 
 All translation units compile in parallel and link with -shared; the CUDA
@@ -26,7 +27,6 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libmla_decode.so")
 HOST_SRC = os.path.join(CSRC, "host", "mla_host.cpp")
-HOST_PATH = os.path.join(HERE, "_mla_host.so")
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -35,6 +35,15 @@ def _nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libmla_decode.so")
+
+
+def host_path() -> str:
+    """The host module that fits this Python and the installed torch (both lay out what it reads)."""
+    import sysconfig
+
+    import torch
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return os.path.join(HERE, f"_mla_host.{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}-{abi}.so")
 
 
 def sources() -> list[str]:
@@ -55,7 +64,7 @@ def _library_up_to_date() -> bool:
 
 
 def _host_up_to_date() -> bool:
-    return importlib.util.find_spec("torch") is None or _newer(HOST_PATH, [HOST_SRC] + _headers())
+    return importlib.util.find_spec("torch") is None or _newer(host_path(), [HOST_SRC] + _headers())
 
 
 def up_to_date() -> bool:
@@ -70,7 +79,8 @@ def _build_host() -> None:
     cuda = os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")
     inc = [INCLUDE, os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
            sysconfig.get_paths()["include"], cuda]
-    tmp = HOST_PATH + f".tmp{os.getpid()}"
+    path = host_path()
+    tmp = path + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *[x for d in inc for x in ("-isystem" if d != INCLUDE else "-I", d)], HOST_SRC, "-o", tmp,
@@ -78,7 +88,7 @@ def _build_host() -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {HOST_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, HOST_PATH)
+    os.replace(tmp, path)
 
 
 def _build_library(ex: cf.Executor, verbose: bool, extra_flags: tuple) -> None:
@@ -118,7 +128,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: tuple = ()) -
             try:
                 host.result()
             except Exception as e:
-                warnings.warn(f"_mla_host.so was not built (calls are marshalled in Python): {e}", stacklevel=2)
+                warnings.warn(f"the host module was not built (calls are marshalled in Python): {e}", stacklevel=2)
     return LIB_PATH
 
 

@@ -48,10 +48,8 @@ def test_a_source_that_does_not_compile_is_an_error(small):
 
 def test_calls_without_the_native_marshalling(monkeypatch):
     """The Python checks take every call (here: refuse it), after one warning."""
-    import sys
     monkeypatch.setattr(binding, "_host", None)
-    monkeypatch.delattr(mla, "_mla_host", raising=False)
-    monkeypatch.setitem(sys.modules, "mla_decode_attention_02_gb300._mla_host", None)
+    monkeypatch.setattr(binding, "_load_host", lambda: exec("raise ImportError('none here')"))
     cpu = torch.zeros(4, 128, 192, dtype=torch.bfloat16)
     with pytest.warns(UserWarning, match="marshalled in Python"):
         with pytest.raises(ValueError, match="CUDA"):
@@ -61,3 +59,15 @@ def test_calls_without_the_native_marshalling(monkeypatch):
                  lambda: mla.cache_commit(None, torch.zeros(1, 1, dtype=torch.int32), None, None, None, None)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_a_host_module_of_another_torch_is_not_used(monkeypatch):
+    """Its name carries the torch and the Python ABI that it was built for: another's is neither up to date nor loaded."""
+    assert B.up_to_date() and binding._load_host() is not None
+    monkeypatch.setattr(torch, "__version__", "1.0.0+other")
+    assert not B.up_to_date()
+    with pytest.raises(ImportError, match="1.0.0"):
+        binding._load_host()
+    monkeypatch.setattr(binding, "_host", None)
+    with pytest.warns(UserWarning, match="1.0.0"):
+        assert binding._native() is binding._PythonOnly

@@ -927,7 +927,9 @@ def _tree_decode(p, q_latent, q_rope, kv_cache, block_table, scale, out, lse, st
         need = p.batch * p.max_pages * EXPANDED_PAGE_BYTES
         wanted = p.scratch_fits and T >= 2 * p.batch and need <= EXPAND_LIMIT_BYTES and p.batch <= 65535
         scratch = need if wanted else False
-    if stream is None and scratch is not True:
+    elif scratch is not None and scratch is not False and not hasattr(scratch, "data_ptr"):
+        raise TypeError("scratch must be a torch.Tensor, False or None")
+    if stream is None:
         call = (_host or _native()).tree_decode
         args = (p.batch, T, p.max_pages, ws, q_latent, q_rope, kv_cache, block_table, scale, out, lse,
                 MLA_FLAG_POW2_MAX if pow2_max else 0, fp8)
@@ -943,8 +945,6 @@ def _tree_decode(p, q_latent, q_rope, kv_cache, block_table, scale, out, lse, st
     qr = _dense(q_rope, "q_rope", torch.bfloat16, (T, NUM_HEADS, D_ROPE), index)
     cache = _cache_ptr(kv_cache, fp8, index)
     bt = _dense(block_table, "block_table", torch.int32, (p.batch, p.max_pages), index, 4)
-    if scratch is not False and (scratch is True or not isinstance(scratch, (int, torch.Tensor))):
-        raise TypeError("scratch must be a torch.Tensor, False or None")
     lib = load_library()
     with _launch_on(index, stream, ws, q_latent, q_rope, kv_cache, block_table, out, lse,
                     None if isinstance(scratch, int) else scratch):

@@ -277,3 +277,13 @@ def test_native_marshalling_leaves_what_is_not_plain():
         h.bind(1)
     with pytest.raises(ValueError):
         h.bind(*[0] * len(binding._HOST_ENTRIES))
+
+
+def test_scratch_is_a_tensor_or_nothing():
+    """A number of bytes is no scratch (0 ran without one, others were allocated)."""
+    p = mla.TreePlan(1, 2, 4, torch.zeros(64, dtype=torch.uint8))
+    for bad in (0, 1, 1 << 20, True, "room", [1]):
+        with pytest.raises(TypeError, match="scratch"):
+            mla.tree_decode_fp8(p, None, None, None, None, scratch=bad)
+    with pytest.raises(TypeError, match="q_latent"):
+        mla.tree_decode_fp8(p, None, None, None, None, scratch=False)

@@ -601,8 +601,8 @@ def _launch_on(index, stream, *tensors):
         return _HERE_ALREADY if torch.cuda.current_device() == index else torch.cuda.device(index)
     if stream.device.index != index:
         raise ValueError(f"stream must be one of cuda:{index}, the tensors' device")
-    for t in tensors:
-        if t is not None and t is not False:
+    for t in tensors:   # (what is no CUDA tensor is refused, or not looked at, later)
+        if isinstance(t, torch.Tensor) and t.is_cuda:
             t.record_stream(stream)
     return torch.cuda.stream(stream)
 
@@ -946,8 +946,7 @@ def _tree_decode(p, q_latent, q_rope, kv_cache, block_table, scale, out, lse, st
     cache = _cache_ptr(kv_cache, fp8, index)
     bt = _dense(block_table, "block_table", torch.int32, (p.batch, p.max_pages), index, 4)
     lib = load_library()
-    with _launch_on(index, stream, ws, q_latent, q_rope, kv_cache, block_table, out, lse,
-                    None if isinstance(scratch, int) else scratch):
+    with _launch_on(index, stream, ws, q_latent, q_rope, kv_cache, block_table, out, lse, scratch):
         out = _out(out, "out", torch.bfloat16, (T, NUM_HEADS, D_LATENT), index)
         lse = _out(lse, "lse", torch.float32, (T, NUM_HEADS), index)
         _used_on(ws, None, torch.cuda.current_stream())

@@ -287,3 +287,14 @@ def test_scratch_is_a_tensor_or_nothing():
             mla.tree_decode_fp8(p, None, None, None, None, scratch=bad)
     with pytest.raises(TypeError, match="q_latent"):
         mla.tree_decode_fp8(p, None, None, None, None, scratch=False)
+
+
+def test_arguments_of_no_device_on_a_given_stream():
+    """What is no CUDA tensor is not recorded on the stream: the argument's own check names it."""
+    class Stream:
+        device = torch.device("cuda", 0)
+        cuda_stream = 0
+    cpu = torch.zeros(4)
+    assert binding._launch_on(0, Stream(), cpu, None, False, "text", 7) is not None
+    with pytest.raises(ValueError, match="cuda:1"):
+        binding._launch_on(1, Stream(), cpu)

@@ -702,6 +702,12 @@ def _out(t, name, dtype, shape, index):
     return t
 
 
+def _bytes(t, name, index):
+    """Address and size of the caller's bytes, of any shape."""
+    import torch
+    return _dense(t, name, torch.uint8, getattr(t, "shape", None), index), t.numel()
+
+
 def _status_word(status, index):
     import torch
     if status is None:
@@ -880,8 +886,7 @@ def tree_plan(seq_lens, token_offsets, masks, *, max_pages_per_seq: int, workspa
             n = ctypes.c_size_t(0)
             _check(lib.mla_tree_workspace_size(ctypes.byref(prob), ctypes.byref(n)), "mla_tree_workspace_size")
             workspace = torch.empty(n.value, dtype=torch.uint8, device=seq_lens.device)
-        nbytes = workspace.numel()
-        ws = _dense(workspace, "workspace", torch.uint8, (nbytes,), index)
+        ws, nbytes = _bytes(workspace, "workspace", index)
         _used_on(workspace, None, torch.cuda.current_stream())
         _check(lib.mla_tree_plan(ctypes.byref(prob), sl, off, m, ws, nbytes, _current_stream(index)), "mla_tree_plan")
     return TreePlan(B, T, int(max_pages_per_seq), workspace)
@@ -963,8 +968,7 @@ def _tree_decode(p, q_latent, q_rope, kv_cache, block_table, scale, out, lse, st
                 p.scratch_fits = scratch = False
         room = (None, 0)
         if scratch is not False:
-            n = scratch.numel()
-            room = (_dense(scratch, "scratch", torch.uint8, (n,), index), n)
+            room = _bytes(scratch, "scratch", index)
         _check(lib.mla_tree_decode_fp8(*args, *room, _current_stream(index)), "mla_tree_decode_fp8")
     return out, lse
 

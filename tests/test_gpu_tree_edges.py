@@ -8,7 +8,7 @@ import torch
 import mla_decode_attention_02_gb300 as mla
 import oracle.tree as OT
 import tree_util as TU
-from test_gpu_tree import SCALE, check_rows, f64
+from test_gpu_tree import BF, SCALE, check_rows, f64
 
 pytestmark = pytest.mark.gpu
 BF16 = torch.bfloat16
@@ -274,3 +274,30 @@ def test_calls_marshalled_in_python_are_the_same(fp8, monkeypatch):
     for a, b in zip(native, step()):
         assert a.dtype == b.dtype and torch.equal(a.view(torch.uint8) if a.is_contiguous() else a, b.view(torch.uint8) if b.is_contiguous() else b)
     assert all(s.item() == 0 for s in native[-3:])
+
+
+def test_bytes_of_any_shape_on_a_given_stream():
+    """Workspace and scratch are bytes: their shape does not matter, with stream= as without."""
+    c = TU.case([5, 9], [70, 300], "tree", seed=101)
+    ql, qr, cache = TU.tensors(c, seed=102, quiet=True)
+    d = TU.index_tensors(c)
+    width = d["block_table"].shape[1]
+    kv, qlc, qrc = mla.quantize_cache_fp8(cache.cuda()), ql.cuda(), qr.cuda()
+    n = (mla.tree_workspace_size(2, c["T"], width) + 255) // 256
+    room = 2 * width * mla.EXPANDED_PAGE_BYTES // 64
+    s = torch.cuda.Stream()
+    got = []
+    for stream in (None, s):
+        ws, scratch = (torch.empty(k, dtype=torch.uint8, device="cuda") for k in ((n, 16, 16), (room, 64)))
+        s.wait_stream(torch.cuda.current_stream())
+        p = mla.tree_plan(d["seq_lens"], d["offsets"], d["masks"], max_pages_per_seq=width, workspace=ws, stream=stream)
+        got.append(mla.tree_decode_fp8(p, qlc, qrc, kv, d["block_table"], scale=SCALE, scratch=scratch, stream=stream))
+        torch.cuda.synchronize()
+        assert mla.check(p) == 0
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    with pytest.raises(TypeError, match="workspace"):
+        mla.tree_plan(d["seq_lens"], d["offsets"], d["masks"], max_pages_per_seq=width, workspace=[1], stream=s)
+    with pytest.raises(ValueError, match="table"):
+        mla.query(torch.zeros(1, 128, 128, dtype=BF16, device="cuda"), torch.zeros(1, 128, 64, dtype=BF16, device="cuda"),
+                  torch.zeros(128, 128, 512, dtype=BF16, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda"),
+                  table=torch.zeros(64), stream=s)

@@ -301,3 +301,56 @@ def test_bytes_of_any_shape_on_a_given_stream():
         mla.query(torch.zeros(1, 128, 128, dtype=BF16, device="cuda"), torch.zeros(1, 128, 64, dtype=BF16, device="cuda"),
                   torch.zeros(128, 128, 512, dtype=BF16, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda"),
                   table=torch.zeros(64), stream=s)
+
+
+# ---------------------------------------------------------------- every row of long calls
+
+@pytest.mark.parametrize("T", [81, 1537, 2049, 4097, 33000])
+def test_every_row_of_many_queries(T):
+    """The persistent kernel's rows, all tiles of all its CTAs, are those of calls of 80 tokens bit for bit."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    q = torch.randn(T, 128, 192, generator=g, device="cuda", dtype=BF16)
+    w = torch.randn(128, 128, 512, generator=g, device="cuda", dtype=BF16) * 128 ** -0.5
+    pos = torch.randint(0, 1 << 20, (T,), generator=g, device="cuda", dtype=torch.int32)
+    pos[::7] = -1                                                  # left out, in every tile
+    ql = torch.full((T, 128, 512), 7.0, dtype=BF16, device="cuda")
+    qr = torch.full((T, 128, 64), 7.0, dtype=BF16, device="cuda")
+    for _ in range(2):                                             # the second over the first one's rows
+        _, _, st = mla.query(q[..., :128], q[..., 128:], w, pos, q_latent=ql, q_rope=qr)
+        assert st.item() == 0
+    assert (ql[::7] == 7).all() and (qr[::7] == 7).all()
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for at in range(0, T, 80):
+        few = slice(at, min(at + 80, T))
+        a, b, _ = mla.query(q[few, :, :128], q[few, :, 128:], w, pos[few])
+        keep = pos[few] >= 0
+        wrong += (ql[few] != a).flatten(1).any(1).logical_and(keep).sum()
+        wrong += (qr[few] != b).flatten(1).any(1).logical_and(keep).sum()
+    assert wrong.item() == 0
+
+
+# ---------------------------------------------------------------- the step's value projection
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_the_value_projection_of_a_tree(fp8):
+    """Heads of a drafted tree's attention, projected: against fp64 from the outputs, and from the cache itself."""
+    import oracle.epilog as OE
+    c = TU.case([7, 12, 1], [90, 400, 64], "tree", seed=103)
+    ql, qr, cache = TU.tensors(c, seed=104, quiet=True)
+    d = TU.index_tensors(c)
+    kv = mla.quantize_cache_fp8(cache.cuda()) if fp8 else cache.cuda()
+    w = (torch.randn(128, 128, 512, generator=torch.Generator().manual_seed(105)) * 512 ** -0.5).to(BF16)
+    p = mla.tree_plan(d["seq_lens"], d["offsets"], d["masks"], max_pages_per_seq=d["block_table"].shape[1])
+    f = mla.tree_decode_fp8 if fp8 else mla.tree_decode
+    o, _ = f(p, ql.cuda(), qr.cuda(), kv, d["block_table"], scale=SCALE)
+    o_v, st = mla.epilog_uv(o.view(c["T"], 1, 128, 512), w.cuda())
+    assert st.item() == 0 and mla.check(p) == 0
+    got = f64(o_v).reshape(c["T"], 128, 128)
+    # one bf16 rounding and 512 fp32 products and sums
+    ref, size = OE.uv_project(o, w), OE.uv_project(np.abs(f64(o)), np.abs(f64(w)))
+    near = BF * np.abs(ref) + 512 * 2.0 ** -24 * size + 1e-6
+    assert (np.abs(got - ref) <= near).all()
+    # and the attention's own bound (test_gpu_tree.py) carried through the projection
+    want, _, spread = OT.tree_decode(ql, qr, _rows64(kv), c["block_table"], c["seq_lens"], c["offsets"], c["masks"], scale=SCALE)
+    far = OE.uv_project((2 * BF + 2.4e-3) * spread + BF * np.abs(want) + 1e-6, np.abs(f64(w)))
+    assert (np.abs(got - OE.uv_project(want, w)) <= near + far).all()

@@ -53,6 +53,11 @@ constexpr int kItemCost = 7;
 constexpr int kMinSplitPages = 4;
 constexpr int kSplitPenalty = 8;
 
+// mla_query: up to this many tokens one CTA per tile quarter, in one wave (four fit an SM); beyond, the
+// persistent kernel.  Measured, one CTA each against persistent: 32 tokens 5.1 / 5.9 us, 80 6.0 / 6.2,
+// 96 8.9 / 6.6 (three fit an SM), 384 24.7 / 17.9, 1537 85.0 / 59.6.
+constexpr int32_t kQuerySmall = 80;
+
 struct PlanHeader {  // 64 bytes at workspace offset 0
     uint32_t magic;
     int32_t batch, s_q, max_pages;

@@ -461,15 +461,15 @@ extern "C" mla_status mla_prolog(const mla_problem *prob, const void *q_nope, co
 
 namespace mla {
 
-// mla_query for few tokens (its arguments are checked): one CTA per (head, token tile, column quarter).
+// mla_query for up to kQuerySmall tokens, one tile (its arguments are checked): one CTA per (head, column quarter).
 mla_status launch_query_small(int32_t tokens, const void *q_nope, int64_t nope_token_stride, int64_t nope_head_stride,
                               const void *q_pe, int64_t pe_token_stride, int64_t pe_head_stride, const void *w_uk,
                               const float *rope_table, const int32_t *positions, void *q_latent, void *q_rope,
                               int32_t *device_status, mla_stream_t stream) {
-    const int64_t ctas = ((int64_t)tokens + kBM - 1) / kBM * kHeads * kNParts;
+    static_assert(kQuerySmall <= kBM, "one token tile");
     if (prepare_prolog() != cudaSuccess) return MLA_ERR_CUDA;
     PrologParams p{};
-    p.a_rows = tokens >= kBM ? kBM : (tokens + 7) / 8 * 8;
+    p.a_rows = (tokens + 7) / 8 * 8;
     if (!encode_bf16_4d(&p.tm_a, q_nope, (cuuint64_t)tokens, kDn / 64, kHeads, (cuuint64_t)nope_token_stride * 2, 128,
                         (cuuint64_t)nope_head_stride * 2, (cuuint32_t)p.a_rows, kDn / 64) ||
         !encode_bf16_4d(&p.tm_b, w_uk, kDn, kDl / 64, kHeads, kDl * 2, 128, (cuuint64_t)kDn * kDl * 2, kDn, kBN / 64))
@@ -483,7 +483,7 @@ mla_status launch_query_small(int32_t tokens, const void *q_nope, int64_t nope_t
     p.q_rope = static_cast<__nv_bfloat16 *>(q_rope);
     p.status = device_status;
     p.tokens = tokens;
-    return launch_prolog(p, false, (unsigned)ctas, stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+    return launch_prolog(p, false, kHeads * kNParts, stream) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 }  // namespace mla

@@ -42,10 +42,6 @@ mla_status launch_query_small(int32_t tokens, const void *q_nope, int64_t nope_t
 namespace {
 using namespace ptx;
 
-// Up to this many tokens one CTA per tile quarter, in one wave (four fit an SM); beyond, the
-// persistent kernel.  Measured, one CTA each against persistent: 32 tokens 5.1 / 5.9 us, 80 6.0 / 6.2,
-// 96 8.9 / 6.6 (three fit an SM), 384 24.7 / 17.9, 1537 85.0 / 59.6.
-constexpr int32_t kQuerySmall = 80;
 constexpr int kTile = 128;                      // tokens per item (MMA M)
 constexpr int kCols = 256;                      // latent columns per item (MMA N)
 constexpr int kHalves = kDl / kCols;

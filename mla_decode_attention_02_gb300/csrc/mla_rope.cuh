@@ -30,15 +30,15 @@ __device__ __forceinline__ void rope_sincos(int32_t pos, float g_hi, float g_lo,
     __sincosf(r * 6.28318530717958648f, &s, &c);
 }
 
+// Rotate a pair of bf16 values by the angle of this sine and cosine.
+__device__ __forceinline__ uint32_t turn2(uint32_t v, float s, float c) {
+    const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&v));
+    return pack_bf16x2(x.x * c - x.y * s, x.x * s + x.y * c);
+}
+
 // Rotate the four pairs held by eight consecutive bf16 values by angles given as sines and cosines.
 __device__ __forceinline__ uint4 turn8(uint4 v, const float (&s)[4], const float (&c)[4]) {
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j]));
-        w[j] = pack_bf16x2(x.x * c[j] - x.y * s[j], x.x * s[j] + x.y * c[j]);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    return make_uint4(turn2(v.x, s[0], c[0]), turn2(v.y, s[1], c[1]), turn2(v.z, s[2], c[2]), turn2(v.w, s[3], c[3]));
 }
 
 // Rotate the four pairs held by eight consecutive bf16 values, pairs p0 .. p0 + 3.
@@ -49,8 +49,7 @@ __device__ __forceinline__ uint4 rope8(uint4 v, int32_t pos, int p0, const float
     for (int j = 0; j < 4; ++j) {
         float s, c;
         rope_sincos(pos, g_hi[p0 + j], g_lo[p0 + j], s, c);
-        const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j]));
-        w[j] = pack_bf16x2(x.x * c - x.y * s, x.x * s + x.y * c);
+        w[j] = turn2(w[j], s, c);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }

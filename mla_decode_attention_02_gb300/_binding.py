@@ -184,19 +184,20 @@ class Plan:
     max_pages: int
     workspace: object   # torch.uint8 CUDA tensor, owned by this Plan
     seq_lens: object    # the device seq_lens it was built from
-    home: object = None  # handle of the stream that the workspace was allocated on, if known
+    home: object = None  # handle of the stream that plan() allocated the workspace on (None: the caller's own)
 
     def problem(self, flags: int = 0) -> _Problem:
         return _problem(self.batch, self.s_q, self.max_pages, flags)
 
 
 def _used_on(workspace, home, stream):
-    """A plan's workspace is about to be used on `stream` (a torch stream).
+    """The workspace that plan() allocated is about to be used on `stream` (a torch stream).
 
     The plan owns it and may be dropped while that work is still queued: unless its memory
     belongs to that stream already, the allocator is told, and gives it out again only after.
+    (A caller's own workspace is the caller's to keep.)
     """
-    if home is None or stream.cuda_stream != home:
+    if home is not None and stream.cuda_stream != home:
         workspace.record_stream(stream)
 
 
@@ -213,14 +214,13 @@ def plan(seq_lens, *, s_q: int, max_pages_per_seq: int, workspace=None, stream=N
     batch = seq_lens.shape[0]
     with torch.cuda.device(seq_lens.device):
         need = workspace_size(batch, s_q, max_pages_per_seq)
-        here = torch.cuda.current_stream()
+        s = torch.cuda.current_stream() if stream is None else stream
         home = None
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=seq_lens.device)
-            home = here.cuda_stream
+            home = s.cuda_stream if stream is None else torch.cuda.current_stream().cuda_stream
         _req(workspace, "workspace", torch.uint8, None, seq_lens.device)
         prob = _problem(batch, s_q, max_pages_per_seq)
-        s = here if stream is None else stream
         _used_on(workspace, home, s)
         _check(load_library().mla_decode_plan(ctypes.byref(prob), seq_lens.data_ptr(),
                                               workspace.data_ptr(), workspace.numel(),
@@ -887,7 +887,7 @@ def tree_plan(seq_lens, token_offsets, masks, *, max_pages_per_seq: int, workspa
             _check(lib.mla_tree_workspace_size(ctypes.byref(prob), ctypes.byref(n)), "mla_tree_workspace_size")
             workspace = torch.empty(n.value, dtype=torch.uint8, device=seq_lens.device)
         ws, nbytes = _bytes(workspace, "workspace", index)
-        _used_on(workspace, None, torch.cuda.current_stream())
+        workspace.record_stream(torch.cuda.current_stream())   # (the plan's, however it was made)
         _check(lib.mla_tree_plan(ctypes.byref(prob), sl, off, m, ws, nbytes, _current_stream(index)), "mla_tree_plan")
     return TreePlan(B, T, int(max_pages_per_seq), workspace)
 
@@ -954,7 +954,7 @@ def _tree_decode(p, q_latent, q_rope, kv_cache, block_table, scale, out, lse, st
     with _launch_on(index, stream, ws, q_latent, q_rope, kv_cache, block_table, out, lse, scratch):
         out = _out(out, "out", torch.bfloat16, (T, NUM_HEADS, D_LATENT), index)
         lse = _out(lse, "lse", torch.float32, (T, NUM_HEADS), index)
-        _used_on(ws, None, torch.cuda.current_stream())
+        ws.record_stream(torch.cuda.current_stream())
         prob = _Ragged(p.batch, T, NUM_HEADS, PAGE_SIZE, p.max_pages, MLA_FLAG_POW2_MAX if pow2_max else 0)
         args = (ctypes.byref(prob), ql, qr, cache, kv_cache.shape[0], bt, float(scale), out.data_ptr(), lse.data_ptr(),
                 ws.data_ptr(), ws.numel())

@@ -2,7 +2,7 @@
 
 The computation runs in hand-written CUDA kernels behind the C ABI in
 ``include/mla_decode.h`` (``libmla_decode.so``); this package is a thin
-ctypes binding with the same names:
+binding with the same names:
 
     p = plan(seq_lens, s_q=1, max_pages_per_seq=maxp)       # mla_decode_plan
     o_latent, lse = decode(p, q_latent, q_rope, kv_cache, block_table)   # mla_decode

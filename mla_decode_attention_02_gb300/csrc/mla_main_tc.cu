@@ -25,6 +25,13 @@
 //   O_c += [P_0 | P_1] . V_c   tcgen05 M=128 N=256 K=64, V_c = the page's
 //                       latent dims [256c, 256c + 256) of all 64 tokens
 //
+// Scores, maxima, row sums and O are fp32.  P alone has fewer bits, the 8 of the bf16 operand
+// that PV takes: rounded once, twice if its half is scaled to the pair's maximum (exactly, with
+// power-of-two maxima).  So o is off by up to sqrt(2) of what its own rounding costs: 2.36e-3 of
+// its norm over 200 keys (2.31e-3 with power-of-two maxima), 2.0e-3 over 4000, 1.69e-3 over
+// 131072, against 1.66e-3; lse by 6e-7 of its own at most.  P as a sum of two bf16 values would double PV's
+// MMAs, 512 of a page's 1400 clocks of MMAs.
+//
 // Three rings, so that no stage waits for a later one: the K ring (this
 // CTA's 32 tokens of a page, all 576 dims, 36 KB) is freed by the score
 // MMAs; the V ring (the page's 64 tokens of this CTA's 256 output dims,
@@ -1462,8 +1469,12 @@ cudaError_t launch_main(const void *q_latent, const void *q_rope, const void *kv
     p.test_flags = test_flags;
     p.flags = flags;
     // From eight nodes per request on average the nodes warm the pages for one another, and the
-    // prefetches only take the copy engine's time: 64 requests of 4096 keys with 1 node 78.7 us with and
-    // 81.0 without, 4 nodes 263.8 and 264.4, 16 nodes 953 and 942.
+    // prefetches only take the copy engine's time.  Requests x nodes x keys, plan and decode with / without
+    // prefetch, us in a run of a second: 64 x 1 x 8192 157.1 / 160.1, 16 x 1 x 8192 62.6 / 63.9,
+    // 64 x 4 x 4096 286.8 / 285.9, 64 x 7 x 4096 442 / 437, 64 x 8 x 1024 169.4 / 168.3, 4 x 8 x 32768
+    // 279.1 / 279.3 (in a burst 265 / 271), 2 x 12 x 131072 731 / 729 (705 / 713), 24 x 16 x 8192 732 / 726,
+    // 16 x 32 x 4096 506.6 / 500.6, 64 x 16 x 4096 1001 / 987: 2% for one node, 1.4% against from 16 on, and
+    // within 1% (2% of a burst) between, where the border could lie elsewhere.
     p.prefetch = !tree || s_q < 8 * (int64_t)batch;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.batch = batch;

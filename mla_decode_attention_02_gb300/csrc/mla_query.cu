@@ -14,7 +14,8 @@
 //   warps 9-12  q_pe, apart from the items: whole tokens, a quarter of the heads at a time
 // Bound by memory: 384 bytes in and 1152 out per token and head (the outputs are
 // three quarters), against 2 x 128 x 512 flops: 1537 tokens in 59.6 us, 5.4 TB/s.  q_pe by
-// items (each CTA its head's share, angles anew for every head) had taken 79.8.  The small-tile kernel of mla_prolog.cu
+// items (each CTA its head's share, angles anew for every head) had cost ten us more in an earlier form
+// (79.8 against 69.5).  The small-tile kernel of mla_prolog.cu
 // (one CTA per item of a quarter) does few tokens in one wave; from a few tiles on its
 // CTAs spend their time on latency: each loads, multiplies and stores once.
 #include <cuda.h>
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(kQueryThreads, 1) mla_query_kernel(const __gri
     pdl_launch_dependents();
 
     // Items: CTA c takes head-half c over all tiles, so that the CTAs move along the tokens together
-    // and write neighbouring rows at the same time (1537 tokens: 58.6 us against 69.5 with one contiguous
+    // and write neighbouring rows at the same time (1537 tokens: 59.4 us against 67.0 with one contiguous
     // run of (head, half, tile) per CTA), then a share of the other head-halves' items.
     const int64_t rest = ((int64_t)kHeads * kHalves - gridDim.x) * P.tiles;
     const int64_t r0 = rest * blockIdx.x / gridDim.x - P.tiles;

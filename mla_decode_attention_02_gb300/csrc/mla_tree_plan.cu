@@ -21,9 +21,20 @@
 // Measured (decode alone) against the line in token order: 64 requests of 16
 // nodes over 4096 keys 1001 -> 957 us (whole rows), 268 nodes of 80 keys 52 -> 44,
 // 138 nodes of mixed lengths 118 -> 114 (cut rows).  Even pieces against cut rows (at least
-// four pages each): 8 nodes of 700 keys 21.3 -> 19.3, 16 of 1500 28.4 -> 25.3, one of 8192
-// 22.9 -> 20.8; 24 of 131072 in three pieces each 697 against 683 in a short burst, but 735
-// against 760 in a run of seconds under the power cap (DRAM reads a twelfth).
+// four pages each), requests x nodes x keys, us in a short burst / in a run of a second:
+//
+//                      even           cut                              even           cut
+//   1 x 8 x 700      20.2 / 19.4   22.4 / 21.7     1 x 64 x 8192    142.8 / 141.3  137.0 / 136.0
+//   1 x 16 x 1500    26.4 / 25.4   29.3 / 28.6     2 x 12 x 32768   189.3 / 191.3  185.6 / 191.5
+//   1 x 1 x 8192     21.4 / 20.6   24.0 / 23.3     1 x 24 x 65536   359.3 / 366.5  348.6 / 364.3
+//   3 x 5 x 5000     37.4 / 36.5   40.9 / 39.9     2 x 12 x 131072  701.5 / 725.5  687.3 / 744.6
+//   1 x 8 x 16384    49.7 / 48.5   48.9 / 47.7
+//   4 x 8 x 8192     82.2 / 80.6   77.9 / 76.8
+//
+// So they win up to 13% where a unit has a few pages, and lose 1 to 5% of a burst from some ten
+// pages a unit on.  In the longest runs, under the power cap, a request's nodes at the same pages
+// (a twelfth of the DRAM reads) win 2.6%.  The 1/12 decides 1 x 64 x 8192, 1 x 24 x 65536 and
+// 2 x 12 x 131072, which would be cut without it.
 //
 // One CTA; every choice is a function of the inputs alone, and the host twin
 // below makes the same ones.

@@ -64,7 +64,13 @@ def _library_up_to_date() -> bool:
 
 
 def _host_up_to_date() -> bool:
-    return importlib.util.find_spec("torch") is None or _newer(host_path(), [HOST_SRC] + _headers())
+    if importlib.util.find_spec("torch") is None:
+        return True
+    try:
+        path = host_path()
+    except Exception:   # a torch that does not import: building says why
+        return False
+    return _newer(path, [HOST_SRC] + _headers())
 
 
 def up_to_date() -> bool:

@@ -40,6 +40,16 @@ def test_the_library_is_built_without_torch(small, monkeypatch):
     assert not B.up_to_date()
 
 
+def test_the_library_is_built_beside_a_torch_that_does_not_import(small, monkeypatch):
+    def broken():
+        raise ImportError("libtorch is broken")
+    monkeypatch.setattr(B, "host_path", broken)
+    assert not B.up_to_date()
+    with pytest.warns(UserWarning, match="libtorch is broken"):
+        B.build()
+    assert os.path.getsize(B.LIB_PATH) > 0
+
+
 def test_a_source_that_does_not_compile_is_an_error(small):
     (small / "one.cu").write_text("int x = ;\n")
     with pytest.raises(RuntimeError, match="nvcc failed"):

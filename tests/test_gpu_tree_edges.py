@@ -148,7 +148,7 @@ def test_a_dropped_plan_outlives_its_calls(kind, way):
         home, user, kw = here, here, {}
     user.wait_stream(home)
     with torch.cuda.stream(user):
-        _wait_ms(50)
+        _wait_ms(400)
     with torch.cuda.stream(home):
         p = plan()
     user.wait_stream(home)
@@ -165,6 +165,43 @@ def test_a_dropped_plan_outlives_its_calls(kind, way):
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
+@pytest.mark.parametrize("kind", ["tree", "plain"])
+def test_an_eager_plan_in_a_captured_decode(kind):
+    """A plan made outside a graph serves the decode captured in it, over replays, and is dropped after."""
+    c = TU.case([2, 2, 2], [90, 700, 64], "chain", seed=106)
+    ql, qr, cache = TU.tensors(c, seed=107, quiet=True)
+    d = TU.index_tensors(c)
+    ql, qr, kv = ql.cuda(), qr.cuda(), cache.cuda()
+    table = torch.where(d["block_table"] == 1 << 30, -1, d["block_table"])
+    if kind == "tree":
+        p = mla.tree_plan(d["seq_lens"], d["offsets"], d["masks"], max_pages_per_seq=table.shape[1])
+        run = lambda **kw: mla.tree_decode(p, ql, qr, kv, table, scale=SCALE, **kw)  # noqa: E731
+    else:
+        p = mla.plan(d["seq_lens"], s_q=2, max_pages_per_seq=table.shape[1])
+        run = lambda **kw: mla.decode(p, ql.view(3, 2, 128, 512), qr.view(3, 2, 128, 64), kv, table, scale=SCALE, **kw)  # noqa: E731
+    o, lse = run()
+    want = [o.clone(), lse.clone()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(out=o, lse=lse)
+    for _ in range(3):
+        o.zero_(), lse.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1]) and mla.check(p) == 0
+    other = torch.cuda.CUDAGraph()                                  # dropped while another capture runs
+    x = torch.zeros(8, device="cuda")
+    del graph
+    with torch.cuda.graph(other):
+        x += 1
+        del p, run
+    other.replay()
+    assert (x == 1).all()
+    got = [torch.zeros(1 << 20, device="cuda") for _ in range(30)]
+    torch.cuda.synchronize()
+    assert not any(t.any() for t in got)
+
+
 def test_a_decode_plan_made_on_a_given_stream():
     """plan(stream=s): the workspace comes from the current stream's memory and is written on s."""
     c = TU.case([2], [400], "chain", seed=97)
@@ -174,7 +211,7 @@ def test_a_decode_plan_made_on_a_given_stream():
     torch.cuda.empty_cache()
     s = torch.cuda.Stream()
     with torch.cuda.stream(s):
-        _wait_ms(50)
+        _wait_ms(400)
     p = mla.plan(d["seq_lens"], s_q=2, max_pages_per_seq=d["block_table"].shape[1], stream=s)
     at, n = p.workspace.data_ptr(), p.workspace.numel()
     del p

@@ -34,6 +34,19 @@ token arrays, each function with an _fp8 twin for an fp8 cache):
     o_latent, lse = tree_decode(p, q_latent, q_rope, kv_cache, block_table)  # mla_tree_decode
     new_seq_lens, st = cache_commit(kv_cache, block_table, seq_lens, token_offsets,
                                     paths, path_lens)                   # mla_cache_commit
+
+A layer step over chunks of prompts (``include/mla_chunk.h``; cache_append puts the
+chunks' rows into the cache, chunk_attend has an _fp8 twin):
+
+    table = rope_table_scaled(1e4, factor=40.0)              # mla_rope_table_scaled
+    rotate(q[..., 128:], positions, table=table, out=q[..., 128:])      # mla_rotate
+    p = chunk_plan(seq_lens, token_offsets, tokens=T, max_pages_per_seq=maxp,
+                   kv_tokens=n)                              # mla_chunk_plan, once per step
+    o_v = chunk_attend(p, q[..., :128], q[..., 128:], w_uk, w_uv, kv_cache,
+                       block_table)                          # mla_chunk_attend
+    out = epilog_oproj(o_v, w_o)
+    y, residual = residual_norm(out, residual, weight)       # mla_residual_norm
+    codes, scales, residual = residual_norm_fp8(out, residual, weight)  # mla_residual_norm_fp8
 """
 
 from ._binding import (D_V, HIDDEN, DEFAULT_ROPE_BASE, DEFAULT_RMS_EPS, DEFAULT_SCALE, D_LATENT, D_NOPE, D_ROPE, LIB_PATH, NUM_HEADS, PAGE_SIZE,
@@ -45,6 +58,8 @@ from ._binding import (D_V, HIDDEN, DEFAULT_ROPE_BASE, DEFAULT_RMS_EPS, DEFAULT_
 from ._binding import (MLA_DEV_BAD_OFFSETS, MLA_DEV_BAD_PATH, EXPANDED_PAGE_BYTES, EXPAND_LIMIT_BYTES, TREE_MAX_NODES, TreePlan, cache_append, cache_append_fp8,
                        cache_commit, cache_commit_fp8, query, tree_decode, tree_decode_fp8, tree_plan,
                        tree_plan_device, tree_plan_host, tree_workspace_size)
+from ._chunk import (CHUNK_SCRATCH_BYTES, MLA_DEV_BAD_KV_TOKENS, ROTARY_DIMS, ChunkPlan, chunk_attend, chunk_attend_fp8,
+                     chunk_plan, chunk_scratch_size, residual_norm, residual_norm_fp8, rope_table_scaled, rotate)
 
 __all__ = ["D_V", "HIDDEN", "epilog_oproj", "epilog_uv",
            "quantize_cache_fp8",
@@ -56,4 +71,6 @@ __all__ = ["D_V", "HIDDEN", "epilog_oproj", "epilog_uv",
            "plan", "plan_device_bytes", "prolog", "rope_table", "plan_host", "plan_layout", "workspace_size",
            "MLA_DEV_BAD_OFFSETS", "MLA_DEV_BAD_PATH", "EXPANDED_PAGE_BYTES", "EXPAND_LIMIT_BYTES", "TREE_MAX_NODES", "TreePlan", "cache_append", "cache_append_fp8",
            "cache_commit", "cache_commit_fp8", "query", "tree_decode", "tree_decode_fp8", "tree_plan",
-           "tree_plan_device", "tree_plan_host", "tree_workspace_size"]
+           "tree_plan_device", "tree_plan_host", "tree_workspace_size",
+           "CHUNK_SCRATCH_BYTES", "MLA_DEV_BAD_KV_TOKENS", "ROTARY_DIMS", "ChunkPlan", "chunk_attend", "chunk_attend_fp8",
+           "chunk_plan", "chunk_scratch_size", "residual_norm", "residual_norm_fp8", "rope_table_scaled", "rotate"]

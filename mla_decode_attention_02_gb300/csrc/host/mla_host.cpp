@@ -26,6 +26,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "mla_chunk.h"
 #include "mla_fp8.h"
 #include "mla_tree.h"
 
@@ -39,6 +40,9 @@ struct Entry {
     decltype(&mla_tree_decode) tree_decode;
     decltype(&mla_tree_decode_fp8) tree_decode_fp8;
     decltype(&mla_cache_commit) commit;
+    decltype(&mla_rotate) rotate;
+    decltype(&mla_residual_norm) residual_norm;
+    decltype(&mla_residual_norm_fp8) residual_norm_fp8;
 };
 Entry g_entry;
 bool g_bound = false;
@@ -315,6 +319,73 @@ PyObject *py_commit(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// x, positions, table, layout, inverse, magnitude, out -> out
+PyObject *py_rotate(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        const at::Tensor *x = n == 7 ? tensor(a[0]) : nullptr;
+        if (!here(x) || x->dim() != 3 || x->numel() < 1 || x->size(0) > INT32_MAX || x->size(1) > INT32_MAX ||
+            x->size(2) > 256 || !PyFloat_Check(a[5]))
+            MLA_NOT_PLAIN;
+        const int dev = x->get_device();
+        const int64_t T = x->size(0), H = x->size(1), D = x->size(2);
+        const long layout = PyLong_AsLong(a[3]);
+        int64_t xs[2], os[2] = {H * D, D};
+        void *src = strided(a[0], {T, H, D}, dev, xs), *pos = dense(a[1], at::kInt, {T}, dev, 4);
+        void *table = dense(a[2], at::kFloat, {D}, dev, 4);
+        if (!src || !pos || !table) MLA_NOT_PLAIN;
+        at::Tensor out;
+        if (a[6] == Py_None) {
+            if (D % 16) MLA_NOT_PLAIN;
+            out = make({T, H, D}, at::kBFloat16, dev);
+        } else {
+            if (!strided(a[6], {T, H, D}, dev, os)) MLA_NOT_PLAIN;
+            out = *tensor(a[6]);
+        }
+        const mla_status rc = g_entry.rotate((int32_t)T, (int32_t)H, (int32_t)D, src, xs[0], xs[1], (const int32_t *)pos,
+                                             (const float *)table, (int32_t)layout, a[4] == Py_True,
+                                             (float)PyFloat_AS_DOUBLE(a[5]), out.data_ptr(), os[0], os[1], stream_of(dev));
+        if (rc != MLA_OK) return status_error(rc);
+        return wrap(out);
+    });
+}
+
+// x, residual, weight, rms_eps, group (-1: bf16), out (codes), scales, residual_out -> (out, scales, residual_out)
+PyObject *py_residual_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        const at::Tensor *x = n == 8 ? tensor(a[0]) : nullptr;
+        if (!here(x) || x->dim() != 2 || x->numel() < 1 || x->size(0) > INT32_MAX || x->size(1) > 16384 ||
+            !PyFloat_Check(a[3]) || !PyLong_Check(a[4]))
+            MLA_NOT_PLAIN;
+        const int dev = x->get_device();
+        const int64_t T = x->size(0), N = x->size(1);
+        const long group = PyLong_AsLong(a[4]);
+        const bool added = a[1] != Py_None, fp8 = group >= 0;
+        int64_t xs, rs = 8;
+        void *src = strided(a[0], {T, N}, dev, &xs), *res = added ? strided(a[1], {T, N}, dev, &rs) : nullptr;
+        void *w = dense(a[2], at::kBFloat16, {N}, dev, 16);
+        if (!src || (added && !res) || !w || (!added && a[7] != Py_None)) MLA_NOT_PLAIN;
+        at::Tensor out, scales, kept;
+        if (!output(a[5], fp8 ? at::kFloat8_e4m3fn : at::kBFloat16, {T, N}, dev, &out) ||
+            (fp8 && !output(a[6], at::kFloat, {T, group ? (N + group - 1) / group : 1}, dev, &scales)) ||
+            (added && !output(a[7], at::kBFloat16, {T, N}, dev, &kept)))
+            MLA_NOT_PLAIN;
+        const float eps = (float)PyFloat_AS_DOUBLE(a[3]);
+        void *to = added ? kept.data_ptr() : nullptr;
+        const mla_status rc =
+            fp8 ? g_entry.residual_norm_fp8((int32_t)T, (int32_t)N, src, xs, res, rs, w, eps, (int32_t)group,
+                                            out.data_ptr(), (float *)scales.data_ptr(), to, stream_of(dev))
+                : g_entry.residual_norm((int32_t)T, (int32_t)N, src, xs, res, rs, w, eps, out.data_ptr(), to,
+                                        stream_of(dev));
+        if (rc != MLA_OK) return status_error(rc);
+        auto or_none = [](const at::Tensor &t) {
+            if (t.defined()) return wrap(t);
+            Py_INCREF(Py_None);
+            return Py_None;
+        };
+        return Py_BuildValue("(NNN)", wrap(out), or_none(scales), or_none(kept));
+    });
+}
+
 // The C ABI's addresses, in the order of Entry.
 PyObject *py_bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     constexpr int kEntries = sizeof(Entry) / sizeof(void *);
@@ -343,6 +414,8 @@ PyMethodDef kMethods[] = {
     {"tree_plan", reinterpret_cast<PyCFunction>(py_tree_plan), METH_FASTCALL, nullptr},
     {"tree_decode", reinterpret_cast<PyCFunction>(py_tree_decode), METH_FASTCALL, nullptr},
     {"commit", reinterpret_cast<PyCFunction>(py_commit), METH_FASTCALL, nullptr},
+    {"rotate", reinterpret_cast<PyCFunction>(py_rotate), METH_FASTCALL, nullptr},
+    {"residual_norm", reinterpret_cast<PyCFunction>(py_residual_norm), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_mla_host", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

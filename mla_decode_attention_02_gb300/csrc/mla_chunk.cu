@@ -1,0 +1,530 @@
+// Attention of a step's chunks over the heads' keys and values (include/mla_chunk.h):
+//
+//   o[t][h] = sum_j softmax(scale q[t][h] . k[j][h])_j v[j][h]      192-value scores, 128-value outputs,
+//   j from the first slot of t's request to t's own
+//
+// An item is one head of one tile of 256 tokens (mla_chunk_plan.cu), taken as two MMA tiles
+// of 128 tokens that share every key tile of 128.  GB300 design, one CTA per SM:
+//   warp 8      TMA: the queries (96 KB), then keys and values as 16 KB blocks of 64 dims through a ring
+//               of eight (a key tile's three blocks, its two value blocks, the next key tile's ...)
+//   warp 9      MMAs: S = q K^T (M = 128, N = 128, K = 192) into TMEM, and O += P V with P read from
+//               TMEM; the two tiles take turns, so that one's softmax runs while the other's products do
+//   warps 0-3   softmax of the first tile, one thread a row: S from TMEM, the running maximum and sum in
+//   warps 4-7   registers, P as bf16 back over S; the second tile's likewise
+// TMEM: S and O of both tiles, 4 x 128 columns, all of it.  A thread whose row's maximum grows by more than 2^8
+// rescales the row's O itself, which waits for the product before; smaller growth leaves the reference as it
+// is (exact: the reference is a shift).  Weights are rounded to bf16 for their product; the sum is taken of the
+// unrounded ones.
+// Bound by the tensor cores: 81,920 flops a (token, key) pair and 128 heads.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "mla_chunk.cuh"
+#include "mla_fp8.h"
+#include "mla_internal.h"
+#include "mla_rope.cuh"
+#include "sm103_ptx.cuh"
+
+namespace mla {
+bool encode_bf16_4d(CUtensorMap *m, const void *base, cuuint64_t d1, cuuint64_t d2, cuuint64_t d3,
+                    cuuint64_t s1, cuuint64_t s2, cuuint64_t s3, cuuint32_t rows, cuuint32_t blocks);
+cudaError_t main_units(int32_t *units);
+mla_status check_chunk(const mla_chunk *p);
+cudaError_t launch_chunk_expand(const mla_chunk *prob, const void *w_uk, const void *w_uv, const void *cache, bool fp8,
+                                int64_t num_pages, const int32_t *block_table, void *ws, void *rope, void *kv,
+                                int32_t head0, int32_t heads, cudaStream_t stream);
+namespace {
+using namespace ptx;
+
+constexpr int kSoftWarps = 8, kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kChunkThreads = 32 * 10;
+constexpr int kSlots = 8;
+constexpr int kKeys = 128;                              // keys of a tile
+constexpr uint32_t kBlk = 128 * 128;                    // 128 rows x 64 dims
+constexpr uint32_t kQTile = 3 * kBlk;                   // 128 tokens x 192 dims
+constexpr uint32_t kOffRing = 2 * kQTile;
+constexpr uint32_t kChunkSmem = kOffRing + kSlots * kBlk + 1024;
+constexpr uint32_t kColS = 0, kColO = 256;              // + 128 per tile
+constexpr uint64_t kChunkWaitNs = 2000000000ull;
+constexpr float kRescale = 8.0f;                        // log2 units
+static_assert(kChunkSmem <= 232448 - 1024, "shared memory budget");
+
+struct ChunkParams {
+    CUtensorMap tm_qn, tm_qr;   // queries as (64 dims, tokens, dim blocks, heads), box 64 x 128 x 2 (1) x 1
+    CUtensorMap tm_kv;          // scratch as (64 dims, rows, 4 blocks, heads), box 64 x 128 x 1 x 1
+    CUtensorMap tm_kr;          // its rotary parts as (64 dims, rows, 1, 1), box 64 x 128 x 1 x 1
+    uint8_t *ws;
+    __nv_bfloat16 *out;
+    float *lse;
+    int64_t kv_tokens;
+    float scale_log2;
+    int32_t batch, tokens, max_pages, head0, heads;
+};
+
+struct Wait {
+    volatile int *abort;
+    int32_t *status;
+};
+
+// Bounded wait; on time-out flags the CTA (every other wait then gives up at once).
+__device__ __noinline__ bool wait_slow(const Wait w, uint32_t bar, uint32_t parity) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 0;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 63) == 63) {
+            if (*w.abort) return false;
+            const uint64_t t = globaltimer_ns();
+            if (t0 == 0) t0 = t;
+            else if (t - t0 > kChunkWaitNs) {
+                *w.abort = 1;
+                atomicOr(w.status, MLA_DEV_TIMEOUT);
+                return false;
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ bool wait(const Wait &w, uint32_t bar, uint32_t parity) {
+    return mbar_try_wait(bar, parity) || wait_slow(w, bar, parity);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Teardown: what is in flight lands, whatever the abort flag says (bounded).
+__device__ __noinline__ void wait_landed(const Wait w, uint32_t bar, uint32_t parity) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (globaltimer_ns() - t0 > kChunkWaitNs) {
+            atomicOr(w.status, MLA_DEV_TIMEOUT);
+            return;
+        }
+    }
+}
+
+// A tile in error: its rows' outputs are NaN.
+__device__ __noinline__ void write_nan(const ChunkParams &P, const ChunkTile t, int head, int thread, int threads) {
+    const uint32_t nan2 = 0x7fff7fffu;
+    for (int i = thread; i < t.count * (kDv / 8); i += threads) {
+        const int row = t.t0 + i / (kDv / 8);
+        reinterpret_cast<uint4 *>(P.out + ((size_t)row * kHeads + head) * kDv)[i % (kDv / 8)] =
+            make_uint4(nan2, nan2, nan2, nan2);
+    }
+    if (P.lse)
+        for (int i = thread; i < t.count; i += threads)
+            P.lse[(size_t)(t.t0 + i) * kHeads + head] = __int_as_float(0x7fffffff);
+}
+
+__global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __grid_constant__ ChunkParams P) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[2 * kSlots + 13];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    const uint32_t s_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // + ring slot: landed, read; + tile: queries landed, queries read, S complete, P written, product done
+    enum { B_FULL = 0, B_EMPTY = kSlots, B_QFULL = 2 * kSlots, B_QFREE = B_QFULL + 2, B_S = B_QFREE + 2, B_P = B_S + 2,
+           B_PV = B_P + 2, B_DRAIN = B_PV + 2 };
+    static_assert(B_DRAIN + 1 <= 2 * kSlots + 13, "barriers");
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(bar(B_FULL + s), 1);
+            mbar_init(bar(B_EMPTY + s), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bar(B_QFULL + s), 1);
+            mbar_init(bar(B_QFREE + s), 1);
+            mbar_init(bar(B_S + s), 1);
+            mbar_init(bar(B_P + s), kSoftWarps / 2);
+            mbar_init(bar(B_PV + s), 1);
+        }
+        mbar_init(bar(B_DRAIN), 1);
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(smem_u32(&tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    pdl_wait_prior();
+    pdl_launch_dependents();
+
+    PlanHeader *hdr = reinterpret_cast<PlanHeader *>(P.ws);
+    const Wait w = {&abort_flag, &hdr->status};
+    const bool fits = hdr->magic == kChunkMagic && hdr->batch == P.batch && hdr->s_q == P.tokens &&
+                      hdr->max_pages == P.max_pages && hdr->total_cost == P.kv_tokens;
+    if (!fits && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&hdr->status, MLA_DEV_BAD_PLAN);
+    const ChunkTile *tiles = reinterpret_cast<const ChunkTile *>(P.ws + chunk_layout(P.batch, P.tokens, P.kv_tokens).tiles);
+    // Items: head by head, a head's tiles together (they read the same keys), longest first.
+    const int64_t num_tiles = fits ? hdr->num_items : 0, items = num_tiles * P.heads;
+    // Key tiles of MMA tile s: up to the one with its last token's slot.
+    auto key_tiles = [](const ChunkTile &t, int s) {
+        const int last = (t.count < 128 * (s + 1) ? t.count : 128 * (s + 1)) - 1;
+        return last < 128 * s ? 0 : (t.slot0 + last) / kKeys + 1;
+    };
+
+    if (warp == kTmaWarp) {
+        if (elect_one()) {
+            prefetch_tmap(&P.tm_qn);
+            prefetch_tmap(&P.tm_qr);
+            prefetch_tmap(&P.tm_kv);
+            prefetch_tmap(&P.tm_kr);
+            uint32_t n = 0, loads[2] = {0, 0};
+            bool ok = true;
+            auto load = [&](const CUtensorMap *tm, int row, int blk, int h) {
+                const uint32_t s = n % kSlots;
+                if (n >= kSlots) ok = ok && wait(w, bar(B_EMPTY + s), (n / kSlots - 1) & 1);
+                if (!ok) return;
+                mbar_arrive_expect_tx(bar(B_FULL + s), kBlk);
+                tma_load_4d(s_base + kOffRing + s * kBlk, tm, 0, row, blk, h, bar(B_FULL + s));
+                ++n;
+            };
+            for (int64_t i = blockIdx.x; i < items && ok; i += gridDim.x) {
+                const ChunkTile t = tiles[i % num_tiles];
+                if (t.slot0 < 0) continue;
+                const int hl = (int)(i / num_tiles), h = P.head0 + hl;
+                const int n0 = key_tiles(t, 0), n1 = key_tiles(t, 1);
+                for (int s = 0; s < (n1 ? 2 : 1) && ok; ++s) {
+                    if (loads[s]) ok = wait(w, bar(B_QFREE + s), (loads[s] - 1) & 1);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(bar(B_QFULL + s), kQTile);
+                    tma_load_4d(s_base + s * kQTile, &P.tm_qn, 0, t.t0 + 128 * s, 0, h, bar(B_QFULL + s));
+                    tma_load_4d(s_base + s * kQTile + 2 * kBlk, &P.tm_qr, 0, t.t0 + 128 * s, 0, h, bar(B_QFULL + s));
+                    ++loads[s];
+                }
+                const int n_max = n1 > n0 ? n1 : n0;
+                for (int j = 0; j < n_max && ok; ++j) {
+                    const int row = t.base + j * kKeys;
+                    load(&P.tm_kv, row, 0, hl);
+                    load(&P.tm_kv, row, 1, hl);
+                    load(&P.tm_kr, row, 0, 0);
+                    load(&P.tm_kv, row, 2, hl);
+                    load(&P.tm_kv, row, 3, hl);
+                }
+            }
+            // every copy has landed before the CTA gives its memory up
+            for (uint32_t k = n > kSlots ? n - kSlots : 0; k < n; ++k)
+                wait_landed(w, bar(B_FULL + k % kSlots), (k / kSlots) & 1);
+            for (int s = 0; s < 2; ++s)
+                if (loads[s]) wait_landed(w, bar(B_QFULL + s), (loads[s] - 1) & 1);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        if (elect_one()) {
+            constexpr uint32_t idesc_s = idesc_bf16(128, kKeys, 0, 0), idesc_o = idesc_bf16(128, 64, 0, 1);
+            uint32_t n = 0, q_used[2] = {0, 0}, p_used[2] = {0, 0};   // n: ring blocks before this item's
+            bool ok = true;
+            auto landed = [&](uint32_t k) { ok = ok && wait(w, bar(B_FULL + k % kSlots), (k / kSlots) & 1); };
+            auto scores = [&](int s, uint32_t k) {   // S = q K^T, the key tile's blocks being k, k + 1, k + 2
+#pragma unroll
+                for (int b = 0; b < 3; ++b) {
+                    landed(k + b);
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint32_t at = s_base + kOffRing + (k + b) % kSlots * kBlk;
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_ss(tmem + kColS + s * 128, smem_desc(s_base + s * kQTile + b * kBlk + ks * 32, 16, 1024, 2),
+                               smem_desc(at + ks * 32, 16, 1024, 2), idesc_s, (b | ks) ? 1u : 0u);
+                }
+                mma_commit(bar(B_S + s));
+            };
+            auto product = [&](int s, uint32_t k, bool add) {   // O (+)= P V, the value blocks being k, k + 1
+                ok = ok && wait(w, bar(B_P + s), p_used[s]++ & 1);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    landed(k + b);
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint32_t at = s_base + kOffRing + (k + b) % kSlots * kBlk;
+#pragma unroll
+                    for (int ks = 0; ks < kKeys / 16; ++ks)
+                        mma_ts(tmem + kColO + s * 128 + b * 64, tmem + kColS + s * 128 + ks * 8,
+                               smem_desc(at + ks * 2048, kBlk, 1024, 2), idesc_o, (add || ks) ? 1u : 0u);
+                }
+                mma_commit(bar(B_PV + s));
+            };
+            auto release = [&](uint32_t k, int count) {
+                for (int b = 0; b < count; ++b) mma_commit(bar(B_EMPTY + (k + b) % kSlots));
+            };
+            for (int64_t i = blockIdx.x; i < items && ok; i += gridDim.x) {
+                const ChunkTile t = tiles[i % num_tiles];
+                if (t.slot0 < 0) continue;
+                const int nk[2] = {key_tiles(t, 0), key_tiles(t, 1)};
+                const int n_max = nk[1] > nk[0] ? nk[1] : nk[0];
+                for (int s = 0; s < 2; ++s) {
+                    if (!nk[s]) continue;
+                    ok = ok && wait(w, bar(B_QFULL + s), q_used[s]++ & 1);
+                    if (ok) scores(s, n);
+                }
+                if (!ok) break;
+                release(n, 3);
+                for (int s = 0; s < 2; ++s)
+                    if (nk[s] == 1) mma_commit(bar(B_QFREE + s));
+                for (int j = 0; j < n_max && ok; ++j) {
+                    const uint32_t v = n + 5 * j + 3, next = v + 2;
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        if (j < nk[s]) product(s, v, j > 0);
+                        if (ok && j + 1 < nk[s]) scores(s, next);
+                        if (ok && j + 2 == nk[s]) mma_commit(bar(B_QFREE + s));
+                        if (!ok) break;
+                    }
+                    if (!ok) break;
+                    release(v, 2);
+                    if (j + 1 < n_max) release(next, 3);
+                }
+                n += 5 * n_max;
+            }
+            mma_commit(bar(B_DRAIN));   // every MMA is done before the CTA gives its memory up
+            wait_landed(w, bar(B_DRAIN), 0);
+        }
+        __syncwarp();
+    } else {
+        // ---- softmax of MMA tile s: a thread's row is accumulator lane 32 quarter + lane
+        const int s = warp >> 2, quarter = warp & 3;
+        const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t col_s = lanes + kColS + s * 128, col_o = lanes + kColO + s * 128;
+        uint32_t phase = 0;   // key tiles before this item's
+        bool ok = true;
+        for (int64_t i = blockIdx.x; i < items && ok; i += gridDim.x) {
+            const ChunkTile t = tiles[i % num_tiles];
+            const int h = P.head0 + (int)(i / num_tiles);
+            if (t.slot0 < 0) {
+                write_nan(P, t, h, threadIdx.x, 32 * kSoftWarps);
+                continue;
+            }
+            const int nk = key_tiles(t, s), row = 128 * s + quarter * 32 + lane;
+            const bool mine = row < t.count;
+            const int slot = t.slot0 + (mine ? row : t.count - 1);   // (a row past the tile's end: any legal slot)
+            const int least = __shfl_sync(0xffffffffu, slot, 0);     // the warp's first row sees the fewest keys
+            float m = -INFINITY, sum = 0.f;
+            for (int j = 0; j < nk; ++j, ++phase) {
+                if (!__all_sync(0xffffffffu, wait(w, bar(B_S + s), phase & 1))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                float x[kKeys];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t r[32];
+                    tmem_ld32(col_s + c * 32, r);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[c * 32 + e] = __uint_as_float(r[e]);
+                }
+                tmem_wait_ld();
+                const int limit = slot - j * kKeys;   // the last key of the tile that the row sees
+                if (least - j * kKeys < kKeys - 1) {
+#pragma unroll
+                    for (int e = 0; e < kKeys; ++e) x[e] = e <= limit ? x[e] : -INFINITY;
+                }
+                float top = x[0];
+#pragma unroll
+                for (int e = 1; e < kKeys; ++e) top = fmaxf(top, x[e]);
+                // raise the reference if the row's maximum outgrew it (the first tile: from nothing)
+                const bool raise = (top - m) * P.scale_log2 > kRescale;
+                if (__any_sync(0xffffffffu, raise)) {
+                    const float f = raise ? ex2((m - top) * P.scale_log2) : 1.f;
+                    if (raise) {
+                        m = top;
+                        sum *= f;
+                    }
+                    if (j > 0) {   // O holds the tiles before: once their product is done
+                        if (!__all_sync(0xffffffffu, wait(w, bar(B_PV + s), (phase - 1) & 1))) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t r[32];
+                            tmem_ld32(col_o + c * 32, r);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+                            tmem_st32(col_o + c * 32, r);
+                        }
+                    }
+                }
+                const float shift = m * P.scale_log2;
+                float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t r[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const float a = ex2(fmaf(x[c * 64 + 2 * e], P.scale_log2, -shift));
+                        const float b = ex2(fmaf(x[c * 64 + 2 * e + 1], P.scale_log2, -shift));
+                        part[e & 3] += a + b;
+                        r[e] = pack_bf16x2(a, b);
+                    }
+                    tmem_st32(col_s + c * 32, r);
+                }
+                sum += (part[0] + part[1]) + (part[2] + part[3]);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_P + s));
+            }
+            if (!ok || !nk) continue;
+            // ---- the item's output, once its last product is done
+            if (!__all_sync(0xffffffffu, wait(w, bar(B_PV + s), (phase - 1) & 1))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const float inv = 1.f / sum;
+            uint4 *dst = reinterpret_cast<uint4 *>(P.out + ((size_t)(t.t0 + row) * kHeads + h) * kDv);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t r[32];
+                tmem_ld32(col_o + c * 32, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (mine)
+                        dst[c * 4 + q] = make_uint4(
+                            pack_bf16x2(__uint_as_float(r[8 * q]) * inv, __uint_as_float(r[8 * q + 1]) * inv),
+                            pack_bf16x2(__uint_as_float(r[8 * q + 2]) * inv, __uint_as_float(r[8 * q + 3]) * inv),
+                            pack_bf16x2(__uint_as_float(r[8 * q + 4]) * inv, __uint_as_float(r[8 * q + 5]) * inv),
+                            pack_bf16x2(__uint_as_float(r[8 * q + 6]) * inv, __uint_as_float(r[8 * q + 7]) * inv));
+            }
+            if (mine && P.lse)
+                P.lse[(size_t)(t.t0 + row) * kHeads + h] = (m * P.scale_log2 + log2f(sum)) * 0.6931471805599453f;
+            tc_fence_before();   // the next item's first product writes over O: after its P, which these threads write
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+std::mutex g_chunk_mutex;
+bool g_chunk_attr[64];
+
+bool aligned(const void *p, uintptr_t a) { return p && (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+mla_status attend(const mla_chunk *prob, const void *q_nope, int64_t nope_token, int64_t nope_head, const void *q_rope,
+                  int64_t rope_token, int64_t rope_head, const void *w_uk, const void *w_uv, const void *cache, bool fp8,
+                  int64_t num_pages, const int32_t *block_table, float scale, void *out, float *lse, void *workspace,
+                  size_t workspace_bytes, void *scratch, size_t scratch_bytes, mla_stream_t stream) {
+    const mla_status st = check_chunk(prob);
+    if (st != MLA_OK) return st;
+    if (!aligned(q_nope, 16) || !aligned(q_rope, 16) || !aligned(w_uk, 16) || !aligned(w_uv, 16) || !aligned(cache, 16) ||
+        !aligned(block_table, 4) || !aligned(out, 16) || (reinterpret_cast<uintptr_t>(lse) & 3u) ||
+        !aligned(workspace, 16) || !aligned(scratch, 128))
+        return MLA_ERR_INVALID_ARG;
+    for (const int64_t s : {nope_token, nope_head, rope_token, rope_head})
+        if (s < 1 || s % 8 || s >= (int64_t)1 << 31) return MLA_ERR_INVALID_ARG;
+    if (num_pages < 1 || num_pages >= (int64_t)1 << 31 || !std::isfinite(scale) || !(scale > 0.f))
+        return MLA_ERR_INVALID_ARG;
+    if (workspace_bytes < chunk_layout(prob->batch, prob->tokens, prob->kv_tokens).total) return MLA_ERR_WORKSPACE;
+    const size_t rope_bytes = chunk_rope_bytes(prob->kv_tokens), head_bytes = chunk_head_bytes(prob->kv_tokens);
+    if (scratch_bytes < rope_bytes + head_bytes) return MLA_ERR_WORKSPACE;
+    const size_t room = (scratch_bytes - rope_bytes) / head_bytes;
+    const int32_t fit = room < (size_t)kHeads ? (int32_t)room : kHeads;
+    const int32_t passes = (kHeads + fit - 1) / fit;
+    int dev = 0;
+    int32_t units = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MLA_ERR_CUDA;
+    if (main_units(&units) != cudaSuccess) return MLA_ERR_CUDA;
+    {
+        std::lock_guard<std::mutex> lock(g_chunk_mutex);
+        if (!g_chunk_attr[dev]) {
+            if (cudaFuncSetAttribute(mla_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kChunkSmem) !=
+                cudaSuccess)
+                return MLA_ERR_CUDA;
+            g_chunk_attr[dev] = true;
+        }
+    }
+    uint8_t *rope = static_cast<uint8_t *>(scratch), *kv = rope + rope_bytes;
+    const cuuint64_t rows = (cuuint64_t)chunk_rows(prob->kv_tokens), T = (cuuint64_t)prob->tokens;
+    ChunkParams p{};
+    if (!encode_bf16_4d(&p.tm_qn, q_nope, T, kDn / 64, kHeads, (cuuint64_t)nope_token * 2, 128, (cuuint64_t)nope_head * 2,
+                        128, kDn / 64) ||
+        !encode_bf16_4d(&p.tm_qr, q_rope, T, 1, kHeads, (cuuint64_t)rope_token * 2, 128, (cuuint64_t)rope_head * 2, 128, 1) ||
+        !encode_bf16_4d(&p.tm_kr, rope, rows, 1, 1, kDr * 2, rows * kDr * 2, rows * kDr * 2, 128, 1) ||
+        !encode_bf16_4d(&p.tm_kv, kv, rows, 4, (cuuint64_t)fit, (kDn + kDv) * 2, 128, rows * (kDn + kDv) * 2, 128, 1))
+        return MLA_ERR_CUDA;
+    p.ws = static_cast<uint8_t *>(workspace);
+    p.out = static_cast<__nv_bfloat16 *>(out);
+    p.lse = lse;
+    p.kv_tokens = prob->kv_tokens;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.batch = prob->batch;
+    p.tokens = prob->tokens;
+    p.max_pages = prob->max_pages_per_seq;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * units));   // one CTA per SM
+    cfg.blockDim = dim3(kChunkThreads);
+    cfg.dynamicSmemBytes = kChunkSmem;
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    // passes of about the same number of heads
+    for (int32_t pass = 0; pass < passes; ++pass) {
+        p.head0 = (int32_t)((int64_t)kHeads * pass / passes);
+        p.heads = (int32_t)((int64_t)kHeads * (pass + 1) / passes) - p.head0;
+        if (launch_chunk_expand(prob, w_uk, w_uv, cache, fp8, num_pages, block_table, workspace, rope, kv, p.head0, p.heads,
+                                cfg.stream) != cudaSuccess ||
+            cudaLaunchKernelEx(&cfg, mla_chunk_kernel, p) != cudaSuccess)
+            return MLA_ERR_CUDA;
+    }
+    return MLA_OK;
+}
+
+}  // namespace
+}  // namespace mla
+
+extern "C" mla_status mla_chunk_scratch_size(const mla_chunk *prob, int32_t heads, size_t *bytes) {
+    const mla_status st = mla::check_chunk(prob);
+    if (st != MLA_OK) return st;
+    if (!bytes || heads < 1 || heads > mla::kHeads) return MLA_ERR_INVALID_ARG;
+    *bytes = mla::chunk_rope_bytes(prob->kv_tokens) + (size_t)heads * mla::chunk_head_bytes(prob->kv_tokens);
+    return MLA_OK;
+}
+
+extern "C" mla_status mla_chunk_attend(const mla_chunk *prob, const void *q_nope, int64_t nope_token_stride,
+                                       int64_t nope_head_stride, const void *q_rope, int64_t rope_token_stride,
+                                       int64_t rope_head_stride, const void *w_uk, const void *w_uv,
+                                       const void *kv_cache, int64_t num_pages, const int32_t *block_table, float scale,
+                                       void *out, float *lse, void *workspace, size_t workspace_bytes, void *scratch,
+                                       size_t scratch_bytes, mla_stream_t stream) {
+    mla::NvtxRange nvtx_range("mla_chunk_attend");
+    return mla::attend(prob, q_nope, nope_token_stride, nope_head_stride, q_rope, rope_token_stride, rope_head_stride, w_uk,
+                       w_uv, kv_cache, false, num_pages, block_table, scale, out, lse, workspace, workspace_bytes,
+                       scratch, scratch_bytes, stream);
+}
+
+extern "C" mla_status mla_chunk_attend_fp8(const mla_chunk *prob, const void *q_nope, int64_t nope_token_stride,
+                                           int64_t nope_head_stride, const void *q_rope, int64_t rope_token_stride,
+                                           int64_t rope_head_stride, const void *w_uk, const void *w_uv,
+                                           const void *kv_cache_fp8, int64_t num_pages, const int32_t *block_table,
+                                           float scale, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                                           void *scratch, size_t scratch_bytes, mla_stream_t stream) {
+    mla::NvtxRange nvtx_range("mla_chunk_attend_fp8");
+    return mla::attend(prob, q_nope, nope_token_stride, nope_head_stride, q_rope, rope_token_stride, rope_head_stride, w_uk,
+                       w_uv, kv_cache_fp8, true, num_pages, block_table, scale, out, lse, workspace, workspace_bytes,
+                       scratch, scratch_bytes, stream);
+}

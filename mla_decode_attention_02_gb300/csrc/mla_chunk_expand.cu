@@ -1,0 +1,435 @@
+// The keys and values of a step's chunks (include/mla_chunk.h): every cached row
+// that the chunks read, through W_UK and W_UV of a range of heads, into scratch.
+//
+//   K[h][j] = W_UK[h] r_j[0:512],  V[h][j] = W_UV[h] r_j[0:512]      512 -> 128 + 128, rounded to bf16
+//
+// A row's keys and values are worked out once, for all tokens that see them: 2 x
+// 131072 flops a head and row.  Left to the attention kernel they would be worked
+// out again for every tile of 256 tokens, more than doubling its products.
+//
+// GB300 design.  An SM pair holds 256 rows (four pages, 128 KB a CTA) as the A operand in
+// shared memory and runs heads against them: tcgen05.mma of both SMs (cta_group::2,
+// M = 256 rows, N = 256: the even CTA holds W_UK[h]'s half of B, the odd one W_UV[h]'s), so
+// that each SM reads 16 KB of weights per 512 clocks of MMA; one SM alone would have to take in 32 KB.
+//   warp 0       this CTA's half of the weights: 64-value K blocks through a ring of four
+//   warp 1       MMAs (even CTA): eight K blocks an item into one of two TMEM accumulators
+//   warps 2-3    the rows: by TMA from the pages (bf16), or expanded from e4m3 codes (exact), whose
+//                row scale multiplies the sums instead
+//   warps 4-11   the previous item's epilogue: TMEM -> bf16 -> 4 KB of swizzled staging a warp -> 128-byte
+//                pieces of rows; the even four take the keys, the others the values
+// Pages are packed one behind the other over all requests, so no row of the MMAs is wasted but in the last
+// pair's tile.  Rows past a request's end become zeros, so that a zero weight times them is zero; a
+// value that is not finite is kept finite and its key NaN, so that it spoils what sees it and nothing else.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <cstdint>
+#include <mutex>
+
+#include "mla_chunk.cuh"
+#include "mla_fp8.h"
+#include "mla_internal.h"
+#include "mla_rope.cuh"
+#include "sm103_ptx.cuh"
+
+namespace mla {
+bool encode_bf16_4d(CUtensorMap *m, const void *base, cuuint64_t d1, cuuint64_t d2, cuuint64_t d3,
+                    cuuint64_t s1, cuuint64_t s2, cuuint64_t s3, cuuint32_t rows, cuuint32_t blocks);
+cudaError_t main_units(int32_t *units);
+namespace {
+using namespace ptx;
+
+constexpr int kKBlocks = kDl / 64;
+constexpr int kStages = 4;
+constexpr int kEpiWarps = 8;
+constexpr int kExpandThreads = 32 * (4 + kEpiWarps);
+constexpr uint32_t kBlk = 128 * 128;                   // 128 rows x 64 values
+constexpr uint32_t kABytes = kKBlocks * kBlk;          // 128 KB
+constexpr uint32_t kOffB = kABytes, kOffStage = kOffB + kStages * kBlk;
+constexpr uint32_t kWarpStage = 32 * 128;              // a warp's staging: 32 rows x 64 values
+constexpr uint32_t kExpandSmem = kOffStage + kEpiWarps * kWarpStage + 1024;
+constexpr uint64_t kExpandWaitNs = 2000000000ull, kSettleNs = 1000000ull;
+constexpr float kBf16Max = 3.3895313892515355e38f;
+static_assert(kExpandSmem <= 232448 - 1024, "shared memory budget");
+static_assert(kDn == 128 && kDv == 128, "a CTA's half of B is one weight matrix's 128 rows");
+
+struct ExpandParams {
+    CUtensorMap tm_rows;   // bf16 cache as (64 dims, 64 tokens, 9 dim blocks, pages), box 64 x 64 x 1 x 1
+    CUtensorMap tm_uk;     // W_UK, W_UV as (64 values, 128 rows, 8 K blocks, heads), box 64 x 128 x 1 x 1
+    CUtensorMap tm_uv;
+    const uint8_t *cache;
+    const int32_t *block_table;
+    uint8_t *ws;
+    __nv_bfloat16 *rope, *kv;
+    int64_t num_pages, rows, kv_tokens;
+    int32_t batch, tokens, max_pages;
+    int32_t head0, heads;  // this pass's
+};
+
+struct Wait {
+    volatile int *abort;
+    int32_t *status;
+};
+
+// Bounded wait; on time-out flags the CTA (every other wait then gives up at once).  Phases that the
+// pair's other CTA completes are acquired at cluster scope.
+__device__ __noinline__ bool expand_wait(const Wait w, uint32_t bar, uint32_t parity) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 0;; ++i) {
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if ((i & 63) == 63) {
+            if (*w.abort) return false;
+            const uint64_t t = globaltimer_ns();
+            if (t0 == 0) t0 = t;
+            else if (t - t0 > kExpandWaitNs) {
+                *w.abort = 1;
+                atomicOr(w.status, MLA_DEV_TIMEOUT);
+                return false;
+            }
+        }
+    }
+}
+
+// Two e4m3 codes -> two bf16 values (exact).
+__device__ __forceinline__ uint32_t codes2(uint32_t codes) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes & 0xFFFFu), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    return pack_bf16x2(f.x, f.y);
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+template <bool kFp8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpandThreads, 1)
+mla_chunk_expand_kernel(const __grid_constant__ ExpandParams P) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 7];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    const uint32_t s_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    // full, rows landed and accumulator free are the even CTA's (both CTAs arrive there); the others are
+    // each CTA's own, which the MMAs' commits reach in both
+    enum { B_FULL = 0, B_EMPTY = kStages, B_AFULL = 2 * kStages, B_AFREE, B_ACC, B_ACCFREE = B_ACC + 2,
+           B_DRAIN = B_ACCFREE + 2 };
+    static_assert(B_DRAIN + 1 == 2 * kStages + 7, "barriers");
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    auto even = [&](int i) { return mapa(smem_u32(&bars[i]), 0); };
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(bar(B_FULL + s), 2);
+            mbar_init(bar(B_EMPTY + s), 1);
+        }
+        mbar_init(bar(B_AFULL), kFp8 ? 4 : 2);
+        mbar_init(bar(B_AFREE), 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar(B_ACC + b), 1);
+            mbar_init(bar(B_ACCFREE + b), 2 * kEpiWarps);
+        }
+        mbar_init(bar(B_DRAIN), 1);
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc_pair(smem_u32(&tmem_slot), 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // the pair's barriers are set up
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    pdl_wait_prior();
+    pdl_launch_dependents();
+
+    PlanHeader *hdr = reinterpret_cast<PlanHeader *>(P.ws);
+    const Wait w = {&abort_flag, &hdr->status};
+    const bool fits = hdr->magic == kChunkMagic && hdr->batch == P.batch && hdr->s_q == P.tokens &&
+                      hdr->max_pages == P.max_pages && hdr->total_cost == P.kv_tokens;   // (else flagged by the attention)
+    const int32_t num_pages = fits ? hdr->num_parts : 0;
+    const ChunkPage *pages =
+        reinterpret_cast<const ChunkPage *>(P.ws + chunk_layout(P.batch, P.tokens, P.kv_tokens).pages);
+    // An item is one head of four pages (of which the last may be the page of zeros).  Each pair takes a contiguous run,
+    // so that it loads rows a few times only.
+    const int32_t groups = num_pages > 0 ? num_pages / 4 + 1 : 0;
+    const int64_t items = (int64_t)groups * P.heads, pairs = gridDim.x / 2, c = blockIdx.x / 2;
+    const int64_t i0 = items * c / pairs, i1 = items * (c + 1) / pairs;
+
+    if (warp == 0) {
+        if (elect_one()) {
+            const CUtensorMap *tm = rank == 0 ? &P.tm_uk : &P.tm_uv;
+            prefetch_tmap(tm);
+            uint32_t n = 0;
+            bool ok = true;
+            for (int64_t i = i0; i < i1 && ok; ++i) {
+                const int h = P.head0 + (int)(i % P.heads);
+                for (int kb = 0; kb < kKBlocks; ++kb, ++n) {
+                    const uint32_t s = n % kStages;
+                    if (n >= kStages && !expand_wait(w, bar(B_EMPTY + s), (n / kStages - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx_cluster(even(B_FULL + s), kBlk);
+                    tma_load_4d_pair(s_base + kOffB + s * kBlk, tm, 0, 0, kb, h, even(B_FULL + s));
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (rank == 0 && elect_one()) {
+            constexpr uint32_t idesc = idesc_bf16(256, 256, 0, 0);
+            uint32_t n = 0, loads = 0;
+            int64_t group = -1;
+            bool ok = true;
+            for (int64_t i = i0; i < i1 && ok; ++i) {
+                const uint32_t k = (uint32_t)(i - i0), buf = k & 1;
+                if (i / P.heads != group) {
+                    group = i / P.heads;
+                    ok = expand_wait(w, bar(B_AFULL), loads++ & 1);
+                }
+                if (k >= 2) ok = ok && expand_wait(w, bar(B_ACCFREE + buf), (k / 2 - 1) & 1);
+                for (int kb = 0; kb < kKBlocks && ok; ++kb, ++n) {
+                    const uint32_t s = n % kStages;
+                    ok = expand_wait(w, bar(B_FULL + s), (n / kStages) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_ss_pair(tmem + buf * 256, smem_desc(s_base + kb * kBlk + ks * 32, 16, 1024, 2),
+                                    smem_desc(s_base + kOffB + s * kBlk + ks * 32, 16, 1024, 2), idesc,
+                                    (kb | ks) ? 1u : 0u);
+                    mma_commit_pair(bar(B_EMPTY + s));
+                }
+                if (!ok) break;
+                mma_commit_pair(bar(B_ACC + buf));
+                if (i + 1 == i1 || (i + 1) / P.heads != group) mma_commit_pair(bar(B_AFREE));
+            }
+            // every MMA is done before the CTAs give their memory up
+            mma_commit_pair(bar(B_DRAIN));
+        }
+        __syncwarp();
+    } else if (warp < 4) {
+        // ---- the rows of each group of pages
+        uint32_t loads = 0;
+        for (int64_t i = i0; i < i1; i = (i / P.heads + 1) * P.heads, ++loads) {
+            if (loads > 0 && !__all_sync(0xffffffffu, expand_wait(w, bar(B_AFREE), (loads - 1) & 1))) break;
+            const int32_t p0 = (int32_t)(i / P.heads) * 4 + (int32_t)rank * 2;
+            int32_t page[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                page[q] = p0 + q < num_pages ? P.block_table[pages[p0 + q].entry] : -1;
+                if (page[q] >= P.num_pages) page[q] = -1;
+            }
+            if constexpr (!kFp8) {
+                if (warp == 2 && elect_one()) {
+                    const uint32_t there = (page[0] >= 0) + (page[1] >= 0);
+                    mbar_arrive_expect_tx_cluster(even(B_AFULL), there * (kABytes / 2));
+                    for (int kb = 0; kb < kKBlocks; ++kb)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+                            if (page[q] >= 0)
+                                tma_load_4d_pair(s_base + kb * kBlk + q * (kBlk / 2), &P.tm_rows, 0, 0, kb, page[q],
+                                                 even(B_AFULL));
+                }
+                __syncwarp();
+            } else {
+                // a row a warp at a time: lane l expands codes 16 l .. 16 l + 15
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    if (page[q] < 0) continue;
+                    const uint8_t *src = P.cache + (size_t)page[q] * kPage * MLA_FP8_ROW_BYTES;
+#pragma unroll 8
+                    for (int r = warp - 2; r < kPage; r += 2) {
+                        const uint4 v = reinterpret_cast<const uint4 *>(src + r * MLA_FP8_ROW_BYTES)[lane];
+                        const uint32_t at = s_base + (lane >> 2) * kBlk + (q * kPage + r) * 128;
+                        const uint32_t u = (lane & 3) * 2, x = r & 7;
+                        st_shared_v4(at + ((u ^ x) << 4), codes2(v.x), codes2(v.x >> 16), codes2(v.y), codes2(v.y >> 16));
+                        st_shared_v4(at + (((u + 1) ^ x) << 4), codes2(v.z), codes2(v.z >> 16), codes2(v.w),
+                                     codes2(v.w >> 16));
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(even(B_AFULL));
+            }
+        }
+    } else {
+        // ---- accumulator rows [32 quarter, +32), the keys' or the values' 128 columns
+        const int quarter = warp & 3, part = (warp - 4) >> 2, row = quarter * 32 + lane;
+        const uint32_t stage = s_base + kOffStage + (warp - 4) * kWarpStage;
+        const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + part * 128;
+        int64_t group = -1;
+        bool there = false, spoilt = false;
+        float s_row = 1.f;
+        for (int64_t i = i0; i < i1; ++i) {
+            const uint32_t k = (uint32_t)(i - i0), buf = k & 1;
+            const int hl = (int)(i % P.heads);
+            const int64_t row0 = (i / P.heads) * kPairRows + rank * 128 + quarter * 32;   // the warp's first scratch row
+            if (i / P.heads != group) {
+                group = i / P.heads;
+                const int32_t p = (int32_t)group * 4 + (int32_t)rank * 2 + (row >> 6), r = row & 63;
+                there = spoilt = false;
+                s_row = 1.f;
+                int32_t page = -1;
+                if (p < num_pages) {
+                    const ChunkPage e = pages[p];
+                    page = P.block_table[e.entry];
+                    there = r < e.valid;
+                    spoilt = there && (page < 0 || page >= P.num_pages);
+                    if (spoilt) atomicOr(w.status, MLA_DEV_BAD_PAGE);
+                }
+                const bool read = there && !spoilt;
+                const uint8_t *src = P.cache + ((size_t)(read ? page : 0) * kPage + r) * (kFp8 ? MLA_FP8_ROW_BYTES : 2 * kDrow);
+                if (kFp8 && read) s_row = *reinterpret_cast<const float *>(src + kDl + 2 * kDr);
+                // the rotary part, once for all heads
+                if (P.head0 == 0 && hl == 0 && part == 0) {
+                    uint4 v[kDr / 8];
+#pragma unroll
+                    for (int j = 0; j < kDr / 8; ++j)
+                        v[j] = read ? reinterpret_cast<const uint4 *>(src + (kFp8 ? kDl : 2 * kDl))[j] : make_uint4(0, 0, 0, 0);
+                    uint4 *dst = reinterpret_cast<uint4 *>(P.rope + (row0 + lane) * kDr);
+#pragma unroll
+                    for (int j = 0; j < kDr / 8; ++j) {
+                        if constexpr (kFp8) {
+                            uint32_t *x = reinterpret_cast<uint32_t *>(&v[j]);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const float2 f = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&x[q]));
+                                x[q] = pack_bf16x2(f.x * s_row, f.y * s_row);
+                            }
+                        }
+                        dst[j] = v[j];
+                    }
+                }
+            }
+            if (!__all_sync(0xffffffffu, expand_wait(w, bar(B_ACC + buf), (k / 2) & 1))) break;
+            tc_fence_after();
+            const int j = lane & 7;
+            __nv_bfloat16 *out = P.kv + ((size_t)hl * P.rows + row0) * (kDn + kDv) + part * 128 + j * 8;
+            const float fill = part == 0 && spoilt ? __int_as_float(0x7fffffff) : 0.f;
+#pragma unroll 1
+            for (int c64 = 0; c64 < 2; ++c64) {   // 64 columns at a time
+#pragma unroll
+                for (int d = 0; d < 2; ++d) {
+                    uint32_t r[32];
+                    tmem_ld32(acc + buf * 256 + c64 * 64 + d * 32, r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        float f = __uint_as_float(r[e]);
+                        if constexpr (kFp8) f *= s_row;
+                        if (part == 0)
+                            f = fabsf(f) <= kBf16Max ? f : __int_as_float(0x7fffffff);
+                        else
+                            f = fminf(fmaxf(f, -kBf16Max), kBf16Max);   // (of a NaN: -kBf16Max)
+                        r[e] = __float_as_uint(there && !spoilt ? f : fill);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        st_shared_v4(stage + lane * 128 + (((d * 4 + q) ^ (lane & 7)) << 4),
+                                     pack_bf16x2(__uint_as_float(r[8 * q]), __uint_as_float(r[8 * q + 1])),
+                                     pack_bf16x2(__uint_as_float(r[8 * q + 2]), __uint_as_float(r[8 * q + 3])),
+                                     pack_bf16x2(__uint_as_float(r[8 * q + 4]), __uint_as_float(r[8 * q + 5])),
+                                     pack_bf16x2(__uint_as_float(r[8 * q + 6]), __uint_as_float(r[8 * q + 7])));
+                }
+                if (c64 == 1) tc_fence_before();
+                __syncwarp();
+                if (c64 == 1 && lane == 0) mbar_arrive_cluster(even(B_ACCFREE + buf));
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {   // four rows' 128 bytes at a time
+                    const int rr = 4 * q + (lane >> 3);
+                    uint4 v;
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                 : "r"(stage + rr * 128 + ((j ^ (rr & 7)) << 4))
+                                 : "memory");
+                    *reinterpret_cast<uint4 *>(out + c64 * 64 + (size_t)rr * (kDn + kDv)) = v;
+                }
+                __syncwarp();   // the staging is read before the next columns go in
+            }
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        expand_wait(w, bar(B_DRAIN), 0);
+        if (abort_flag) {   // copies may be in flight: they land within microseconds
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < kSettleNs) {
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // the other CTA reads nothing of this one's any more
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+std::mutex g_expand_mutex;
+bool g_expand_attr[64];
+
+}  // namespace
+
+// head0 .. head0 + heads - 1 of every page of the plan in ws, into kv (and the rotary parts into rope, with head 0).
+cudaError_t launch_chunk_expand(const mla_chunk *prob, const void *w_uk, const void *w_uv, const void *cache, bool fp8,
+                                int64_t num_pages, const int32_t *block_table, void *ws, void *rope, void *kv,
+                                int32_t head0, int32_t heads, cudaStream_t stream) {
+    int dev = 0;
+    int32_t units = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if ((e = main_units(&units)) != cudaSuccess) return e;
+    auto *kernel = fp8 ? mla_chunk_expand_kernel<true> : mla_chunk_expand_kernel<false>;
+    {
+        std::lock_guard<std::mutex> lock(g_expand_mutex);
+        if (!g_expand_attr[dev]) {
+            for (auto *k : {mla_chunk_expand_kernel<true>, mla_chunk_expand_kernel<false>})
+                if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kExpandSmem)) !=
+                    cudaSuccess)
+                    return e;
+            g_expand_attr[dev] = true;
+        }
+    }
+    ExpandParams p{};
+    if ((!fp8 && !encode_bf16_4d(&p.tm_rows, cache, kPage, kDrow / 64, (cuuint64_t)num_pages, kDrow * 2, 128,
+                                 (cuuint64_t)kPage * kDrow * 2, kPage, 1)) ||
+        !encode_bf16_4d(&p.tm_uk, w_uk, kDn, kKBlocks, kHeads, kDl * 2, 128, (cuuint64_t)kDn * kDl * 2, kDn, 1) ||
+        !encode_bf16_4d(&p.tm_uv, w_uv, kDv, kKBlocks, kHeads, kDl * 2, 128, (cuuint64_t)kDv * kDl * 2, kDv, 1))
+        return cudaErrorInvalidValue;
+    p.cache = static_cast<const uint8_t *>(cache);
+    p.block_table = block_table;
+    p.ws = static_cast<uint8_t *>(ws);
+    p.rope = static_cast<__nv_bfloat16 *>(rope);
+    p.kv = static_cast<__nv_bfloat16 *>(kv);
+    p.num_pages = num_pages;
+    p.rows = chunk_rows(prob->kv_tokens);
+    p.kv_tokens = prob->kv_tokens;
+    p.batch = prob->batch;
+    p.tokens = prob->tokens;
+    p.max_pages = prob->max_pages_per_seq;
+    p.head0 = head0;
+    p.heads = heads;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * units));   // an SM pair per unit
+    cfg.blockDim = dim3(kExpandThreads);
+    cfg.dynamicSmemBytes = kExpandSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace mla

@@ -75,12 +75,13 @@ struct Wait {
     int32_t *status;
 };
 
-// Bounded wait; on time-out flags the CTA (every other wait then gives up at once).  Phases that the
-// pair's other CTA completes are acquired at cluster scope.
-__device__ __noinline__ bool expand_wait(const Wait w, uint32_t bar, uint32_t parity) {
+// Bounded wait; on time-out flags the CTA (every other wait then gives up at once).  What the other CTA of the
+// pair completes carries data in one case only, the expanded rows, which is waited for at cluster scope.
+template <bool kCluster>
+__device__ __noinline__ bool wait_slow(const Wait w, uint32_t bar, uint32_t parity) {
     uint64_t t0 = 0;
     for (uint32_t i = 0;; ++i) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
         if ((i & 63) == 63) {
             if (*w.abort) return false;
             const uint64_t t = globaltimer_ns();
@@ -92,6 +93,10 @@ __device__ __noinline__ bool expand_wait(const Wait w, uint32_t bar, uint32_t pa
             }
         }
     }
+}
+
+__device__ __forceinline__ bool expand_wait(const Wait &w, uint32_t bar, uint32_t parity) {
+    return mbar_try_wait(bar, parity) || wait_slow<false>(w, bar, parity);
 }
 
 // Two e4m3 codes -> two bf16 values (exact).
@@ -176,7 +181,7 @@ mla_chunk_expand_kernel(const __grid_constant__ ExpandParams P) {
                         ok = false;
                         break;
                     }
-                    mbar_arrive_expect_tx_cluster(even(B_FULL + s), kBlk);
+                    mbar_expect_tx_cluster(even(B_FULL + s), kBlk);
                     tma_load_4d_pair(s_base + kOffB + s * kBlk, tm, 0, 0, kb, h, even(B_FULL + s));
                 }
             }
@@ -192,7 +197,7 @@ mla_chunk_expand_kernel(const __grid_constant__ ExpandParams P) {
                 const uint32_t k = (uint32_t)(i - i0), buf = k & 1;
                 if (i / P.heads != group) {
                     group = i / P.heads;
-                    ok = expand_wait(w, bar(B_AFULL), loads++ & 1);
+                    ok = wait_slow<kFp8>(w, bar(B_AFULL), loads++ & 1);
                 }
                 if (k >= 2) ok = ok && expand_wait(w, bar(B_ACCFREE + buf), (k / 2 - 1) & 1);
                 for (int kb = 0; kb < kKBlocks && ok; ++kb, ++n) {
@@ -230,7 +235,7 @@ mla_chunk_expand_kernel(const __grid_constant__ ExpandParams P) {
             if constexpr (!kFp8) {
                 if (warp == 2 && elect_one()) {
                     const uint32_t there = (page[0] >= 0) + (page[1] >= 0);
-                    mbar_arrive_expect_tx_cluster(even(B_AFULL), there * (kABytes / 2));
+                    mbar_expect_tx_cluster(even(B_AFULL), there * (kABytes / 2));
                     for (int kb = 0; kb < kKBlocks; ++kb)
 #pragma unroll
                         for (int q = 0; q < 2; ++q)
@@ -341,7 +346,7 @@ mla_chunk_expand_kernel(const __grid_constant__ ExpandParams P) {
                 }
                 if (c64 == 1) tc_fence_before();
                 __syncwarp();
-                if (c64 == 1 && lane == 0) mbar_arrive_cluster(even(B_ACCFREE + buf));
+                if (c64 == 1 && lane == 0) mbar_signal_cluster(even(B_ACCFREE + buf));
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {   // four rows' 128 bytes at a time
                     const int rr = 4 * q + (lane >> 3);

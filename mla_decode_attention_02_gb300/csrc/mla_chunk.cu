@@ -10,14 +10,15 @@
 //   warp 9      MMAs: S = q K^T (M = 128, N = 128, K = 192) into TMEM, and O += P V with P read from
 //               TMEM; the two tiles take turns, so that one's softmax runs while the other's products do
 //   warps 0-3   softmax of the first tile, one thread a row: S from TMEM, the running maximum and sum in
-//   warps 4-7   registers, P as bf16 back over S; the second tile's likewise
+//   warps 4-7   registers, P as fp16 back over S; the second tile's likewise
 // TMEM: S and O of both tiles, 4 x 128 columns, all of it.  A thread whose row's maximum grows by more than 2^8
 // rescales the row's O itself, which waits for the product before; smaller growth leaves the reference as it
-// is (exact: the reference is a shift).  Weights are rounded to bf16 for their product; the sum is taken of the
-// unrounded ones.
+// is (exact: the reference is a shift).  Weights (up to 2^8) and values are fp16 for their product, three bits
+// more than bf16; the sum is taken of the unrounded weights.
 // Bound by the tensor cores: 81,920 flops a (token, key) pair and 128 heads.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
@@ -67,6 +68,12 @@ struct ChunkParams {
     int32_t batch, tokens, max_pages, head0, heads;
 };
 
+// One head of a tile, on its way from the TMA warp to the others (head < 0: there are no more).
+struct ChunkItem {
+    ChunkTile tile;
+    int32_t head, pad[3];
+};
+
 struct Wait {
     volatile int *abort;
     int32_t *status;
@@ -92,6 +99,11 @@ __device__ __noinline__ bool wait_slow(const Wait w, uint32_t bar, uint32_t pari
 
 __device__ __forceinline__ bool wait(const Wait &w, uint32_t bar, uint32_t parity) {
     return mbar_try_wait(bar, parity) || wait_slow(w, bar, parity);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -126,15 +138,17 @@ __device__ __noinline__ void write_nan(const ChunkParams &P, const ChunkTile t, 
 
 __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __grid_constant__ ChunkParams P) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * kSlots + 13];
+    __shared__ __align__(8) uint64_t bars[2 * kSlots + 15];
+    __shared__ ChunkItem s_item[2];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const uint32_t s_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // + ring slot: landed, read; + tile: queries landed, queries read, S complete, P written, product done
+    // + ring slot: landed, read; + tile: queries landed, queries read, S complete, P written, product done;
+    // + item parity: item there, item read
     enum { B_FULL = 0, B_EMPTY = kSlots, B_QFULL = 2 * kSlots, B_QFREE = B_QFULL + 2, B_S = B_QFREE + 2, B_P = B_S + 2,
-           B_PV = B_P + 2, B_DRAIN = B_PV + 2 };
-    static_assert(B_DRAIN + 1 <= 2 * kSlots + 13, "barriers");
+           B_PV = B_P + 2, B_ITEM = B_PV + 2, B_TAKEN = B_ITEM + 2, B_DRAIN = B_TAKEN + 2 };
+    static_assert(B_DRAIN + 1 == 2 * kSlots + 15, "barriers");
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     if (threadIdx.x == 0) {
         abort_flag = 0;
@@ -148,6 +162,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
             mbar_init(bar(B_S + s), 1);
             mbar_init(bar(B_P + s), kSoftWarps / 2);
             mbar_init(bar(B_PV + s), 1);
+            mbar_init(bar(B_ITEM + s), 1);
+            mbar_init(bar(B_TAKEN + s), 1 + kSoftWarps);
         }
         mbar_init(bar(B_DRAIN), 1);
         fence_mbar_init();
@@ -169,12 +185,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
                       hdr->max_pages == P.max_pages && hdr->total_cost == P.kv_tokens;
     if (!fits && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&hdr->status, MLA_DEV_BAD_PLAN);
     const ChunkTile *tiles = reinterpret_cast<const ChunkTile *>(P.ws + chunk_layout(P.batch, P.tokens, P.kv_tokens).tiles);
-    // Items: head by head, a head's tiles together (they read the same keys), longest first.
-    const int64_t num_tiles = fits ? hdr->num_items : 0, items = num_tiles * P.heads;
+    // Items: head by head, a head's tiles together (they read the same keys), longest first.  A CTA begins with the
+    // item of its index and then takes whatever is next.
+    const int32_t num_tiles = fits ? hdr->num_items : 0;
+    const int64_t items = (int64_t)num_tiles * P.heads;
     // Key tiles of MMA tile s: up to the one with its last token's slot.
     auto key_tiles = [](const ChunkTile &t, int s) {
         const int last = (t.count < 128 * (s + 1) ? t.count : 128 * (s + 1)) - 1;
         return last < 128 * s ? 0 : (t.slot0 + last) / kKeys + 1;
+    };
+    // The k-th item of this CTA, as the MMA thread or a softmax warp sees it.
+    auto item_of = [&](uint32_t k, bool &ok) {
+        ChunkItem it;
+        it.head = -1;
+        if (ok) ok = wait(w, bar(B_ITEM + (k & 1)), (k >> 1) & 1);
+        if (ok) it = s_item[k & 1];
+        return it;
     };
 
     if (warp == kTmaWarp) {
@@ -193,25 +219,37 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
                 tma_load_4d(s_base + kOffRing + s * kBlk, tm, 0, row, blk, h, bar(B_FULL + s));
                 ++n;
             };
-            for (int64_t i = blockIdx.x; i < items && ok; i += gridDim.x) {
-                const ChunkTile t = tiles[i % num_tiles];
+            int64_t i = blockIdx.x;
+            for (uint32_t k = 0; ok; ++k) {
+                ChunkItem it;
+                it.head = i < items ? (int32_t)(i / num_tiles) : -1;
+                if (it.head >= 0) it.tile = tiles[(int32_t)(i % num_tiles)];
+                if (k >= 2) ok = wait(w, bar(B_TAKEN + (k & 1)), ((k >> 1) - 1) & 1);
+                if (!ok) break;
+                s_item[k & 1] = it;
+                mbar_arrive(bar(B_ITEM + (k & 1)));
+                if (it.head < 0) break;
+                i = gridDim.x + (int64_t)atomicAdd(reinterpret_cast<unsigned long long *>(&hdr->target), 1ull);
+                const ChunkTile &t = it.tile;
                 if (t.slot0 < 0) continue;
-                const int hl = (int)(i / num_tiles), h = P.head0 + hl;
+                const int hl = it.head, h = P.head0 + hl;
                 const int n0 = key_tiles(t, 0), n1 = key_tiles(t, 1);
-                for (int s = 0; s < (n1 ? 2 : 1) && ok; ++s) {
-                    if (loads[s]) ok = wait(w, bar(B_QFREE + s), (loads[s] - 1) & 1);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(bar(B_QFULL + s), kQTile);
-                    tma_load_4d(s_base + s * kQTile, &P.tm_qn, 0, t.t0 + 128 * s, 0, h, bar(B_QFULL + s));
-                    tma_load_4d(s_base + s * kQTile + 2 * kBlk, &P.tm_qr, 0, t.t0 + 128 * s, 0, h, bar(B_QFULL + s));
-                    ++loads[s];
-                }
                 const int n_max = n1 > n0 ? n1 : n0;
                 for (int j = 0; j < n_max && ok; ++j) {
                     const int row = t.base + j * kKeys;
                     load(&P.tm_kv, row, 0, hl);
                     load(&P.tm_kv, row, 1, hl);
                     load(&P.tm_kr, row, 0, 0);
+                    if (j == 0) {   // the queries, once the item before has read its own
+                        for (int s = 0; s < (n1 ? 2 : 1) && ok; ++s) {
+                            if (loads[s]) ok = wait(w, bar(B_QFREE + s), (loads[s] - 1) & 1);
+                            if (!ok) break;
+                            mbar_arrive_expect_tx(bar(B_QFULL + s), kQTile);
+                            tma_load_4d(s_base + s * kQTile, &P.tm_qn, 0, t.t0 + 128 * s, 0, h, bar(B_QFULL + s));
+                            tma_load_4d(s_base + s * kQTile + 2 * kBlk, &P.tm_qr, 0, t.t0 + 128 * s, 0, h, bar(B_QFULL + s));
+                            ++loads[s];
+                        }
+                    }
                     load(&P.tm_kv, row, 2, hl);
                     load(&P.tm_kv, row, 3, hl);
                 }
@@ -225,7 +263,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
         __syncwarp();
     } else if (warp == kMmaWarp) {
         if (elect_one()) {
-            constexpr uint32_t idesc_s = idesc_bf16(128, kKeys, 0, 0), idesc_o = idesc_bf16(128, 64, 0, 1);
+            constexpr uint32_t idesc_s = idesc_bf16(128, kKeys, 0, 0), idesc_o = idesc_f16(128, 64, 0, 1);
             uint32_t n = 0, q_used[2] = {0, 0}, p_used[2] = {0, 0};   // n: ring blocks before this item's
             bool ok = true;
             auto landed = [&](uint32_t k) { ok = ok && wait(w, bar(B_FULL + k % kSlots), (k / kSlots) & 1); };
@@ -261,8 +299,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
             auto release = [&](uint32_t k, int count) {
                 for (int b = 0; b < count; ++b) mma_commit(bar(B_EMPTY + (k + b) % kSlots));
             };
-            for (int64_t i = blockIdx.x; i < items && ok; i += gridDim.x) {
-                const ChunkTile t = tiles[i % num_tiles];
+            for (uint32_t item = 0; ok; ++item) {
+                const ChunkItem it = item_of(item, ok);
+                if (it.head < 0) break;
+                mbar_arrive(bar(B_TAKEN + (item & 1)));
+                const ChunkTile &t = it.tile;
                 if (t.slot0 < 0) continue;
                 const int nk[2] = {key_tiles(t, 0), key_tiles(t, 1)};
                 const int n_max = nk[1] > nk[0] ? nk[1] : nk[0];
@@ -301,9 +342,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
         const uint32_t col_s = lanes + kColS + s * 128, col_o = lanes + kColO + s * 128;
         uint32_t phase = 0;   // key tiles before this item's
         bool ok = true;
-        for (int64_t i = blockIdx.x; i < items && ok; i += gridDim.x) {
-            const ChunkTile t = tiles[i % num_tiles];
-            const int h = P.head0 + (int)(i / num_tiles);
+        for (uint32_t item = 0; ok; ++item) {
+            const ChunkItem it = item_of(item, ok);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok || it.head < 0) break;
+            if (lane == 0) mbar_arrive(bar(B_TAKEN + (item & 1)));
+            const ChunkTile &t = it.tile;
+            const int h = P.head0 + it.head;
             if (t.slot0 < 0) {
                 write_nan(P, t, h, threadIdx.x, 32 * kSoftWarps);
                 continue;
@@ -371,7 +416,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
                         const float a = ex2(fmaf(x[c * 64 + 2 * e], P.scale_log2, -shift));
                         const float b = ex2(fmaf(x[c * 64 + 2 * e + 1], P.scale_log2, -shift));
                         part[e & 3] += a + b;
-                        r[e] = pack_bf16x2(a, b);
+                        r[e] = pack_f16x2(a, b);
                     }
                     tmem_st32(col_s + c * 32, r);
                 }

@@ -1,7 +1,11 @@
 // The keys and values of a step's chunks (include/mla_chunk.h): every cached row
 // that the chunks read, through W_UK and W_UV of a range of heads, into scratch.
 //
-//   K[h][j] = W_UK[h] r_j[0:512],  V[h][j] = W_UV[h] r_j[0:512]      512 -> 128 + 128, rounded to bf16
+//   K[h][j] = W_UK[h] r_j[0:512],  V[h][j] = W_UV[h] r_j[0:512]      512 -> 128 + 128
+//
+// Keys are rounded to bf16, the queries' type; values to fp16, which has three bits more (the product with the
+// weights would be the larger part of the output's error: 700 keys 2.9e-3 of its norm with bf16 values and
+// weights) and reaches 65504; a value beyond that is infinite and shows.
 //
 // A row's keys and values are worked out once, for all tokens that see them: 2 x
 // 131072 flops a head and row.  Left to the attention kernel they would be worked
@@ -15,11 +19,12 @@
 //   warp 1       MMAs (even CTA): eight K blocks an item into one of two TMEM accumulators
 //   warps 2-3    the rows: by TMA from the pages (bf16), or expanded from e4m3 codes (exact), whose
 //                row scale multiplies the sums instead
-//   warps 4-11   the previous item's epilogue: TMEM -> bf16 -> 4 KB of swizzled staging a warp -> 128-byte
-//                pieces of rows; the even four take the keys, the others the values
+//   warps 4-11   the previous item's epilogue: TMEM -> 16 bits -> 4 KB of swizzled staging a warp -> 128-byte
+//                pieces of rows; the first four take the keys, the others the values
 // Pages are packed one behind the other over all requests, so no row of the MMAs is wasted but in the last
-// pair's tile.  Rows past a request's end become zeros, so that a zero weight times them is zero; a
-// value that is not finite is kept finite and its key NaN, so that it spoils what sees it and nothing else.
+// pair's tile.  Rows past a request's end become zeros, so that a zero weight times them is zero; the
+// key of a row that is not finite becomes NaN and its values zeros, so that it spoils what sees it and nothing
+// else.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -53,7 +58,6 @@ constexpr uint32_t kOffB = kABytes, kOffStage = kOffB + kStages * kBlk;
 constexpr uint32_t kWarpStage = 32 * 128;              // a warp's staging: 32 rows x 64 values
 constexpr uint32_t kExpandSmem = kOffStage + kEpiWarps * kWarpStage + 1024;
 constexpr uint64_t kExpandWaitNs = 2000000000ull, kSettleNs = 1000000ull;
-constexpr float kBf16Max = 3.3895313892515355e38f;
 static_assert(kExpandSmem <= 232448 - 1024, "shared memory budget");
 static_assert(kDn == 128 && kDv == 128, "a CTA's half of B is one weight matrix's 128 rows");
 
@@ -106,8 +110,125 @@ __device__ __forceinline__ uint32_t codes2(uint32_t codes) {
     return pack_bf16x2(f.x, f.y);
 }
 
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
 __device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// A warp's share of the items: 32 accumulator rows (lane: one row), the keys' 128 columns (kPart 0) or the
+// values' (1).  The accumulator is given back as soon as it is in registers, rounded; what is not an ordinary
+// finite row is mended there, in a branch that no other takes.
+template <bool kFp8, int kPart>
+__device__ __forceinline__ void epilogue(const ExpandParams &P, const Wait &w, const ChunkPage *pages, int32_t num_pages,
+                                         int64_t i0, int64_t i1, uint32_t rank, int row, uint32_t stage, uint32_t acc,
+                                         uint32_t b_acc, uint32_t b_free) {
+    const int lane = row & 31, j = lane & 7;
+    bool there = false, spoilt = false;
+    float s_row = 1.f;
+    int32_t group = (int32_t)(i0 / P.heads), hl = (int32_t)(i0 % P.heads);
+    bool fresh = true;
+    for (uint32_t k = 0; k < (uint32_t)(i1 - i0); ++k) {
+        const uint32_t buf = k & 1;
+        const int64_t row0 = (int64_t)group * kPairRows + rank * 128 + (row - lane);   // the warp's first scratch row
+        if (fresh) {
+            fresh = false;
+            const int32_t p = group * 4 + (int32_t)rank * 2 + (row >> 6), r = row & 63;
+            there = spoilt = false;
+            s_row = 1.f;
+            int32_t page = -1;
+            if (p < num_pages) {
+                const ChunkPage e = pages[p];
+                page = P.block_table[e.entry];
+                there = r < e.valid;
+                spoilt = there && (page < 0 || page >= P.num_pages);
+                if (spoilt) atomicOr(w.status, MLA_DEV_BAD_PAGE);
+            }
+            const bool read = there && !spoilt;
+            const uint8_t *src = P.cache + ((size_t)(read ? page : 0) * kPage + r) * (kFp8 ? MLA_FP8_ROW_BYTES : 2 * kDrow);
+            if (kFp8 && read) s_row = *reinterpret_cast<const float *>(src + kDl + 2 * kDr);
+            if (kPart == 0 && P.head0 == 0 && hl == 0) {   // the rotary part, once for all heads
+                uint4 v[kDr / 8];
+#pragma unroll
+                for (int q = 0; q < kDr / 8; ++q)
+                    v[q] = read ? reinterpret_cast<const uint4 *>(src + (kFp8 ? kDl : 2 * kDl))[q] : make_uint4(0, 0, 0, 0);
+                uint4 *dst = reinterpret_cast<uint4 *>(P.rope + (row0 + lane) * kDr);
+#pragma unroll
+                for (int q = 0; q < kDr / 8; ++q) {
+                    if constexpr (kFp8) {
+                        uint32_t *x = reinterpret_cast<uint32_t *>(&v[q]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 f = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&x[e]));
+                            x[e] = pack_bf16x2(f.x * s_row, f.y * s_row);
+                        }
+                    }
+                    dst[q] = v[q];
+                }
+            }
+        }
+        if (!__all_sync(0xffffffffu, expand_wait(w, b_acc + 8 * buf, (k / 2) & 1))) break;
+        tc_fence_after();
+        uint32_t x[64];
+        bool odd = !there || spoilt;   // a row that is no ordinary one, or holds a value that is not finite
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            uint32_t r[2][32];
+            tmem_ld32(acc + buf * 256 + c * 64, r[0]);
+            tmem_ld32(acc + buf * 256 + c * 64 + 32, r[1]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float a = __uint_as_float(r[d][2 * e]), b = __uint_as_float(r[d][2 * e + 1]);
+                    if constexpr (kFp8) {
+                        a *= s_row;
+                        b *= s_row;
+                    }
+                    odd |= !(fabsf(a) < INFINITY);
+                    odd |= !(fabsf(b) < INFINITY);
+                    x[c * 32 + d * 16 + e] = kPart == 0 ? pack_bf16x2(a, b) : pack_f16x2(a, b);
+                }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_signal_cluster(b_free + 8 * buf);
+        if (__any_sync(0xffffffffu, odd) && odd) {
+            // a row that is not there: zeros; else the key is NaN, and the value a number
+            const uint32_t fill = kPart == 0 && there ? 0x7fff7fffu : 0u;
+#pragma unroll
+            for (int e = 0; e < 64; ++e) x[e] = fill;
+        }
+        __nv_bfloat16 *out = P.kv + ((size_t)hl * P.rows + row0) * (kDn + kDv) + kPart * 128 + j * 8;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {   // 64 columns at a time
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                st_shared_v4(stage + lane * 128 + ((q ^ j) << 4), x[c * 32 + 4 * q], x[c * 32 + 4 * q + 1],
+                             x[c * 32 + 4 * q + 2], x[c * 32 + 4 * q + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {   // four rows' 128 bytes at a time
+                const int rr = 4 * q + (lane >> 3);
+                uint4 v;
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                             : "r"(stage + rr * 128 + ((j ^ (rr & 7)) << 4))
+                             : "memory");
+                *reinterpret_cast<uint4 *>(out + c * 64 + (size_t)rr * (kDn + kDv)) = v;
+            }
+            __syncwarp();   // the staging is read before the next columns go in
+        }
+        if (++hl == P.heads) {
+            hl = 0;
+            ++group;
+            fresh = true;
+        }
+    }
 }
 
 template <bool kFp8>
@@ -159,6 +280,7 @@ mla_chunk_expand_kernel(const __grid_constant__ ExpandParams P) {
     const bool fits = hdr->magic == kChunkMagic && hdr->batch == P.batch && hdr->s_q == P.tokens &&
                       hdr->max_pages == P.max_pages && hdr->total_cost == P.kv_tokens;   // (else flagged by the attention)
     const int32_t num_pages = fits ? hdr->num_parts : 0;
+    if (fits && blockIdx.x == 0 && threadIdx.x == 0) hdr->target = 0;   // the attention's items taken so far
     const ChunkPage *pages =
         reinterpret_cast<const ChunkPage *>(P.ws + chunk_layout(P.batch, P.tokens, P.kv_tokens).pages);
     // An item is one head of four pages (of which the last may be the page of zeros).  Each pair takes a contiguous run,
@@ -173,8 +295,9 @@ mla_chunk_expand_kernel(const __grid_constant__ ExpandParams P) {
             prefetch_tmap(tm);
             uint32_t n = 0;
             bool ok = true;
-            for (int64_t i = i0; i < i1 && ok; ++i) {
-                const int h = P.head0 + (int)(i % P.heads);
+            int hl = (int)(i0 % P.heads);
+            for (int64_t i = i0; i < i1 && ok; ++i, hl = hl + 1 == P.heads ? 0 : hl + 1) {
+                const int h = P.head0 + hl;
                 for (int kb = 0; kb < kKBlocks; ++kb, ++n) {
                     const uint32_t s = n % kStages;
                     if (n >= kStages && !expand_wait(w, bar(B_EMPTY + s), (n / kStages - 1) & 1)) {
@@ -191,14 +314,11 @@ mla_chunk_expand_kernel(const __grid_constant__ ExpandParams P) {
         if (rank == 0 && elect_one()) {
             constexpr uint32_t idesc = idesc_bf16(256, 256, 0, 0);
             uint32_t n = 0, loads = 0;
-            int64_t group = -1;
+            int hl = (int)(i0 % P.heads);
             bool ok = true;
-            for (int64_t i = i0; i < i1 && ok; ++i) {
+            for (int64_t i = i0; i < i1 && ok; ++i, hl = hl + 1 == P.heads ? 0 : hl + 1) {
                 const uint32_t k = (uint32_t)(i - i0), buf = k & 1;
-                if (i / P.heads != group) {
-                    group = i / P.heads;
-                    ok = wait_slow<kFp8>(w, bar(B_AFULL), loads++ & 1);
-                }
+                if (i == i0 || hl == 0) ok = wait_slow<kFp8>(w, bar(B_AFULL), loads++ & 1);
                 if (k >= 2) ok = ok && expand_wait(w, bar(B_ACCFREE + buf), (k / 2 - 1) & 1);
                 for (int kb = 0; kb < kKBlocks && ok; ++kb, ++n) {
                     const uint32_t s = n % kStages;
@@ -214,7 +334,7 @@ mla_chunk_expand_kernel(const __grid_constant__ ExpandParams P) {
                 }
                 if (!ok) break;
                 mma_commit_pair(bar(B_ACC + buf));
-                if (i + 1 == i1 || (i + 1) / P.heads != group) mma_commit_pair(bar(B_AFREE));
+                if (i + 1 == i1 || hl + 1 == P.heads) mma_commit_pair(bar(B_AFREE));
             }
             // every MMA is done before the CTAs give their memory up
             mma_commit_pair(bar(B_DRAIN));
@@ -267,99 +387,13 @@ mla_chunk_expand_kernel(const __grid_constant__ ExpandParams P) {
         }
     } else {
         // ---- accumulator rows [32 quarter, +32), the keys' or the values' 128 columns
-        const int quarter = warp & 3, part = (warp - 4) >> 2, row = quarter * 32 + lane;
-        const uint32_t stage = s_base + kOffStage + (warp - 4) * kWarpStage;
-        const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + part * 128;
-        int64_t group = -1;
-        bool there = false, spoilt = false;
-        float s_row = 1.f;
-        for (int64_t i = i0; i < i1; ++i) {
-            const uint32_t k = (uint32_t)(i - i0), buf = k & 1;
-            const int hl = (int)(i % P.heads);
-            const int64_t row0 = (i / P.heads) * kPairRows + rank * 128 + quarter * 32;   // the warp's first scratch row
-            if (i / P.heads != group) {
-                group = i / P.heads;
-                const int32_t p = (int32_t)group * 4 + (int32_t)rank * 2 + (row >> 6), r = row & 63;
-                there = spoilt = false;
-                s_row = 1.f;
-                int32_t page = -1;
-                if (p < num_pages) {
-                    const ChunkPage e = pages[p];
-                    page = P.block_table[e.entry];
-                    there = r < e.valid;
-                    spoilt = there && (page < 0 || page >= P.num_pages);
-                    if (spoilt) atomicOr(w.status, MLA_DEV_BAD_PAGE);
-                }
-                const bool read = there && !spoilt;
-                const uint8_t *src = P.cache + ((size_t)(read ? page : 0) * kPage + r) * (kFp8 ? MLA_FP8_ROW_BYTES : 2 * kDrow);
-                if (kFp8 && read) s_row = *reinterpret_cast<const float *>(src + kDl + 2 * kDr);
-                // the rotary part, once for all heads
-                if (P.head0 == 0 && hl == 0 && part == 0) {
-                    uint4 v[kDr / 8];
-#pragma unroll
-                    for (int j = 0; j < kDr / 8; ++j)
-                        v[j] = read ? reinterpret_cast<const uint4 *>(src + (kFp8 ? kDl : 2 * kDl))[j] : make_uint4(0, 0, 0, 0);
-                    uint4 *dst = reinterpret_cast<uint4 *>(P.rope + (row0 + lane) * kDr);
-#pragma unroll
-                    for (int j = 0; j < kDr / 8; ++j) {
-                        if constexpr (kFp8) {
-                            uint32_t *x = reinterpret_cast<uint32_t *>(&v[j]);
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const float2 f = __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&x[q]));
-                                x[q] = pack_bf16x2(f.x * s_row, f.y * s_row);
-                            }
-                        }
-                        dst[j] = v[j];
-                    }
-                }
-            }
-            if (!__all_sync(0xffffffffu, expand_wait(w, bar(B_ACC + buf), (k / 2) & 1))) break;
-            tc_fence_after();
-            const int j = lane & 7;
-            __nv_bfloat16 *out = P.kv + ((size_t)hl * P.rows + row0) * (kDn + kDv) + part * 128 + j * 8;
-            const float fill = part == 0 && spoilt ? __int_as_float(0x7fffffff) : 0.f;
-#pragma unroll 1
-            for (int c64 = 0; c64 < 2; ++c64) {   // 64 columns at a time
-#pragma unroll
-                for (int d = 0; d < 2; ++d) {
-                    uint32_t r[32];
-                    tmem_ld32(acc + buf * 256 + c64 * 64 + d * 32, r);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        float f = __uint_as_float(r[e]);
-                        if constexpr (kFp8) f *= s_row;
-                        if (part == 0)
-                            f = fabsf(f) <= kBf16Max ? f : __int_as_float(0x7fffffff);
-                        else
-                            f = fminf(fmaxf(f, -kBf16Max), kBf16Max);   // (of a NaN: -kBf16Max)
-                        r[e] = __float_as_uint(there && !spoilt ? f : fill);
-                    }
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        st_shared_v4(stage + lane * 128 + (((d * 4 + q) ^ (lane & 7)) << 4),
-                                     pack_bf16x2(__uint_as_float(r[8 * q]), __uint_as_float(r[8 * q + 1])),
-                                     pack_bf16x2(__uint_as_float(r[8 * q + 2]), __uint_as_float(r[8 * q + 3])),
-                                     pack_bf16x2(__uint_as_float(r[8 * q + 4]), __uint_as_float(r[8 * q + 5])),
-                                     pack_bf16x2(__uint_as_float(r[8 * q + 6]), __uint_as_float(r[8 * q + 7])));
-                }
-                if (c64 == 1) tc_fence_before();
-                __syncwarp();
-                if (c64 == 1 && lane == 0) mbar_signal_cluster(even(B_ACCFREE + buf));
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {   // four rows' 128 bytes at a time
-                    const int rr = 4 * q + (lane >> 3);
-                    uint4 v;
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                                 : "r"(stage + rr * 128 + ((j ^ (rr & 7)) << 4))
-                                 : "memory");
-                    *reinterpret_cast<uint4 *>(out + c64 * 64 + (size_t)rr * (kDn + kDv)) = v;
-                }
-                __syncwarp();   // the staging is read before the next columns go in
-            }
-        }
+        const int quarter = warp & 3, row = quarter * 32 + lane;
+        if (warp < 8)
+            epilogue<kFp8, 0>(P, w, pages, num_pages, i0, i1, rank, row, s_base + kOffStage + (warp - 4) * kWarpStage,
+                              tmem + ((uint32_t)(quarter * 32) << 16), bar(B_ACC), even(B_ACCFREE));
+        else
+            epilogue<kFp8, 1>(P, w, pages, num_pages, i0, i1, rank, row, s_base + kOffStage + (warp - 4) * kWarpStage,
+                              tmem + ((uint32_t)(quarter * 32) << 16) + 128, bar(B_ACC), even(B_ACCFREE));
     }
     __syncthreads();
     if (threadIdx.x == 0) {

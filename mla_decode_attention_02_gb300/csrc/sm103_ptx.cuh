@@ -413,5 +413,10 @@ __host__ __device__ constexpr uint32_t idesc_bf16(uint32_t M, uint32_t N, uint32
            | ((M >> 4) << 24);  // M / 16
 }
 
+// The same with fp16 A and B.
+__host__ __device__ constexpr uint32_t idesc_f16(uint32_t M, uint32_t N, uint32_t a_mn, uint32_t b_mn) {
+    return idesc_bf16(M, N, a_mn, b_mn) & ~((7u << 7) | (7u << 10));
+}
+
 }  // namespace ptx
 }  // namespace mla

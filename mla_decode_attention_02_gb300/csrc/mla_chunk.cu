@@ -378,9 +378,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
 #pragma unroll
                     for (int e = 0; e < kKeys; ++e) x[e] = e <= limit ? x[e] : -INFINITY;
                 }
-                float top = x[0];
+                float tops[8];   // eight chains: one would be 128 dependent steps
 #pragma unroll
-                for (int e = 1; e < kKeys; ++e) top = fmaxf(top, x[e]);
+                for (int e = 0; e < 8; ++e) tops[e] = fmaxf(x[e], x[8 + e]);
+#pragma unroll
+                for (int e = 16; e < kKeys; e += 16)
+#pragma unroll
+                    for (int g = 0; g < 8; ++g) tops[g] = fmaxf(fmaxf(tops[g], x[e + g]), x[e + 8 + g]);
+                const float top = fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
+                                        fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
                 // raise the reference if the row's maximum outgrew it (the first tile: from nothing)
                 const bool raise = (top - m) * P.scale_log2 > kRescale;
                 if (__any_sync(0xffffffffu, raise)) {
@@ -406,21 +412,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
                         }
                     }
                 }
-                const float shift = m * P.scale_log2;
-                float part[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t scale2 = pair(P.scale_log2, P.scale_log2), shift2 = pair(-m * P.scale_log2, -m * P.scale_log2);
+                uint64_t part[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t r[32];
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t r[16];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const float a = ex2(fmaf(x[c * 64 + 2 * e], P.scale_log2, -shift));
-                        const float b = ex2(fmaf(x[c * 64 + 2 * e + 1], P.scale_log2, -shift));
-                        part[e & 3] += a + b;
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 y = unpair(fma_pair(pair(x[c * 32 + 2 * e], x[c * 32 + 2 * e + 1]), scale2, shift2));
+                        const float a = ex2(y.x), b = ex2(y.y);
+                        part[e & 3] = add_pair(part[e & 3], pair(a, b));
                         r[e] = pack_f16x2(a, b);
                     }
-                    tmem_st32(col_s + c * 32, r);
+                    tmem_st16(col_s + c * 16, r);
                 }
-                sum += (part[0] + part[1]) + (part[2] + part[3]);
+                const float2 all = unpair(add_pair(add_pair(part[0], part[1]), add_pair(part[2], part[3])));
+                sum += all.x + all.y;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();

@@ -122,6 +122,20 @@ __device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t a, uint32_t b
 // A warp's share of the items: 32 accumulator rows (lane: one row), the keys' 128 columns (kPart 0) or the
 // values' (1).  The accumulator is given back as soon as it is in registers, rounded; what is not an ordinary
 // finite row is mended there, in a branch that no other takes.
+// Stores whose lines leave L2 before others: the scratch is larger than L2 in the cases that take long, and
+// would drive out the weights that every group of rows reads again.
+__device__ __forceinline__ uint64_t l2_evict_first() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
+__device__ __forceinline__ void st_global_first(void *at, uint4 v, uint64_t policy) {
+    asm volatile("st.global.L2::cache_hint.v4.b32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(at), "r"(v.x), "r"(v.y), "r"(v.z),
+                 "r"(v.w), "l"(policy)
+                 : "memory");
+}
+
 template <bool kFp8, int kPart>
 __device__ __forceinline__ void epilogue(const ExpandParams &P, const Wait &w, const ChunkPage *pages, int32_t num_pages,
                                          int64_t i0, int64_t i1, uint32_t rank, int row, uint32_t stage, uint32_t acc,
@@ -129,6 +143,7 @@ __device__ __forceinline__ void epilogue(const ExpandParams &P, const Wait &w, c
     const int lane = row & 31, j = lane & 7;
     bool there = false, spoilt = false;
     float s_row = 1.f;
+    const uint64_t policy = l2_evict_first();
     int32_t group = (int32_t)(i0 / P.heads), hl = (int32_t)(i0 % P.heads);
     bool fresh = true;
     for (uint32_t k = 0; k < (uint32_t)(i1 - i0); ++k) {
@@ -219,7 +234,7 @@ __device__ __forceinline__ void epilogue(const ExpandParams &P, const Wait &w, c
                              : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                              : "r"(stage + rr * 128 + ((j ^ (rr & 7)) << 4))
                              : "memory");
-                *reinterpret_cast<uint4 *>(out + c * 64 + (size_t)rr * (kDn + kDv)) = v;
+                st_global_first(out + c * 64 + (size_t)rr * (kDn + kDv), v, policy);
             }
             __syncwarp();   // the staging is read before the next columns go in
         }

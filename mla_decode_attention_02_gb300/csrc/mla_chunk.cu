@@ -123,6 +123,20 @@ __device__ __noinline__ void wait_landed(const Wait w, uint32_t bar, uint32_t pa
     }
 }
 
+// Multiply a row's 128 output values in TMEM.
+__device__ __noinline__ void rescale(uint32_t col, float f) {
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        uint32_t r[32];
+        tmem_ld32(col + c * 32, r);
+        tmem_wait_ld(r);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+        tmem_st32(col + c * 32, r);
+    }
+    tmem_wait_st();
+}
+
 // A tile in error: its rows' outputs are NaN.
 __device__ __noinline__ void write_nan(const ChunkParams &P, const ChunkTile t, int head, int thread, int threads) {
     const uint32_t nan2 = 0x7fff7fffu;
@@ -241,7 +255,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
                     load(&P.tm_kv, row, 1, hl);
                     load(&P.tm_kr, row, 0, 0);
                     if (j == 0) {   // the queries, once the item before has read its own
-                        for (int s = 0; s < (n1 ? 2 : 1) && ok; ++s) {
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            if (s == 1 && !n1) break;
                             if (loads[s]) ok = wait(w, bar(B_QFREE + s), (loads[s] - 1) & 1);
                             if (!ok) break;
                             mbar_arrive_expect_tx(bar(B_QFULL + s), kQTile);
@@ -257,6 +273,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
             // every copy has landed before the CTA gives its memory up
             for (uint32_t k = n > kSlots ? n - kSlots : 0; k < n; ++k)
                 wait_landed(w, bar(B_FULL + k % kSlots), (k / kSlots) & 1);
+#pragma unroll
             for (int s = 0; s < 2; ++s)
                 if (loads[s]) wait_landed(w, bar(B_QFULL + s), (loads[s] - 1) & 1);
         }
@@ -307,6 +324,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
                 if (t.slot0 < 0) continue;
                 const int nk[2] = {key_tiles(t, 0), key_tiles(t, 1)};
                 const int n_max = nk[1] > nk[0] ? nk[1] : nk[0];
+#pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     if (!nk[s]) continue;
                     ok = ok && wait(w, bar(B_QFULL + s), q_used[s]++ & 1);
@@ -314,6 +332,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
                 }
                 if (!ok) break;
                 release(n, 3);
+#pragma unroll
                 for (int s = 0; s < 2; ++s)
                     if (nk[s] == 1) mma_commit(bar(B_QFREE + s));
                 for (int j = 0; j < n_max && ok; ++j) {
@@ -364,32 +383,47 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
                     break;
                 }
                 tc_fence_after();
-                float x[kKeys];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t r[32];
-                    tmem_ld32(col_s + c * 32, r);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) x[c * 32 + e] = __uint_as_float(r[e]);
-                }
-                tmem_wait_ld();
                 const int limit = slot - j * kKeys;   // the last key of the tile that the row sees
-                if (least - j * kKeys < kKeys - 1) {
+                const bool masked = least - j * kKeys < kKeys - 1;
+                // The weights by the reference as it is, while the row's maximum is found: the tile is read once, chunk by
+                // chunk.  If the reference has to be raised (always at a row's first tile, seldom later) it is read
+                // again.
+                uint32_t wgt[kKeys / 2];
+                float2 all;
+                for (;;) {
+                    const float neg = -m * P.scale_log2;
+                    const uint64_t scale2 = pair(P.scale_log2, P.scale_log2), shift2 = pair(neg, neg);
+                    uint64_t part[2] = {0, 0};
+                    float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    uint32_t r[2][32];
+                    tmem_ld32(col_s, r[0]);
 #pragma unroll
-                    for (int e = 0; e < kKeys; ++e) x[e] = e <= limit ? x[e] : -INFINITY;
-                }
-                float tops[8];   // eight chains: one would be 128 dependent steps
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t(&x)[32] = r[c & 1];
+                        tmem_wait_ld(x);
+                        if (c < 3) tmem_ld32(col_s + (c + 1) * 32, r[(c + 1) & 1]);
+                        if (masked) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) tops[e] = fmaxf(x[e], x[8 + e]);
+                            for (int e = 0; e < 32; ++e) x[e] = c * 32 + e <= limit ? x[e] : 0xff800000u;
+                        }
 #pragma unroll
-                for (int e = 16; e < kKeys; e += 16)
+                        for (int e = 0; e < 32; e += 8)
 #pragma unroll
-                    for (int g = 0; g < 8; ++g) tops[g] = fmaxf(fmaxf(tops[g], x[e + g]), x[e + 8 + g]);
-                const float top = fmaxf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])),
-                                        fmaxf(fmaxf(tops[4], tops[5]), fmaxf(tops[6], tops[7])));
-                // raise the reference if the row's maximum outgrew it (the first tile: from nothing)
-                const bool raise = (top - m) * P.scale_log2 > kRescale;
-                if (__any_sync(0xffffffffu, raise)) {
+                            for (int g = 0; g < 4; ++g)
+                                tops[g] = fmaxf(fmaxf(tops[g], __uint_as_float(x[e + g])), __uint_as_float(x[e + 4 + g]));
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 y = unpair(fma_pair(
+                                pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), scale2, shift2));
+                            const float a = ex2(y.x), b = ex2(y.y);
+                            part[e & 1] = add_pair(part[e & 1], pair(a, b));
+                            wgt[c * 16 + e] = pack_f16x2(a, b);
+                        }
+                    }
+                    all = unpair(add_pair(part[0], part[1]));
+                    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                    const bool raise = (top - m) * P.scale_log2 > kRescale;
+                    if (!__any_sync(0xffffffffu, raise)) break;
                     const float f = raise ? ex2((m - top) * P.scale_log2) : 1.f;
                     if (raise) {
                         m = top;
@@ -401,33 +435,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
                             break;
                         }
                         tc_fence_after();
-#pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t r[32];
-                            tmem_ld32(col_o + c * 32, r);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-                            tmem_st32(col_o + c * 32, r);
-                        }
+                        rescale(col_o, f);
                     }
                 }
-                const uint64_t scale2 = pair(P.scale_log2, P.scale_log2), shift2 = pair(-m * P.scale_log2, -m * P.scale_log2);
-                uint64_t part[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t r[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float2 y = unpair(fma_pair(pair(x[c * 32 + 2 * e], x[c * 32 + 2 * e + 1]), scale2, shift2));
-                        const float a = ex2(y.x), b = ex2(y.y);
-                        part[e & 3] = add_pair(part[e & 3], pair(a, b));
-                        r[e] = pack_f16x2(a, b);
-                    }
-                    tmem_st16(col_s + c * 16, r);
-                }
-                const float2 all = unpair(add_pair(add_pair(part[0], part[1]), add_pair(part[2], part[3])));
+                if (!ok) break;
                 sum += all.x + all.y;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) tmem_st32(col_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&wgt[c * 32]));
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();

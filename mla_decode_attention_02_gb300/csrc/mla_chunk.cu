@@ -4,10 +4,11 @@
 //   j from the first slot of t's request to t's own
 //
 // An item is one head of one tile of 256 tokens (mla_chunk_plan.cu), taken as two MMA tiles
-// of 128 tokens that share every key tile of 128.  GB300 design, one CTA per SM:
+// of 128 tokens that share every key tile of 128; a tile of up to 128 tokens as two halves of its
+// keys, merged at the end.  GB300 design, one CTA per SM:
 //   warp 8      TMA: the queries (96 KB), then keys and values as 16 KB blocks of 64 dims through a ring
 //               of eight (a key tile's three blocks, its two value blocks, the next key tile's ...)
-//   warp 9      MMAs: S = q K^T (M = 128, N = 128, K = 192) into TMEM, and O += P V with P read from
+//   warp 9      MMAs of 128 x 128: S = q K^T (K = 192) into TMEM, and O += P V (K = 128) with P read from
 //               TMEM; the two tiles take turns, so that one's softmax runs while the other's products do
 //   warps 0-3   softmax of the first tile, one thread a row: S from TMEM, the running maximum and sum in
 //   warps 4-7   registers, P as fp16 back over S; the second tile's likewise
@@ -137,6 +138,23 @@ __device__ __noinline__ void rescale(uint32_t col, float f) {
     tmem_wait_st();
 }
 
+// A row's 128 output values in TMEM times f0, with f1 times those of the other half 128 columns on added.
+__device__ __noinline__ void add_half(uint32_t col, float f0, float f1) {
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        uint32_t r[32], x[32];
+        tmem_ld32(col + c * 32, r);
+        tmem_ld32(col + 128 + c * 32, x);
+        tmem_wait_ld(r);
+        tmem_wait_ld(x);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            r[e] = __float_as_uint(fmaf(__uint_as_float(x[e]), f1, __uint_as_float(r[e]) * f0));
+        tmem_st32(col + c * 32, r);
+    }
+    tmem_wait_st();
+}
+
 // A tile in error: its rows' outputs are NaN.
 __device__ __noinline__ void write_nan(const ChunkParams &P, const ChunkTile t, int head, int thread, int threads) {
     const uint32_t nan2 = 0x7fff7fffu;
@@ -152,17 +170,19 @@ __device__ __noinline__ void write_nan(const ChunkParams &P, const ChunkTile t, 
 
 __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __grid_constant__ ChunkParams P) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * kSlots + 15];
+    __shared__ __align__(8) uint64_t bars[2 * kSlots + 17];
     __shared__ ChunkItem s_item[2];
+    __shared__ float2 s_stat[128];   // maximum and sum of the second half's rows
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const uint32_t s_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // + ring slot: landed, read; + tile: queries landed, queries read, S complete, P written, product done;
-    // + item parity: item there, item read
+    // + item parity: item there, item read; the second half's rows handed over, merged
     enum { B_FULL = 0, B_EMPTY = kSlots, B_QFULL = 2 * kSlots, B_QFREE = B_QFULL + 2, B_S = B_QFREE + 2, B_P = B_S + 2,
-           B_PV = B_P + 2, B_ITEM = B_PV + 2, B_TAKEN = B_ITEM + 2, B_DRAIN = B_TAKEN + 2 };
-    static_assert(B_DRAIN + 1 == 2 * kSlots + 15, "barriers");
+           B_PV = B_P + 2, B_ITEM = B_PV + 2, B_TAKEN = B_ITEM + 2, B_HALF = B_TAKEN + 2, B_MERGED,
+           B_DRAIN };
+    static_assert(B_DRAIN + 1 == 2 * kSlots + 17, "barriers");
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     if (threadIdx.x == 0) {
         abort_flag = 0;
@@ -179,6 +199,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
             mbar_init(bar(B_ITEM + s), 1);
             mbar_init(bar(B_TAKEN + s), 1 + kSoftWarps);
         }
+        mbar_init(bar(B_HALF), kSoftWarps / 2);
+        mbar_init(bar(B_MERGED), kSoftWarps / 2);
         mbar_init(bar(B_DRAIN), 1);
         fence_mbar_init();
     }
@@ -203,10 +225,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
     // item of its index and then takes whatever is next.
     const int32_t num_tiles = fits ? hdr->num_items : 0;
     const int64_t items = (int64_t)num_tiles * P.heads;
-    // Key tiles of MMA tile s: up to the one with its last token's slot.
+    // Key tiles of one MMA tile of tokens: up to the one with its last token's slot.  An item of one such tile (up to 128
+    // tokens) is run as two, which take its key tiles in turn and are merged at the end.
     auto key_tiles = [](const ChunkTile &t, int s) {
-        const int last = (t.count < 128 * (s + 1) ? t.count : 128 * (s + 1)) - 1;
-        return last < 128 * s ? 0 : (t.slot0 + last) / kKeys + 1;
+        const bool split = t.count <= 128;
+        const int last = (split || t.count < 128 * (s + 1) ? t.count : 128 * (s + 1)) - 1, n = (t.slot0 + last) / kKeys + 1;
+        return split ? (n + 1 - s) / 2 : n;
     };
     // The k-th item of this CTA, as the MMA thread or a softmax warp sees it.
     auto item_of = [&](uint32_t k, bool &ok) {
@@ -225,13 +249,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
             prefetch_tmap(&P.tm_kr);
             uint32_t n = 0, loads[2] = {0, 0};
             bool ok = true;
-            auto load = [&](const CUtensorMap *tm, int row, int blk, int h) {
-                const uint32_t s = n % kSlots;
-                if (n >= kSlots) ok = ok && wait(w, bar(B_EMPTY + s), (n / kSlots - 1) & 1);
-                if (!ok) return;
-                mbar_arrive_expect_tx(bar(B_FULL + s), kBlk);
-                tma_load_4d(s_base + kOffRing + s * kBlk, tm, 0, row, blk, h, bar(B_FULL + s));
-                ++n;
+            // blocks [b0, b1) of a key tile: its keys' two, their rotary part, its values' two
+            auto load = [&](int row, int hl, int b0, int b1) {
+#pragma unroll 1
+                for (int b = b0; b < b1; ++b) {
+                    const uint32_t s = n % kSlots;
+                    if (n >= kSlots) ok = ok && wait(w, bar(B_EMPTY + s), (n / kSlots - 1) & 1);
+                    if (!ok) return;
+                    mbar_arrive_expect_tx(bar(B_FULL + s), kBlk);
+                    // (a pair of value blocks that wraps around the ring is swapped: the first 64 dims lie lower)
+                    const bool swap = b >= 3 && (n - (b - 3)) % kSlots == kSlots - 1;
+                    const int blk = b < 2 ? b : b == 2 ? 0 : swap ? 6 - b : b - 1;
+                    tma_load_4d(s_base + kOffRing + s * kBlk, b == 2 ? &P.tm_kr : &P.tm_kv, 0, row, blk, b == 2 ? 0 : hl,
+                                bar(B_FULL + s));
+                    ++n;
+                }
             };
             int64_t i = blockIdx.x;
             for (uint32_t k = 0; ok; ++k) {
@@ -248,17 +280,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
                 if (t.slot0 < 0) continue;
                 const int hl = it.head, h = P.head0 + hl;
                 const int n0 = key_tiles(t, 0), n1 = key_tiles(t, 1);
-                const int n_max = n1 > n0 ? n1 : n0;
-                for (int j = 0; j < n_max && ok; ++j) {
-                    const int row = t.base + j * kKeys;
-                    load(&P.tm_kv, row, 0, hl);
-                    load(&P.tm_kv, row, 1, hl);
-                    load(&P.tm_kr, row, 0, 0);
+                // in the order of their use: of two halves, a tile's products come after the next tile's scores
+                const bool split = t.count <= 128;
+                const int tiles_of_keys = split ? n0 + n1 : n1, behind = split;
+                for (int j = 0; j < tiles_of_keys + behind && ok; ++j) {
+                    if (j < tiles_of_keys) load(t.base + j * kKeys, hl, 0, 3);
                     if (j == 0) {   // the queries, once the item before has read its own
 #pragma unroll
                         for (int s = 0; s < 2; ++s) {
-                            if (s == 1 && !n1) break;
-                            if (loads[s]) ok = wait(w, bar(B_QFREE + s), (loads[s] - 1) & 1);
+                            if (s == 1 && split) break;
+                            if (loads[s]) ok = ok && wait(w, bar(B_QFREE + s), (loads[s] - 1) & 1);
                             if (!ok) break;
                             mbar_arrive_expect_tx(bar(B_QFULL + s), kQTile);
                             tma_load_4d(s_base + s * kQTile, &P.tm_qn, 0, t.t0 + 128 * s, 0, h, bar(B_QFULL + s));
@@ -266,8 +297,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
                             ++loads[s];
                         }
                     }
-                    load(&P.tm_kv, row, 2, hl);
-                    load(&P.tm_kv, row, 3, hl);
+                    if (j >= behind) load(t.base + (j - behind) * kKeys, hl, 3, 5);
                 }
             }
             // every copy has landed before the CTA gives its memory up
@@ -280,75 +310,77 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
         __syncwarp();
     } else if (warp == kMmaWarp) {
         if (elect_one()) {
-            constexpr uint32_t idesc_s = idesc_bf16(128, kKeys, 0, 0), idesc_o = idesc_f16(128, 64, 0, 1);
-            uint32_t n = 0, q_used[2] = {0, 0}, p_used[2] = {0, 0};   // n: ring blocks before this item's
+            constexpr uint32_t idesc_s = idesc_bf16(128, kKeys, 0, 0), idesc_o = idesc_f16(128, kDv, 0, 1);
+            uint32_t n = 0, q_phase = 0, p_phase = 0;   // n: ring blocks before this item's; phases: bit s is tile s's
             bool ok = true;
-            auto landed = [&](uint32_t k) { ok = ok && wait(w, bar(B_FULL + k % kSlots), (k / kSlots) & 1); };
-            auto scores = [&](int s, uint32_t k) {   // S = q K^T, the key tile's blocks being k, k + 1, k + 2
-#pragma unroll
-                for (int b = 0; b < 3; ++b) {
-                    landed(k + b);
-                    if (!ok) return;
-                    tc_fence_after();
-                    const uint32_t at = s_base + kOffRing + (k + b) % kSlots * kBlk;
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_ss(tmem + kColS + s * 128, smem_desc(s_base + s * kQTile + b * kBlk + ks * 32, 16, 1024, 2),
-                               smem_desc(at + ks * 32, 16, 1024, 2), idesc_s, (b | ks) ? 1u : 0u);
-                }
-                mma_commit(bar(B_S + s));
-            };
-            auto product = [&](int s, uint32_t k, bool add) {   // O (+)= P V, the value blocks being k, k + 1
-                ok = ok && wait(w, bar(B_P + s), p_used[s]++ & 1);
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    landed(k + b);
-                    if (!ok) return;
-                    tc_fence_after();
-                    const uint32_t at = s_base + kOffRing + (k + b) % kSlots * kBlk;
-#pragma unroll
-                    for (int ks = 0; ks < kKeys / 16; ++ks)
-                        mma_ts(tmem + kColO + s * 128 + b * 64, tmem + kColS + s * 128 + ks * 8,
-                               smem_desc(at + ks * 2048, kBlk, 1024, 2), idesc_o, (add || ks) ? 1u : 0u);
-                }
-                mma_commit(bar(B_PV + s));
-            };
-            auto release = [&](uint32_t k, int count) {
-                for (int b = 0; b < count; ++b) mma_commit(bar(B_EMPTY + (k + b) % kSlots));
-            };
             for (uint32_t item = 0; ok; ++item) {
                 const ChunkItem it = item_of(item, ok);
                 if (it.head < 0) break;
                 mbar_arrive(bar(B_TAKEN + (item & 1)));
                 const ChunkTile &t = it.tile;
                 if (t.slot0 < 0) continue;
-                const int nk[2] = {key_tiles(t, 0), key_tiles(t, 1)};
-                const int n_max = nk[1] > nk[0] ? nk[1] : nk[0];
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    if (!nk[s]) continue;
-                    ok = ok && wait(w, bar(B_QFULL + s), q_used[s]++ & 1);
-                    if (ok) scores(s, n);
-                }
-                if (!ok) break;
-                release(n, 3);
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-                    if (nk[s] == 1) mma_commit(bar(B_QFREE + s));
-                for (int j = 0; j < n_max && ok; ++j) {
-                    const uint32_t v = n + 5 * j + 3, next = v + 2;
+                const int n0 = key_tiles(t, 0), n1 = key_tiles(t, 1), most = n0 > n1 ? n0 : n1;
+                const bool split = t.count <= 128;
+                // The two tiles in turn: the products of key tile j, then the scores of the next, so that one's softmax runs
+                // while the other's products do.  Two tiles of tokens share every block; two halves of the keys have their own,
+                // in this order.
+                uint32_t next = n;
+#pragma unroll 1
+                for (int j = -1; j < most && ok; ++j) {
 #pragma unroll
                     for (int s = 0; s < 2; ++s) {
-                        if (j < nk[s]) product(s, v, j > 0);
-                        if (ok && j + 1 < nk[s]) scores(s, next);
-                        if (ok && j + 2 == nk[s]) mma_commit(bar(B_QFREE + s));
-                        if (!ok) break;
+                        const int nk = s ? n1 : n0;
+                        if (j >= 0 && j < nk) {   // O (+)= P V
+                            const uint32_t k = split ? next : n + 5 * j + 3, a = k % kSlots, b = (k + 1) % kSlots;
+                            next += 2;
+                            ok = wait(w, bar(B_P + s), p_phase >> s & 1) && wait(w, bar(B_FULL + a), (k / kSlots) & 1) &&
+                                 wait(w, bar(B_FULL + b), ((k + 1) / kSlots) & 1);
+                            p_phase ^= 1u << s;
+                            if (!ok) break;
+                            tc_fence_after();
+                            // (the first 64 dims are in the lower of the two slots)
+                            const uint64_t d = smem_desc(s_base + kOffRing + (a < b ? a : b) * kBlk, a < b ? kBlk : 7 * kBlk,
+                                                         1024, 2);
+#pragma unroll
+                            for (int ks = 0; ks < kKeys / 16; ++ks)
+                                mma_ts(tmem + kColO + s * 128, tmem + kColS + s * 128 + ks * 8, d + ks * (2048 >> 4), idesc_o,
+                                       (j > 0 || ks) ? 1u : 0u);
+                            if (split || s == 1) {
+                                mma_commit(bar(B_EMPTY + a));
+                                mma_commit(bar(B_EMPTY + b));
+                            }
+                            mma_commit(bar(B_PV + s));
+                        }
+                        if (j + 1 < nk) {   // S = q K^T
+                            const uint32_t k = split ? next : n + 5 * (j + 1);
+                            next += 3;
+                            if (j < 0 && (s == 0 || !split)) {
+                                ok = wait(w, bar(B_QFULL + s), q_phase >> s & 1);
+                                q_phase ^= 1u << s;
+                            }
+                            const uint64_t dq = smem_desc(s_base + (split ? 0 : s) * kQTile, 16, 1024, 2);
+#pragma unroll
+                            for (int b = 0; b < 3; ++b) {
+                                const uint32_t slot = (k + b) % kSlots;
+                                ok = ok && wait(w, bar(B_FULL + slot), ((k + b) / kSlots) & 1);
+                                if (!ok) break;
+                                tc_fence_after();
+                                const uint64_t d = smem_desc(s_base + kOffRing + slot * kBlk, 16, 1024, 2);
+#pragma unroll
+                                for (int ks = 0; ks < 4; ++ks)
+                                    mma_ss(tmem + kColS + s * 128, dq + b * (kBlk >> 4) + ks * 2, d + ks * 2, idesc_s,
+                                           (b | ks) ? 1u : 0u);
+                                if (split || s == 1) mma_commit(bar(B_EMPTY + slot));
+                            }
+                            if (!ok) break;
+                            mma_commit(bar(B_S + s));
+                            // the last scores of a tile's queries (two halves have one tile: n1 is n0 or one less)
+                            if (split ? j + 1 == (n1 == n0 ? n1 : n0) - 1 && s == (n1 == n0) : j + 2 == nk)
+                                mma_commit(bar(B_QFREE + (split ? 0 : s)));
+                        }
                     }
-                    if (!ok) break;
-                    release(v, 2);
-                    if (j + 1 < n_max) release(next, 3);
                 }
-                n += 5 * n_max;
+                n += split ? 5 * (n0 + n1) : 5 * n1;
             }
             mma_commit(bar(B_DRAIN));   // every MMA is done before the CTA gives its memory up
             wait_landed(w, bar(B_DRAIN), 0);
@@ -359,7 +391,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
         const int s = warp >> 2, quarter = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t col_s = lanes + kColS + s * 128, col_o = lanes + kColO + s * 128;
-        uint32_t phase = 0;   // key tiles before this item's
+        uint32_t phase = 0, merges = 0;   // key tiles and merges before this item's
         bool ok = true;
         for (uint32_t item = 0; ok; ++item) {
             const ChunkItem it = item_of(item, ok);
@@ -372,7 +404,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
                 write_nan(P, t, h, threadIdx.x, 32 * kSoftWarps);
                 continue;
             }
-            const int nk = key_tiles(t, s), row = 128 * s + quarter * 32 + lane;
+            const bool split = t.count <= 128;
+            const int nk = key_tiles(t, s), row = (split ? 0 : 128 * s) + quarter * 32 + lane;
             const bool mine = row < t.count;
             const int slot = t.slot0 + (mine ? row : t.count - 1);   // (a row past the tile's end: any legal slot)
             const int least = __shfl_sync(0xffffffffu, slot, 0);     // the warp's first row sees the fewest keys
@@ -383,15 +416,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
                     break;
                 }
                 tc_fence_after();
-                const int limit = slot - j * kKeys;   // the last key of the tile that the row sees
-                const bool masked = least - j * kKeys < kKeys - 1;
+                const int first = (split ? 2 * j + s : j) * kKeys;
+                const int limit = slot - first;   // the last key of the tile that the row sees
+                const bool masked = least - first < kKeys - 1;
                 // The weights by the reference as it is, while the row's maximum is found: the tile is read once, chunk by
                 // chunk.  If the reference has to be raised (always at a row's first tile, seldom later) it is read
                 // again.
                 uint32_t wgt[kKeys / 2];
                 float2 all;
                 for (;;) {
-                    const float neg = -m * P.scale_log2;
+                    const float neg = m == -INFINITY ? 0.f : -m * P.scale_log2;   // (no key seen so far: weights of 0)
                     const uint64_t scale2 = pair(P.scale_log2, P.scale_log2), shift2 = pair(neg, neg);
                     uint64_t part[2] = {0, 0};
                     float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -454,13 +488,39 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
                 break;
             }
             tc_fence_after();
+            const bool merge = split && key_tiles(t, 1) > 0;
+            if (merge) {
+                float2 *stat = &s_stat[quarter * 32 + lane];
+                if (s == 1) {   // hands its row over and goes on when it has been read
+                    *stat = make_float2(m, sum);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_HALF));
+                    ok = __all_sync(0xffffffffu, wait(w, bar(B_MERGED), merges++ & 1));
+                    continue;
+                }
+                if (!__all_sync(0xffffffffu, wait(w, bar(B_HALF), merges++ & 1))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const float2 other = *stat;   // (its maximum is -infinity if the row sees none of its keys)
+                const float top = fmaxf(m, other.x);
+                const float f0 = ex2((m - top) * P.scale_log2), f1 = ex2((other.x - top) * P.scale_log2);
+                sum = sum * f0 + other.y * f1;
+                m = top;
+                add_half(col_o, f0, f1);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_MERGED));
+            }
             const float inv = 1.f / sum;
             uint4 *dst = reinterpret_cast<uint4 *>(P.out + ((size_t)(t.t0 + row) * kHeads + h) * kDv);
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 uint32_t r[32];
                 tmem_ld32(col_o + c * 32, r);
-                tmem_wait_ld();
+                tmem_wait_ld(r);
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     if (mine)

@@ -221,10 +221,32 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
                       hdr->max_pages == P.max_pages && hdr->total_cost == P.kv_tokens;
     if (!fits && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&hdr->status, MLA_DEV_BAD_PLAN);
     const ChunkTile *tiles = reinterpret_cast<const ChunkTile *>(P.ws + chunk_layout(P.batch, P.tokens, P.kv_tokens).tiles);
-    // Items: head by head, a head's tiles together (they read the same keys), longest first.  A CTA begins with the
-    // item of its index and then takes whatever is next.
+    // Items: request by request, and head by head a request's tiles together (they read the same keys).  The last
+    // request's last heads go tile by tile, the longest first, so that all CTAs end with short items.  A CTA begins with
+    // the item of its index and then takes whatever is next.
     const int32_t num_tiles = fits ? hdr->num_items : 0;
     const int64_t items = (int64_t)num_tiles * P.heads;
+    auto item_at = [&](int64_t i) {
+        ChunkItem it;
+        it.head = -1;
+        if (i >= items) return it;
+        const ChunkTile any = tiles[(int32_t)(i / P.heads)];
+        const int32_t nt = any.end - any.first;
+        int64_t at = i - (int64_t)any.first * P.heads;
+        const int32_t few = ((int32_t)gridDim.x + nt - 1) / nt, late = any.end < num_tiles || few > P.heads ? 0 : few;
+        const int64_t split = (int64_t)(P.heads - late) * nt;
+        int32_t tile;
+        if (at < split) {
+            it.head = (int32_t)(at / nt);
+            tile = (int32_t)(at % nt);
+        } else {
+            at -= split;
+            it.head = P.heads - late + (int32_t)(at % late);
+            tile = (int32_t)(at / late);
+        }
+        it.tile = tiles[any.first + tile];
+        return it;
+    };
     // Key tiles of one MMA tile of tokens: up to the one with its last token's slot.  An item of one such tile (up to 128
     // tokens) is run as two, which take its key tiles in turn and are merged at the end.
     auto key_tiles = [](const ChunkTile &t, int s) {
@@ -267,9 +289,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
             };
             int64_t i = blockIdx.x;
             for (uint32_t k = 0; ok; ++k) {
-                ChunkItem it;
-                it.head = i < items ? (int32_t)(i / num_tiles) : -1;
-                if (it.head >= 0) it.tile = tiles[(int32_t)(i % num_tiles)];
+                const ChunkItem it = item_at(i);
                 if (k >= 2) ok = wait(w, bar(B_TAKEN + (k & 1)), ((k >> 1) - 1) & 1);
                 if (!ok) break;
                 s_item[k & 1] = it;

@@ -16,10 +16,12 @@ constexpr int kDn = 128, kDv = 128;             // no-position and value dims of
 constexpr int kPairRows = 256;                  // scratch rows that an SM pair fills at a time: four pages
 
 // The tokens of a tile: rows t0 .. t0 + count - 1 of the token arrays, the first at slot slot0 of its
-// request (-1: the request is in error, its rows become NaN), whose keys begin at scratch row base.
+// request (-1: the request is in error, its rows become NaN), whose keys begin at scratch row base; the
+// request's tiles are first .. end - 1.
 struct ChunkTile {
-    int32_t t0, count, slot0, base;
+    int32_t t0, count, slot0, base, first, end, pad[2];
 };
+static_assert(sizeof(ChunkTile) == 32, "tile layout");
 // A page that the chunks read, in the order of the scratch: its block table entry (-1: none, a page of
 // zeros) and the tokens in it.
 struct ChunkPage {

@@ -1,9 +1,13 @@
 // The plan of a step's chunks (include/mla_chunk.h, mla_chunk_plan): tiles of up
-// to 256 tokens, those that read the most keys first, and the list of the pages
-// that the requests read, in the order of the scratch.
+// to 256 tokens, and the list of the pages that the requests read, in the order of
+// the scratch.
 //
-// One CTA: a scan over the requests (their pages and tiles), the tiles ranked by
-// counting, then the pages written by whole warps.
+// A request's tiles stand together, its last (which reads the most keys) first, the
+// requests with the longest tiles first: what runs at the same time then shares keys, and
+// what runs last is short.
+// One CTA: a scan over the requests (their pages and tiles), then tiles and pages
+// by all threads, each finding its request in the scan; the tiles are ranked by
+// counting.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -15,152 +19,171 @@ namespace mla {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-// Tiles are put in order of their keys up to this many (every tile is compared with every other); more
-// run in token order, where so many even out by themselves.
-constexpr int kRankTiles = 2048;
+// Tiles are put in order up to this many (every tile is compared with every other); more run in token order,
+// where so many even out by themselves.
+constexpr int kRankTiles = 1024;
+
+struct RankKey {
+    int32_t longest;      // key tiles of the request's longest tile
+    int32_t first, tiles; // the request's first tile in token order, and how many it has
+};
 
 // Inclusive scan of a and b over the block.
-__device__ __forceinline__ void block_scan(int64_t &a, int64_t &b, int64_t (*sums)[2]) {
+__device__ __forceinline__ void block_scan(int32_t &a, int32_t &b, int32_t (*sums)[2]) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
+        const int32_t x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
         if (lane >= o) {
             a += x;
             b += y;
         }
     }
-    __syncthreads();
     if (lane == 31) {
         sums[warp][0] = a;
         sums[warp][1] = b;
     }
     __syncthreads();
-    for (int w = 0; w < warp; ++w) {
-        a += sums[w][0];
-        b += sums[w][1];
+    int32_t x = sums[lane][0], y = sums[lane][1];   // 32 warps: a sum a lane
+    x = lane < warp ? x : 0;
+    y = lane < warp ? y : 0;
+    a += __reduce_add_sync(0xffffffffu, x);
+    b += __reduce_add_sync(0xffffffffu, y);
+    __syncthreads();
+}
+static_assert(kPlanThreads == 1024, "a warp's lanes hold the warps' sums");
+
+// The entry e of the prefix sums with sum[e] <= i < sum[e + 1].
+__device__ __forceinline__ int find(const int32_t *sum, int n, int32_t i) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (sum[mid] <= i) lo = mid;
+        else hi = mid;
     }
+    return lo;
 }
 
 __global__ void __launch_bounds__(kPlanThreads)
 mla_chunk_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__restrict__ off, uint8_t *ws, int32_t batch,
                       int32_t tokens, int32_t max_pages, int64_t kv_tokens) {
-    __shared__ int64_t sums[kPlanThreads / 32][2];
-    __shared__ int64_t carry[2];
-    __shared__ ChunkTile s_tile[kRankTiles];
+    __shared__ int32_t sums[kPlanThreads / 32][2];
+    __shared__ unsigned long long all_pages;
+    __shared__ int32_t s_page[kPlanThreads + 1], s_first[kPlanThreads + 1];   // pages and tiles before each request
+    __shared__ int4 s_tile[kRankTiles];   // t0, count, slot0, base
+    __shared__ RankKey s_key[kRankTiles];
     const ChunkLayout L = chunk_layout(batch, tokens, kv_tokens);
     PlanHeader *hdr = reinterpret_cast<PlanHeader *>(ws);
     ChunkTile *tiles = reinterpret_cast<ChunkTile *>(ws + L.tiles);
     ChunkPage *pages = reinterpret_cast<ChunkPage *>(ws + L.pages);
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const int t = threadIdx.x;
+    if (t == 0) all_pages = 0;
     ptx::pdl_wait_prior();
     ptx::pdl_launch_dependents();
-    // The offsets as a whole, and the pages of all requests.
-    bool bad_off = false, bad_len = false;
-    if (t == 0) bad_off = off[0] != 0 || off[batch] > tokens;
-    int64_t total_pages = 0, total_tiles = 0;
-    // a request's pages and tiles (none if it has no tokens); false: its seq_len is in error
-    auto request = [&](int32_t b, int64_t &np, int64_t &nt) {
-        const int32_t n = off[b + 1] - off[b], len = seq_lens[b];
-        np = nt = 0;
-        if (n <= 0) return true;
-        nt = (n + kChunkTile - 1) / kChunkTile;
-        const bool ok = len >= n && len <= (int64_t)max_pages * kPage;
-        if (ok) np = (len + kPage - 1) / kPage;
-        return ok;
+    // A request's tokens, length, pages and tiles (none without tokens); ok: its seq_len is sound.
+    struct Request {
+        int32_t begin, n, len, np, nt;
+        bool ok;
     };
-    for (int32_t b = t; b < batch; b += kPlanThreads) {
-        if (off[b] > off[b + 1] || off[b] < 0) {
-            bad_off = true;
-            continue;
-        }
-        int64_t np, nt;
-        bad_len |= !request(b, np, nt);
-        total_pages += np;
-        total_tiles += nt;
+    auto request = [&](int32_t b) {
+        Request r = {};
+        r.ok = true;
+        if (b >= batch) return r;
+        r.begin = off[b];
+        r.n = off[b + 1] - r.begin;
+        r.len = seq_lens[b];
+        if (r.n <= 0) return r;
+        r.nt = (r.n - 1) / kChunkTile + 1;
+        r.ok = r.len >= r.n && r.len <= (int64_t)max_pages * kPage;
+        if (r.ok) r.np = (r.len - 1) / kPage + 1;
+        return r;
+    };
+    // The offsets as a whole, and the pages of all requests.
+    bool bad_off = t == 0 && (off[0] != 0 || off[batch] > tokens), bad_len = false;
+    int64_t mine = 0;
+    Request own;
+    for (int32_t b = t; b < batch || b == t; b += kPlanThreads) {
+        own = request(b);
+        bad_off |= b < batch && (own.begin < 0 || own.n < 0);
+        bad_len |= !own.ok;
+        mine += own.np;
     }
     bad_off = __syncthreads_or(bad_off);
     bad_len = __syncthreads_or(bad_len);
-    block_scan(total_pages, total_tiles, sums);
-    if (t == kPlanThreads - 1) {
-        carry[0] = total_pages;
-        carry[1] = total_tiles;
+    if (mine) atomicAdd(&all_pages, (unsigned long long)mine);
+    __syncthreads();
+    const bool over = !bad_off && (int64_t)all_pages * kPage > kv_tokens;
+    const int32_t num_pages = bad_off || over ? 0 : (int32_t)all_pages;
+    int32_t num_tiles = 0, done_pages = 0;
+    if (bad_off) {   // every row becomes NaN
+        num_tiles = (tokens - 1) / kChunkTile + 1;
+        for (int32_t i = t; i < num_tiles; i += kPlanThreads) {
+            const int32_t left = tokens - i * kChunkTile;
+            tiles[i] = {i * kChunkTile, left < kChunkTile ? left : kChunkTile, -1, 0, i, i + 1, {0, 0}};
+        }
+    } else {
+        for (int32_t b0 = 0; b0 < batch; b0 += kPlanThreads) {
+            const int32_t left = batch - b0 < kPlanThreads ? batch - b0 : kPlanThreads;
+            if (batch > kPlanThreads) own = request(b0 + t);
+            int32_t p = over ? 0 : own.np, i = own.nt;
+            block_scan(p, i, sums);
+            s_page[t + 1] = p;
+            s_first[t + 1] = i;
+            if (t == 0) s_page[0] = s_first[0] = 0;
+            __syncthreads();
+            const int32_t n_pages = s_page[kPlanThreads], n_tiles = s_first[kPlanThreads];
+            for (int32_t k = t; k < n_tiles; k += kPlanThreads) {
+                const int e = find(s_first, left, k);
+                const Request r = request(b0 + e);
+                const int32_t skip = (k - s_first[e]) * kChunkTile, rest = r.n - skip;
+                const ChunkTile tile = {r.begin + skip, rest < kChunkTile ? rest : kChunkTile,
+                                        r.ok && !over ? r.len - r.n + skip : -1, (done_pages + s_page[e]) * kPage,
+                                        num_tiles + s_first[e], num_tiles + s_first[e + 1], {0, 0}};
+                const int32_t at = num_tiles + k;
+                if (at < kRankTiles) {
+                    s_tile[at] = make_int4(tile.t0, tile.count, tile.slot0, tile.base);
+                    // the last tile reads the most keys, but takes half the time with up to 128 tokens
+                    const int32_t last = r.n - (r.nt - 1) * kChunkTile <= 128 ? r.len / 2 : r.len;
+                    const int32_t before = r.nt > 1 ? r.len - (r.n - (r.nt - 1) * kChunkTile) : 0;
+                    s_key[at] = {tile.slot0 < 0 ? 0 : last > before ? last : before, tile.first, r.nt};
+                }
+                tiles[at] = tile;
+            }
+            for (int32_t k = t; k < n_pages; k += kPlanThreads) {
+                const int e = find(s_page, left, k);
+                const int32_t j = k - s_page[e], rest = seq_lens[b0 + e] - j * kPage;
+                pages[done_pages + k] = {(int32_t)((int64_t)(b0 + e) * max_pages + j), rest < kPage ? rest : kPage};
+            }
+            num_tiles += n_tiles;
+            done_pages += n_pages;
+            __syncthreads();
+        }
+        if (num_tiles <= kRankTiles)
+            for (int32_t i = t; i < num_tiles; i += kPlanThreads) {
+                const RankKey k = s_key[i];
+                int32_t at = 0;
+                for (int32_t j = 0; j < num_tiles; ++j) {
+                    const RankKey o = s_key[j];
+                    at += o.longest > k.longest ||
+                          (o.longest == k.longest && (o.first < k.first || (o.first == k.first && j > i)));
+                }
+                const int4 v = s_tile[i];
+                const int32_t first = at - (k.first + k.tiles - 1 - i);
+                tiles[at] = {v.x, v.y, v.z, v.w, first, first + k.tiles, {0, 0}};
+            }
     }
-    __syncthreads();
-    total_pages = carry[0];
-    total_tiles = carry[1];
-    __syncthreads();
-    const bool over = !bad_off && total_pages * kPage > kv_tokens;
     if (t == 0) {
         PlanHeader h = {};
         h.magic = kChunkMagic;
         h.batch = batch;
         h.s_q = tokens;
         h.max_pages = max_pages;
-        h.num_items = bad_off ? (tokens + kChunkTile - 1) / kChunkTile : (int32_t)total_tiles;
-        h.num_parts = bad_off || over ? 0 : (int32_t)total_pages;
+        h.num_items = num_tiles;
+        h.num_parts = num_pages;
         h.status = bad_off ? MLA_DEV_BAD_OFFSETS
                            : (over ? MLA_DEV_BAD_KV_TOKENS : 0) | (bad_len ? MLA_DEV_BAD_SEQ_LEN : 0);
         h.total_cost = kv_tokens;
         *hdr = h;
-        carry[0] = carry[1] = 0;
-    }
-    __syncthreads();
-    if (bad_off) {   // every row becomes NaN
-        for (int32_t i = t; i < (tokens + kChunkTile - 1) / kChunkTile; i += kPlanThreads) {
-            const int32_t left = tokens - i * kChunkTile;
-            tiles[i] = {i * kChunkTile, left < kChunkTile ? left : kChunkTile, -1, 0};
-        }
-        return;
-    }
-    const bool rank = total_tiles <= kRankTiles;
-    ChunkTile *to = rank ? s_tile : tiles;
-    for (int32_t b0 = 0; b0 < batch; b0 += kPlanThreads) {
-        const int32_t b = b0 + t;
-        int64_t np = 0, nt = 0;
-        const bool ok = b >= batch || request(b, np, nt);
-        if (over) np = 0;
-        int64_t p = np, i = nt;
-        block_scan(p, i, sums);
-        const int64_t first_page = carry[0] + p - np, first_tile = carry[1] + i - nt;
-        __syncthreads();
-        if (t == kPlanThreads - 1) {
-            carry[0] += p;
-            carry[1] += i;
-        }
-        __syncthreads();
-        // each warp writes its requests' tiles and pages one request after another
-        for (int l = 0; l < 32; ++l) {
-            const int64_t n_tiles = __shfl_sync(0xffffffffu, nt, l);
-            if (n_tiles == 0) continue;
-            const int64_t at = __shfl_sync(0xffffffffu, first_tile, l), page0 = __shfl_sync(0xffffffffu, first_page, l);
-            const int64_t n_pages = __shfl_sync(0xffffffffu, np, l);
-            const bool good = __shfl_sync(0xffffffffu, (int)(ok && !over), l);
-            const int32_t r = b0 + warp * 32 + l, begin = off[r], n = off[r + 1] - begin, len = seq_lens[r];
-            for (int64_t k = lane; k < n_tiles; k += 32) {
-                const int32_t skip = (int32_t)k * kChunkTile, left = n - skip;
-                to[at + k] = {begin + skip, left < kChunkTile ? left : kChunkTile, good ? len - n + skip : -1,
-                              (int32_t)(page0 * kPage)};
-            }
-            for (int64_t k = lane; k < n_pages; k += 32) {
-                const int32_t left = len - (int32_t)k * kPage;
-                pages[page0 + k] = {(int32_t)((int64_t)r * max_pages + k), left < kPage ? left : kPage};
-            }
-        }
-    }
-    if (!rank) return;
-    __syncthreads();
-    // longest first (ties: in token order); a tile in error reads no key
-    const int32_t n = (int32_t)total_tiles;
-    auto keys = [&](int32_t i) { return s_tile[i].slot0 < 0 ? 0 : s_tile[i].slot0 + s_tile[i].count; };
-    for (int32_t i = t; i < n; i += kPlanThreads) {
-        const int32_t mine = keys(i);
-        int32_t at = 0;
-        for (int32_t j = 0; j < n; ++j) {
-            const int32_t other = keys(j);
-            at += other > mine || (other == mine && j < i);
-        }
-        tiles[at] = s_tile[i];
     }
 }
 

@@ -118,14 +118,23 @@ typedef struct mla_chunk {
     int64_t kv_tokens;
 } mla_chunk;
 
-/* Workspace bytes of mla_chunk_plan / mla_chunk_attend. */
+/*
+ * Two forms compute a step, chosen from the problem alone (tokens and keys spread evenly over the requests, the
+ * faster by both forms' measured times): every head's keys and values worked out once from the cached rows, or,
+ * for few tokens a request over long contexts, the absorbed form of mla_decode with its roundings (absorbed
+ * queries and latent outputs in bf16).
+ *
+ * Workspace bytes of mla_chunk_plan / mla_chunk_attend on the current device.
+ */
 mla_status mla_chunk_workspace_size(const mla_chunk *prob, size_t *bytes);
 
 /*
- * Scratch bytes of mla_chunk_attend with the keys and values of `heads` heads at once (1 .. 128): 128 bytes
- * a key and 512 a key and head.
+ * Scratch bytes of mla_chunk_attend (fp8 = 1: mla_chunk_attend_fp8) with the keys and values of `heads` heads at
+ * once (1 .. 128): 128 bytes a key and 512 a key and head, rounded up to 256 keys.  In the absorbed form instead 279 KB a token
+ * whatever `heads`, and over an fp8 cache room to expand each page once for all tokens (mla_tree_scratch_size) if
+ * they average two a request and it takes no more than 8 GiB; less than that runs without.
  */
-mla_status mla_chunk_scratch_size(const mla_chunk *prob, int32_t heads, size_t *bytes);
+mla_status mla_chunk_scratch_size(const mla_chunk *prob, int32_t heads, int32_t fp8, size_t *bytes);
 
 /*
  * Lay out a step's chunks: tiles of up to 256 tokens, longest first, and the pages that they read.  Valid for
@@ -133,7 +142,8 @@ mla_status mla_chunk_scratch_size(const mla_chunk *prob, int32_t heads, size_t *
  * the status word (mla_decode_check reads it).
  * A request whose seq_len is below its token count or beyond max_pages_per_seq pages: MLA_DEV_BAD_SEQ_LEN and
  * NaN outputs for its tokens.  Bad offsets (MLA_DEV_BAD_OFFSETS) or more pages than kv_tokens
- * (MLA_DEV_BAD_KV_TOKENS): NaN outputs for every row.
+ * (MLA_DEV_BAD_KV_TOKENS): NaN outputs for every row.  (The absorbed form does not depend on kv_tokens and
+ * does not check it.)
  */
 mla_status mla_chunk_plan(const mla_chunk *prob, const int32_t *seq_lens, const int32_t *token_offsets,
                           void *workspace, size_t workspace_bytes, mla_stream_t stream);
@@ -149,8 +159,8 @@ mla_status mla_chunk_plan(const mla_chunk *prob, const int32_t *seq_lens, const 
  *   lse             [tokens][128] fp32 or NULL
  *   scratch         at least mla_chunk_scratch_size for one head; with room for fewer than 128 heads the call
  *                   runs in passes of as many heads as fit (128-byte aligned)
- * Keys and values are rounded to bf16 (as the weights of the softmax are): a score over one key is off by
- * 2^-9 of its no-position part at most, and lse with it.  A page index outside the pool: MLA_DEV_BAD_PAGE, and NaN for
+ * Keys are rounded to bf16, values and the softmax's weights to fp16 (a value beyond 65504 is infinite): a
+ * score is off by the rounding of its key, and lse with it.  A page index outside the pool: MLA_DEV_BAD_PAGE, and NaN for
  * the tokens that see it.  Slots that a token does not see may hold anything.  Calls that share a workspace
  * or a scratch must be ordered.  scale finite and > 0.
  */

@@ -34,7 +34,7 @@ _SIGS.update({
     "mla_residual_norm": (ctypes.c_int, [_i32, _i32, _vp, _i64, _vp, _i64, _vp, _f32, _vp, _vp, _vp]),
     "mla_residual_norm_fp8": (ctypes.c_int, [_i32, _i32, _vp, _i64, _vp, _i64, _vp, _f32, _i32, _vp, _vp, _vp, _vp]),
     "mla_chunk_workspace_size": (ctypes.c_int, [_C, ctypes.POINTER(_size)]),
-    "mla_chunk_scratch_size": (ctypes.c_int, [_C, _i32, ctypes.POINTER(_size)]),
+    "mla_chunk_scratch_size": (ctypes.c_int, [_C, _i32, _i32, ctypes.POINTER(_size)]),
     "mla_chunk_plan": (ctypes.c_int, [_C, _vp, _vp, _vp, _size, _vp]),
     "mla_chunk_attend": (ctypes.c_int, _ATTEND),
     "mla_chunk_attend_fp8": (ctypes.c_int, _ATTEND),
@@ -224,10 +224,10 @@ def chunk_plan(seq_lens, token_offsets, *, tokens: int, max_pages_per_seq: int, 
     return p
 
 
-def chunk_scratch_size(p: ChunkPlan, heads: int = NUM_HEADS) -> int:
+def chunk_scratch_size(p: ChunkPlan, heads: int = NUM_HEADS, *, fp8: bool = False) -> int:
     """Bytes of the scratch that holds the keys and values of `heads` heads at once (``mla_chunk_scratch_size``)."""
     size, prob = ctypes.c_size_t(0), p.problem()
-    _check(load_library().mla_chunk_scratch_size(ctypes.byref(prob), int(heads), ctypes.byref(size)),
+    _check(load_library().mla_chunk_scratch_size(ctypes.byref(prob), int(heads), int(bool(fp8)), ctypes.byref(size)),
            "mla_chunk_scratch_size")
     return size.value
 
@@ -244,9 +244,9 @@ def chunk_attend(p: ChunkPlan, q_nope, q_rope, w_uk, w_uv, kv_cache, block_table
 
     Keys and values of all heads are worked out once per call from the cached rows, into scratch: a uint8 tensor of
     ``chunk_scratch_size(p, heads)`` bytes for as many heads at a time as it shall hold, by default one for
-    the call with all 128, or as many as CHUNK_SCRATCH_BYTES hold.
-    For a few tokens a request (below some 200) over long contexts the absorbed form costs less: ``query``,
-    ``tree_decode`` or ``decode``, ``epilog_uv``.
+    the call with all 128, or as many as CHUNK_SCRATCH_BYTES hold.  A few tokens a request (below some 200) over long
+    contexts are computed in the absorbed form instead (``query``, the tree step's attention, ``epilog_uv``), chosen
+    from the plan's sizes.
     """
     return _attend(p, q_nope, q_rope, w_uk, w_uv, kv_cache, block_table, scale, out, lse, scratch, stream, False)
 
@@ -255,6 +255,19 @@ def chunk_attend_fp8(p: ChunkPlan, q_nope, q_rope, w_uk, w_uv, kv_cache_fp8, blo
                      out=None, lse=None, scratch=None, stream=None):
     """``chunk_attend`` over an fp8 cache (``mla_chunk_attend_fp8``; uint8 [pages][64][656])."""
     return _attend(p, q_nope, q_rope, w_uk, w_uv, kv_cache_fp8, block_table, scale, out, lse, scratch, stream, True)
+
+
+def _scratch_bytes(p, fp8):
+    """All heads at once, or passes of as many as CHUNK_SCRATCH_BYTES hold."""
+    need = chunk_scratch_size(p, fp8=fp8)
+    passes = 1
+    while need > CHUNK_SCRATCH_BYTES and passes < NUM_HEADS:
+        passes *= 2
+        less = chunk_scratch_size(p, NUM_HEADS // passes, fp8=fp8)
+        if less == need:    # (the absorbed form's does not go by heads)
+            break
+        need = less
+    return need
 
 
 def _attend(p, q_nope, q_rope, w_uk, w_uv, kv_cache, block_table, scale, out, lse, scratch, stream, fp8):
@@ -272,10 +285,7 @@ def _attend(p, q_nope, q_rope, w_uk, w_uv, kv_cache, block_table, scale, out, ls
     with _launch_on(index, stream, ws, q_nope, q_rope, w_uk, w_uv, kv_cache, block_table, out, lse, scratch):
         out = _out(out, "out", torch.bfloat16, (T, NUM_HEADS, D_V), index)
         if scratch is None:
-            one, two = chunk_scratch_size(p, 1), chunk_scratch_size(p, 2)
-            heads = max(1, min(NUM_HEADS, 1 + (CHUNK_SCRATCH_BYTES - one) // (two - one)))
-            passes = -(-NUM_HEADS // heads)
-            scratch = torch.empty(chunk_scratch_size(p, -(-NUM_HEADS // passes)), dtype=torch.uint8, device=ws.device)
+            scratch = torch.empty(_scratch_bytes(p, fp8), dtype=torch.uint8, device=ws.device)
         room = B._bytes(scratch, "scratch", index)
         ws.record_stream(torch.cuda.current_stream())
         prob = p.problem()

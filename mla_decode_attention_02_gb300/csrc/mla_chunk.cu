@@ -37,7 +37,6 @@ namespace mla {
 bool encode_bf16_4d(CUtensorMap *m, const void *base, cuuint64_t d1, cuuint64_t d2, cuuint64_t d3,
                     cuuint64_t s1, cuuint64_t s2, cuuint64_t s3, cuuint32_t rows, cuuint32_t blocks);
 cudaError_t main_units(int32_t *units);
-mla_status check_chunk(const mla_chunk *p);
 cudaError_t launch_chunk_expand(const mla_chunk *prob, const void *w_uk, const void *w_uv, const void *cache, bool fp8,
                                 int64_t num_pages, const int32_t *block_table, void *ws, void *rope, void *kv,
                                 int32_t head0, int32_t heads, cudaStream_t stream);
@@ -582,16 +581,23 @@ mla_status attend(const mla_chunk *prob, const void *q_nope, int64_t nope_token,
         if (s < 1 || s % 8 || s >= (int64_t)1 << 31) return MLA_ERR_INVALID_ARG;
     if (num_pages < 1 || num_pages >= (int64_t)1 << 31 || !std::isfinite(scale) || !(scale > 0.f))
         return MLA_ERR_INVALID_ARG;
+    int dev = 0;
+    int32_t units = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MLA_ERR_CUDA;
+    if (main_units(&units) != cudaSuccess) return MLA_ERR_CUDA;
+    if (chunk_absorbed(prob, units)) {
+        if (workspace_bytes < absorbed_workspace_bytes(prob, units) || scratch_bytes < absorbed_scratch_bytes(prob, false))
+            return MLA_ERR_WORKSPACE;
+        return absorbed_attend(prob, q_nope, nope_token, nope_head, q_rope, rope_token, rope_head, w_uk, w_uv, cache, fp8,
+                               num_pages, block_table, scale, out, lse, workspace, static_cast<uint8_t *>(scratch),
+                               scratch_bytes, units, stream);
+    }
     if (workspace_bytes < chunk_layout(prob->batch, prob->tokens, prob->kv_tokens).total) return MLA_ERR_WORKSPACE;
     const size_t rope_bytes = chunk_rope_bytes(prob->kv_tokens), head_bytes = chunk_head_bytes(prob->kv_tokens);
     if (scratch_bytes < rope_bytes + head_bytes) return MLA_ERR_WORKSPACE;
     const size_t room = (scratch_bytes - rope_bytes) / head_bytes;
     const int32_t fit = room < (size_t)kHeads ? (int32_t)room : kHeads;
     const int32_t passes = (kHeads + fit - 1) / fit;
-    int dev = 0;
-    int32_t units = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MLA_ERR_CUDA;
-    if (main_units(&units) != cudaSuccess) return MLA_ERR_CUDA;
     {
         std::lock_guard<std::mutex> lock(g_chunk_mutex);
         if (!g_chunk_attr[dev]) {
@@ -643,11 +649,15 @@ mla_status attend(const mla_chunk *prob, const void *q_nope, int64_t nope_token,
 }  // namespace
 }  // namespace mla
 
-extern "C" mla_status mla_chunk_scratch_size(const mla_chunk *prob, int32_t heads, size_t *bytes) {
+extern "C" mla_status mla_chunk_scratch_size(const mla_chunk *prob, int32_t heads, int32_t fp8, size_t *bytes) {
     const mla_status st = mla::check_chunk(prob);
     if (st != MLA_OK) return st;
-    if (!bytes || heads < 1 || heads > mla::kHeads) return MLA_ERR_INVALID_ARG;
-    *bytes = mla::chunk_rope_bytes(prob->kv_tokens) + (size_t)heads * mla::chunk_head_bytes(prob->kv_tokens);
+    if (!bytes || heads < 1 || heads > mla::kHeads || (fp8 != 0 && fp8 != 1)) return MLA_ERR_INVALID_ARG;
+    int32_t units = 0;
+    if (mla::main_units(&units) != cudaSuccess) return MLA_ERR_CUDA;
+    *bytes = mla::chunk_absorbed(prob, units)
+                 ? mla::absorbed_scratch_bytes(prob, fp8 != 0)
+                 : mla::chunk_rope_bytes(prob->kv_tokens) + (size_t)heads * mla::chunk_head_bytes(prob->kv_tokens);
     return MLA_OK;
 }
 

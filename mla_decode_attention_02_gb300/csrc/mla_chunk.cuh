@@ -5,6 +5,8 @@
 #include <cstddef>
 #include <cstdint>
 
+#include <cuda_runtime_api.h>
+
 #include "mla_chunk.h"
 #include "mla_internal.h"
 
@@ -53,5 +55,20 @@ MLA_HD int64_t chunk_rows(int64_t kv_tokens) {
 // The scratch: k_rope of every row [rows][64], then [heads][rows][256]: keys (128) and values (128).
 MLA_HD size_t chunk_rope_bytes(int64_t kv_tokens) { return (size_t)chunk_rows(kv_tokens) * kDr * 2; }
 MLA_HD size_t chunk_head_bytes(int64_t kv_tokens) { return (size_t)chunk_rows(kv_tokens) * (kDn + kDv) * 2; }
+
+// Checks of a chunk problem that make no CUDA call.
+mla_status check_chunk(const mla_chunk *p);
+
+// The absorbed form (mla_chunk_absorbed.cu): whether a problem takes it, its workspace and scratch, its calls.
+bool chunk_absorbed(const mla_chunk *p, int32_t units);
+size_t absorbed_workspace_bytes(const mla_chunk *p, int32_t units);
+size_t absorbed_scratch_bytes(const mla_chunk *p, bool fp8);
+mla_status absorbed_plan(const mla_chunk *p, const int32_t *seq_lens, const int32_t *offsets, void *ws, int32_t units,
+                         cudaStream_t stream);
+mla_status absorbed_attend(const mla_chunk *p, const void *q_nope, int64_t nope_token, int64_t nope_head,
+                           const void *q_rope, int64_t rope_token, int64_t rope_head, const void *w_uk, const void *w_uv,
+                           const void *cache, bool fp8, int64_t num_pages, const int32_t *block_table, float scale,
+                           void *out, float *lse, void *ws, uint8_t *scratch, size_t scratch_bytes, int32_t units,
+                           mla_stream_t stream);
 
 }  // namespace mla

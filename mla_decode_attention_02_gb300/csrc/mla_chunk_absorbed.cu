@@ -1,0 +1,125 @@
+// Chunks of few tokens over long contexts (include/mla_chunk.h), in the absorbed form:
+//
+//   q_latent = q_nope W_UK[h],  o_latent = attention over the cached rows themselves,  o = W_UV[h] o_latent
+//
+// Every (token, key) pair costs 2 x 1088 flops a head instead of 2 x 320, but no
+// key is brought into the heads' space (2 x 131072 flops a head and key), which is what
+// a few tokens over a long context spend their time on otherwise.  The kernels are those of the
+// decode step: the queries (their rotary parts turned by nothing, which only packs
+// them), the tree variants of the main kernel with a row per token that sees its request's slots
+// up to its own, and the value projection.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "mla_chunk.cuh"
+#include "mla_internal.h"
+#include "mla_prolog.h"
+
+namespace mla {
+cudaError_t main_units(int32_t *units);
+bool tree_plan_fits(int32_t rows, int32_t units);
+cudaError_t launch_tree_plan(const int32_t *seq_lens, const int32_t *offsets, const uint64_t *masks, void *ws,
+                             int32_t batch, int32_t tokens, int32_t max_pages, int32_t num_units, cudaStream_t stream);
+cudaError_t launch_main(const void *q_latent, const void *q_rope, const void *kv, int64_t num_pages,
+                        const int32_t *block_table, float scale, void *ws, void *o_latent, float *lse, int32_t batch,
+                        int32_t s_q, int32_t max_pages, int32_t num_units, uint64_t wait_limit_ns, uint32_t test_flags,
+                        uint32_t flags, bool fp8, bool tree, const void *expanded, cudaStream_t stream);
+cudaError_t launch_expand(const void *ws, const void *kv_cache_fp8, int64_t num_pages, const int32_t *block_table,
+                          void *expanded, int32_t batch, int32_t tokens, int32_t max_pages, int32_t num_units,
+                          cudaStream_t stream);
+cudaError_t launch_combine(const void *ws, void *o_latent, float *lse, int32_t batch, int32_t s_q, int32_t num_units,
+                           bool tree, cudaStream_t stream);
+mla_status launch_epilog_uv(int64_t tokens, const void *o_latent, const void *w_uv, void *o_v, const int32_t *row_parts,
+                            int32_t *device_status, mla_stream_t stream);
+namespace {
+
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+// Scratch: absorbed queries, packed rotary parts, latent outputs, lse.
+struct AbsorbedScratch {
+    size_t q_latent, q_rope, o_latent, lse, total;
+};
+
+AbsorbedScratch absorbed_scratch(int32_t tokens) {
+    const size_t rows = (size_t)tokens * kHeads;
+    AbsorbedScratch S;
+    S.q_latent = 0;
+    S.q_rope = S.q_latent + rows * kDl * 2;
+    S.o_latent = S.q_rope + rows * kDr * 2;
+    S.lse = S.o_latent + rows * kDl * 2;
+    S.total = align_up(S.lse + rows * 4, 256);
+    return S;
+}
+
+// Workspace: the schedule, then positions and a rotary table of zeros.
+size_t zeros_at(const mla_chunk *p, int32_t units) { return make_layout(p->tokens, units, p->batch).total; }
+size_t zeros_bytes(const mla_chunk *p) { return align_up(4 * ((size_t)p->tokens + MLA_ROPE_TABLE_FLOATS), 256); }
+
+// Room for the expanded pages of an fp8 cache, as a tree step takes it: from two tokens a request on, up to 8 GiB.
+bool expands(const mla_chunk *p) {
+    return p->tokens >= 2 * (int64_t)p->batch && p->batch <= 65535 &&
+           expanded_bytes(p->batch, p->max_pages_per_seq) <= (size_t)8 << 30;
+}
+
+}  // namespace
+
+// Whether a problem is run in the absorbed form, from what the host knows: by the two forms' times in
+// microseconds, with tokens and keys spread evenly over the requests.
+bool chunk_absorbed(const mla_chunk *p, int32_t units) {
+    if (!tree_plan_fits(p->tokens, units)) return false;
+    const double tokens = p->tokens, keys = (double)p->kv_tokens, batch = p->batch;
+    const double n = tokens / batch, len = keys / batch;
+    const double blocks = n > 128 ? (double)(((int64_t)n + 127) / 128) : 1;
+    const double absorbed = 45 + 0.1 * tokens + tokens * (len / kPage + kItemCost) / units;
+    const double whole = 30 + 0.0245 * keys + 0.0122 * batch * blocks * len;
+    return absorbed < whole;
+}
+
+size_t absorbed_workspace_bytes(const mla_chunk *p, int32_t units) { return zeros_at(p, units) + zeros_bytes(p); }
+
+size_t absorbed_scratch_bytes(const mla_chunk *p, bool fp8) {
+    return absorbed_scratch(p->tokens).total + (fp8 && expands(p) ? expanded_bytes(p->batch, p->max_pages_per_seq) : 0);
+}
+
+mla_status absorbed_plan(const mla_chunk *p, const int32_t *seq_lens, const int32_t *offsets, void *ws, int32_t units,
+                         cudaStream_t stream) {
+    if (cudaMemsetAsync(static_cast<uint8_t *>(ws) + zeros_at(p, units), 0, zeros_bytes(p), stream) != cudaSuccess ||
+        launch_tree_plan(seq_lens, offsets, nullptr, ws, p->batch, p->tokens, p->max_pages_per_seq, units, stream) !=
+            cudaSuccess)
+        return MLA_ERR_CUDA;
+    return MLA_OK;
+}
+
+mla_status absorbed_attend(const mla_chunk *p, const void *q_nope, int64_t nope_token, int64_t nope_head,
+                           const void *q_rope, int64_t rope_token, int64_t rope_head, const void *w_uk, const void *w_uv,
+                           const void *cache, bool fp8, int64_t num_pages, const int32_t *block_table, float scale,
+                           void *out, float *lse, void *ws, uint8_t *scratch, size_t scratch_bytes, int32_t units,
+                           mla_stream_t stream) {
+    const AbsorbedScratch S = absorbed_scratch(p->tokens);
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    uint8_t *w = static_cast<uint8_t *>(ws);
+    int32_t *status = &reinterpret_cast<PlanHeader *>(ws)->status;
+    const int32_t *zeros = reinterpret_cast<const int32_t *>(w + zeros_at(p, units));
+    void *ql = scratch + S.q_latent, *qr = scratch + S.q_rope, *ol = scratch + S.o_latent;
+    float *l = lse ? lse : reinterpret_cast<float *>(scratch + S.lse);
+    const mla_status st = mla_query(p->tokens, q_nope, nope_token, nope_head, q_rope, rope_token, rope_head, w_uk,
+                                    reinterpret_cast<const float *>(zeros + p->tokens), zeros, ql, qr, status, stream);
+    if (st != MLA_OK) return st;
+    uint8_t *expanded = nullptr;
+    if (fp8 && expands(p) && scratch_bytes >= absorbed_scratch_bytes(p, true)) {
+        expanded = scratch + S.total;
+        if (launch_expand(ws, cache, num_pages, block_table, expanded, p->batch, p->tokens, p->max_pages_per_seq, units, s) !=
+            cudaSuccess)
+            return MLA_ERR_CUDA;
+    }
+    // (over an fp8 cache power-of-two maxima round a weight once: see tree_decode_fp8's binding)
+    if (launch_main(ql, qr, cache, num_pages, block_table, scale, ws, ol, l, p->batch, p->tokens, p->max_pages_per_seq, units,
+                    kWaitNs, 0, fp8 ? MLA_FLAG_POW2_MAX : 0, fp8, true, expanded, s) != cudaSuccess ||
+        launch_combine(ws, ol, l, p->batch, p->tokens, units, true, s) != cudaSuccess)
+        return MLA_ERR_CUDA;
+    const int32_t *parts = reinterpret_cast<const int32_t *>(w + make_layout(p->tokens, units, p->batch).row_nparts);
+    return launch_epilog_uv(p->tokens, ol, w_uv, out, parts, status, stream);
+}
+
+}  // namespace mla

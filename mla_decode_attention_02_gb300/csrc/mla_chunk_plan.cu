@@ -16,6 +16,7 @@
 #include "sm103_ptx.cuh"
 
 namespace mla {
+cudaError_t main_units(int32_t *units);
 namespace {
 
 constexpr int kPlanThreads = 1024;
@@ -191,7 +192,6 @@ bool aligned(const void *p, uintptr_t a) { return p && (reinterpret_cast<uintptr
 
 }  // namespace
 
-// Checks of a chunk problem that make no CUDA call.
 mla_status check_chunk(const mla_chunk *p) {
     if (!p) return MLA_ERR_INVALID_ARG;
     const mla_ragged r = {p->batch, p->tokens, p->num_heads, p->page_size, p->max_pages_per_seq, p->flags};
@@ -207,7 +207,10 @@ extern "C" mla_status mla_chunk_workspace_size(const mla_chunk *prob, size_t *by
     const mla_status st = mla::check_chunk(prob);
     if (st != MLA_OK) return st;
     if (!bytes) return MLA_ERR_INVALID_ARG;
-    *bytes = mla::chunk_layout(prob->batch, prob->tokens, prob->kv_tokens).total;
+    int32_t units = 0;
+    if (mla::main_units(&units) != cudaSuccess) return MLA_ERR_CUDA;
+    *bytes = mla::chunk_absorbed(prob, units) ? mla::absorbed_workspace_bytes(prob, units)
+                                              : mla::chunk_layout(prob->batch, prob->tokens, prob->kv_tokens).total;
     return MLA_OK;
 }
 
@@ -218,6 +221,12 @@ extern "C" mla_status mla_chunk_plan(const mla_chunk *prob, const int32_t *seq_l
     const mla_status st = check_chunk(prob);
     if (st != MLA_OK) return st;
     if (!aligned(seq_lens, 4) || !aligned(token_offsets, 4) || !aligned(workspace, 16)) return MLA_ERR_INVALID_ARG;
+    int32_t units = 0;
+    if (main_units(&units) != cudaSuccess) return MLA_ERR_CUDA;
+    if (chunk_absorbed(prob, units)) {
+        if (workspace_bytes < absorbed_workspace_bytes(prob, units)) return MLA_ERR_WORKSPACE;
+        return absorbed_plan(prob, seq_lens, token_offsets, workspace, units, reinterpret_cast<cudaStream_t>(stream));
+    }
     if (workspace_bytes < chunk_layout(prob->batch, prob->tokens, prob->kv_tokens).total) return MLA_ERR_WORKSPACE;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1);

@@ -59,6 +59,7 @@ struct EpilogParams {
     CUtensorMap tm_a;   // o_latent viewed as (64 values, tokens, 8 K blocks, heads)
     CUtensorMap tm_b;   // W_UV viewed as (64 values, 128 rows, 8 K blocks, heads)
     __nv_bfloat16 *o_v;
+    const int32_t *row_parts;   // or null; a token whose entry is kRowUnused is not written
     int32_t *status;
     int32_t tokens, a_rows, stages;
 };
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kThreadsE, 2) mla_epilog_uv_kernel(const __gri
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                          : "r"(base + b * kOBlkE + r * 128 + ((j ^ (r & 7)) * 16)));
-            if (tok < P.tokens)
+            if (tok < P.tokens && (!P.row_parts || P.row_parts[tok] != kRowUnused))
                 *reinterpret_cast<uint4 *>(P.o_v + ((size_t)tok * kHeads + h) * kDv + j16 * 8) = v;
         }
     }
@@ -219,22 +220,10 @@ bool g_attr[64];
 bool aligned16(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
-}  // namespace mla
 
-extern "C" mla_status mla_epilog_uv(const mla_problem *prob, const void *o_latent, const void *w_uv,
-                                    void *o_v, int32_t *device_status, mla_stream_t stream) {
-    mla::NvtxRange nvtx_range("mla_epilog_uv");
-    using namespace mla;
-    if (!prob || prob->batch < 1 || prob->max_pages_per_seq < 1 || prob->flags != 0)
-        return MLA_ERR_INVALID_ARG;
-    if (prob->s_q != 1 && prob->s_q != 2) return MLA_ERR_UNSUPPORTED;
-    if (prob->num_heads != kHeads || prob->page_size != kPage) return MLA_ERR_UNSUPPORTED;
-    const int64_t tokens = (int64_t)prob->batch * prob->s_q;
+mla_status launch_epilog_uv(int64_t tokens, const void *o_latent, const void *w_uv, void *o_v, const int32_t *row_parts,
+                            int32_t *device_status, mla_stream_t stream) {
     const int64_t ctas = (tokens + 127) / 128 * kHeads;
-    if (tokens * kHeads >= (int64_t)1 << 31 || ctas >= (int64_t)1 << 31) return MLA_ERR_UNSUPPORTED;
-    if (!aligned16(o_latent) || !aligned16(w_uv) || !aligned16(o_v) || !device_status ||
-        (reinterpret_cast<uintptr_t>(device_status) & 3u))
-        return MLA_ERR_INVALID_ARG;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MLA_ERR_CUDA;
     EpilogParams p{};
@@ -259,6 +248,7 @@ extern "C" mla_status mla_epilog_uv(const mla_problem *prob, const void *o_laten
         !encode_bf16_4d(&p.tm_b, w_uv, kDv, kKBlocks, H, kDl * 2, 128, (cuuint64_t)kDv * kDl * 2, kDv, 1))
         return MLA_ERR_CUDA;
     p.o_v = static_cast<__nv_bfloat16 *>(o_v);
+    p.row_parts = row_parts;
     p.status = device_status;
     p.tokens = (int32_t)tokens;
     cudaLaunchConfig_t cfg = {};
@@ -272,4 +262,23 @@ extern "C" mla_status mla_epilog_uv(const mla_problem *prob, const void *o_laten
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, mla_epilog_uv_kernel, p) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+}  // namespace mla
+
+extern "C" mla_status mla_epilog_uv(const mla_problem *prob, const void *o_latent, const void *w_uv,
+                                    void *o_v, int32_t *device_status, mla_stream_t stream) {
+    mla::NvtxRange nvtx_range("mla_epilog_uv");
+    using namespace mla;
+    if (!prob || prob->batch < 1 || prob->max_pages_per_seq < 1 || prob->flags != 0)
+        return MLA_ERR_INVALID_ARG;
+    if (prob->s_q != 1 && prob->s_q != 2) return MLA_ERR_UNSUPPORTED;
+    if (prob->num_heads != kHeads || prob->page_size != kPage) return MLA_ERR_UNSUPPORTED;
+    const int64_t tokens = (int64_t)prob->batch * prob->s_q;
+    const int64_t ctas = (tokens + 127) / 128 * kHeads;
+    if (tokens * kHeads >= (int64_t)1 << 31 || ctas >= (int64_t)1 << 31) return MLA_ERR_UNSUPPORTED;
+    if (!aligned16(o_latent) || !aligned16(w_uv) || !aligned16(o_v) || !device_status ||
+        (reinterpret_cast<uintptr_t>(device_status) & 3u))
+        return MLA_ERR_INVALID_ARG;
+    return launch_epilog_uv(tokens, o_latent, w_uv, o_v, nullptr, device_status, stream);
 }

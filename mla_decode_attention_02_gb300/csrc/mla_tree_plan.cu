@@ -38,6 +38,8 @@
 //
 // One CTA; every choice is a function of the inputs alone, and the host twin
 // below makes the same ones.
+// Without masks the rows are those of chunks of prompts (mla_chunk_absorbed.cu): any
+// number of tokens a request, each seeing the slots up to its own.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -78,6 +80,15 @@ MLA_HD int32_t tree_row(int32_t seq_len, int32_t nodes, int32_t req, uint64_t ma
 // Whether request b's stretch of the token array is sound.
 MLA_HD bool tree_offsets_ok(int32_t o0, int32_t o1, int32_t b, int32_t tokens) {
     return o0 >= 0 && o0 <= o1 && o1 <= tokens && (b > 0 || o0 == 0) && (int64_t)o1 - o0 <= MLA_TREE_MAX_NODES;
+}
+
+// The i-th token of a chunk (no masks): every slot up to its own is context.
+__device__ __forceinline__ int32_t chunk_row(int32_t seq_len, int32_t tokens, int32_t i, int32_t req, int32_t max_pages,
+                                             TreeRow *row) {
+    const int32_t p = tree_row(seq_len, tokens, req, 0, max_pages, row);
+    if (p == kNoneBad) return p;
+    row->context += i + 1;
+    return (row->context - 1) / kPage + 1;
 }
 
 // Row at position k of the cost line: every units-th row together.
@@ -173,9 +184,31 @@ mla_tree_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__rest
 
     // ---- every request's rows; with bad offsets no row belongs to any (all NaN)
     bool wrong = false;
-    for (int32_t b = tid; b < batch; b += kTreeThreads) wrong |= !tree_offsets_ok(offsets[b], offsets[b + 1], b, R);
+    for (int32_t b = tid; b < batch; b += kTreeThreads) {
+        const int32_t o0 = offsets[b], o1 = offsets[b + 1];
+        // (a chunk's tokens are not counted)
+        wrong |= masks ? !tree_offsets_ok(o0, o1, b, R) : o0 < 0 || o0 > o1 || o1 > R || (b == 0 && o0 != 0);
+    }
     wrong = __syncthreads_or(wrong) != 0;
-    if (wrong) {
+    if (!wrong && !masks) {   // a warp a request
+        for (int32_t b = warp; b < batch; b += kTreeThreads / 32) {
+            const int32_t o0 = offsets[b], n = offsets[b + 1] - o0, len = seq_lens[b];
+            int32_t most = 0;
+            for (int32_t i = lane; i < n; i += 32) {
+                TreeRow row;
+                const int32_t p = chunk_row(len, n, i, b, max_pages, &row);
+                tree_rows[o0 + i] = row;
+                s_end[o0 + i] = p > 0 ? row.context : p;
+                most = max(most, p);
+                if (p == kNoneBad) {
+                    bad = MLA_DEV_BAD_SEQ_LEN;
+                    special = 1;
+                }
+            }
+            most = __reduce_max_sync(0xffffffffu, most);
+            if (lane == 0) tree_pages[b] = most;
+        }
+    } else if (wrong) {
         for (int32_t r = tid; r < R; r += kTreeThreads) s_end[r] = kNoneBad;
         for (int32_t b = tid; b < batch; b += kTreeThreads) tree_pages[b] = 0;
         if (tid == 0) {

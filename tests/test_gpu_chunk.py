@@ -87,3 +87,32 @@ def test_parity(counts, lens, fp8):
     assert (out[c["n"]:] == 7).all() and (lse[c["n"]:] == 7).all()      # rows behind the last request
     again = attend(c, p)                                                  # the plan serves another call, without lse
     assert torch.equal(again[:c["n"]], out[:c["n"]])
+
+
+# A form is chosen by its expected time; these take the absorbed one (few tokens, long contexts) ...
+ABSORBED = [([3], [3000]), ([1, 0, 40, 7], [5000, 0, 3001, 2048]), ([65, 70], [9000, 6400])]
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("counts,lens", ABSORBED, ids=[f"{i}" for i in range(len(ABSORBED))])
+def test_few_tokens_over_long_contexts(counts, lens, fp8):
+    """Roundings of the absorbed form: queries, weights, latent outputs and outputs once in bf16.
+
+    The queries move a score by at most BF scale sum |q_latent c| over 512 values (their mean square: BF / sqrt(3)
+    of 0.82); weights (rounded twice at most), latent outputs and outputs make 2.25e-3 of o each (weights twice
+    that), and the projection sums 512 rounded values: in the mean square below 6e-3 of o's norm altogether, a row three times that.
+    """
+    c = CU.case(counts, lens, seed=5, pad=2, fp8=fp8)
+    p = plan(c)
+    out = torch.full((c["T"], 128, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((c["T"], 128), 7.0, device="cuda")
+    attend(c, p, out=out, lse=lse)
+    assert mla.check(p) == 0
+    o, l, _, _ = OC.chunk_attend(c["q"], c["w_uk"], c["w_uv"], c["cache"], c["block_table"], c["seq_lens"].tolist(),
+                                 c["offsets"].tolist(), scale=SCALE)
+    n = c["n"]
+    off, size = (out[:n].double() - o[:n]).norm(dim=-1), o[:n].norm(dim=-1)
+    assert off.norm() <= 6e-3 * size.norm() and (off <= 1.8e-2 * size).all(), (off.norm() / size.norm(), (off / size).max())
+    # sum |q_latent c| over 512 products of a normal q_latent of size 1 / sqrt(2) ... 0.82 and a normal c: below 512
+    assert (lse[:n].double() - l[:n]).abs().max() <= BF * SCALE * 512
+    assert (out[n:] == 7).all() and (lse[n:] == 7).all()

@@ -531,13 +531,15 @@ MLA_DEV_BAD_PATH = 0x20
 _host = None
 _HOST_ENTRIES = ("mla_query", "mla_cache_append", "mla_cache_append_fp8", "mla_tree_workspace_size", "mla_tree_plan",
                  "mla_tree_decode", "mla_tree_decode_fp8", "mla_cache_commit", "mla_rotate", "mla_residual_norm",
-                 "mla_residual_norm_fp8")
+                 "mla_residual_norm_fp8", "mla_chunk_workspace_size", "mla_chunk_plan", "mla_chunk_attend",
+                 "mla_chunk_attend_fp8")
 
 
 class _PythonOnly:
     """Stands for the native marshalling where there is none: no call is the plain case."""
 
-    query = append = tree_plan = tree_decode = commit = rotate = residual_norm = staticmethod(lambda *a: None)
+    query = append = tree_plan = tree_decode = commit = staticmethod(lambda *a: None)
+    rotate = residual_norm = chunk_plan = chunk_attend = query
 
 
 def _native():

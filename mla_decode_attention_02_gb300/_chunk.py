@@ -8,7 +8,7 @@ workspaces made with PyTorch, pointers and the current stream passed through the
 from __future__ import annotations
 
 import ctypes
-from dataclasses import dataclass
+from dataclasses import dataclass, field
 
 from . import _binding as B
 from ._binding import (D_LATENT, D_NOPE, D_ROPE, D_V, DEFAULT_RMS_EPS, DEFAULT_ROPE_BASE, DEFAULT_SCALE, NUM_HEADS,
@@ -188,6 +188,7 @@ class ChunkPlan:
     max_pages: int
     kv_tokens: int
     workspace: object   # torch.uint8 CUDA tensor, owned by this ChunkPlan
+    scratch_bytes: dict = field(default_factory=dict)   # of a call's own scratch, by whether the cache is fp8
 
     def problem(self) -> _Chunk:
         return _Chunk(self.batch, self.tokens, NUM_HEADS, PAGE_SIZE, self.max_pages, 0, self.kv_tokens)
@@ -207,11 +208,15 @@ def chunk_plan(seq_lens, token_offsets, *, tokens: int, max_pages_per_seq: int, 
     import torch
     index = _index_of(seq_lens, "seq_lens", 1, torch.int32)
     n = seq_lens.shape[0]
-    sl = _dense(seq_lens, "seq_lens", torch.int32, (n,), index, 4)
-    off = _dense(token_offsets, "token_offsets", torch.int32, (n + 1,), index, 4)
     if kv_tokens is None:
         kv_tokens = n * int(max_pages_per_seq) * PAGE_SIZE
     kv_tokens = -(-int(kv_tokens) // PAGE_SIZE) * PAGE_SIZE
+    if stream is None:
+        r = (B._host or B._native()).chunk_plan(seq_lens, token_offsets, tokens, max_pages_per_seq, kv_tokens, workspace)
+        if r is not None:
+            return ChunkPlan(n, tokens, max_pages_per_seq, kv_tokens, B._made(r, "mla_chunk_plan"))
+    sl = _dense(seq_lens, "seq_lens", torch.int32, (n,), index, 4)
+    off = _dense(token_offsets, "token_offsets", torch.int32, (n + 1,), index, 4)
     p = ChunkPlan(n, int(tokens), int(max_pages_per_seq), kv_tokens, workspace)
     prob, size, lib = p.problem(), ctypes.c_size_t(0), load_library()
     _check(lib.mla_chunk_workspace_size(ctypes.byref(prob), ctypes.byref(size)), "mla_chunk_workspace_size")
@@ -259,6 +264,9 @@ def chunk_attend_fp8(p: ChunkPlan, q_nope, q_rope, w_uk, w_uv, kv_cache_fp8, blo
 
 def _scratch_bytes(p, fp8):
     """All heads at once, or passes of as many as CHUNK_SCRATCH_BYTES hold."""
+    need = p.scratch_bytes.get(fp8)
+    if need is not None:
+        return need
     need = chunk_scratch_size(p, fp8=fp8)
     passes = 1
     while need > CHUNK_SCRATCH_BYTES and passes < NUM_HEADS:
@@ -267,12 +275,21 @@ def _scratch_bytes(p, fp8):
         if less == need:    # (the absorbed form's does not go by heads)
             break
         need = less
+    p.scratch_bytes[fp8] = need
     return need
 
 
 def _attend(p, q_nope, q_rope, w_uk, w_uv, kv_cache, block_table, scale, out, lse, scratch, stream, fp8):
-    import torch
     T, ws = p.tokens, p.workspace
+    if scratch is not None and not hasattr(scratch, "data_ptr"):
+        raise TypeError("scratch must be a torch.Tensor or None")
+    if stream is None:
+        r = (B._host or B._native()).chunk_attend(p.batch, T, p.max_pages, p.kv_tokens, ws, q_nope, q_rope, w_uk, w_uv,
+                                                  kv_cache, block_table, scale, out, lse,
+                                                  _scratch_bytes(p, fp8) if scratch is None else scratch, fp8)
+        if r is not None:
+            return B._made(r, "mla_chunk_attend_fp8" if fp8 else "mla_chunk_attend")
+    import torch
     index = ws.get_device()
     q = (*_strided(q_nope, "q_nope", torch.bfloat16, (T, NUM_HEADS, D_NOPE), index),
          *_strided(q_rope, "q_rope", torch.bfloat16, (T, NUM_HEADS, D_ROPE), index))

@@ -1,5 +1,5 @@
-// Argument marshalling of the tree step's calls in C++ (a CPython extension on
-// torch's own tensor objects).
+// Argument marshalling of the tree step's and the chunk step's calls in C++ (a CPython
+// extension on torch's own tensor objects).
 //
 // A call of a small operator takes 2-5 us on the GPU; checking a dozen tensors
 // from Python and passing them through ctypes takes 10-20 us, so such calls were
@@ -43,6 +43,10 @@ struct Entry {
     decltype(&mla_rotate) rotate;
     decltype(&mla_residual_norm) residual_norm;
     decltype(&mla_residual_norm_fp8) residual_norm_fp8;
+    decltype(&mla_chunk_workspace_size) chunk_workspace_size;
+    decltype(&mla_chunk_plan) chunk_plan;
+    decltype(&mla_chunk_attend) chunk_attend;
+    decltype(&mla_chunk_attend_fp8) chunk_attend_fp8;
 };
 Entry g_entry;
 bool g_bound = false;
@@ -386,6 +390,85 @@ PyObject *py_residual_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// seq_lens, offsets, tokens, max_pages, kv_tokens, workspace -> workspace
+PyObject *py_chunk_plan(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        const at::Tensor *lens = n == 6 ? tensor(a[0]) : nullptr;
+        if (!here(lens) || lens->dim() != 1 || lens->numel() < 1 || lens->numel() >= INT32_MAX) MLA_NOT_PLAIN;
+        const int dev = lens->get_device();
+        const int64_t B = lens->size(0);
+        const int64_t T = PyLong_AsLongLong(a[2]), pages = PyLong_AsLongLong(a[3]), kv = PyLong_AsLongLong(a[4]);
+        if (PyErr_Occurred()) {
+            PyErr_Clear();
+            MLA_NOT_PLAIN;
+        }
+        void *sl = dense(a[0], at::kInt, {B}, dev, 4), *off = dense(a[1], at::kInt, {B + 1}, dev, 4);
+        if (!sl || !off || T < 1 || T > INT32_MAX || pages < 1 || pages > INT32_MAX) MLA_NOT_PLAIN;
+        const mla_chunk prob = {(int32_t)B, (int32_t)T, (int32_t)kH, (int32_t)kP, (int32_t)pages, 0, kv};
+        at::Tensor ws;
+        if (a[5] == Py_None) {
+            size_t bytes = 0;
+            const mla_status rc = g_entry.chunk_workspace_size(&prob, &bytes);
+            if (rc != MLA_OK) return status_error(rc);
+            ws = make({(int64_t)bytes}, at::kByte, dev);
+        } else {
+            const at::Tensor *given = tensor(a[5]);
+            if (!given || !is(*given, at::kByte, given->sizes(), dev, 16)) MLA_NOT_PLAIN;
+            ws = *given;
+            used_here(ws, dev);
+        }
+        const mla_status rc = g_entry.chunk_plan(&prob, (const int32_t *)sl, (const int32_t *)off, ws.data_ptr(),
+                                                 (size_t)ws.numel(), stream_of(dev));
+        if (rc != MLA_OK) return status_error(rc);
+        return wrap(ws);
+    });
+}
+
+// batch, tokens, max_pages, kv_tokens, workspace, q_nope, q_rope, w_uk, w_uv, cache, block_table, scale, out, lse,
+// scratch (a tensor, or how many bytes of it to make), fp8 -> out
+PyObject *py_chunk_attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded([&]() -> PyObject * {
+        const at::Tensor *ws = n == 16 ? tensor(a[4]) : nullptr;
+        if (!here(ws) || !PyFloat_Check(a[11])) MLA_NOT_PLAIN;
+        const int dev = ws->get_device();
+        const int64_t B = PyLong_AsLongLong(a[0]), T = PyLong_AsLongLong(a[1]), pages = PyLong_AsLongLong(a[2]);
+        const int64_t kv = PyLong_AsLongLong(a[3]), room = PyLong_Check(a[14]) ? PyLong_AsLongLong(a[14]) : 1;
+        if (PyErr_Occurred()) {
+            PyErr_Clear();
+            MLA_NOT_PLAIN;
+        }
+        if (B < 1 || B > INT32_MAX || T < 1 || T > INT32_MAX || pages < 1 || pages > INT32_MAX || room < 1) MLA_NOT_PLAIN;
+        const bool fp8 = a[15] == Py_True;
+        int64_t ns[2], rs[2];
+        void *qn = strided(a[5], {T, kH, kN}, dev, ns), *qr = strided(a[6], {T, kH, kR}, dev, rs);
+        void *uk = dense(a[7], at::kBFloat16, {kH, kN, kL}, dev, 16), *uv = dense(a[8], at::kBFloat16, {kH, kN, kL}, dev, 16);
+        const at::Tensor *cache = tensor(a[9]);
+        void *bt = dense(a[10], at::kInt, {B, pages}, dev, 4);
+        void *lse = a[13] == Py_None ? nullptr : dense(a[13], at::kFloat, {T, kH}, dev, 4);
+        if (!qn || !qr || !uk || !uv || !bt || (!lse && a[13] != Py_None) || !cache_shape(cache, fp8, false) ||
+            !is(*cache, fp8 ? at::kByte : at::kBFloat16, cache->sizes(), dev, 16) ||
+            !is(*ws, at::kByte, ws->sizes(), dev, 16))
+            MLA_NOT_PLAIN;
+        at::Tensor out, scratch;
+        if (!output(a[12], at::kBFloat16, {T, kH, kN}, dev, &out)) MLA_NOT_PLAIN;
+        if (PyLong_Check(a[14])) {
+            scratch = make({room}, at::kByte, dev);
+        } else {
+            const at::Tensor *given = tensor(a[14]);
+            if (!given || !is(*given, at::kByte, given->sizes(), dev, 128)) MLA_NOT_PLAIN;
+            scratch = *given;
+        }
+        used_here(*ws, dev);
+        const mla_chunk prob = {(int32_t)B, (int32_t)T, (int32_t)kH, (int32_t)kP, (int32_t)pages, 0, kv};
+        const mla_status rc = (fp8 ? g_entry.chunk_attend_fp8 : g_entry.chunk_attend)(
+            &prob, qn, ns[0], ns[1], qr, rs[0], rs[1], uk, uv, cache->data_ptr(), cache->size(0), (const int32_t *)bt,
+            (float)PyFloat_AS_DOUBLE(a[11]), out.data_ptr(), (float *)lse, ws->data_ptr(), (size_t)ws->numel(),
+            scratch.data_ptr(), (size_t)scratch.numel(), stream_of(dev));
+        if (rc != MLA_OK) return status_error(rc);
+        return wrap(out);
+    });
+}
+
 // The C ABI's addresses, in the order of Entry.
 PyObject *py_bind(PyObject *, PyObject *const *a, Py_ssize_t n) {
     constexpr int kEntries = sizeof(Entry) / sizeof(void *);
@@ -416,6 +499,8 @@ PyMethodDef kMethods[] = {
     {"commit", reinterpret_cast<PyCFunction>(py_commit), METH_FASTCALL, nullptr},
     {"rotate", reinterpret_cast<PyCFunction>(py_rotate), METH_FASTCALL, nullptr},
     {"residual_norm", reinterpret_cast<PyCFunction>(py_residual_norm), METH_FASTCALL, nullptr},
+    {"chunk_plan", reinterpret_cast<PyCFunction>(py_chunk_plan), METH_FASTCALL, nullptr},
+    {"chunk_attend", reinterpret_cast<PyCFunction>(py_chunk_attend), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_mla_host", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

@@ -65,14 +65,20 @@ bool expands(const mla_chunk *p) {
 }  // namespace
 
 // Whether a problem is run in the absorbed form, from what the host knows: by the two forms' times in
-// microseconds, with tokens and keys spread evenly over the requests.
+// microseconds, with tokens and keys spread evenly over the requests.  Fitted to plan and attention in a graph
+// (requests x keys: tokens a request: absorbed / whole):
+//   1 x 512: 8: 40 / 40, 64: 47 / 40           4 x 512: 8: 42 / 100, 32: 64 / 103, 64: 108 / 106
+//   1 x 2048: 64: 69 / 98, 128: 110 / 100      4 x 2048: 32: 111 / 318, 64: 203 / 324, 128: 329 / 327
+//   1 x 8192: 64: 166 / 307, 128: 287 / 309    4 x 8192: 64: 515 / 1160, 128: 974 / 1165, 192: 1429 / 1305
+//   1 x 32768: 1: 63 / 1135, 128: 935 / 1125, 192: 1371 / 1269
+// (an fp8 cache adds some 12 us to both).
 bool chunk_absorbed(const mla_chunk *p, int32_t units) {
     if (!tree_plan_fits(p->tokens, units)) return false;
     const double tokens = p->tokens, keys = (double)p->kv_tokens, batch = p->batch;
-    const double n = tokens / batch, len = keys / batch;
-    const double blocks = n > 128 ? (double)(((int64_t)n + 127) / 128) : 1;
-    const double absorbed = 45 + 0.1 * tokens + tokens * (len / kPage + kItemCost) / units;
-    const double whole = 30 + 0.0245 * keys + 0.0122 * batch * blocks * len;
+    const int64_t n = (p->tokens + (int64_t)p->batch - 1) / p->batch;   // tokens a request
+    const double absorbed = 33 + 0.06 * tokens + 1.05 * tokens * (keys / batch / kPage + kItemCost) / units;
+    const double a_key = 0.0245 + (n <= 128 ? 0.0098 : 0.0071 * (double)((n + 127) / 128));
+    const double whole = 21 + a_key * keys + 3 * batch * (double)((n + 255) / 256) * kHeads / (2 * units);
     return absorbed < whole;
 }
 

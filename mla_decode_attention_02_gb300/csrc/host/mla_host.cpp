@@ -328,10 +328,11 @@ PyObject *py_rotate(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
         const at::Tensor *x = n == 7 ? tensor(a[0]) : nullptr;
         if (!here(x) || x->dim() != 3 || x->numel() < 1 || x->size(0) > INT32_MAX || x->size(1) > INT32_MAX ||
-            x->size(2) > 256 || !PyFloat_Check(a[5]))
+            !PyFloat_Check(a[5]))
             MLA_NOT_PLAIN;
         const int dev = x->get_device();
         const int64_t T = x->size(0), H = x->size(1), D = x->size(2);
+        if (D != 16 && D != 32 && D != 64 && D != 128 && D != 256) MLA_NOT_PLAIN;
         const long layout = PyLong_AsLong(a[3]);
         int64_t xs[2], os[2] = {H * D, D};
         void *src = strided(a[0], {T, H, D}, dev, xs), *pos = dense(a[1], at::kInt, {T}, dev, 4);
@@ -339,7 +340,6 @@ PyObject *py_rotate(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (!src || !pos || !table) MLA_NOT_PLAIN;
         at::Tensor out;
         if (a[6] == Py_None) {
-            if (D % 16) MLA_NOT_PLAIN;
             out = make({T, H, D}, at::kBFloat16, dev);
         } else {
             if (!strided(a[6], {T, H, D}, dev, os)) MLA_NOT_PLAIN;
@@ -358,7 +358,7 @@ PyObject *py_residual_norm(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
         const at::Tensor *x = n == 8 ? tensor(a[0]) : nullptr;
         if (!here(x) || x->dim() != 2 || x->numel() < 1 || x->size(0) > INT32_MAX || x->size(1) > 16384 ||
-            !PyFloat_Check(a[3]) || !PyLong_Check(a[4]))
+            x->size(1) % 8 || !PyFloat_Check(a[3]) || !PyLong_Check(a[4]))
             MLA_NOT_PLAIN;
         const int dev = x->get_device();
         const int64_t T = x->size(0), N = x->size(1);

@@ -49,14 +49,13 @@ namespace {
 using namespace ptx;
 
 constexpr int kKBlocks = kDl / 64;
-constexpr int kStages = 4;
+constexpr int kStages = 6;
 constexpr int kEpiWarps = 8;
 constexpr int kExpandThreads = 32 * (4 + kEpiWarps);
 constexpr uint32_t kBlk = 128 * 128;                   // 128 rows x 64 values
 constexpr uint32_t kABytes = kKBlocks * kBlk;          // 128 KB
-constexpr uint32_t kOffB = kABytes, kOffStage = kOffB + kStages * kBlk;
-constexpr uint32_t kWarpStage = 32 * 128;              // a warp's staging: 32 rows x 64 values
-constexpr uint32_t kExpandSmem = kOffStage + kEpiWarps * kWarpStage + 1024;
+constexpr uint32_t kOffB = kABytes;
+constexpr uint32_t kExpandSmem = kOffB + kStages * kBlk + 1024;
 constexpr uint64_t kExpandWaitNs = 2000000000ull, kSettleNs = 1000000ull;
 static_assert(kExpandSmem <= 232448 - 1024, "shared memory budget");
 static_assert(kDn == 128 && kDv == 128, "a CTA's half of B is one weight matrix's 128 rows");
@@ -130,17 +129,17 @@ __device__ __forceinline__ uint64_t l2_evict_first() {
     return p;
 }
 
-__device__ __forceinline__ void st_global_first(void *at, uint4 v, uint64_t policy) {
-    asm volatile("st.global.L2::cache_hint.v4.b32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(at), "r"(v.x), "r"(v.y), "r"(v.z),
-                 "r"(v.w), "l"(policy)
+__device__ __forceinline__ void st_global_first(void *at, const uint32_t *x, uint64_t policy) {
+    asm volatile("st.global.L2::cache_hint.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8}, %9;" ::"l"(at), "r"(x[0]),
+                 "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]), "l"(policy)
                  : "memory");
 }
 
 template <bool kFp8, int kPart>
 __device__ __forceinline__ void epilogue(const ExpandParams &P, const Wait &w, const ChunkPage *pages, int32_t num_pages,
-                                         int64_t i0, int64_t i1, uint32_t rank, int row, uint32_t stage, uint32_t acc,
-                                         uint32_t b_acc, uint32_t b_free) {
-    const int lane = row & 31, j = lane & 7;
+                                         int64_t i0, int64_t i1, uint32_t rank, int row, uint32_t acc, uint32_t b_acc,
+                                         uint32_t b_free) {
+    const int lane = row & 31;
     bool there = false, spoilt = false;
     float s_row = 1.f;
     const uint64_t policy = l2_evict_first();
@@ -218,26 +217,10 @@ __device__ __forceinline__ void epilogue(const ExpandParams &P, const Wait &w, c
 #pragma unroll
             for (int e = 0; e < 64; ++e) x[e] = fill;
         }
-        __nv_bfloat16 *out = P.kv + ((size_t)hl * P.rows + row0) * (kDn + kDv) + kPart * 128 + j * 8;
+        // a row's 256 bytes as eight whole sectors
+        __nv_bfloat16 *out = P.kv + ((size_t)hl * P.rows + row0 + lane) * (kDn + kDv) + kPart * 128;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {   // 64 columns at a time
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                st_shared_v4(stage + lane * 128 + ((q ^ j) << 4), x[c * 32 + 4 * q], x[c * 32 + 4 * q + 1],
-                             x[c * 32 + 4 * q + 2], x[c * 32 + 4 * q + 3]);
-            __syncwarp();
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {   // four rows' 128 bytes at a time
-                const int rr = 4 * q + (lane >> 3);
-                uint4 v;
-                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                             : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                             : "r"(stage + rr * 128 + ((j ^ (rr & 7)) << 4))
-                             : "memory");
-                st_global_first(out + c * 64 + (size_t)rr * (kDn + kDv), v, policy);
-            }
-            __syncwarp();   // the staging is read before the next columns go in
-        }
+        for (int q = 0; q < 8; ++q) st_global_first(out + q * 16, &x[q * 8], policy);
         if (++hl == P.heads) {
             hl = 0;
             ++group;
@@ -404,11 +387,11 @@ mla_chunk_expand_kernel(const __grid_constant__ ExpandParams P) {
         // ---- accumulator rows [32 quarter, +32), the keys' or the values' 128 columns
         const int quarter = warp & 3, row = quarter * 32 + lane;
         if (warp < 8)
-            epilogue<kFp8, 0>(P, w, pages, num_pages, i0, i1, rank, row, s_base + kOffStage + (warp - 4) * kWarpStage,
-                              tmem + ((uint32_t)(quarter * 32) << 16), bar(B_ACC), even(B_ACCFREE));
+            epilogue<kFp8, 0>(P, w, pages, num_pages, i0, i1, rank, row, tmem + ((uint32_t)(quarter * 32) << 16), bar(B_ACC),
+                              even(B_ACCFREE));
         else
-            epilogue<kFp8, 1>(P, w, pages, num_pages, i0, i1, rank, row, s_base + kOffStage + (warp - 4) * kWarpStage,
-                              tmem + ((uint32_t)(quarter * 32) << 16) + 128, bar(B_ACC), even(B_ACCFREE));
+            epilogue<kFp8, 1>(P, w, pages, num_pages, i0, i1, rank, row, tmem + ((uint32_t)(quarter * 32) << 16) + 128,
+                              bar(B_ACC), even(B_ACCFREE));
     }
     __syncthreads();
     if (threadIdx.x == 0) {

@@ -123,6 +123,18 @@ __device__ __noinline__ void wait_landed(const Wait w, uint32_t bar, uint32_t pa
     }
 }
 
+// 32 bytes: a sector at once if they are one.
+__device__ __forceinline__ void st_global_v8(void *at, const uint32_t *x, bool whole) {
+    if (!whole) {
+        reinterpret_cast<uint4 *>(at)[0] = make_uint4(x[0], x[1], x[2], x[3]);
+        reinterpret_cast<uint4 *>(at)[1] = make_uint4(x[4], x[5], x[6], x[7]);
+        return;
+    }
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                 "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+}
+
 // Multiply a row's 128 output values in TMEM.
 __device__ __noinline__ void rescale(uint32_t col, float f) {
 #pragma unroll 1
@@ -534,20 +546,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
                 if (lane == 0) mbar_arrive(bar(B_MERGED));
             }
             const float inv = 1.f / sum;
-            uint4 *dst = reinterpret_cast<uint4 *>(P.out + ((size_t)(t.t0 + row) * kHeads + h) * kDv);
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
+            __nv_bfloat16 *dst = P.out + ((size_t)(t.t0 + row) * kHeads + h) * kDv;
+            const bool whole = (reinterpret_cast<uintptr_t>(P.out) & 31) == 0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {   // (in whole sectors)
                 uint32_t r[32];
                 tmem_ld32(col_o + c * 32, r);
                 tmem_wait_ld(r);
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (mine)
-                        dst[c * 4 + q] = make_uint4(
-                            pack_bf16x2(__uint_as_float(r[8 * q]) * inv, __uint_as_float(r[8 * q + 1]) * inv),
-                            pack_bf16x2(__uint_as_float(r[8 * q + 2]) * inv, __uint_as_float(r[8 * q + 3]) * inv),
-                            pack_bf16x2(__uint_as_float(r[8 * q + 4]) * inv, __uint_as_float(r[8 * q + 5]) * inv),
-                            pack_bf16x2(__uint_as_float(r[8 * q + 6]) * inv, __uint_as_float(r[8 * q + 7]) * inv));
+                for (int e = 0; e < 16; ++e)
+                    r[e] = pack_bf16x2(__uint_as_float(r[2 * e]) * inv, __uint_as_float(r[2 * e + 1]) * inv);
+                if (mine) {
+                    st_global_v8(dst + c * 32, &r[0], whole);
+                    st_global_v8(dst + c * 32 + 16, &r[8], whole);
+                }
             }
             if (mine && P.lse)
                 P.lse[(size_t)(t.t0 + row) * kHeads + h] = (m * P.scale_log2 + log2f(sum)) * 0.6931471805599453f;

@@ -67,18 +67,18 @@ bool expands(const mla_chunk *p) {
 // Whether a problem is run in the absorbed form, from what the host knows: by the two forms' times in
 // microseconds, with tokens and keys spread evenly over the requests.  Fitted to plan and attention in a graph
 // (requests x keys: tokens a request: absorbed / whole):
-//   1 x 512: 8: 40 / 40, 64: 47 / 40           4 x 512: 8: 42 / 100, 32: 64 / 103, 64: 108 / 106
-//   1 x 2048: 64: 69 / 98, 128: 110 / 100      4 x 2048: 32: 111 / 318, 64: 203 / 324, 128: 329 / 327
-//   1 x 8192: 64: 166 / 307, 128: 287 / 309    4 x 8192: 64: 515 / 1160, 128: 974 / 1165, 192: 1429 / 1305
-//   1 x 32768: 1: 63 / 1135, 128: 935 / 1125, 192: 1371 / 1269
-// (an fp8 cache adds some 12 us to both).
+//   1 x 512: 8: 40 / 39, 64: 46 / 40           4 x 512: 8: 43 / 94, 32: 63 / 96, 64: 107 / 99
+//   1 x 2048: 64: 69 / 92, 128: 109 / 93       4 x 2048: 32: 110 / 278, 64: 202 / 281, 128: 326 / 286
+//   1 x 8192: 64: 167 / 270, 128: 286 / 271    4 x 8192: 64: 515 / 1023, 128: 970 / 1027, 192: 1428 / 1158
+//   1 x 32768: 1: 63 / 971, 64: 496 / 989, 128: 933 / 994, 192: 1367 / 1169
+// (an fp8 cache adds some 12 us to both).  Over 212 such points the choice costs 0.2% in the mean, 13% at worst.
 bool chunk_absorbed(const mla_chunk *p, int32_t units) {
     if (!tree_plan_fits(p->tokens, units)) return false;
     const double tokens = p->tokens, keys = (double)p->kv_tokens, batch = p->batch;
     const int64_t n = (p->tokens + (int64_t)p->batch - 1) / p->batch;   // tokens a request
-    const double absorbed = 33 + 0.06 * tokens + 1.05 * tokens * (keys / batch / kPage + kItemCost) / units;
-    const double a_key = 0.0245 + (n <= 128 ? 0.0098 : 0.0071 * (double)((n + 127) / 128));
-    const double whole = 21 + a_key * keys + 3 * batch * (double)((n + 255) / 256) * kHeads / (2 * units);
+    const double absorbed = 36 + 0.034 * tokens + 1.044 * tokens * (keys / batch / kPage + kItemCost) / units;
+    const double whole = 19 + keys * (0.0248 + 0.005 * (double)((n + 127) / 128)) +
+                         4.55 * batch * (double)((n + 255) / 256) * kHeads / (2 * units);
     return absorbed < whole;
 }
 

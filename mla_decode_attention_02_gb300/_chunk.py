@@ -60,11 +60,12 @@ def rope_table_scaled(rope_base: float = DEFAULT_ROPE_BASE, *, dims: int = D_ROP
     dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
     if dims not in ROTARY_DIMS:
         raise ValueError(f"dims must be one of {ROTARY_DIMS}, got {dims}")
-    with torch.cuda.device(dev), torch.cuda.stream(stream):
-        table = torch.empty(dims, dtype=torch.float32, device=dev)
+    index = torch.cuda.current_device() if dev.index is None else dev.index
+    with _launch_on(index, stream):
+        table = torch.empty(dims, dtype=torch.float32, device=torch.device("cuda", index))
         _check(load_library().mla_rope_table_scaled(float(rope_base), int(dims), float(factor), int(original_positions),
                                                     float(beta_fast), float(beta_slow), table.data_ptr(),
-                                                    _current_stream(table.get_device())), "mla_rope_table_scaled")
+                                                    _current_stream(index)), "mla_rope_table_scaled")
     return table
 
 
@@ -188,7 +189,7 @@ class ChunkPlan:
     max_pages: int
     kv_tokens: int
     workspace: object   # torch.uint8 CUDA tensor, owned by this ChunkPlan
-    scratch_bytes: dict = field(default_factory=dict)   # of a call's own scratch, by whether the cache is fp8
+    scratch: dict = field(default_factory=dict)   # heads and bytes of a call's own scratch, by whether the cache is fp8
 
     def problem(self) -> _Chunk:
         return _Chunk(self.batch, self.tokens, NUM_HEADS, PAGE_SIZE, self.max_pages, 0, self.kv_tokens)
@@ -218,10 +219,11 @@ def chunk_plan(seq_lens, token_offsets, *, tokens: int, max_pages_per_seq: int, 
     sl = _dense(seq_lens, "seq_lens", torch.int32, (n,), index, 4)
     off = _dense(token_offsets, "token_offsets", torch.int32, (n + 1,), index, 4)
     p = ChunkPlan(n, int(tokens), int(max_pages_per_seq), kv_tokens, workspace)
-    prob, size, lib = p.problem(), ctypes.c_size_t(0), load_library()
-    _check(lib.mla_chunk_workspace_size(ctypes.byref(prob), ctypes.byref(size)), "mla_chunk_workspace_size")
+    prob, lib = p.problem(), load_library()
     with _launch_on(index, stream, seq_lens, token_offsets, workspace):
         if workspace is None:
+            size = ctypes.c_size_t(0)
+            _check(lib.mla_chunk_workspace_size(ctypes.byref(prob), ctypes.byref(size)), "mla_chunk_workspace_size")
             p.workspace = torch.empty(size.value, dtype=torch.uint8, device=seq_lens.device)
         ws, nbytes = B._bytes(p.workspace, "workspace", index)
         p.workspace.record_stream(torch.cuda.current_stream())
@@ -232,8 +234,9 @@ def chunk_plan(seq_lens, token_offsets, *, tokens: int, max_pages_per_seq: int, 
 def chunk_scratch_size(p: ChunkPlan, heads: int = NUM_HEADS, *, fp8: bool = False) -> int:
     """Bytes of the scratch that holds the keys and values of `heads` heads at once (``mla_chunk_scratch_size``)."""
     size, prob = ctypes.c_size_t(0), p.problem()
-    _check(load_library().mla_chunk_scratch_size(ctypes.byref(prob), int(heads), int(bool(fp8)), ctypes.byref(size)),
-           "mla_chunk_scratch_size")
+    with _launch_on(p.workspace.get_device(), None):
+        _check(load_library().mla_chunk_scratch_size(ctypes.byref(prob), int(heads), int(bool(fp8)), ctypes.byref(size)),
+               "mla_chunk_scratch_size")
     return size.value
 
 
@@ -262,31 +265,41 @@ def chunk_attend_fp8(p: ChunkPlan, q_nope, q_rope, w_uk, w_uv, kv_cache_fp8, blo
     return _attend(p, q_nope, q_rope, w_uk, w_uv, kv_cache_fp8, block_table, scale, out, lse, scratch, stream, True)
 
 
-def _scratch_bytes(p, fp8):
-    """All heads at once, or passes of as many as CHUNK_SCRATCH_BYTES hold."""
-    need = p.scratch_bytes.get(fp8)
-    if need is not None:
-        return need
-    need = chunk_scratch_size(p, fp8=fp8)
-    passes = 1
-    while need > CHUNK_SCRATCH_BYTES and passes < NUM_HEADS:
-        passes *= 2
-        less = chunk_scratch_size(p, NUM_HEADS // passes, fp8=fp8)
-        if less == need:    # (the absorbed form's does not go by heads)
-            break
-        need = less
-    p.scratch_bytes[fp8] = need
-    return need
+def _own_scratch(p, fp8, call):
+    """call(bytes) with a scratch for all heads at once, or for as many as CHUNK_SCRATCH_BYTES and the memory hold."""
+    import torch
+    heads, need = p.scratch.get(fp8, (NUM_HEADS, None))
+    if need is None:
+        need = chunk_scratch_size(p, heads, fp8=fp8)
+        while need > CHUNK_SCRATCH_BYTES and heads > 1 and chunk_scratch_size(p, heads // 2, fp8=fp8) < need:
+            heads //= 2      # (the absorbed form's does not go by heads)
+            need = chunk_scratch_size(p, heads, fp8=fp8)
+        p.scratch[fp8] = heads, need
+    while True:
+        try:
+            return call(need)
+        except torch.OutOfMemoryError:
+            less = chunk_scratch_size(p, heads // 2, fp8=fp8) if heads > 1 else need
+            if less >= need:
+                raise
+            heads, need = p.scratch[fp8] = heads // 2, less
 
 
 def _attend(p, q_nope, q_rope, w_uk, w_uv, kv_cache, block_table, scale, out, lse, scratch, stream, fp8):
-    T, ws = p.tokens, p.workspace
     if scratch is not None and not hasattr(scratch, "data_ptr"):
         raise TypeError("scratch must be a torch.Tensor or None")
+    if scratch is None:
+        return _own_scratch(p, fp8, lambda need: _attend_in(p, q_nope, q_rope, w_uk, w_uv, kv_cache, block_table, scale, out,
+                                                            lse, need, stream, fp8))
+    return _attend_in(p, q_nope, q_rope, w_uk, w_uv, kv_cache, block_table, scale, out, lse, scratch, stream, fp8)
+
+
+def _attend_in(p, q_nope, q_rope, w_uk, w_uv, kv_cache, block_table, scale, out, lse, scratch, stream, fp8):
+    """One call with a scratch: a tensor, or how many bytes of it to make."""
+    T, ws = p.tokens, p.workspace
     if stream is None:
         r = (B._host or B._native()).chunk_attend(p.batch, T, p.max_pages, p.kv_tokens, ws, q_nope, q_rope, w_uk, w_uv,
-                                                  kv_cache, block_table, scale, out, lse,
-                                                  _scratch_bytes(p, fp8) if scratch is None else scratch, fp8)
+                                                  kv_cache, block_table, scale, out, lse, scratch, fp8)
         if r is not None:
             return B._made(r, "mla_chunk_attend_fp8" if fp8 else "mla_chunk_attend")
     import torch
@@ -301,8 +314,8 @@ def _attend(p, q_nope, q_rope, w_uk, w_uv, kv_cache, block_table, scale, out, ls
     lib = load_library()
     with _launch_on(index, stream, ws, q_nope, q_rope, w_uk, w_uv, kv_cache, block_table, out, lse, scratch):
         out = _out(out, "out", torch.bfloat16, (T, NUM_HEADS, D_V), index)
-        if scratch is None:
-            scratch = torch.empty(_scratch_bytes(p, fp8), dtype=torch.uint8, device=ws.device)
+        if isinstance(scratch, int):
+            scratch = torch.empty(scratch, dtype=torch.uint8, device=ws.device)
         room = B._bytes(scratch, "scratch", index)
         ws.record_stream(torch.cuda.current_stream())
         prob = p.problem()

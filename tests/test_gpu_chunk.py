@@ -422,3 +422,29 @@ def test_refusals():
     out = torch.full((20, 128, 128), 7.0, dtype=torch.bfloat16, device="cuda")
     mla.chunk_attend(q, *args, out=out, **good)
     assert mla.check(q) & mla.MLA_DEV_BAD_PLAN and (out == 7).all()
+
+
+def test_a_scratch_that_the_memory_does_not_hold(monkeypatch):
+    """The call's own scratch: as many heads as a limit or the memory allow, the same bits."""
+    import mla_decode_attention_02_gb300._chunk as chunk
+    c = CU.case([300, 90], [900, 500], seed=29)
+    ref = attend(c)
+    asked = []
+    real = chunk._attend_in
+
+    def small(*a):
+        asked.append(a[10])
+        if len(asked) < 4:
+            raise torch.OutOfMemoryError("no room")
+        return real(*a)
+
+    monkeypatch.setattr(chunk, "_attend_in", small)
+    p = plan(c)
+    assert equal(attend(c, p), ref, c["n"])
+    assert asked == [mla.chunk_scratch_size(p, h) for h in (128, 64, 32, 16)]
+    asked.append(0)
+    assert equal(attend(c, p), ref, c["n"]) and asked[-1] == asked[3]           # the plan remembers
+    monkeypatch.setattr(chunk, "_attend_in", real)
+    p = plan(c)
+    monkeypatch.setattr(chunk, "CHUNK_SCRATCH_BYTES", mla.chunk_scratch_size(p, 9))
+    assert equal(attend(c, p), ref, c["n"]) and p.scratch[False][0] == 8

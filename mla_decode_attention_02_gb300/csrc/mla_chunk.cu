@@ -181,19 +181,20 @@ __device__ __noinline__ void write_nan(const ChunkParams &P, const ChunkTile t, 
 
 __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __grid_constant__ ChunkParams P) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * kSlots + 17];
+    __shared__ __align__(8) uint64_t bars[2 * kSlots + 21];
     __shared__ ChunkItem s_item[2];
     __shared__ float2 s_stat[128];   // maximum and sum of the second half's rows
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     const uint32_t s_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // + ring slot: landed, read; + tile: queries landed, queries read, S complete, P written, product done;
+    // + ring slot: landed, read; + tile: queries landed, queries read, S complete; + 2 half + tile: P written, product
+    // done (of half a key tile);
     // + item parity: item there, item read; the second half's rows handed over, merged
     enum { B_FULL = 0, B_EMPTY = kSlots, B_QFULL = 2 * kSlots, B_QFREE = B_QFULL + 2, B_S = B_QFREE + 2, B_P = B_S + 2,
-           B_PV = B_P + 2, B_ITEM = B_PV + 2, B_TAKEN = B_ITEM + 2, B_HALF = B_TAKEN + 2, B_MERGED,
+           B_PV = B_P + 4, B_ITEM = B_PV + 4, B_TAKEN = B_ITEM + 2, B_HALF = B_TAKEN + 2, B_MERGED,
            B_DRAIN };
-    static_assert(B_DRAIN + 1 == 2 * kSlots + 17, "barriers");
+    static_assert(B_DRAIN + 1 == 2 * kSlots + 21, "barriers");
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     if (threadIdx.x == 0) {
         abort_flag = 0;
@@ -205,8 +206,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
             mbar_init(bar(B_QFULL + s), 1);
             mbar_init(bar(B_QFREE + s), 1);
             mbar_init(bar(B_S + s), 1);
-            mbar_init(bar(B_P + s), kSoftWarps / 2);
-            mbar_init(bar(B_PV + s), 1);
+            for (int half = 0; half < 2; ++half) {
+                mbar_init(bar(B_P + 2 * half + s), kSoftWarps / 2);
+                mbar_init(bar(B_PV + 2 * half + s), 1);
+            }
             mbar_init(bar(B_ITEM + s), 1);
             mbar_init(bar(B_TAKEN + s), 1 + kSoftWarps);
         }
@@ -364,23 +367,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
                         if (j >= 0 && j < nk) {   // O (+)= P V
                             const uint32_t k = split ? next : n + 5 * j + 3, a = k % kSlots, b = (k + 1) % kSlots;
                             next += 2;
-                            ok = wait(w, bar(B_P + s), p_phase >> s & 1) && wait(w, bar(B_FULL + a), (k / kSlots) & 1) &&
-                                 wait(w, bar(B_FULL + b), ((k + 1) / kSlots) & 1);
-                            p_phase ^= 1u << s;
-                            if (!ok) break;
-                            tc_fence_after();
                             // (the first 64 dims are in the lower of the two slots)
                             const uint64_t d = smem_desc(s_base + kOffRing + (a < b ? a : b) * kBlk, a < b ? kBlk : 7 * kBlk,
                                                          1024, 2);
+                            ok = wait(w, bar(B_FULL + a), (k / kSlots) & 1) && wait(w, bar(B_FULL + b), ((k + 1) / kSlots) & 1);
 #pragma unroll
-                            for (int ks = 0; ks < kKeys / 16; ++ks)
-                                mma_ts(tmem + kColO + s * 128, tmem + kColS + s * 128 + ks * 8, d + ks * (2048 >> 4), idesc_o,
-                                       (j > 0 || ks) ? 1u : 0u);
+                            for (int half = 0; half < 2; ++half) {   // 64 keys each, as their weights come
+                                ok = ok && wait(w, bar(B_P + 2 * half + s), p_phase >> s & 1);
+                                if (!ok) break;
+                                tc_fence_after();
+#pragma unroll
+                                for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+                                    mma_ts(tmem + kColO + s * 128, tmem + kColS + s * 128 + ks * 8, d + ks * (2048 >> 4),
+                                           idesc_o, (j > 0 || ks) ? 1u : 0u);
+                                mma_commit(bar(B_PV + 2 * half + s));
+                            }
+                            p_phase ^= 1u << s;
+                            if (!ok) break;
                             if (split || s == 1) {
                                 mma_commit(bar(B_EMPTY + a));
                                 mma_commit(bar(B_EMPTY + b));
                             }
-                            mma_commit(bar(B_PV + s));
                         }
                         if (j + 1 < nk) {   // S = q K^T
                             const uint32_t k = split ? next : n + 5 * (j + 1);
@@ -450,71 +457,78 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
                 const int first = (split ? 2 * j + s : j) * kKeys;
                 const int limit = slot - first;   // the last key of the tile that the row sees
                 const bool masked = least - first < kKeys - 1;
-                // The weights by the reference as it is, while the row's maximum is found: the tile is read once, chunk by
-                // chunk.  If the reference has to be raised (always at a row's first tile, seldom later) it is read
-                // again.
-                uint32_t wgt[kKeys / 2];
-                float2 all;
-                for (;;) {
-                    const float neg = m == -INFINITY ? 0.f : -m * P.scale_log2;   // (no key seen so far: weights of 0)
-                    const uint64_t scale2 = pair(P.scale_log2, P.scale_log2), shift2 = pair(neg, neg);
-                    uint64_t part[2] = {0, 0};
-                    float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    uint32_t r[2][32];
-                    tmem_ld32(col_s, r[0]);
+                // Half of the tile at a time.  The weights by the reference as it is, while the half's maximum is found: it
+                // is read once.  If the reference has to be raised (always at a row's first tile, seldom later) it is
+                // read again.
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t wgt[32];
+                    float2 all;
+                    const int seen = limit - 64 * half;
+                    for (;;) {
+                        const float neg = m == -INFINITY ? 0.f : -m * P.scale_log2;   // (no key seen so far: weights of 0)
+                        const uint64_t scale2 = pair(P.scale_log2, P.scale_log2), shift2 = pair(neg, neg);
+                        uint64_t part[2] = {0, 0};
+                        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        uint32_t r[2][32];
+                        tmem_ld32(col_s + 64 * half, r[0]);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t(&x)[32] = r[c & 1];
-                        tmem_wait_ld(x);
-                        if (c < 3) tmem_ld32(col_s + (c + 1) * 32, r[(c + 1) & 1]);
-                        if (masked) {
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t(&x)[32] = r[c];
+                            tmem_wait_ld(x);
+                            if (c == 0) tmem_ld32(col_s + 64 * half + 32, r[1]);
+                            if (masked) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) x[e] = c * 32 + e <= limit ? x[e] : 0xff800000u;
+                                for (int e = 0; e < 32; ++e) x[e] = c * 32 + e <= seen ? x[e] : 0xff800000u;
+                            }
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                                for (int g = 0; g < 4; ++g)
+                                    tops[g] =
+                                        fmaxf(fmaxf(tops[g], __uint_as_float(x[e + g])), __uint_as_float(x[e + 4 + g]));
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const float2 y = unpair(fma_pair(
+                                    pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), scale2, shift2));
+                                const float a = ex2(y.x), b = ex2(y.y);
+                                part[e & 1] = add_pair(part[e & 1], pair(a, b));
+                                wgt[c * 16 + e] = pack_f16x2(a, b);
+                            }
                         }
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-#pragma unroll
-                            for (int g = 0; g < 4; ++g)
-                                tops[g] = fmaxf(fmaxf(tops[g], __uint_as_float(x[e + g])), __uint_as_float(x[e + 4 + g]));
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float2 y = unpair(fma_pair(
-                                pair(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), scale2, shift2));
-                            const float a = ex2(y.x), b = ex2(y.y);
-                            part[e & 1] = add_pair(part[e & 1], pair(a, b));
-                            wgt[c * 16 + e] = pack_f16x2(a, b);
+                        all = unpair(add_pair(part[0], part[1]));
+                        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                        const bool raise = (top - m) * P.scale_log2 > kRescale;
+                        if (!__any_sync(0xffffffffu, raise)) break;
+                        const float f = raise ? ex2((m - top) * P.scale_log2) : 1.f;
+                        if (raise) {
+                            m = top;
+                            sum *= f;
+                        }
+                        // O holds what came before: once its last product is done
+                        if (j > 0 || half > 0) {
+                            if (!__all_sync(0xffffffffu, half ? wait(w, bar(B_PV + s), phase & 1)
+                                                              : wait(w, bar(B_PV + 2 + s), (phase - 1) & 1))) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            rescale(col_o, f);
                         }
                     }
-                    all = unpair(add_pair(part[0], part[1]));
-                    const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-                    const bool raise = (top - m) * P.scale_log2 > kRescale;
-                    if (!__any_sync(0xffffffffu, raise)) break;
-                    const float f = raise ? ex2((m - top) * P.scale_log2) : 1.f;
-                    if (raise) {
-                        m = top;
-                        sum *= f;
-                    }
-                    if (j > 0) {   // O holds the tiles before: once their product is done
-                        if (!__all_sync(0xffffffffu, wait(w, bar(B_PV + s), (phase - 1) & 1))) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        rescale(col_o, f);
-                    }
+                    if (!ok) break;
+                    sum += all.x + all.y;
+                    tmem_st32(col_s + 32 * half, wgt);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_P + 2 * half + s));
                 }
                 if (!ok) break;
-                sum += all.x + all.y;
-#pragma unroll
-                for (int c = 0; c < 2; ++c) tmem_st32(col_s + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&wgt[c * 32]));
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_P + s));
             }
             if (!ok || !nk) continue;
             // ---- the item's output, once its last product is done
-            if (!__all_sync(0xffffffffu, wait(w, bar(B_PV + s), (phase - 1) & 1))) {
+            if (!__all_sync(0xffffffffu, wait(w, bar(B_PV + 2 + s), (phase - 1) & 1))) {
                 ok = false;
                 break;
             }

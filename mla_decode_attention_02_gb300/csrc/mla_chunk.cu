@@ -8,15 +8,21 @@
 // keys, merged at the end.  GB300 design, one CTA per SM:
 //   warp 8      TMA: the queries (96 KB), then keys and values as 16 KB blocks of 64 dims through a ring
 //               of eight (a key tile's three blocks, its two value blocks, the next key tile's ...)
-//   warp 9      MMAs of 128 x 128: S = q K^T (K = 192) into TMEM, and O += P V (K = 128) with P read from
+//   warp 9      MMAs of 128 x 128: S = q K^T (K = 192) into TMEM, and O += P V (K = 64 twice) with P read from
 //               TMEM; the two tiles take turns, so that one's softmax runs while the other's products do
-//   warps 0-3   softmax of the first tile, one thread a row: S from TMEM, the running maximum and sum in
-//   warps 4-7   registers, P as fp16 back over S; the second tile's likewise
+//   warps 0-3   softmax of the first tile, one thread a row, 64 keys at a time: S from TMEM, the running maximum and
+//   warps 4-7   sum in registers, P as fp16 back over S and each half handed over; the second tile's likewise
 // TMEM: S and O of both tiles, 4 x 128 columns, all of it.  A thread whose row's maximum grows by more than 2^8
 // rescales the row's O itself, which waits for the product before; smaller growth leaves the reference as it
 // is (exact: the reference is a shift).  Weights (up to 2^8) and values are fp16 for their product, three bits
 // more than bf16; the sum is taken of the unrounded weights.
-// Bound by the tensor cores: 81,920 flops a (token, key) pair and 128 heads.
+// Bound by the tensor cores, 81,920 flops a (token, key) pair and 128 heads, and by the power they draw: 2048 tokens over
+// 32768 keys 3.02 ms (1.77 PFLOP/s; without the softmax's arithmetic 2.72, with keys from L2 alone 2.91), a prompt of 4096
+// 457 us (1.5, the diagonal's masked halves and 13 items' beginnings and ends a CTA; tensor pipe 71% of the clocks).
+// Measured on the way: items by index instead of in turn 705 -> 552 us (prompt), maxima in eight chains 523, weights before
+// the maximum is known 505, requests together and the last heads tile by tile 480, halves 457; value products as two of
+// 64 columns 3200 instead of 3030 us (long), with run-time loops around the MMAs 4170 (their issue then takes longer than
+// they do), S in pieces of 16 columns 3215.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

@@ -14,17 +14,22 @@
 // GB300 design.  An SM pair holds 256 rows (four pages, 128 KB a CTA) as the A operand in
 // shared memory and runs heads against them: tcgen05.mma of both SMs (cta_group::2,
 // M = 256 rows, N = 256: the even CTA holds W_UK[h]'s half of B, the odd one W_UV[h]'s), so
-// that each SM reads 16 KB of weights per 512 clocks of MMA; one SM alone would have to take in 32 KB.
-//   warp 0       this CTA's half of the weights: 64-value K blocks through a ring of four
+// that each SM takes in 16 KB of weights per 512 clocks of MMA; one SM alone would have to take in 32 KB.
+//   warp 0       this CTA's half of the weights: 64-value K blocks through a ring of six
 //   warp 1       MMAs (even CTA): eight K blocks an item into one of two TMEM accumulators
 //   warps 2-3    the rows: by TMA from the pages (bf16), or expanded from e4m3 codes (exact), whose
 //                row scale multiplies the sums instead
-//   warps 4-11   the previous item's epilogue: TMEM -> 16 bits -> 4 KB of swizzled staging a warp -> 128-byte
-//                pieces of rows; the first four take the keys, the others the values
+//   warps 4-11   the previous item's epilogue: TMEM -> 16 bits -> the thread's row of scratch, 32 bytes (a whole
+//                sector) a store; the first four take the keys, the others the values
 // Pages are packed one behind the other over all requests, so no row of the MMAs is wasted but in the last
 // pair's tile.  Rows past a request's end become zeros, so that a zero weight times them is zero; the
 // key of a row that is not finite becomes NaN and its values zeros, so that it spoils what sees it and nothing
 // else.
+// Bound by its stores, 64 KB a row: 32768 rows (2.1 GB) in 645 us, 3.3 TB/s where a fill of as much memory takes
+// 4.06, and 1.7 PFLOP/s; without the stores 510.  Staging in shared memory and a ring of four took 795; arrivals between
+// the CTAs with release semantics, which wait for the stores, 1475.  No gain: TMA stores (836), clusters of two pairs that
+// share the weights by multicast (835: 36 of them fit, 144 SMs), the rows in tensor memory with a ring of fourteen (658, and
+// 700 rows 41 us instead of 27).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -118,9 +123,6 @@ __device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t a, uint32_t b
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// A warp's share of the items: 32 accumulator rows (lane: one row), the keys' 128 columns (kPart 0) or the
-// values' (1).  The accumulator is given back as soon as it is in registers, rounded; what is not an ordinary
-// finite row is mended there, in a branch that no other takes.
 // Stores whose lines leave L2 before others: the scratch is larger than L2 in the cases that take long, and
 // would drive out the weights that every group of rows reads again.
 __device__ __forceinline__ uint64_t l2_evict_first() {
@@ -135,6 +137,9 @@ __device__ __forceinline__ void st_global_first(void *at, const uint32_t *x, uin
                  : "memory");
 }
 
+// A warp's share of the items: 32 accumulator rows (lane: one row), the keys' 128 columns (kPart 0) or the
+// values' (1).  The accumulator is given back as soon as it is in registers, rounded; what is not an ordinary
+// finite row is mended there, in a branch that no other takes.
 template <bool kFp8, int kPart>
 __device__ __forceinline__ void epilogue(const ExpandParams &P, const Wait &w, const ChunkPage *pages, int32_t num_pages,
                                          int64_t i0, int64_t i1, uint32_t rank, int row, uint32_t acc, uint32_t b_acc,

@@ -6,9 +6,10 @@
 //
 // A thread owns eight pairs of a token (16 values: one 32-byte run of the interleaved
 // layout, two 16-byte runs of the half layout), works their angles out once and
-// turns them in one head after another; a warp takes one token's 32 / (dims / 16)
-// heads at a time, and up to kRotateHeads heads, eight loads in flight a lane.
-// Bound by memory: four bytes a value.
+// turns them in up to four heads, all eight loads in flight; a warp's share of a token is
+// 128 / (dims / 16) heads (32 of 64 dims).
+// Bound by memory: four bytes a value (4097 tokens of 128 x 64 values out of rows of 192: 22.7 us in a graph,
+// 5.9 TB/s; 1 token 2.4 us, the launch and two dependent loads).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -24,7 +25,7 @@ namespace mla {
 namespace {
 
 constexpr int kRotateWarps = 4;
-constexpr int kRotateGrid = 152 * 16;
+constexpr int kRotateGrid = 152 * 16;   // CTAs at most (between 6 and 16 an SM: 4097 tokens within 4%)
 
 struct RotateParams {
     const __nv_bfloat16 *x;

@@ -5,7 +5,7 @@
 //
 // Keys are rounded to bf16, the queries' type; values to fp16, which has three bits more (the product with the
 // weights would be the larger part of the output's error: 700 keys 2.9e-3 of its norm with bf16 values and
-// weights) and reaches 65504; a value beyond that is infinite and shows.
+// weights) and reaches 65504; the key of a value beyond that is NaN, so that it shows.
 //
 // A row's keys and values are worked out once, for all tokens that see them: 2 x
 // 131072 flops a head and row.  Left to the attention kernel they would be worked
@@ -23,8 +23,8 @@
 //                sector) a store; the first four take the keys, the others the values
 // Pages are packed one behind the other over all requests, so no row of the MMAs is wasted but in the last
 // pair's tile.  Rows past a request's end become zeros, so that a zero weight times them is zero; the
-// key of a row that is not finite becomes NaN and its values zeros, so that it spoils what sees it and nothing
-// else.
+// key of a row that is not finite, or has a value beyond fp16, becomes NaN and its values zeros, so that it spoils
+// what sees it and nothing else.
 // Bound by its stores, 64 KB a row: 32768 rows (2.1 GB) in 645 us, 3.3 TB/s where a fill of as much memory takes
 // 4.06, and 1.7 PFLOP/s; without the stores 510.  Staging in shared memory and a ring of four took 795; arrivals between
 // the CTAs with release semantics, which wait for the stores, 1475.  No gain: TMA stores (836), clusters of two pairs that
@@ -123,6 +123,19 @@ __device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t a, uint32_t b
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// Maxima of two pairs (NaN if either is).
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // Stores whose lines leave L2 before others: the scratch is larger than L2 in the cases that take long, and
 // would drive out the weights that every group of rows reads again.
 __device__ __forceinline__ uint64_t l2_evict_first() {
@@ -139,11 +152,11 @@ __device__ __forceinline__ void st_global_first(void *at, const uint32_t *x, uin
 
 // A warp's share of the items: 32 accumulator rows (lane: one row), the keys' 128 columns (kPart 0) or the
 // values' (1).  The accumulator is given back as soon as it is in registers, rounded; what is not an ordinary
-// finite row is mended there, in a branch that no other takes.
+// row (a value not finite or beyond fp16) is mended there, in a branch that no other takes.
 template <bool kFp8, int kPart>
 __device__ __forceinline__ void epilogue(const ExpandParams &P, const Wait &w, const ChunkPage *pages, int32_t num_pages,
                                          int64_t i0, int64_t i1, uint32_t rank, int row, uint32_t acc, uint32_t b_acc,
-                                         uint32_t b_free) {
+                                         uint32_t b_free, volatile uint8_t *bad) {
     const int lane = row & 31;
     bool there = false, spoilt = false;
     float s_row = 1.f;
@@ -193,14 +206,17 @@ __device__ __forceinline__ void epilogue(const ExpandParams &P, const Wait &w, c
         tc_fence_after();
         uint32_t x[64];
         bool odd = !there || spoilt;   // a row that is no ordinary one, or holds a value that is not finite
+        uint32_t top[2] = {0, 0};   // the largest magnitudes, NaN above all
+        constexpr int kAt = 2;   // pieces of 32 columns at a time
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            uint32_t r[2][32];
-            tmem_ld32(acc + buf * 256 + c * 64, r[0]);
-            tmem_ld32(acc + buf * 256 + c * 64 + 32, r[1]);
-            tmem_wait_ld();
+        for (int c = 0; c < 4; c += kAt) {
+            uint32_t r[kAt][32];
 #pragma unroll
-            for (int d = 0; d < 2; ++d)
+            for (int d = 0; d < kAt; ++d) tmem_ld32(acc + buf * 256 + (c + d) * 32, r[d]);
+#pragma unroll
+            for (int d = 0; d < kAt; ++d) tmem_wait_ld(r[d]);
+#pragma unroll
+            for (int d = 0; d < kAt; ++d)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     float a = __uint_as_float(r[d][2 * e]), b = __uint_as_float(r[d][2 * e + 1]);
@@ -208,16 +224,23 @@ __device__ __forceinline__ void epilogue(const ExpandParams &P, const Wait &w, c
                         a *= s_row;
                         b *= s_row;
                     }
-                    odd |= !(fabsf(a) < INFINITY);
-                    odd |= !(fabsf(b) < INFINITY);
-                    x[c * 32 + d * 16 + e] = kPart == 0 ? pack_bf16x2(a, b) : pack_f16x2(a, b);
+                    const uint32_t v = kPart == 0 ? pack_bf16x2(a, b) : pack_f16x2(a, b);
+                    x[(c + d) * 16 + e] = v;
+                    top[e & 1] = kPart == 0 ? max_bf16x2(top[e & 1], v & 0x7fff7fffu) : max_f16x2(top[e & 1], v & 0x7fff7fffu);
                 }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_signal_cluster(b_free + 8 * buf);
+        // (two warps a row's halves; the other parity's flags are read before this barrier's next turn)
+        constexpr uint32_t kInf = kPart == 0 ? 0x7f80u : 0x7c00u;
+        top[0] = kPart == 0 ? max_bf16x2(top[0], top[1]) : max_f16x2(top[0], top[1]);
+        odd |= (top[0] & 0xffffu) >= kInf || (top[0] >> 16) >= kInf;
+        if (kPart == 1) bad[buf * 128 + row] = odd;
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + (row >> 5)) : "memory");
+        if (kPart == 0) odd |= bad[buf * 128 + row] != 0;
         if (__any_sync(0xffffffffu, odd) && odd) {
-            // a row that is not there: zeros; else the key is NaN, and the value a number
+            // a row that is not there: zeros; else the key is NaN, and the values are numbers
             const uint32_t fill = kPart == 0 && there ? 0x7fff7fffu : 0u;
 #pragma unroll
             for (int e = 0; e < 64; ++e) x[e] = fill;
@@ -241,6 +264,7 @@ mla_chunk_expand_kernel(const __grid_constant__ ExpandParams P) {
     __shared__ __align__(8) uint64_t bars[2 * kStages + 7];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
+    __shared__ uint8_t s_bad[2 * 128];   // by item parity: rows whose values are out of range
     const uint32_t s_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -393,10 +417,10 @@ mla_chunk_expand_kernel(const __grid_constant__ ExpandParams P) {
         const int quarter = warp & 3, row = quarter * 32 + lane;
         if (warp < 8)
             epilogue<kFp8, 0>(P, w, pages, num_pages, i0, i1, rank, row, tmem + ((uint32_t)(quarter * 32) << 16), bar(B_ACC),
-                              even(B_ACCFREE));
+                              even(B_ACCFREE), s_bad);
         else
             epilogue<kFp8, 1>(P, w, pages, num_pages, i0, i1, rank, row, tmem + ((uint32_t)(quarter * 32) << 16) + 128,
-                              bar(B_ACC), even(B_ACCFREE));
+                              bar(B_ACC), even(B_ACCFREE), s_bad);
     }
     __syncthreads();
     if (threadIdx.x == 0) {

@@ -448,3 +448,24 @@ def test_a_scratch_that_the_memory_does_not_hold(monkeypatch):
     p = plan(c)
     monkeypatch.setattr(chunk, "CHUNK_SCRATCH_BYTES", mla.chunk_scratch_size(p, 9))
     assert equal(attend(c, p), ref, c["n"]) and p.scratch[False][0] == 8
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_values_beyond_fp16_spoil_what_sees_them_alone(fp8):
+    """A later token's row of 1e5 (finite, its values beyond 65504), and weights that hold NaN."""
+    c = CU.case([130, 60], [200, 300], seed=30, fp8=fp8)
+    ref = attend(c)
+    d = CU.case([130, 60], [200, 300], seed=30, fp8=fp8, hold={(0, 150): 1e5})
+    d["w_uv"] = d["w_uv"].abs()                            # every value of that row is beyond 1e5
+    e = dict(c, w_uv=d["w_uv"])
+    ref_abs = attend(e)
+    out = attend(d)
+    at = 150 - 70                                          # the token of slot 150
+    assert equal(out, ref_abs, at) and equal(out[130:], ref_abs[130:], 60)
+    assert torch.isnan(out[at:130].float()).all()
+    broken = dict(c, w_uv=c["w_uv"].clone())
+    broken["w_uv"][3, 5, 7] = float("nan")
+    out = attend(broken)
+    assert torch.isnan(out[:, 3].float()).all()
+    rest = [h for h in range(128) if h != 3]
+    assert torch.equal(out[:, rest], ref[:, rest])

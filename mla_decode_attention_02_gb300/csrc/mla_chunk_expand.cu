@@ -156,7 +156,7 @@ __device__ __forceinline__ void st_global_first(void *at, const uint32_t *x, uin
 template <bool kFp8, int kPart>
 __device__ __forceinline__ void epilogue(const ExpandParams &P, const Wait &w, const ChunkPage *pages, int32_t num_pages,
                                          int64_t i0, int64_t i1, uint32_t rank, int row, uint32_t acc, uint32_t b_acc,
-                                         uint32_t b_free, volatile uint8_t *bad) {
+                                         uint32_t b_free, uint32_t b_bad, uint8_t *bad) {
     const int lane = row & 31;
     bool there = false, spoilt = false;
     float s_row = 1.f;
@@ -229,16 +229,24 @@ __device__ __forceinline__ void epilogue(const ExpandParams &P, const Wait &w, c
                     top[e & 1] = kPart == 0 ? max_bf16x2(top[e & 1], v & 0x7fff7fffu) : max_f16x2(top[e & 1], v & 0x7fff7fffu);
                 }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_signal_cluster(b_free + 8 * buf);
-        // (two warps a row's halves; the other parity's flags are read before this barrier's next turn)
         constexpr uint32_t kInf = kPart == 0 ? 0x7f80u : 0x7c00u;
         top[0] = kPart == 0 ? max_bf16x2(top[0], top[1]) : max_f16x2(top[0], top[1]);
         odd |= (top[0] & 0xffffu) >= kInf || (top[0] >> 16) >= kInf;
-        if (kPart == 1) bad[buf * 128 + row] = odd;
-        asm volatile("bar.sync %0, 64;" ::"r"(1 + (row >> 5)) : "memory");
-        if (kPart == 0) odd |= bad[buf * 128 + row] != 0;
+        // The values' warp tells the keys' warp of the same rows.  (That one gives the accumulator back after it has
+        // read this, so the flags are not written again before.)
+        uint8_t *flag = &bad[buf * 128 + row];
+        const uint32_t b_told = b_bad + 8 * (2 * (row >> 5) + buf);
+        if constexpr (kPart == 1) {
+            *flag = odd;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(b_told);
+        } else {
+            if (!__all_sync(0xffffffffu, expand_wait(w, b_told, (k / 2) & 1))) break;
+            odd |= *flag != 0;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_signal_cluster(b_free + 8 * buf);
         if (__any_sync(0xffffffffu, odd) && odd) {
             // a row that is not there: zeros; else the key is NaN, and the values are numbers
             const uint32_t fill = kPart == 0 && there ? 0x7fff7fffu : 0u;
@@ -261,7 +269,7 @@ template <bool kFp8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpandThreads, 1)
 mla_chunk_expand_kernel(const __grid_constant__ ExpandParams P) {
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * kStages + 7];
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 15];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ uint8_t s_bad[2 * 128];   // by item parity: rows whose values are out of range
@@ -271,8 +279,8 @@ mla_chunk_expand_kernel(const __grid_constant__ ExpandParams P) {
     // full, rows landed and accumulator free are the even CTA's (both CTAs arrive there); the others are
     // each CTA's own, which the MMAs' commits reach in both
     enum { B_FULL = 0, B_EMPTY = kStages, B_AFULL = 2 * kStages, B_AFREE, B_ACC, B_ACCFREE = B_ACC + 2,
-           B_DRAIN = B_ACCFREE + 2 };
-    static_assert(B_DRAIN + 1 == 2 * kStages + 7, "barriers");
+           B_BAD = B_ACCFREE + 2, B_DRAIN = B_BAD + 8 };
+    static_assert(B_DRAIN + 1 == 2 * kStages + 15, "barriers");
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     auto even = [&](int i) { return mapa(smem_u32(&bars[i]), 0); };
     if (threadIdx.x == 0) {
@@ -287,6 +295,7 @@ mla_chunk_expand_kernel(const __grid_constant__ ExpandParams P) {
             mbar_init(bar(B_ACC + b), 1);
             mbar_init(bar(B_ACCFREE + b), 2 * kEpiWarps);
         }
+        for (int b = 0; b < 8; ++b) mbar_init(bar(B_BAD + b), 1);
         mbar_init(bar(B_DRAIN), 1);
         fence_mbar_init();
     }
@@ -417,10 +426,10 @@ mla_chunk_expand_kernel(const __grid_constant__ ExpandParams P) {
         const int quarter = warp & 3, row = quarter * 32 + lane;
         if (warp < 8)
             epilogue<kFp8, 0>(P, w, pages, num_pages, i0, i1, rank, row, tmem + ((uint32_t)(quarter * 32) << 16), bar(B_ACC),
-                              even(B_ACCFREE), s_bad);
+                              even(B_ACCFREE), bar(B_BAD), s_bad);
         else
             epilogue<kFp8, 1>(P, w, pages, num_pages, i0, i1, rank, row, tmem + ((uint32_t)(quarter * 32) << 16) + 128,
-                              bar(B_ACC), even(B_ACCFREE), s_bad);
+                              bar(B_ACC), even(B_ACCFREE), bar(B_BAD), s_bad);
     }
     __syncthreads();
     if (threadIdx.x == 0) {

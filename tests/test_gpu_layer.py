@@ -316,3 +316,33 @@ def test_a_chunk_through_the_layer(fp8):
         exact = OC.residual_norm(out, residual, weight, 1e-6)[0]
         assert ((y8 - exact).abs() <= 2.0 ** -4 * exact.abs() + scales.double().repeat_interleave(128, 1) * 2.0 ** -10 + 1e-4 * exact.abs()).all()
         residual = kept
+
+
+def test_calls_marshalled_in_python_are_the_same(monkeypatch):
+    import chunk_util as CU
+    import mla_decode_attention_02_gb300._binding as binding
+    c = CU.case([70, 9], [200, 150], seed=50)
+    x, r, w = normal(7, 1032, seed=51), normal(7, 1032, seed=52), normal(1032, seed=53)
+    q, positions, table = normal(7, 5, 64, seed=54), torch.arange(7, dtype=torch.int32, device="cuda"), mla.rope_table()
+    s = torch.cuda.Stream()
+
+    def all_of_them(**kw):
+        p = mla.chunk_plan(c["seq_lens"], c["offsets"], tokens=c["T"], max_pages_per_seq=c["block_table"].shape[1],
+                           kv_tokens=c["kv_tokens"], **kw)
+        lse = torch.empty(c["T"], 128, device="cuda")
+        return [mla.rotate(q, positions, table=table, layout="half", **kw),
+                mla.rotate(q, positions, table=table, inverse=True, magnitude=2, out=torch.empty_like(q), **kw),
+                *mla.residual_norm(x, r, w, **kw), mla.residual_norm(x, None, w, **kw)[0], *mla.residual_norm_fp8(x, r, w, **kw),
+                *mla.residual_norm_fp8(x, r, w, group=0, **kw), *mla.residual_norm_fp8(x, None, w, **kw)[:2],
+                mla.chunk_attend(p, c["q"][..., :128], c["q"][..., 128:], c["w_uk"], c["w_uv"], c["cache"], c["block_table"],
+                                 lse=lse, **kw), lse, mla.rope_table_scaled(factor=8.0, **kw)]
+
+    native = all_of_them()
+    s.wait_stream(torch.cuda.current_stream())
+    on_stream = all_of_them(stream=s)
+    s.synchronize()
+    monkeypatch.setattr(binding, "_host", binding._PythonOnly)
+    python = all_of_them()
+    assert len(native) == len(python) == len(on_stream)
+    for a, b, d in zip(native, python, on_stream):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)) and torch.equal(a.view(torch.uint8), d.view(torch.uint8))

@@ -119,8 +119,8 @@ typedef struct mla_chunk {
 } mla_chunk;
 
 /*
- * Two forms compute a step, chosen from the problem alone (tokens and keys spread evenly over the requests, the
- * faster by both forms' measured times): every head's keys and values worked out once from the cached rows, or,
+ * Two forms compute a step, chosen from the problem alone (tokens and keys spread evenly over the requests, by
+ * both forms' measured times): every head's keys and values worked out once from the cached rows, or,
  * for few tokens a request over long contexts, the absorbed form of mla_decode with its roundings (absorbed
  * queries and latent outputs in bf16).
  *

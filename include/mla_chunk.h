@@ -159,8 +159,9 @@ mla_status mla_chunk_plan(const mla_chunk *prob, const int32_t *seq_lens, const 
  *   lse             [tokens][128] fp32 or NULL
  *   scratch         at least mla_chunk_scratch_size for one head; with room for fewer than 128 heads the call
  *                   runs in passes of as many heads as fit (128-byte aligned)
- * Keys are rounded to bf16, values and the softmax's weights to fp16 (a value beyond 65504 gives NaN
- * to the tokens that see it): a score is off by the rounding of its key, and lse with it.  A page index outside the pool: MLA_DEV_BAD_PAGE, and NaN for
+ * Keys are rounded to bf16, values and the softmax's weights to fp16: a score is off by the rounding of its key, and
+ * lse with it; a value beyond 65504 gives NaN to the tokens that see it, and one below 2^-14 is off by up to 2^-25 (the
+ * absorbed form has neither border).  A page index outside the pool: MLA_DEV_BAD_PAGE, and NaN for
  * the tokens that see it.  Slots that a token does not see may hold anything.  Calls that share a workspace
  * or a scratch must be ordered.  scale finite and > 0.
  */

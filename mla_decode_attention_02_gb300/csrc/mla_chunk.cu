@@ -14,8 +14,14 @@
 //   warps 4-7   sum in registers, P as fp16 back over S and each half handed over; the second tile's likewise
 // TMEM: S and O of both tiles, 4 x 128 columns, all of it.  A thread whose row's maximum grows by more than 2^8
 // rescales the row's O itself, which waits for the product before; smaller growth leaves the reference as it
-// is (exact: the reference is a shift).  Weights (up to 2^8) and values are fp16 for their product, three bits
+// is (exact: the reference is a shift).  Weights and values are fp16 for their product, three bits
 // more than bf16; the sum is taken of the unrounded weights.
+// fp16 has those bits down to 2^-14 only and ends at 2^-25, while a row whose first key draws nearly all the weight has
+// thousands of others far below it.  So the weights stand 2^7 above the reference (at most 2^15), and where 64 keys in a row
+// have none within 2^-20 of the reference it falls to their largest (once in eight key tiles at most, so that scores that
+// go up and down cost little, and 2^40 below its highest at most, which fp32's range bears).  32768 keys of which one draws
+// 0.9986 of the weight, with a value of zero: without both 0.33 of the output's norm, with the lift alone 2e-3, now
+// 3e-4; a lift of 2^11 (then raised at 2^4) does as well but takes 11 to 35% longer where scores are twice as wide or more.
 // Bound by the tensor cores, 81,920 flops a (token, key) pair and 128 heads, and by the power they draw: 2048 tokens over
 // 32768 keys 3.02 ms (1.77 PFLOP/s; without the softmax's arithmetic 2.72, with keys from L2 alone 2.91), a prompt of 4096
 // 457 us (1.5, the diagonal's masked halves and 13 items' beginnings and ends a CTA; tensor pipe 71% of the clocks).
@@ -59,7 +65,10 @@ constexpr uint32_t kOffRing = 2 * kQTile;
 constexpr uint32_t kChunkSmem = kOffRing + kSlots * kBlk + 1024;
 constexpr uint32_t kColS = 0, kColO = 256;              // + 128 per tile
 constexpr uint64_t kChunkWaitNs = 2000000000ull;
-constexpr float kRescale = 8.0f;                        // log2 units
+constexpr float kRescale = 8.0f, kLift = 7.0f;          // log2 units
+static_assert(kRescale + kLift <= 15.0f, "a weight is an fp16 value");
+constexpr float kLow = 20.0f, kFall = 40.0f;
+constexpr int kLowEvery = 8;
 static_assert(kChunkSmem <= 232448 - 1024, "shared memory budget");
 
 struct ChunkParams {
@@ -453,7 +462,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
             const bool mine = row < t.count;
             const int slot = t.slot0 + (mine ? row : t.count - 1);   // (a row past the tile's end: any legal slot)
             const int least = __shfl_sync(0xffffffffu, slot, 0);     // the warp's first row sees the fewest keys
-            float m = -INFINITY, sum = 0.f;
+            float m = -INFINITY, sum = 0.f;   // the reference, the weights' sum by it
+            float peak = -INFINITY;           // the highest reference so far
+            int low_from = 1;                 // the key tile from which on references may fall (the same for a warp)
             for (int j = 0; j < nk; ++j, ++phase) {
                 if (!__all_sync(0xffffffffu, wait(w, bar(B_S + s), phase & 1))) {
                     ok = false;
@@ -464,15 +475,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
                 const int limit = slot - first;   // the last key of the tile that the row sees
                 const bool masked = least - first < kKeys - 1;
                 // Half of the tile at a time.  The weights by the reference as it is, while the half's maximum is found: it
-                // is read once.  If the reference has to be raised (always at a row's first tile, seldom later) it is
-                // read again.
+                // is read once.  If the reference has to be raised (always at a row's first tile, seldom later) or falls it
+                // is read again.
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     uint32_t wgt[32];
                     float2 all;
                     const int seen = limit - 64 * half;
                     for (;;) {
-                        const float neg = m == -INFINITY ? 0.f : -m * P.scale_log2;   // (no key seen so far: weights of 0)
+                        const float neg = m == -INFINITY ? 0.f : fmaf(-m, P.scale_log2, kLift);   // (no key seen so far: weights of 0)
                         const uint64_t scale2 = pair(P.scale_log2, P.scale_log2), shift2 = pair(neg, neg);
                         uint64_t part[2] = {0, 0};
                         float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -504,11 +515,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
                         }
                         all = unpair(add_pair(part[0], part[1]));
                         const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-                        const bool raise = (top - m) * P.scale_log2 > kRescale;
-                        if (!__any_sync(0xffffffffu, raise)) break;
-                        const float f = raise ? ex2((m - top) * P.scale_log2) : 1.f;
-                        if (raise) {
-                            m = top;
+                        const float over = (top - m) * P.scale_log2;
+                        const bool raise = over > kRescale;
+                        const bool fall = j >= low_from && over < -kLow && top > -INFINITY;
+                        if (!__any_sync(0xffffffffu, raise || fall)) break;
+                        if (__any_sync(0xffffffffu, fall)) low_from = j + kLowEvery;
+                        float f = 1.f;
+                        if (raise || fall) {
+                            const float to = raise ? top : fmaxf(top, peak - kFall / P.scale_log2);
+                            f = ex2((m - to) * P.scale_log2);
+                            m = to;
+                            peak = fmaxf(peak, m);
                             sum *= f;
                         }
                         // O holds what came before: once its last product is done
@@ -582,7 +599,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
                 }
             }
             if (mine && P.lse)
-                P.lse[(size_t)(t.t0 + row) * kHeads + h] = (m * P.scale_log2 + log2f(sum)) * 0.6931471805599453f;
+                P.lse[(size_t)(t.t0 + row) * kHeads + h] = (m * P.scale_log2 + (log2f(sum) - kLift)) * 0.6931471805599453f;
             tc_fence_before();   // the next item's first product writes over O: after its P, which these threads write
         }
     }

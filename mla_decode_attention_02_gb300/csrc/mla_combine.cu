@@ -140,7 +140,7 @@ __device__ __forceinline__ void merge_task_cta(int32_t r, int32_t h, int32_t n, 
 template <bool kTree>
 __global__ void __launch_bounds__(32 * kCombineWarps, 3)
 mla_combine_kernel(const uint8_t *__restrict__ ws, __nv_bfloat16 *__restrict__ o_latent,
-                   float *__restrict__ lse_out, int32_t batch, int32_t s_q, int32_t num_units) {
+                   float *__restrict__ lse_out, int32_t batch, int32_t s_q, int32_t max_pages, int32_t num_units) {
     __shared__ float4 red[kCombineWarps][4][32];   // per warp: its lanes' 16 partial sums
     __shared__ float red_w[kCombineWarps], red_m[kCombineWarps];
     // launched as a programmatic dependent of the main kernel
@@ -150,7 +150,7 @@ mla_combine_kernel(const uint8_t *__restrict__ ws, __nv_bfloat16 *__restrict__ o
     const PlanHeader *hdr = reinterpret_cast<const PlanHeader *>(ws);
     if constexpr (kTree) {
         // (a workspace that holds another schedule was flagged by the main kernel)
-        if (hdr->magic != kTreeMagic || hdr->batch != batch || hdr->s_q != s_q || hdr->num_units != num_units) return;
+        if (!tree_plan_there({ws, batch, s_q, max_pages, num_units})) return;
         if (hdr->num_parts == 0 && (hdr->split & 2) == 0) return;
     } else {
         if (hdr->num_parts == 0 && (hdr->status & MLA_DEV_BAD_SEQ_LEN) == 0) return;
@@ -244,7 +244,7 @@ mla_combine_kernel(const uint8_t *__restrict__ ws, __nv_bfloat16 *__restrict__ o
 }  // namespace
 
 cudaError_t launch_combine(const void *ws, void *o_latent, float *lse, int32_t batch, int32_t s_q,
-                           int32_t num_units, bool tree, cudaStream_t stream) {
+                           int32_t max_pages, int32_t num_units, bool tree, cudaStream_t stream) {
     const int64_t tasks = (int64_t)(tree ? 1 : batch) * s_q * kHeads;
     const int grid = (int)(tasks < kCombineGrid ? tasks : kCombineGrid);
     cudaLaunchConfig_t cfg = {};
@@ -258,7 +258,7 @@ cudaError_t launch_combine(const void *ws, void *o_latent, float *lse, int32_t b
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, tree ? mla_combine_kernel<true> : mla_combine_kernel<false>,
                               static_cast<const uint8_t *>(ws), static_cast<__nv_bfloat16 *>(o_latent), lse, batch,
-                              s_q, num_units);
+                              s_q, max_pages, num_units);
 }
 
 }  // namespace mla

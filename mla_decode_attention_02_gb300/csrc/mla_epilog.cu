@@ -59,7 +59,7 @@ struct EpilogParams {
     CUtensorMap tm_a;   // o_latent viewed as (64 values, tokens, 8 K blocks, heads)
     CUtensorMap tm_b;   // W_UV viewed as (64 values, 128 rows, 8 K blocks, heads)
     __nv_bfloat16 *o_v;
-    const int32_t *row_parts;   // or null; a token whose entry is kRowUnused is not written
+    TreePlanRef plan;   // with one: only its rows are written, and nothing if it is not there
     int32_t *status;
     int32_t tokens, a_rows, stages;
 };
@@ -115,6 +115,15 @@ __global__ void __launch_bounds__(kThreadsE, 2) mla_epilog_uv_kernel(const __gri
     const uint32_t tmem = tmem_slot;
     pdl_wait_prior();
     pdl_launch_dependents();
+    const int32_t *row_parts = nullptr;
+    if (P.plan.ws) {
+        if (!tree_plan_there(P.plan)) {
+            if (warp == 0) tmem_dealloc(tmem, kTmemColsE);
+            return;
+        }
+        row_parts = reinterpret_cast<const int32_t *>(
+            P.plan.ws + make_layout(P.plan.tokens, P.plan.num_units, P.plan.batch).row_nparts);
+    }
 
     if (warp == 0) {
         if (elect_one()) {   // producer: the tile's A block and W_UV[h]'s block per stage
@@ -200,7 +209,7 @@ __global__ void __launch_bounds__(kThreadsE, 2) mla_epilog_uv_kernel(const __gri
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                          : "r"(base + b * kOBlkE + r * 128 + ((j ^ (r & 7)) * 16)));
-            if (tok < P.tokens && (!P.row_parts || P.row_parts[tok] != kRowUnused))
+            if (tok < P.tokens && (!row_parts || row_parts[tok] != kRowUnused))
                 *reinterpret_cast<uint4 *>(P.o_v + ((size_t)tok * kHeads + h) * kDv + j16 * 8) = v;
         }
     }
@@ -221,7 +230,7 @@ bool aligned16(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 15
 
 }  // namespace
 
-mla_status launch_epilog_uv(int64_t tokens, const void *o_latent, const void *w_uv, void *o_v, const int32_t *row_parts,
+mla_status launch_epilog_uv(int64_t tokens, const void *o_latent, const void *w_uv, void *o_v, const TreePlanRef &plan,
                             int32_t *device_status, mla_stream_t stream) {
     const int64_t ctas = (tokens + 127) / 128 * kHeads;
     int dev = 0;
@@ -248,7 +257,7 @@ mla_status launch_epilog_uv(int64_t tokens, const void *o_latent, const void *w_
         !encode_bf16_4d(&p.tm_b, w_uv, kDv, kKBlocks, H, kDl * 2, 128, (cuuint64_t)kDv * kDl * 2, kDv, 1))
         return MLA_ERR_CUDA;
     p.o_v = static_cast<__nv_bfloat16 *>(o_v);
-    p.row_parts = row_parts;
+    p.plan = plan;
     p.status = device_status;
     p.tokens = (int32_t)tokens;
     cudaLaunchConfig_t cfg = {};
@@ -280,5 +289,5 @@ extern "C" mla_status mla_epilog_uv(const mla_problem *prob, const void *o_laten
     if (!aligned16(o_latent) || !aligned16(w_uv) || !aligned16(o_v) || !device_status ||
         (reinterpret_cast<uintptr_t>(device_status) & 3u))
         return MLA_ERR_INVALID_ARG;
-    return launch_epilog_uv(tokens, o_latent, w_uv, o_v, nullptr, device_status, stream);
+    return launch_epilog_uv(tokens, o_latent, w_uv, o_v, TreePlanRef{}, device_status, stream);
 }

@@ -45,11 +45,8 @@ mla_tree_expand_kernel(const uint8_t *__restrict__ ws, const uint8_t *__restrict
                        int32_t tokens, int32_t max_pages, int32_t num_units) {
     ptx::pdl_wait_prior();
     ptx::pdl_launch_dependents();
-    const PlanHeader *hdr = reinterpret_cast<const PlanHeader *>(ws);
     // (a workspace that holds another schedule is flagged by the main kernel)
-    if (hdr->magic != kTreeMagic || hdr->batch != batch || hdr->s_q != tokens || hdr->num_units != num_units ||
-        hdr->max_pages != max_pages)
-        return;
+    if (!tree_plan_there({ws, batch, tokens, max_pages, num_units})) return;
     const int32_t b = blockIdx.y;
     const int32_t pages = reinterpret_cast<const int32_t *>(ws + make_layout(tokens, num_units, batch).tree_pages)[b];
     float *scales = reinterpret_cast<float *>(out + expanded_scales(batch, max_pages));

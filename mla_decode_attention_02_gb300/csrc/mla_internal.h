@@ -235,6 +235,18 @@ struct NoEmit {
     MLA_HD void operator()(int32_t, int32_t, int32_t, int32_t) const {}
 };
 
+// The tree schedule that a kernel goes by, as its caller sized the workspace (ws null: none).
+struct TreePlanRef {
+    const uint8_t *ws;
+    int32_t batch, tokens, max_pages, num_units;
+};
+// Whether the workspace holds that schedule (if not, the main kernel flags it and nothing is written).
+MLA_HD bool tree_plan_there(const TreePlanRef &t) {
+    const PlanHeader *h = reinterpret_cast<const PlanHeader *>(t.ws);
+    return h->magic == kTreeMagic && h->batch == t.batch && h->s_q == t.tokens && h->max_pages == t.max_pages &&
+           h->num_units == t.num_units;
+}
+
 // Checks of a ragged problem that make no CUDA call (flags: those allowed).
 mla_status check_ragged(const mla_ragged *p, int32_t flags);
 

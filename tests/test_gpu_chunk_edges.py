@@ -165,3 +165,18 @@ def test_scores_that_fall_without_end():
         c["cache"][int(c["block_table"][0, j]), :, 575] = -17.0 * (j // 8) / (16 * SCALE)
     lse = torch.empty(c["T"], 128, device="cuda")
     check_exact(c, attend(c, lse=lse), lse)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("field,value", [("tokens", 22), ("max_pages", 46), ("batch", 2)])
+def test_another_plan_in_the_workspace_of_few_tokens(field, value, fp8):
+    """The absorbed form, as the other: what the plan in the workspace is not for is flagged, and nothing is written."""
+    c = CU.case([3, 0, 20], [3000, 0, 2500], seed=66, fp8=fp8, spare=0)
+    p = plan(c)
+    setattr(p, field, value)
+    d = dict(c, q=c["q"][:p.tokens], block_table=c["block_table"][:p.batch, :p.max_pages].contiguous())
+    out = torch.full((p.tokens, 128, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((p.tokens, 128), 7.0, device="cuda")
+    attend(d, p, out=out, lse=lse)
+    assert mla.check(p) & mla.MLA_DEV_BAD_PLAN
+    assert (out == 7).all() and (lse == 7).all()

@@ -119,10 +119,12 @@ typedef struct mla_chunk {
 } mla_chunk;
 
 /*
- * Two forms compute a step, chosen from the problem alone (tokens and keys spread evenly over the requests, by
- * both forms' measured times): every head's keys and values worked out once from the cached rows, or,
- * for few tokens a request over long contexts, the absorbed form of mla_decode with its roundings (absorbed
- * queries and latent outputs in bf16).
+ * Two forms compute a request: every head's keys and values worked out once from its cached rows (the whole form), or,
+ * for few tokens over a long context, the absorbed form of mla_decode with its roundings (absorbed queries and latent
+ * outputs in bf16).  By both forms' measured times the absorbed one is taken where it saves a quarter at least (up to some
+ * 100 tokens).  Where one form is sound for the whole step from the problem alone (one request, up to 80 tokens,
+ * few keys) the step has that form; any other step is mixed, and mla_chunk_plan takes a form for each request.
+ * Requests without tokens change nothing.
  *
  * Workspace bytes of mla_chunk_plan / mla_chunk_attend on the current device.
  */
@@ -132,7 +134,7 @@ mla_status mla_chunk_workspace_size(const mla_chunk *prob, size_t *bytes);
  * Scratch bytes of mla_chunk_attend (fp8 = 1: mla_chunk_attend_fp8) with the keys and values of `heads` heads at
  * once (1 .. 128): 128 bytes a key and 512 a key and head, rounded up to 256 keys.  In the absorbed form instead 279 KB a token
  * whatever `heads`, and over an fp8 cache room to expand each page once for all tokens (mla_tree_scratch_size) if
- * they average two a request and it takes no more than 8 GiB; less than that runs without.
+ * they average two a request and it takes no more than 8 GiB; less than that runs without.  A mixed step: both.
  */
 mla_status mla_chunk_scratch_size(const mla_chunk *prob, int32_t heads, int32_t fp8, size_t *bytes);
 
@@ -143,7 +145,7 @@ mla_status mla_chunk_scratch_size(const mla_chunk *prob, int32_t heads, int32_t 
  * A request whose seq_len is below its token count or beyond max_pages_per_seq pages: MLA_DEV_BAD_SEQ_LEN and
  * NaN outputs for its tokens.  Bad offsets (MLA_DEV_BAD_OFFSETS) or more pages than kv_tokens
  * (MLA_DEV_BAD_KV_TOKENS): NaN outputs for every row.  (The absorbed form does not depend on kv_tokens and
- * does not check it.)
+ * does not check it: of a mixed step the requests in that form are not counted and keep their outputs.)
  */
 mla_status mla_chunk_plan(const mla_chunk *prob, const int32_t *seq_lens, const int32_t *token_offsets,
                           void *workspace, size_t workspace_bytes, mla_stream_t stream);

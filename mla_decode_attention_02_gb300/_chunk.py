@@ -252,9 +252,9 @@ def chunk_attend(p: ChunkPlan, q_nope, q_rope, w_uk, w_uv, kv_cache, block_table
 
     Keys and values of all heads are worked out once per call from the cached rows, into scratch: a uint8 tensor of
     ``chunk_scratch_size(p, heads)`` bytes for as many heads at a time as it shall hold, by default one for
-    the call with all 128, or as many as CHUNK_SCRATCH_BYTES hold.  A few tokens a request (below some 200) over long
-    contexts are computed in the absorbed form instead (``query``, the tree step's attention, ``epilog_uv``), chosen
-    from the plan's sizes.
+    the call with all 128, or as many as CHUNK_SCRATCH_BYTES hold.  A request of few tokens (some 100 at most) over a long
+    context is computed in the absorbed form instead (``query``, the tree step's attention, ``epilog_uv``): the plan takes
+    a form for each request, or for the step where its sizes say enough (``mla_chunk.h``).
     """
     return _attend(p, q_nope, q_rope, w_uk, w_uv, kv_cache, block_table, scale, out, lse, scratch, stream, False)
 

@@ -31,9 +31,9 @@ cudaError_t launch_expand(const void *ws, const void *kv_cache_fp8, int64_t num_
 bool tree_plan_fits(int32_t rows, int32_t units);
 mla_status tree_plan_host(const mla_ragged *prob, const int32_t *seq_lens, const int32_t *offsets,
                           const uint64_t *masks, int32_t num_units, uint8_t *ws);
-cudaError_t launch_tree_plan(const int32_t *seq_lens, const int32_t *offsets, const uint64_t *masks, void *ws,
-                             int32_t batch, int32_t tokens, int32_t max_pages, int32_t num_units,
-                             cudaStream_t stream);
+cudaError_t launch_tree_plan(const int32_t *seq_lens, const int32_t *offsets, const uint64_t *masks, const uint8_t *forms,
+                             int32_t *zeros, void *ws, int32_t batch, int32_t tokens, int32_t max_pages,
+                             int32_t num_units, cudaStream_t stream);
 constexpr uint64_t kDefaultWaitLimitNs = 2000000000ull;  // a bounded device wait gives up after 2 s
 }  // namespace mla
 
@@ -286,8 +286,9 @@ mla_status mla_tree_plan(const mla_ragged *prob, const int32_t *seq_lens, const 
     if (mla::main_units(&units) != cudaSuccess) return MLA_ERR_CUDA;
     if (!mla::tree_plan_fits(prob->tokens, units)) return MLA_ERR_UNSUPPORTED;
     if (workspace_bytes < mla::make_layout(prob->tokens, units, prob->batch).total) return MLA_ERR_WORKSPACE;
-    const cudaError_t e = mla::launch_tree_plan(seq_lens, token_offsets, masks, workspace, prob->batch, prob->tokens,
-                                                prob->max_pages_per_seq, units, reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e = mla::launch_tree_plan(seq_lens, token_offsets, masks, nullptr, nullptr, workspace, prob->batch,
+                                                prob->tokens, prob->max_pages_per_seq, units,
+                                                reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 

@@ -634,16 +634,31 @@ mla_status attend(const mla_chunk *prob, const void *q_nope, int64_t nope_token,
     int32_t units = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MLA_ERR_CUDA;
     if (main_units(&units) != cudaSuccess) return MLA_ERR_CUDA;
-    if (chunk_absorbed(prob, units)) {
-        if (workspace_bytes < absorbed_workspace_bytes(prob, units) || scratch_bytes < absorbed_scratch_bytes(prob, false))
-            return MLA_ERR_WORKSPACE;
-        return absorbed_attend(prob, q_nope, nope_token, nope_head, q_rope, rope_token, rope_head, w_uk, w_uv, cache, fp8,
-                               num_pages, block_table, scale, out, lse, workspace, static_cast<uint8_t *>(scratch),
-                               scratch_bytes, units, stream);
-    }
-    if (workspace_bytes < chunk_layout(prob->batch, prob->tokens, prob->kv_tokens).total) return MLA_ERR_WORKSPACE;
+    const ChunkForm form = chunk_form(prob, units);
+    if (workspace_bytes < chunk_workspace_bytes(prob, form, units)) return MLA_ERR_WORKSPACE;
     const size_t rope_bytes = chunk_rope_bytes(prob->kv_tokens), head_bytes = chunk_head_bytes(prob->kv_tokens);
-    if (scratch_bytes < rope_bytes + head_bytes) return MLA_ERR_WORKSPACE;
+    const size_t least = form == ChunkForm::kAbsorbed ? 0 : rope_bytes + head_bytes;
+    // the scratch: the absorbed form's, its expanded pages if there is room, the whole form's
+    uint8_t *const ws = static_cast<uint8_t *>(workspace), *const few_space = static_cast<uint8_t *>(scratch);
+    uint8_t *space = few_space, *expanded = nullptr;
+    if (form != ChunkForm::kWhole) {
+        const size_t rows = absorbed_scratch_bytes(prob), pages = fp8 ? absorbed_expanded_bytes(prob) : 0;
+        if (scratch_bytes < rows + least) return MLA_ERR_WORKSPACE;
+        space += rows;
+        if (pages && scratch_bytes - rows - least >= pages) {
+            expanded = space;
+            space += pages;
+        }
+        scratch_bytes -= (size_t)(space - few_space);
+    }
+    auto few = [&]() {
+        const bool mixed = form == ChunkForm::kMixed;
+        return absorbed_attend(prob, q_nope, nope_token, nope_head, q_rope, rope_token, rope_head, w_uk, w_uv, cache, fp8,
+                               num_pages, block_table, scale, out, lse, mixed ? ws + mixed_tree(prob) : ws, mixed,
+                               &reinterpret_cast<PlanHeader *>(ws)->status, few_space, expanded, units, stream);
+    };
+    if (form == ChunkForm::kAbsorbed) return few();
+    if (scratch_bytes < least) return MLA_ERR_WORKSPACE;
     const size_t room = (scratch_bytes - rope_bytes) / head_bytes;
     const int32_t fit = room < (size_t)kHeads ? (int32_t)room : kHeads;
     const int32_t passes = (kHeads + fit - 1) / fit;
@@ -656,7 +671,7 @@ mla_status attend(const mla_chunk *prob, const void *q_nope, int64_t nope_token,
             g_chunk_attr[dev] = true;
         }
     }
-    uint8_t *rope = static_cast<uint8_t *>(scratch), *kv = rope + rope_bytes;
+    uint8_t *rope = space, *kv = rope + rope_bytes;
     const cuuint64_t rows = (cuuint64_t)chunk_rows(prob->kv_tokens), T = (cuuint64_t)prob->tokens;
     ChunkParams p{};
     if (!encode_bf16_4d(&p.tm_qn, q_nope, T, kDn / 64, kHeads, (cuuint64_t)nope_token * 2, 128, (cuuint64_t)nope_head * 2,
@@ -665,7 +680,7 @@ mla_status attend(const mla_chunk *prob, const void *q_nope, int64_t nope_token,
         !encode_bf16_4d(&p.tm_kr, rope, rows, 1, 1, kDr * 2, rows * kDr * 2, rows * kDr * 2, 128, 1) ||
         !encode_bf16_4d(&p.tm_kv, kv, rows, 4, (cuuint64_t)fit, (kDn + kDv) * 2, 128, rows * (kDn + kDv) * 2, 128, 1))
         return MLA_ERR_CUDA;
-    p.ws = static_cast<uint8_t *>(workspace);
+    p.ws = ws;
     p.out = static_cast<__nv_bfloat16 *>(out);
     p.lse = lse;
     p.kv_tokens = prob->kv_tokens;
@@ -692,7 +707,7 @@ mla_status attend(const mla_chunk *prob, const void *q_nope, int64_t nope_token,
             cudaLaunchKernelEx(&cfg, mla_chunk_kernel, p) != cudaSuccess)
             return MLA_ERR_CUDA;
     }
-    return MLA_OK;
+    return form == ChunkForm::kMixed ? few() : MLA_OK;
 }
 
 }  // namespace
@@ -704,9 +719,12 @@ extern "C" mla_status mla_chunk_scratch_size(const mla_chunk *prob, int32_t head
     if (!bytes || heads < 1 || heads > mla::kHeads || (fp8 != 0 && fp8 != 1)) return MLA_ERR_INVALID_ARG;
     int32_t units = 0;
     if (mla::main_units(&units) != cudaSuccess) return MLA_ERR_CUDA;
-    *bytes = mla::chunk_absorbed(prob, units)
-                 ? mla::absorbed_scratch_bytes(prob, fp8 != 0)
-                 : mla::chunk_rope_bytes(prob->kv_tokens) + (size_t)heads * mla::chunk_head_bytes(prob->kv_tokens);
+    const mla::ChunkForm form = mla::chunk_form(prob, units);
+    *bytes = 0;
+    if (form != mla::ChunkForm::kWhole)
+        *bytes += mla::absorbed_scratch_bytes(prob) + (fp8 ? mla::absorbed_expanded_bytes(prob) : 0);
+    if (form != mla::ChunkForm::kAbsorbed)
+        *bytes += mla::chunk_rope_bytes(prob->kv_tokens) + (size_t)heads * mla::chunk_head_bytes(prob->kv_tokens);
     return MLA_OK;
 }
 

@@ -5,6 +5,8 @@
 // A request's tiles stand together, its last (which reads the most keys) first, the
 // requests with the longest tiles first: what runs at the same time then shares keys, and
 // what runs last is short.
+// Of a mixed step the plan first decides which requests the absorbed form takes (mla_chunk_absorbed.cu): those where it
+// saves a quarter at least, if that pays for its launches; they have no tiles and pages here.
 // One CTA: a scan over the requests (their pages and tiles), then tiles and pages
 // by all threads, each finding its request in the scan; the tiles are ranked by
 // counting.
@@ -67,9 +69,9 @@ __device__ __forceinline__ int find(const int32_t *sum, int n, int32_t i) {
 
 __global__ void __launch_bounds__(kPlanThreads)
 mla_chunk_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__restrict__ off, uint8_t *ws, int32_t batch,
-                      int32_t tokens, int32_t max_pages, int64_t kv_tokens) {
+                      int32_t tokens, int32_t max_pages, int64_t kv_tokens, uint8_t *forms, int32_t units) {
     __shared__ int32_t sums[kPlanThreads / 32][2];
-    __shared__ unsigned long long all_pages;
+    __shared__ unsigned long long all_pages, all_gain;
     __shared__ int32_t s_page[kPlanThreads + 1], s_first[kPlanThreads + 1];   // pages and tiles before each request
     __shared__ int4 s_tile[kRankTiles];   // t0, count, slot0, base
     __shared__ RankKey s_key[kRankTiles];
@@ -78,13 +80,19 @@ mla_chunk_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__res
     ChunkTile *tiles = reinterpret_cast<ChunkTile *>(ws + L.tiles);
     ChunkPage *pages = reinterpret_cast<ChunkPage *>(ws + L.pages);
     const int t = threadIdx.x;
-    if (t == 0) all_pages = 0;
+    if (t == 0) all_pages = all_gain = 0;
     ptx::pdl_wait_prior();
     ptx::pdl_launch_dependents();
-    // A request's tokens, length, pages and tiles (none without tokens); ok: its seq_len is sound.
+    // A request's tokens, length, pages and tiles (none without tokens, or in the absorbed form); ok: its seq_len is sound.
     struct Request {
         int32_t begin, n, len, np, nt;
-        bool ok;
+        bool ok, absorbed;
+        __device__ int64_t gain(int32_t units) const { return nt > 0 && ok ? absorbed_gain(n, len, units) : 0; }
+    };
+    bool take = false;   // whether any request is in the absorbed form
+    auto leave = [&](Request &r) {
+        r.absorbed = take && r.gain(units) > 0;
+        if (r.absorbed) r.np = r.nt = 0;
     };
     auto request = [&](int32_t b) {
         Request r = {};
@@ -97,20 +105,41 @@ mla_chunk_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__res
         r.nt = (r.n - 1) / kChunkTile + 1;
         r.ok = r.len >= r.n && r.len <= (int64_t)max_pages * kPage;
         if (r.ok) r.np = (r.len - 1) / kPage + 1;
+        leave(r);
         return r;
     };
     // The offsets as a whole, and the pages of all requests.
-    bool bad_off = t == 0 && (off[0] != 0 || off[batch] > tokens), bad_len = false;
-    int64_t mine = 0;
+    bool bad_off = t == 0 && (off[0] != 0 || off[batch] > tokens), bad_len = false, keeps = false;
+    int64_t mine = 0, gain = 0;
     Request own;
     for (int32_t b = t; b < batch || b == t; b += kPlanThreads) {
         own = request(b);
         bad_off |= b < batch && (own.begin < 0 || own.n < 0);
         bad_len |= !own.ok;
         mine += own.np;
+        if (forms) {
+            const int64_t g = own.gain(units);
+            if (g > 0) gain += g;
+            keeps |= own.nt > 0 && g <= 0;
+        }
     }
     bad_off = __syncthreads_or(bad_off);
     bad_len = __syncthreads_or(bad_len);
+    if (forms) {
+        // (in whole nanoseconds, so that the sum does not depend on its order)
+        if (gain) atomicAdd(&all_gain, (unsigned long long)gain);
+        keeps = __syncthreads_or(keeps);
+        // a step all in the absorbed form saves the other's launches; its queries' kernel goes over all tokens
+        const int64_t fixed = kAbsorbedFixed + 10 * (int64_t)tokens - (keeps ? 0 : kWholeFixed * 3 / 4);
+        take = !bad_off && (int64_t)all_gain > fixed;
+        mine = 0;
+        for (int32_t b = t; b < batch; b += kPlanThreads) {
+            if (batch > kPlanThreads) own = request(b);
+            else leave(own);
+            forms[b] = own.absorbed;
+            mine += own.np;
+        }
+    }
     if (mine) atomicAdd(&all_pages, (unsigned long long)mine);
     __syncthreads();
     const bool over = !bad_off && (int64_t)all_pages * kPage > kv_tokens;
@@ -192,6 +221,12 @@ bool aligned(const void *p, uintptr_t a) { return p && (reinterpret_cast<uintptr
 
 }  // namespace
 
+size_t chunk_workspace_bytes(const mla_chunk *p, ChunkForm form, int32_t units) {
+    return form == ChunkForm::kAbsorbed ? absorbed_workspace_bytes(p, units)
+           : form == ChunkForm::kMixed  ? mixed_tree(p) + absorbed_workspace_bytes(p, units)
+                                        : chunk_layout(p->batch, p->tokens, p->kv_tokens).total;
+}
+
 mla_status check_chunk(const mla_chunk *p) {
     if (!p) return MLA_ERR_INVALID_ARG;
     const mla_ragged r = {p->batch, p->tokens, p->num_heads, p->page_size, p->max_pages_per_seq, p->flags};
@@ -209,8 +244,7 @@ extern "C" mla_status mla_chunk_workspace_size(const mla_chunk *prob, size_t *by
     if (!bytes) return MLA_ERR_INVALID_ARG;
     int32_t units = 0;
     if (mla::main_units(&units) != cudaSuccess) return MLA_ERR_CUDA;
-    *bytes = mla::chunk_absorbed(prob, units) ? mla::absorbed_workspace_bytes(prob, units)
-                                              : mla::chunk_layout(prob->batch, prob->tokens, prob->kv_tokens).total;
+    *bytes = mla::chunk_workspace_bytes(prob, mla::chunk_form(prob, units), units);
     return MLA_OK;
 }
 
@@ -223,22 +257,22 @@ extern "C" mla_status mla_chunk_plan(const mla_chunk *prob, const int32_t *seq_l
     if (!aligned(seq_lens, 4) || !aligned(token_offsets, 4) || !aligned(workspace, 16)) return MLA_ERR_INVALID_ARG;
     int32_t units = 0;
     if (main_units(&units) != cudaSuccess) return MLA_ERR_CUDA;
-    if (chunk_absorbed(prob, units)) {
-        if (workspace_bytes < absorbed_workspace_bytes(prob, units)) return MLA_ERR_WORKSPACE;
-        return absorbed_plan(prob, seq_lens, token_offsets, workspace, units, reinterpret_cast<cudaStream_t>(stream));
-    }
-    if (workspace_bytes < chunk_layout(prob->batch, prob->tokens, prob->kv_tokens).total) return MLA_ERR_WORKSPACE;
+    const ChunkForm form = chunk_form(prob, units);
+    if (workspace_bytes < chunk_workspace_bytes(prob, form, units)) return MLA_ERR_WORKSPACE;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (form == ChunkForm::kAbsorbed) return absorbed_plan(prob, seq_lens, token_offsets, nullptr, workspace, units, s);
+    uint8_t *ws = static_cast<uint8_t *>(workspace), *forms = form == ChunkForm::kMixed ? ws + mixed_forms(prob) : nullptr;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(1);
     cfg.blockDim = dim3(kPlanThreads);
-    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cfg.stream = s;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mla_chunk_plan_kernel, seq_lens, token_offsets, static_cast<uint8_t *>(workspace),
-                              prob->batch, prob->tokens, prob->max_pages_per_seq, prob->kv_tokens) == cudaSuccess
-               ? MLA_OK
-               : MLA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, mla_chunk_plan_kernel, seq_lens, token_offsets, ws, prob->batch, prob->tokens,
+                           prob->max_pages_per_seq, prob->kv_tokens, forms, units) != cudaSuccess)
+        return MLA_ERR_CUDA;
+    return forms ? absorbed_plan(prob, seq_lens, token_offsets, forms, ws + mixed_tree(prob), units, s) : MLA_OK;
 }

@@ -150,7 +150,7 @@ mla_combine_kernel(const uint8_t *__restrict__ ws, __nv_bfloat16 *__restrict__ o
     const PlanHeader *hdr = reinterpret_cast<const PlanHeader *>(ws);
     if constexpr (kTree) {
         // (a workspace that holds another schedule was flagged by the main kernel)
-        if (!tree_plan_there({ws, batch, s_q, max_pages, num_units})) return;
+        if (!tree_plan_there({ws, batch, s_q, max_pages, num_units, false})) return;
         if (hdr->num_parts == 0 && (hdr->split & 2) == 0) return;
     } else {
         if (hdr->num_parts == 0 && (hdr->status & MLA_DEV_BAD_SEQ_LEN) == 0) return;

@@ -51,7 +51,7 @@ constexpr uint32_t kOBlkE = 128 * 128;    // one 64-column block of the staged o
 constexpr uint32_t kTmemColsE = kDv;
 constexpr uint32_t kSmemMinE = 48 * 1024; // never five CTAs on an SM (four fill its TMEM)
 constexpr uint64_t kWaitLimitNsE = 2000000000ull;
-static_assert(kDv == 128 && kDl % 64 == 0, "M=128 x N=128 tiles over 64-value K blocks");
+static_assert(kDv == 128 && kDl % 64 == 0 && kThreadsE == 128, "M=128 x N=128 tiles over 64-value K blocks, a row a thread");
 // dynamic shared memory budget: 227 KB per block, less room for the static barriers
 constexpr uint32_t kSmemMaxE = 232448 - 2048;
 
@@ -59,7 +59,7 @@ struct EpilogParams {
     CUtensorMap tm_a;   // o_latent viewed as (64 values, tokens, 8 K blocks, heads)
     CUtensorMap tm_b;   // W_UV viewed as (64 values, 128 rows, 8 K blocks, heads)
     __nv_bfloat16 *o_v;
-    TreePlanRef plan;   // with one: only its rows are written, and nothing if it is not there
+    TreePlanRef plan;   // with one: only its rows are written, and nothing if it is not there; its status goes to ours
     int32_t *status;
     int32_t tokens, a_rows, stages;
 };
@@ -81,6 +81,11 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 __global__ void __launch_bounds__(kThreadsE, 2) mla_epilog_uv_kernel(const __grid_constant__ EpilogParams P) {
+    if (P.plan.sparse) {
+        pdl_launch_dependents();
+        pdl_wait_prior();
+        if (tree_plan_idle(P.plan)) return;
+    }
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[2 * kMaxStagesE + 1];   // full[s], empty[s], done
     __shared__ uint32_t tmem_slot;
@@ -116,13 +121,18 @@ __global__ void __launch_bounds__(kThreadsE, 2) mla_epilog_uv_kernel(const __gri
     pdl_wait_prior();
     pdl_launch_dependents();
     const int32_t *row_parts = nullptr;
+    bool there = true;
     if (P.plan.ws) {
-        if (!tree_plan_there(P.plan)) {
+        const PlanHeader *hdr = reinterpret_cast<const PlanHeader *>(P.plan.ws);
+        if (blockIdx.x == 0 && threadIdx.x == 0 && hdr->status && &hdr->status != P.status) atomicOr(P.status, hdr->status);
+        row_parts = reinterpret_cast<const int32_t *>(
+            P.plan.ws + make_layout(P.plan.tokens, P.plan.num_units, P.plan.batch).row_nparts);
+        there = tree_plan_there(P.plan);
+        const int tok = mt * 128 + (int)threadIdx.x;
+        if (P.plan.sparse && !__syncthreads_or(there && tok < P.tokens && row_parts[tok] != kRowUnused)) {   // no row of the tile
             if (warp == 0) tmem_dealloc(tmem, kTmemColsE);
             return;
         }
-        row_parts = reinterpret_cast<const int32_t *>(
-            P.plan.ws + make_layout(P.plan.tokens, P.plan.num_units, P.plan.batch).row_nparts);
     }
 
     if (warp == 0) {
@@ -209,7 +219,7 @@ __global__ void __launch_bounds__(kThreadsE, 2) mla_epilog_uv_kernel(const __gri
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                          : "r"(base + b * kOBlkE + r * 128 + ((j ^ (r & 7)) * 16)));
-            if (tok < P.tokens && (!row_parts || row_parts[tok] != kRowUnused))
+            if (there && tok < P.tokens && (!row_parts || row_parts[tok] != kRowUnused))
                 *reinterpret_cast<uint4 *>(P.o_v + ((size_t)tok * kHeads + h) * kDv + j16 * 8) = v;
         }
     }

@@ -46,7 +46,8 @@ mla_tree_expand_kernel(const uint8_t *__restrict__ ws, const uint8_t *__restrict
     ptx::pdl_wait_prior();
     ptx::pdl_launch_dependents();
     // (a workspace that holds another schedule is flagged by the main kernel)
-    if (!tree_plan_there({ws, batch, tokens, max_pages, num_units})) return;
+    const TreePlanRef plan = {ws, batch, tokens, max_pages, num_units, true};
+    if (!tree_plan_there(plan) || tree_plan_idle(plan)) return;
     const int32_t b = blockIdx.y;
     const int32_t pages = reinterpret_cast<const int32_t *>(ws + make_layout(tokens, num_units, batch).tree_pages)[b];
     float *scales = reinterpret_cast<float *>(out + expanded_scales(batch, max_pages));

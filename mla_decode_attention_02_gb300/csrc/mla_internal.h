@@ -235,16 +235,24 @@ struct NoEmit {
     MLA_HD void operator()(int32_t, int32_t, int32_t, int32_t) const {}
 };
 
-// The tree schedule that a kernel goes by, as its caller sized the workspace (ws null: none).
+// The tree schedule that a kernel goes by, as its caller sized the workspace (ws null: none).  sparse: of a mixed step
+// over chunks, with rows of few of the tokens or none.
 struct TreePlanRef {
     const uint8_t *ws;
     int32_t batch, tokens, max_pages, num_units;
+    bool sparse;
 };
 // Whether the workspace holds that schedule (if not, the main kernel flags it and nothing is written).
 MLA_HD bool tree_plan_there(const TreePlanRef &t) {
     const PlanHeader *h = reinterpret_cast<const PlanHeader *>(t.ws);
     return h->magic == kTreeMagic && h->batch == t.batch && h->s_q == t.tokens && h->max_pages == t.max_pages &&
            h->num_units == t.num_units;
+}
+constexpr uint32_t kMainSparse = 0x80000000u;   // among launch_main's flags
+// Whether no row of it has keys or an output of its own.
+MLA_HD bool tree_plan_idle(const TreePlanRef &t) {
+    const PlanHeader *h = reinterpret_cast<const PlanHeader *>(t.ws);
+    return tree_plan_there(t) && h->num_items == 0 && !(h->split & 2);
 }
 
 // Checks of a ragged problem that make no CUDA call (flags: those allowed).

@@ -220,7 +220,7 @@ struct Params {
     float scale_log2;
     int32_t batch, s_q, max_pages, num_units;
     uint32_t test_flags;
-    uint32_t flags;          // mla_problem.flags (MLA_FLAG_POW2_MAX)
+    uint32_t flags;          // mla_problem.flags (MLA_FLAG_POW2_MAX), kMainSparse
     uint32_t prefetch;       // trees: whether pages are warmed in L2 ahead of their loads
 };
 
@@ -557,6 +557,13 @@ __global__ void __launch_bounds__(kFp8 && !kExpanded ? kThreadsFp8 : kThreads, 1
 mla_main_tc_kernel(const __grid_constant__ Params P) {
     constexpr bool kConv = kFp8 && !kExpanded;      // converter warps expand the stages
     constexpr int kScaleStep = kExpanded ? 1 : 4;   // floats from one token's scale to the next
+    if constexpr (kTree) {
+        if (P.flags & kMainSparse) {   // (the same for every CTA)
+            pdl_launch_dependents();
+            pdl_wait_prior();
+            if (tree_plan_idle({P.ws, P.batch, P.s_q, P.max_pages, P.num_units, true})) return;
+        }
+    }
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));

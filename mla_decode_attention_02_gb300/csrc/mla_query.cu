@@ -69,7 +69,10 @@ struct QueryParams {
     int32_t *status;
     int64_t pe_token, pe_head;
     int32_t tokens, tiles;
+    TreePlanRef plan;    // of a mixed step: only tiles with a row in it (a position that is not negative)
 };
+
+constexpr int kMaxPlanTiles = 128;   // (a tree schedule's planner takes some 10,000 rows)
 
 // Bounded wait; on time-out flags the CTA (every other wait then gives up at once).
 __device__ __noinline__ bool query_wait(uint32_t bar, uint32_t parity, volatile int *abort, int32_t *status) {
@@ -101,10 +104,16 @@ __device__ __noinline__ void query_landed(uint32_t bar, uint32_t parity, int32_t
 }
 
 __global__ void __launch_bounds__(kQueryThreads, 1) mla_query_kernel(const __grid_constant__ QueryParams P) {
+    if (P.plan.sparse) {
+        pdl_launch_dependents();
+        pdl_wait_prior();
+        if (tree_plan_idle(P.plan)) return;
+    }
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[11];
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_flag;
+    __shared__ int abort_flag, live_tiles;
+    __shared__ uint8_t live[kMaxPlanTiles];
     const uint32_t s_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
@@ -133,14 +142,36 @@ __global__ void __launch_bounds__(kQueryThreads, 1) mla_query_kernel(const __gri
     pdl_wait_prior();
     pdl_launch_dependents();
 
+    int tiles = P.tiles;
+    if (P.plan.sparse) {
+        const bool any = tree_plan_there(P.plan);
+        for (int t = warp; t < P.tiles; t += kQueryThreads / 32) {
+            bool has = false;
+            if (any)
+                for (int r = t * kTile + lane; r < (t + 1) * kTile && r < P.tokens; r += 32) has |= P.positions[r] >= 0;
+            has = __any_sync(0xffffffffu, has);
+            if (lane == 0) live[t] = has;
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {   // the tiles with rows, in order
+            int n = 0;
+            for (int t = 0; t < P.tiles; ++t)
+                if (live[t]) live[n++] = (uint8_t)t;
+            live_tiles = n;
+        }
+        __syncthreads();
+        tiles = live_tiles;
+    }
+
     // Items: CTA c takes head-half c over all tiles, so that the CTAs move along the tokens together
     // and write neighbouring rows at the same time (1537 tokens: 59.4 us against 67.0 with one contiguous
     // run of (head, half, tile) per CTA), then a share of the other head-halves' items.
-    const int64_t rest = ((int64_t)kHeads * kHalves - gridDim.x) * P.tiles;
-    const int64_t r0 = rest * blockIdx.x / gridDim.x - P.tiles;
+    const int64_t rest = ((int64_t)kHeads * kHalves - gridDim.x) * tiles;
+    const int64_t r0 = rest * blockIdx.x / gridDim.x - tiles;
     const int n = (int)(rest * (blockIdx.x + 1) / gridDim.x - r0);
-    auto head_half = [&](int i) { return i < P.tiles ? (int)blockIdx.x : (int)(gridDim.x + (r0 + i) / P.tiles); };
-    auto tile_of = [&](int i) { return i < P.tiles ? i : (int)((r0 + i) % P.tiles); };
+    auto head_half = [&](int i) { return i < tiles ? (int)blockIdx.x : (int)(gridDim.x + (r0 + i) / tiles); };
+    auto place_of = [&](int i) { return i < tiles ? i : (int)((r0 + i) % tiles); };
+    auto tile_of = [&](int i) { return P.plan.sparse ? (int)live[place_of(i)] : place_of(i); };
 
     if (warp == 0) {
         if (elect_one()) {
@@ -177,7 +208,7 @@ __global__ void __launch_bounds__(kQueryThreads, 1) mla_query_kernel(const __gri
                 if (!ok) break;
                 if (i + 1 < n) load_a(i + 1);
                 if (i == next_w) {   // (every MMA of the items before is done: waited above)
-                    next_w = i + P.tiles - tile_of(i);
+                    next_w = i + tiles - place_of(i);
                     if (next_w < n) load_w(next_w);
                     ok = query_wait(bar(B_W + (w_used & 1)), (w_used >> 1) & 1, &abort_flag, P.status);
                     ++w_used;
@@ -263,10 +294,11 @@ __global__ void __launch_bounds__(kQueryThreads, 1) mla_query_kernel(const __gri
             gh[j] = P.rope_table[pair0 + j];
             gl[j] = P.rope_table[kPairs + pair0 + j];
         }
-        const int64_t units = (int64_t)P.tokens * 4, warps = (int64_t)gridDim.x * kRopeWarps;
+        const int64_t units = tiles > 0 ? (int64_t)P.tokens * 4 : 0, warps = (int64_t)gridDim.x * kRopeWarps;
         const int64_t w = (int64_t)blockIdx.x * kRopeWarps + warp - 1 - kEpiWarps;
         for (int64_t u = units * w / warps, end = units * (w + 1) / warps; u < end; ++u) {
             const int tok = (int)(u >> 2), h0 = (int)(u & 3) * 32 + (lane >> 3);
+            if (P.plan.sparse && P.positions[tok] < 0) continue;
             const __nv_bfloat16 *src = P.q_pe + tok * P.pe_token + h0 * P.pe_head + pair0 * 2;
             uint4 v[8];
 #pragma unroll
@@ -295,15 +327,12 @@ bool g_query_attr[64];
 bool aligned(const void *p, uintptr_t a) { return p && (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 }  // namespace
-}  // namespace mla
 
-extern "C" mla_status mla_query(int32_t tokens, const void *q_nope, int64_t nope_token_stride,
-                                int64_t nope_head_stride, const void *q_pe, int64_t pe_token_stride,
-                                int64_t pe_head_stride, const void *w_uk, const float *rope_table,
-                                const int32_t *positions, void *q_latent, void *q_rope, int32_t *device_status,
-                                mla_stream_t stream) {
-    mla::NvtxRange nvtx_range("mla_query");
-    using namespace mla;
+// mla_query; of a mixed step (plan.sparse), more than kQuerySmall tokens and kMaxPlanTiles tiles at most, for its rows only.
+mla_status launch_query(int32_t tokens, const void *q_nope, int64_t nope_token_stride, int64_t nope_head_stride,
+                        const void *q_pe, int64_t pe_token_stride, int64_t pe_head_stride, const void *w_uk,
+                        const float *rope_table, const int32_t *positions, void *q_latent, void *q_rope,
+                        int32_t *device_status, const TreePlanRef &plan, mla_stream_t stream) {
     if (tokens < 1) return MLA_ERR_INVALID_ARG;
     if ((int64_t)tokens * kHeads >= (int64_t)1 << 31) return MLA_ERR_UNSUPPORTED;
     if (!aligned(q_nope, 16) || !aligned(q_pe, 16) || !aligned(w_uk, 16) || !aligned(q_latent, 16) ||
@@ -311,6 +340,7 @@ extern "C" mla_status mla_query(int32_t tokens, const void *q_nope, int64_t nope
         return MLA_ERR_INVALID_ARG;
     for (const int64_t s : {nope_token_stride, nope_head_stride, pe_token_stride, pe_head_stride})
         if (s < 1 || s % 8 || s >= (int64_t)1 << 31) return MLA_ERR_INVALID_ARG;
+    if (plan.sparse && (tokens <= kQuerySmall || (tokens - 1) / kTile >= kMaxPlanTiles)) return MLA_ERR_UNSUPPORTED;
     if (tokens <= kQuerySmall)
         return launch_query_small(tokens, q_nope, nope_token_stride, nope_head_stride, q_pe, pe_token_stride,
                                   pe_head_stride, w_uk, rope_table, positions, q_latent, q_rope, device_status, stream);
@@ -343,6 +373,7 @@ extern "C" mla_status mla_query(int32_t tokens, const void *q_nope, int64_t nope
     p.status = device_status;
     p.tokens = tokens;
     p.tiles = (tokens + kTile - 1) / kTile;
+    p.plan = plan;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * units < kHeads * kHalves ? 2 * units : kHeads * kHalves));   // one CTA per SM
     cfg.blockDim = dim3(kQueryThreads);
@@ -354,4 +385,16 @@ extern "C" mla_status mla_query(int32_t tokens, const void *q_nope, int64_t nope
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, mla_query_kernel, p) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+}  // namespace mla
+
+extern "C" mla_status mla_query(int32_t tokens, const void *q_nope, int64_t nope_token_stride,
+                                int64_t nope_head_stride, const void *q_pe, int64_t pe_token_stride,
+                                int64_t pe_head_stride, const void *w_uk, const float *rope_table,
+                                const int32_t *positions, void *q_latent, void *q_rope, int32_t *device_status,
+                                mla_stream_t stream) {
+    mla::NvtxRange nvtx_range("mla_query");
+    return mla::launch_query(tokens, q_nope, nope_token_stride, nope_head_stride, q_pe, pe_token_stride, pe_head_stride,
+                             w_uk, rope_table, positions, q_latent, q_rope, device_status, {}, stream);
 }

@@ -39,7 +39,9 @@
 // One CTA; every choice is a function of the inputs alone, and the host twin
 // below makes the same ones.
 // Without masks the rows are those of chunks of prompts (mla_chunk_absorbed.cu): any
-// number of tokens a request, each seeing the slots up to its own.
+// number of tokens a request, each seeing the slots up to its own; of a mixed step (forms) only the
+// requests in that form, the rows of the others left as those behind the last.  For such chunks the planner also lays
+// down the positions and the rotary table of zeros by which mla_query packs their queries (-1: a row without keys).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -47,6 +49,7 @@
 #include <vector>
 
 #include "mla_internal.h"
+#include "mla_prolog.h"
 #include "sm103_ptx.cuh"
 
 namespace mla {
@@ -143,8 +146,8 @@ __device__ int64_t block_scan(int64_t v, int64_t *warp_sums) {
 
 __global__ void __launch_bounds__(kTreeThreads, 1)
 mla_tree_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__restrict__ offsets,
-                     const uint64_t *__restrict__ masks, uint8_t *__restrict__ ws, int32_t batch, int32_t tokens,
-                     int32_t max_pages, int32_t num_units) {
+                     const uint64_t *__restrict__ masks, const uint8_t *__restrict__ forms, int32_t *__restrict__ zeros,
+                     uint8_t *__restrict__ ws, int32_t batch, int32_t tokens, int32_t max_pages, int32_t num_units) {
     __shared__ int64_t warp_sums[kTreeThreads / 32], warp_most[kTreeThreads / 32];
     __shared__ int64_t carry, carry_parts;
     __shared__ __align__(16) uint32_t unit_key[kMaxUnits];
@@ -182,6 +185,24 @@ mla_tree_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__rest
     // the main kernel may start its prologue now; it waits for this grid before it reads the schedule
     ptx::pdl_launch_dependents();
 
+    if (forms) {   // (none: no request, and so with bad offsets)
+        bool any = false;
+        for (int32_t b = tid; b < batch; b += kTreeThreads) any |= forms[b] != 0;
+        if (!__syncthreads_or(any)) {
+            for (int32_t v = tid; v <= U; v += kTreeThreads) unit_begin[v] = 0;
+            if (tid == 0) {
+                PlanHeader h = {};
+                h.magic = kTreeMagic;
+                h.batch = batch;
+                h.s_q = tokens;
+                h.max_pages = max_pages;
+                h.num_units = U;
+                *hdr = h;
+            }
+            return;
+        }
+    }
+
     // ---- every request's rows; with bad offsets no row belongs to any (all NaN)
     bool wrong = false;
     for (int32_t b = tid; b < batch; b += kTreeThreads) {
@@ -192,7 +213,7 @@ mla_tree_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__rest
     wrong = __syncthreads_or(wrong) != 0;
     if (!wrong && !masks) {   // a warp a request
         for (int32_t b = warp; b < batch; b += kTreeThreads / 32) {
-            const int32_t o0 = offsets[b], n = offsets[b + 1] - o0, len = seq_lens[b];
+            const int32_t o0 = offsets[b], n = forms && !forms[b] ? 0 : offsets[b + 1] - o0, len = seq_lens[b];
             int32_t most = 0;
             for (int32_t i = lane; i < n; i += 32) {
                 TreeRow row;
@@ -255,6 +276,9 @@ mla_tree_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__rest
         }
     }
     __syncthreads();
+
+    if (zeros)
+        for (int32_t r = tid; r < R + MLA_ROPE_TABLE_FLOATS; r += kTreeThreads) zeros[r] = r < R && s_end[r] <= 0 ? -1 : 0;
 
     // ---- total cost and largest row
     {
@@ -655,9 +679,10 @@ mla_status tree_plan_host(const mla_ragged *prob, const int32_t *seq_lens, const
 
 bool tree_plan_fits(int32_t rows, int32_t units) { return tree_plan_smem(rows, units) <= kMaxTreeSmem; }
 
-cudaError_t launch_tree_plan(const int32_t *seq_lens, const int32_t *offsets, const uint64_t *masks, void *ws,
-                             int32_t batch, int32_t tokens, int32_t max_pages, int32_t num_units,
-                             cudaStream_t stream) {
+// forms, zeros: of chunks (masks null); zeros has room for a position per token and a rotary table.
+cudaError_t launch_tree_plan(const int32_t *seq_lens, const int32_t *offsets, const uint64_t *masks, const uint8_t *forms,
+                             int32_t *zeros, void *ws, int32_t batch, int32_t tokens, int32_t max_pages,
+                             int32_t num_units, cudaStream_t stream) {
     if (!tree_plan_fits(tokens, num_units)) return cudaErrorInvalidValue;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -685,8 +710,8 @@ cudaError_t launch_tree_plan(const int32_t *seq_lens, const int32_t *offsets, co
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mla_tree_plan_kernel, seq_lens, offsets, masks, static_cast<uint8_t *>(ws), batch,
-                              tokens, max_pages, num_units);
+    return cudaLaunchKernelEx(&cfg, mla_tree_plan_kernel, seq_lens, offsets, masks, forms, zeros,
+                              static_cast<uint8_t *>(ws), batch, tokens, max_pages, num_units);
 }
 
 }  // namespace mla

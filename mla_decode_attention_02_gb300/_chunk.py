@@ -41,6 +41,14 @@ _SIGS.update({
 })
 
 
+def _int(v, name, bits=31) -> int:
+    """An integer that the C ABI's field holds (ctypes would cut it to the field's bits)."""
+    v = int(v)
+    if not -1 << bits <= v < 1 << bits:
+        raise ValueError(f"{name} must be below 2^{bits}, got {v}")
+    return v
+
+
 # ----------------------------------------------------------------------------- rotary positions
 
 ROTARY_DIMS = (16, 32, 64, 128, 256)
@@ -57,13 +65,14 @@ def rope_table_scaled(rope_base: float = DEFAULT_ROPE_BASE, *, dims: int = D_ROP
     ``rope_table``'s (for any dims).  For dims = 64 ``prolog``, ``query`` and ``cache_append`` take it as table=.
     """
     import torch
-    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
     if dims not in ROTARY_DIMS:
         raise ValueError(f"dims must be one of {ROTARY_DIMS}, got {dims}")
+    original_positions = _int(original_positions, "original_positions")
+    dev = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
     index = torch.cuda.current_device() if dev.index is None else dev.index
     with _launch_on(index, stream):
         table = torch.empty(dims, dtype=torch.float32, device=torch.device("cuda", index))
-        _check(load_library().mla_rope_table_scaled(float(rope_base), int(dims), float(factor), int(original_positions),
+        _check(load_library().mla_rope_table_scaled(float(rope_base), int(dims), float(factor), original_positions,
                                                     float(beta_fast), float(beta_slow), table.data_ptr(),
                                                     _current_stream(index)), "mla_rope_table_scaled")
     return table
@@ -207,18 +216,20 @@ def chunk_plan(seq_lens, token_offsets, *, tokens: int, max_pages_per_seq: int, 
     ordered, and it may be dropped once the last is enqueued.
     """
     import torch
+    tokens, max_pages_per_seq = _int(tokens, "tokens"), _int(max_pages_per_seq, "max_pages_per_seq")
+    kv_tokens = None if kv_tokens is None else _int(kv_tokens, "kv_tokens", 62)
     index = _index_of(seq_lens, "seq_lens", 1, torch.int32)
     n = seq_lens.shape[0]
     if kv_tokens is None:
-        kv_tokens = n * int(max_pages_per_seq) * PAGE_SIZE
-    kv_tokens = -(-int(kv_tokens) // PAGE_SIZE) * PAGE_SIZE
+        kv_tokens = n * max_pages_per_seq * PAGE_SIZE
+    kv_tokens = -(-kv_tokens // PAGE_SIZE) * PAGE_SIZE
     if stream is None:
         r = (B._host or B._native()).chunk_plan(seq_lens, token_offsets, tokens, max_pages_per_seq, kv_tokens, workspace)
         if r is not None:
             return ChunkPlan(n, tokens, max_pages_per_seq, kv_tokens, B._made(r, "mla_chunk_plan"))
     sl = _dense(seq_lens, "seq_lens", torch.int32, (n,), index, 4)
     off = _dense(token_offsets, "token_offsets", torch.int32, (n + 1,), index, 4)
-    p = ChunkPlan(n, int(tokens), int(max_pages_per_seq), kv_tokens, workspace)
+    p = ChunkPlan(n, tokens, max_pages_per_seq, kv_tokens, workspace)
     prob, lib = p.problem(), load_library()
     with _launch_on(index, stream, seq_lens, token_offsets, workspace):
         if workspace is None:
@@ -233,9 +244,9 @@ def chunk_plan(seq_lens, token_offsets, *, tokens: int, max_pages_per_seq: int, 
 
 def chunk_scratch_size(p: ChunkPlan, heads: int = NUM_HEADS, *, fp8: bool = False) -> int:
     """Bytes of the scratch that holds the keys and values of `heads` heads at once (``mla_chunk_scratch_size``)."""
-    size, prob = ctypes.c_size_t(0), p.problem()
+    size, prob, heads = ctypes.c_size_t(0), p.problem(), _int(heads, "heads")
     with _launch_on(p.workspace.get_device(), None):
-        _check(load_library().mla_chunk_scratch_size(ctypes.byref(prob), int(heads), int(bool(fp8)), ctypes.byref(size)),
+        _check(load_library().mla_chunk_scratch_size(ctypes.byref(prob), heads, int(bool(fp8)), ctypes.byref(size)),
                "mla_chunk_scratch_size")
     return size.value
 

@@ -122,9 +122,9 @@ typedef struct mla_chunk {
  * Two forms compute a request: every head's keys and values worked out once from its cached rows (the whole form), or,
  * for few tokens over a long context, the absorbed form of mla_decode with its roundings (absorbed queries and latent
  * outputs in bf16).  By both forms' measured times the absorbed one is taken where it saves a quarter at least (up to some
- * 100 tokens).  Where one form is sound for the whole step from the problem alone (one request, up to 80 tokens,
- * few keys) the step has that form; any other step is mixed, and mla_chunk_plan takes a form for each request.
- * Requests without tokens change nothing.
+ * 100 tokens).  A step of one request, of up to 80 tokens or of few keys (below some 9000, unless the absorbed form suits
+ * them spread evenly) has one form, chosen from the problem alone; any other step is mixed, and mla_chunk_plan takes a form
+ * for each request, whatever the others hold.
  *
  * Workspace bytes of mla_chunk_plan / mla_chunk_attend on the current device.
  */

@@ -20,11 +20,11 @@
 // thousands of others far below it.  So the weights stand 2^7 above the reference (at most 2^15), and where 64 keys in a row
 // have none within 2^-20 of the reference it falls to their largest (once in eight key tiles at most, so that scores that
 // go up and down cost little, and 2^40 below its highest at most, which fp32's range bears).  32768 keys of which one draws
-// 0.9986 of the weight, with a value of zero: without both 0.33 of the output's norm, with the lift alone 2e-3, now
-// 3e-4; a lift of 2^11 (then raised at 2^4) does as well but takes 11 to 35% longer where scores are twice as wide or more.
+// 0.9986 of the weight, with a value of zero: this rounding is without both 0.33 of the output's norm, with the lift alone 2e-3,
+// with both 3e-4; a lift of 2^11 (then raised at 2^4) does as well but takes 11 to 35% longer where scores are twice as wide or more.
 // Bound by the tensor cores, 81,920 flops a (token, key) pair and 128 heads, and by the power they draw: 2048 tokens over
-// 32768 keys 3.02 ms (1.77 PFLOP/s; without the softmax's arithmetic 2.72, with keys from L2 alone 2.91), a prompt of 4096
-// 457 us (1.5, the diagonal's masked halves and 13 items' beginnings and ends a CTA; tensor pipe 71% of the clocks).
+// 32768 keys 3.04 ms (1.76 PFLOP/s; without the softmax's arithmetic 2.72, with keys from L2 alone 2.91), a prompt of 4096
+// 460 us (1.5, the diagonal's masked halves and 13 items' beginnings and ends a CTA; tensor pipe 71% of the clocks).
 // Measured on the way: items by index instead of in turn 705 -> 552 us (prompt), maxima in eight chains 523, weights before
 // the maximum is known 505, requests together and the last heads tile by tile 480, halves 457; value products as two of
 // 64 columns 3200 instead of 3030 us (long), with run-time loops around the MMAs 4170 (their issue then takes longer than

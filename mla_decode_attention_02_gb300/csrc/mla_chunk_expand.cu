@@ -25,7 +25,7 @@
 // pair's tile.  Rows past a request's end become zeros, so that a zero weight times them is zero; the
 // key of a row that is not finite, or has a value beyond fp16, becomes NaN and its values zeros, so that it spoils
 // what sees it and nothing else.
-// Bound by its stores, 64 KB a row: 32768 rows (2.1 GB) in 645 us, 3.3 TB/s where a fill of as much memory takes
+// Bound by its stores, 64 KB a row: 32768 rows (2.1 GB) in 651 us, 3.3 TB/s where a fill of as much memory takes
 // 4.06, and 1.7 PFLOP/s; without the stores 510.  Staging in shared memory and a ring of four took 795; arrivals between
 // the CTAs with release semantics, which wait for the stores, 1475.  No gain: TMA stores (836), clusters of two pairs that
 // share the weights by multicast (835: 36 of them fit, 144 SMs), the rows in tensor memory with a ring of fourteen (658, and

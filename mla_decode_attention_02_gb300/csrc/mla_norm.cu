@@ -4,13 +4,13 @@
 //   z = x + residual,  y = z / sqrt(mean z^2 + eps) * weight
 //   fp8: s = max |y| / 448 over the group,  code = e4m3(y / s)
 //
-// One CTA per row (8191 rows of 7168 to e4m3: 62.6 us, 6.6 TB/s; with CTAs that stay and take row after
+// One CTA per row (8191 rows of 7168 to e4m3: 62.3 us, 6.6 TB/s; with CTAs that stay and take row after
 // row 65 to 70, as their number fits the SMs or not).  A thread holds up to kMaxPer runs of eight values
 // (16-byte loads, contiguous over a warp) from the load to the last store, so a row
 // is read once; one block-wide sum, and for a scale per row one block-wide maximum.
 // A group of 128 values is 16 neighbouring lanes' runs.  y / s = 448 (z w) / max |z w|: the
 // norm's factor cancels, and one division a group is left.  Bound by memory: six bytes a value in and kept, one or
-// two out (2049 rows to bf16: 19.0 us, 6.2 TB/s).
+// two out (2049 rows to bf16: 19.4 us, 6.1 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>

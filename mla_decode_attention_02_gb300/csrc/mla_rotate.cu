@@ -8,8 +8,8 @@
 // layout, two 16-byte runs of the half layout), works their angles out once and
 // turns them in up to four heads, all eight loads in flight; a warp's share of a token is
 // 128 / (dims / 16) heads (32 of 64 dims).
-// Bound by memory: four bytes a value (4097 tokens of 128 x 64 values out of rows of 192: 22.7 us in a graph,
-// 5.9 TB/s; 1 token 2.4 us, the launch and two dependent loads).
+// Bound by memory: four bytes a value (4097 tokens of 128 x 64 values out of rows of 192: 23.7 us in a graph,
+// 5.7 TB/s; 1 token 2.4 us, the launch and two dependent loads).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -17,7 +17,7 @@ mla_status plan_host(const mla_problem *prob, const int32_t *seq_lens, int32_t n
 cudaError_t launch_plan(const int32_t *seq_lens, void *ws, int32_t batch, int32_t s_q,
                         int32_t max_pages, int32_t num_units, cudaStream_t stream);
 cudaError_t launch_combine(const void *ws, void *o_latent, float *lse, int32_t batch, int32_t s_q,
-                           int32_t max_pages, int32_t num_units, bool tree, cudaStream_t stream);
+                           int32_t max_pages, int32_t num_units, bool tree, bool sparse, cudaStream_t stream);
 cudaError_t main_units(int32_t *units);
 bool plan_fits(int32_t rows, int32_t units);
 cudaError_t launch_main(const void *q_latent, const void *q_rope, const void *kv,
@@ -184,7 +184,7 @@ static mla_status decode_impl(const mla_problem *prob, const void *q_latent, con
                                      prob->max_pages_per_seq, units, wait_limit_ns, test_flags,
                                      (uint32_t)prob->flags, fp8, false, nullptr, s);
     if (e != cudaSuccess || !mark(1)) return MLA_ERR_CUDA;
-    e = mla::launch_combine(workspace, o_latent, lse, prob->batch, prob->s_q, prob->max_pages_per_seq, units, false, s);
+    e = mla::launch_combine(workspace, o_latent, lse, prob->batch, prob->s_q, prob->max_pages_per_seq, units, false, false, s);
     if (e != cudaSuccess || !mark(2)) return MLA_ERR_CUDA;
     return MLA_OK;
 }
@@ -322,7 +322,7 @@ static mla_status tree_impl(const mla_ragged *prob, const void *q_latent, const 
                          prob->batch, prob->tokens, prob->max_pages_per_seq, units, mla::kDefaultWaitLimitNs, 0,
                          (uint32_t)prob->flags, fp8, true, scratch, s);
     if (e != cudaSuccess) return MLA_ERR_CUDA;
-    e = mla::launch_combine(workspace, o_latent, lse, prob->batch, prob->tokens, prob->max_pages_per_seq, units, true, s);
+    e = mla::launch_combine(workspace, o_latent, lse, prob->batch, prob->tokens, prob->max_pages_per_seq, units, true, false, s);
     return e == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 

@@ -35,7 +35,7 @@ cudaError_t launch_expand(const void *ws, const void *kv_cache_fp8, int64_t num_
                           void *expanded, int32_t batch, int32_t tokens, int32_t max_pages, int32_t num_units,
                           cudaStream_t stream);
 cudaError_t launch_combine(const void *ws, void *o_latent, float *lse, int32_t batch, int32_t s_q, int32_t max_pages,
-                           int32_t num_units, bool tree, cudaStream_t stream);
+                           int32_t num_units, bool tree, bool sparse, cudaStream_t stream);
 mla_status launch_epilog_uv(int64_t tokens, const void *o_latent, const void *w_uv, void *o_v, const TreePlanRef &plan,
                             int32_t *device_status, mla_stream_t stream);
 namespace {
@@ -142,7 +142,7 @@ mla_status absorbed_attend(const mla_chunk *p, const void *q_nope, int64_t nope_
     // (over an fp8 cache power-of-two maxima round a weight once: see tree_decode_fp8's binding)
     if (launch_main(ql, qr, cache, num_pages, block_table, scale, ws, ol, l, p->batch, p->tokens, p->max_pages_per_seq, units,
                     kWaitNs, 0, (fp8 ? MLA_FLAG_POW2_MAX : 0) | (mixed ? kMainSparse : 0), fp8, true, expanded, s) != cudaSuccess ||
-        launch_combine(ws, ol, l, p->batch, p->tokens, p->max_pages_per_seq, units, true, s) != cudaSuccess)
+        launch_combine(ws, ol, l, p->batch, p->tokens, p->max_pages_per_seq, units, true, mixed, s) != cudaSuccess)
         return MLA_ERR_CUDA;
     return launch_epilog_uv(p->tokens, ol, w_uv, out, plan, status, stream);
 }

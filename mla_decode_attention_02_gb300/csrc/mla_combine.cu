@@ -33,6 +33,7 @@ constexpr int kWarpParts = 8;      // rows with more parts are merged by a whole
 // made mixed and MTP slower.
 constexpr int kBatch = 2;
 static_assert(kWarpParts <= 32, "one part's lse per lane");
+constexpr int kSparseRows = 12288;   // rows of a sparse schedule at most (its planner takes some 10,000)
 
 // o = acc / W -> bf16 (lane owns four float4 columns of the 512), lse = M + ln W.
 __device__ __forceinline__ void store_row(__nv_bfloat16 *orow, float *lse, const float4 (&acc)[4], float W,
@@ -136,8 +137,9 @@ __device__ __forceinline__ void merge_task_cta(int32_t r, int32_t h, int32_t n, 
 }
 
 // kTree: s_q is the number of tokens (rows); rows that see no key are written
-// here, rows behind the last request are not written at all.
-template <bool kTree>
+// here, rows behind the last request are not written at all.  kSparse: of a mixed step over chunks, most rows not this
+// schedule's.
+template <bool kTree, bool kSparse>
 __global__ void __launch_bounds__(32 * kCombineWarps, 3)
 mla_combine_kernel(const uint8_t *__restrict__ ws, __nv_bfloat16 *__restrict__ o_latent,
                    float *__restrict__ lse_out, int32_t batch, int32_t s_q, int32_t max_pages, int32_t num_units) {
@@ -163,26 +165,21 @@ mla_combine_kernel(const uint8_t *__restrict__ ws, __nv_bfloat16 *__restrict__ o
     const float *lse_part = reinterpret_cast<const float *>(ws + L.lse_part);
     const float *o_part = reinterpret_cast<const float *>(ws + L.o_part);
 
-    // Rows of a few parts: one warp per (row, head) task, warps strided over
-    // the tasks; the parts are summed in index order.
-    for (int64_t task = (int64_t)blockIdx.x * kCombineWarps + warp; task < tasks;
-         task += (int64_t)gridDim.x * kCombineWarps) {
-        const int32_t r = (int32_t)(task / kHeads);
-        const int32_t h = (int32_t)(task % kHeads);
-        const int32_t n = row_nparts[r];
-        if (n == 1 || n > kWarpParts) continue;  // written by the main kernel / merged below
-        if (kTree && n == kRowUnused) continue;
+    // Rows of a few parts: one warp per (row, head) task; the parts are summed in index order.
+    auto merge = [&](int32_t r, int32_t h, int32_t n) {
+        if (n == 1 || n > kWarpParts) return;  // written by the main kernel / merged below
+        if (kTree && n == kRowUnused) return;
         __nv_bfloat16 *orow = o_latent + ((size_t)r * kHeads + h) * kDl;
         if (kTree && n == kRowEmpty) {
             for (int d = lane; d < kDl; d += 32) orow[d] = __float2bfloat16(0.f);
             if (lane == 0) lse_out[(size_t)r * kHeads + h] = -INFINITY;
-            continue;
+            return;
         }
         if (n == 0) {          // invalid row (bad seq_len): NaN, flagged in the status word
             const __nv_bfloat16 nan = __float2bfloat16(__int_as_float(0x7fc00000));
             for (int d = lane; d < kDl; d += 32) orow[d] = nan;
             if (lane == 0) lse_out[(size_t)r * kHeads + h] = __int_as_float(0x7fc00000);
-            continue;
+            return;
         }
         const int32_t part0 = row_part0[r];
         // lane i < n holds part i's lse and weight
@@ -225,6 +222,58 @@ mla_combine_kernel(const uint8_t *__restrict__ ws, __nv_bfloat16 *__restrict__ o
             }
         }
         store_row(orow, lse_out + (size_t)r * kHeads + h, acc, W, M, lane);
+    };
+    auto merge_cta = [&](int32_t r, int32_t h, int32_t n) {   // (the same for every thread)
+        merge_task_cta(r, h, n, row_part0, lse_part, o_part, o_latent, lse_out, lane, warp, red, red_w, red_m);
+    };
+    const int32_t warp0 = (int32_t)blockIdx.x * kCombineWarps + warp, warps = (int32_t)gridDim.x * kCombineWarps;
+    if constexpr (kSparse) {
+        // Few of the rows, or none, are this schedule's: each CTA lists those to merge, in their order, and the tasks are
+        // theirs (31 rows among 9431: 33 us; all rows gone over instead, 111).
+        __shared__ uint16_t list[kSparseRows];
+        __shared__ int32_t found[kCombineWarps];
+        __shared__ int32_t any_big;
+        if (threadIdx.x == 0) any_big = 0;
+        // a warp's share of the rows, counted and then written behind the shares before it
+        const int32_t share = (L.num_rows + 32 * kCombineWarps - 1) / (32 * kCombineWarps) * 32;
+        const int32_t end = min((warp + 1) * share, L.num_rows);
+        auto each = [&](auto use) {
+            for (int32_t r0 = warp * share; r0 < end; r0 += 32) {
+                const int32_t n = r0 + lane < end ? row_nparts[r0 + lane] : 1;
+                use(r0, n, __ballot_sync(0xffffffffu, n != 1 && n != kRowUnused));
+            }
+        };
+        int32_t count = 0;
+        each([&](int32_t, int32_t, unsigned here) { count += __popc(here); });
+        if (lane == 0) found[warp] = count;
+        __syncthreads();
+        int32_t at = 0, listed = 0;
+        for (int32_t w = 0; w < kCombineWarps; ++w) {
+            at += w < warp ? found[w] : 0;
+            listed += found[w];
+        }
+        each([&](int32_t r0, int32_t n, unsigned here) {
+            if (here >> lane & 1) list[at + __popc(here & ((1u << lane) - 1))] = (uint16_t)(r0 + lane);
+            at += __popc(here);
+            if (n > kWarpParts) any_big = 1;
+        });
+        __syncthreads();
+        const int64_t todo = (int64_t)listed * kHeads;
+        for (int64_t task = warp0; task < todo; task += warps) {
+            const int32_t r = list[task / kHeads];
+            merge(r, (int32_t)(task % kHeads), row_nparts[r]);
+        }
+        if (any_big)
+            for (int64_t task = blockIdx.x; task < todo; task += gridDim.x) {
+                const int32_t r = list[task / kHeads], n = row_nparts[r];
+                if (n > kWarpParts) merge_cta(r, (int32_t)(task % kHeads), n);
+            }
+        return;
+    }
+    // Rows of a few parts: warps strided over the tasks.
+    for (int64_t task = warp0; task < tasks; task += warps) {
+        const int32_t r = (int32_t)(task / kHeads);
+        merge(r, (int32_t)(task % kHeads), row_nparts[r]);
     }
 
     // Rows of many parts (one long request over many SM pairs): one (row,
@@ -235,16 +284,15 @@ mla_combine_kernel(const uint8_t *__restrict__ ws, __nv_bfloat16 *__restrict__ o
     if (!__syncthreads_or(big)) return;
     for (int64_t task = blockIdx.x; task < tasks; task += gridDim.x) {
         const int32_t n = row_nparts[task / kHeads];
-        if (n <= kWarpParts) continue;   // CTA-uniform: every thread skips together
-        merge_task_cta((int32_t)(task / kHeads), (int32_t)(task % kHeads), n, row_part0, lse_part, o_part,
-                       o_latent, lse_out, lane, warp, red, red_w, red_m);
+        if (n > kWarpParts) merge_cta((int32_t)(task / kHeads), (int32_t)(task % kHeads), n);
     }
 }
 
 }  // namespace
 
 cudaError_t launch_combine(const void *ws, void *o_latent, float *lse, int32_t batch, int32_t s_q,
-                           int32_t max_pages, int32_t num_units, bool tree, cudaStream_t stream) {
+                           int32_t max_pages, int32_t num_units, bool tree, bool sparse, cudaStream_t stream) {
+    if (sparse && s_q > kSparseRows) return cudaErrorInvalidValue;
     const int64_t tasks = (int64_t)(tree ? 1 : batch) * s_q * kHeads;
     const int grid = (int)(tasks < kCombineGrid ? tasks : kCombineGrid);
     cudaLaunchConfig_t cfg = {};
@@ -256,7 +304,8 @@ cudaError_t launch_combine(const void *ws, void *o_latent, float *lse, int32_t b
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree ? mla_combine_kernel<true> : mla_combine_kernel<false>,
+    auto *kernel = sparse ? mla_combine_kernel<true, true> : tree ? mla_combine_kernel<true, false> : mla_combine_kernel<false, false>;
+    return cudaLaunchKernelEx(&cfg, kernel,
                               static_cast<const uint8_t *>(ws), static_cast<__nv_bfloat16 *>(o_latent), lse, batch,
                               s_q, max_pages, num_units);
 }

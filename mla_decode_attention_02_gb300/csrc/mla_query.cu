@@ -103,8 +103,10 @@ __device__ __noinline__ void query_landed(uint32_t bar, uint32_t parity, int32_t
     }
 }
 
+// kSparse: of a mixed step over chunks (P.plan).
+template <bool kSparse>
 __global__ void __launch_bounds__(kQueryThreads, 1) mla_query_kernel(const __grid_constant__ QueryParams P) {
-    if (P.plan.sparse) {
+    if constexpr (kSparse) {
         pdl_launch_dependents();
         pdl_wait_prior();
         if (tree_plan_idle(P.plan)) return;
@@ -113,7 +115,7 @@ __global__ void __launch_bounds__(kQueryThreads, 1) mla_query_kernel(const __gri
     __shared__ __align__(8) uint64_t bars[11];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag, live_tiles;
-    __shared__ uint8_t live[kMaxPlanTiles];
+    __shared__ uint8_t live[kSparse ? kMaxPlanTiles : 1];
     const uint32_t s_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(kQueryThreads, 1) mla_query_kernel(const __gri
     pdl_launch_dependents();
 
     int tiles = P.tiles;
-    if (P.plan.sparse) {
+    if constexpr (kSparse) {
         const bool any = tree_plan_there(P.plan);
         for (int t = warp; t < P.tiles; t += kQueryThreads / 32) {
             bool has = false;
@@ -171,7 +173,7 @@ __global__ void __launch_bounds__(kQueryThreads, 1) mla_query_kernel(const __gri
     const int n = (int)(rest * (blockIdx.x + 1) / gridDim.x - r0);
     auto head_half = [&](int i) { return i < tiles ? (int)blockIdx.x : (int)(gridDim.x + (r0 + i) / tiles); };
     auto place_of = [&](int i) { return i < tiles ? i : (int)((r0 + i) % tiles); };
-    auto tile_of = [&](int i) { return P.plan.sparse ? (int)live[place_of(i)] : place_of(i); };
+    auto tile_of = [&](int i) { return kSparse ? (int)live[place_of(i)] : place_of(i); };
 
     if (warp == 0) {
         if (elect_one()) {
@@ -294,11 +296,15 @@ __global__ void __launch_bounds__(kQueryThreads, 1) mla_query_kernel(const __gri
             gh[j] = P.rope_table[pair0 + j];
             gl[j] = P.rope_table[kPairs + pair0 + j];
         }
-        const int64_t units = tiles > 0 ? (int64_t)P.tokens * 4 : 0, warps = (int64_t)gridDim.x * kRopeWarps;
+        const int64_t units = kSparse ? (int64_t)tiles * kTile * 4 : (int64_t)P.tokens * 4, warps = (int64_t)gridDim.x * kRopeWarps;
         const int64_t w = (int64_t)blockIdx.x * kRopeWarps + warp - 1 - kEpiWarps;
         for (int64_t u = units * w / warps, end = units * (w + 1) / warps; u < end; ++u) {
-            const int tok = (int)(u >> 2), h0 = (int)(u & 3) * 32 + (lane >> 3);
-            if (P.plan.sparse && P.positions[tok] < 0) continue;
+            int tok = (int)(u >> 2);
+            const int h0 = (int)(u & 3) * 32 + (lane >> 3);
+            if constexpr (kSparse) {
+                tok = live[tok / kTile] * kTile + tok % kTile;
+                if (tok >= P.tokens || P.positions[tok] < 0) continue;
+            }
             const __nv_bfloat16 *src = P.q_pe + tok * P.pe_token + h0 * P.pe_head + pair0 * 2;
             uint4 v[8];
 #pragma unroll
@@ -351,9 +357,9 @@ mla_status launch_query(int32_t tokens, const void *q_nope, int64_t nope_token_s
     {
         std::lock_guard<std::mutex> lock(g_query_mutex);
         if (!g_query_attr[dev]) {
-            if (cudaFuncSetAttribute(mla_query_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kQuerySmem) !=
-                cudaSuccess)
-                return MLA_ERR_CUDA;
+            for (auto *k : {mla_query_kernel<false>, mla_query_kernel<true>})
+                if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kQuerySmem) != cudaSuccess)
+                    return MLA_ERR_CUDA;
             g_query_attr[dev] = true;
         }
     }
@@ -384,7 +390,8 @@ mla_status launch_query(int32_t tokens, const void *q_nope, int64_t nope_token_s
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mla_query_kernel, p) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+    auto *kernel = plan.sparse ? mla_query_kernel<true> : mla_query_kernel<false>;
+    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
 }  // namespace mla

@@ -144,6 +144,8 @@ __device__ int64_t block_scan(int64_t v, int64_t *warp_sums) {
     return v + before;
 }
 
+// kChunk: of chunks (no masks).
+template <bool kChunk>
 __global__ void __launch_bounds__(kTreeThreads, 1)
 mla_tree_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__restrict__ offsets,
                      const uint64_t *__restrict__ masks, const uint8_t *__restrict__ forms, int32_t *__restrict__ zeros,
@@ -185,7 +187,7 @@ mla_tree_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__rest
     // the main kernel may start its prologue now; it waits for this grid before it reads the schedule
     ptx::pdl_launch_dependents();
 
-    if (forms) {   // (none: no request, and so with bad offsets)
+    if (kChunk && forms) {   // (none: no request, and so with bad offsets)
         bool any = false;
         for (int32_t b = tid; b < batch; b += kTreeThreads) any |= forms[b] != 0;
         if (!__syncthreads_or(any)) {
@@ -208,10 +210,10 @@ mla_tree_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__rest
     for (int32_t b = tid; b < batch; b += kTreeThreads) {
         const int32_t o0 = offsets[b], o1 = offsets[b + 1];
         // (a chunk's tokens are not counted)
-        wrong |= masks ? !tree_offsets_ok(o0, o1, b, R) : o0 < 0 || o0 > o1 || o1 > R || (b == 0 && o0 != 0);
+        wrong |= !kChunk ? !tree_offsets_ok(o0, o1, b, R) : o0 < 0 || o0 > o1 || o1 > R || (b == 0 && o0 != 0);
     }
     wrong = __syncthreads_or(wrong) != 0;
-    if (!wrong && !masks) {   // a warp a request
+    if (kChunk && !wrong) {   // a warp a request
         for (int32_t b = warp; b < batch; b += kTreeThreads / 32) {
             const int32_t o0 = offsets[b], n = forms && !forms[b] ? 0 : offsets[b + 1] - o0, len = seq_lens[b];
             int32_t most = 0;
@@ -277,7 +279,7 @@ mla_tree_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__rest
     }
     __syncthreads();
 
-    if (zeros)
+    if constexpr (kChunk)
         for (int32_t r = tid; r < R + MLA_ROPE_TABLE_FLOATS; r += kTreeThreads) zeros[r] = r < R && s_end[r] <= 0 ? -1 : 0;
 
     // ---- total cost and largest row
@@ -694,9 +696,10 @@ cudaError_t launch_tree_plan(const int32_t *seq_lens, const int32_t *offsets, co
     {
         std::lock_guard<std::mutex> lock(mutex);
         if (!set[dev]) {
-            e = cudaFuncSetAttribute(mla_tree_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)kMaxTreeSmem);
-            if (e != cudaSuccess) return e;
+            for (auto *k : {mla_tree_plan_kernel<false>, mla_tree_plan_kernel<true>})
+                if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxTreeSmem)) !=
+                    cudaSuccess)
+                    return e;
             set[dev] = true;
         }
     }
@@ -710,7 +713,8 @@ cudaError_t launch_tree_plan(const int32_t *seq_lens, const int32_t *offsets, co
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mla_tree_plan_kernel, seq_lens, offsets, masks, forms, zeros,
+    auto *kernel = masks ? mla_tree_plan_kernel<false> : mla_tree_plan_kernel<true>;
+    return cudaLaunchKernelEx(&cfg, kernel, seq_lens, offsets, masks, forms, zeros,
                               static_cast<uint8_t *>(ws), batch, tokens, max_pages, num_units);
 }
 

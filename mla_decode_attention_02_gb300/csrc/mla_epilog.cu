@@ -109,7 +109,8 @@ __global__ void __launch_bounds__(kThreadsE, 2) mla_epilog_uv_kernel(const __gri
         row_parts = reinterpret_cast<const int32_t *>(
             P.plan.ws + make_layout(P.plan.tokens, P.plan.num_units, P.plan.batch).row_nparts);
     if constexpr (kSparse) {
-        pdl_launch_dependents();
+        // (what follows starts only once this kernel's CTAs have their tensor memory, or are gone: it may take its own first
+        // thing, and then wait for this kernel)
         pdl_wait_prior();
         if (tree_plan_idle(P.plan)) return;
         const int32_t status = reinterpret_cast<const PlanHeader *>(P.plan.ws)->status;

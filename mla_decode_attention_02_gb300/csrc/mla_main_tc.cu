@@ -559,8 +559,7 @@ mla_main_tc_kernel(const __grid_constant__ Params P) {
     constexpr int kScaleStep = kExpanded ? 1 : 4;   // floats from one token's scale to the next
     if constexpr (kTree) {
         if (P.flags & kMainSparse) {   // (the same for every CTA)
-            pdl_launch_dependents();
-            pdl_wait_prior();
+            pdl_wait_prior();   // (what follows starts only once this kernel's CTAs have their tensor memory, or are gone)
             if (tree_plan_idle({P.ws, P.batch, P.s_q, P.max_pages, P.num_units, true})) return;
         }
     }

@@ -107,8 +107,7 @@ __device__ __noinline__ void query_landed(uint32_t bar, uint32_t parity, int32_t
 template <bool kSparse>
 __global__ void __launch_bounds__(kQueryThreads, 1) mla_query_kernel(const __grid_constant__ QueryParams P) {
     if constexpr (kSparse) {
-        pdl_launch_dependents();
-        pdl_wait_prior();
+        pdl_wait_prior();   // (what follows starts only once this kernel's CTAs have their tensor memory, or are gone)
         if (tree_plan_idle(P.plan)) return;
     }
     extern __shared__ uint8_t smem_raw[];

@@ -285,3 +285,43 @@ def test_a_captured_step_whose_requests_change_forms():
         elif sum(counts):
             lse = torch.empty(T, 128, device="cuda")
             close(f, attend(f, lse=lse), lse, slice(0, sum(counts)))
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "fp8"])
+def test_layers_behind_one_another(fp8):
+    """Mixed steps with what follows them in a layer at once behind: each kernel may start before the one ahead is done, and
+    takes tensor memory of its own; the results are those of steps with a pause between."""
+    c = CU.case(COUNTS, LENS, seed=90, fp8=fp8)
+    none = CU.case([200, 100, 0, 300], [900, 3000, 70, 7000], seed=91, fp8=fp8)          # (no request in the absorbed form)
+    g = torch.Generator(device="cuda").manual_seed(92)
+    w_o = (torch.randn(1024, 16384, generator=g, device="cuda") / 128).to(torch.bfloat16)
+    table = mla.rope_table()
+
+    def layer(d, p, wait):
+        o = attend(d, p)
+        if wait:
+            torch.cuda.synchronize()
+        out = mla.epilog_oproj(o, w_o)
+        ql, _, _ = mla.query(d["q"][..., :128], d["q"][..., 128:], d["w_uk"], torch.zeros(d["T"], dtype=torch.int32, device="cuda"),
+                             table=table)
+        return o, out, ql
+
+    plans = [(d, plan(d)) for d in (c, none)]
+    assert forms(plans[0][1]) == FORMS and not any(forms(plans[1][1]))
+    refs = []
+    for d, p in plans:
+        refs.append([x.clone() for x in layer(d, p, True)])
+        torch.cuda.synchronize()
+    outs = [layer(d, p, False) for _ in range(4) for d, p in plans]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            outs += [layer(d, p, False) for _ in range(2) for d, p in plans]
+    graph.replay()
+    torch.cuda.synchronize()
+    for i, got in enumerate(outs):
+        for a, b in zip(got, refs[i % 2]):
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16)), i
+    assert all(mla.check(p) == 0 for _, p in plans)

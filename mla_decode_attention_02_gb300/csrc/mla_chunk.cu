@@ -21,7 +21,8 @@
 // have none within 2^-20 of the reference it falls to their largest (once in eight key tiles at most, so that scores that
 // go up and down cost little, and 2^40 below its highest at most, which fp32's range bears).  32768 keys of which one draws
 // 0.9986 of the weight, with a value of zero: this rounding is without both 0.33 of the output's norm, with the lift alone 2e-3,
-// with both 3e-4; a lift of 2^11 (then raised at 2^4) does as well but takes 11 to 35% longer where scores are twice as wide or more.
+// with both 3e-4; a lift of 2^11 (then raised at 2^4) does as well but takes 11 to 35% longer where scores are twice as
+// wide or more.
 // Bound by the tensor cores, 81,920 flops a (token, key) pair and 128 heads, and by the power they draw: 2048 tokens over
 // 32768 keys 3.04 ms (1.76 PFLOP/s; without the softmax's arithmetic 2.72, with keys from L2 alone 2.91), a prompt of 4096
 // 460 us (1.5, the diagonal's masked halves and 13 items' beginnings and ends a CTA; tensor pipe 71% of the clocks).
@@ -483,7 +484,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) mla_chunk_kernel(const __gri
                     float2 all;
                     const int seen = limit - 64 * half;
                     for (;;) {
-                        const float neg = m == -INFINITY ? 0.f : fmaf(-m, P.scale_log2, kLift);   // (no key seen so far: weights of 0)
+                        // (no key seen so far: weights of 0)
+                        const float neg = m == -INFINITY ? 0.f : fmaf(-m, P.scale_log2, kLift);
                         const uint64_t scale2 = pair(P.scale_log2, P.scale_log2), shift2 = pair(neg, neg);
                         uint64_t part[2] = {0, 0};
                         float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};

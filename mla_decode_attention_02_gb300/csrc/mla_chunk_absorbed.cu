@@ -81,7 +81,7 @@ size_t zeros_bytes(const mla_chunk *p) { return align_up(4 * ((size_t)p->tokens 
 //    the table allow;
 //  - up to a tile of tokens: absorbed if it saves a quarter even so;
 //  - few keys: the absorbed form could save no more than twice its fixed part.
-// The launches of a form that no request takes cost some 10 us (18 over an fp8 cache), so steps of less than kMixedLeast are
+// The launches of a form that no request takes cost some 10 us (15 over an fp8 cache), so steps of less than kMixedLeast are
 // mixed only if an even spread would be absorbed.
 constexpr int64_t kMixedLeast = 300000;
 ChunkForm chunk_form(const mla_chunk *p, int32_t units) {
@@ -140,8 +140,9 @@ mla_status absorbed_attend(const mla_chunk *p, const void *q_nope, int64_t nope_
                                   units, s) != cudaSuccess)
         return MLA_ERR_CUDA;
     // (over an fp8 cache power-of-two maxima round a weight once: see tree_decode_fp8's binding)
+    const uint32_t flags = (fp8 ? MLA_FLAG_POW2_MAX : 0) | (mixed ? kMainSparse : 0);
     if (launch_main(ql, qr, cache, num_pages, block_table, scale, ws, ol, l, p->batch, p->tokens, p->max_pages_per_seq, units,
-                    kWaitNs, 0, (fp8 ? MLA_FLAG_POW2_MAX : 0) | (mixed ? kMainSparse : 0), fp8, true, expanded, s) != cudaSuccess ||
+                    kWaitNs, 0, flags, fp8, true, expanded, s) != cudaSuccess ||
         launch_combine(ws, ol, l, p->batch, p->tokens, p->max_pages_per_seq, units, true, mixed, s) != cudaSuccess)
         return MLA_ERR_CUDA;
     return launch_epilog_uv(p->tokens, ol, w_uv, out, plan, status, stream);

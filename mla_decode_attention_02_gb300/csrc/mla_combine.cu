@@ -304,7 +304,9 @@ cudaError_t launch_combine(const void *ws, void *o_latent, float *lse, int32_t b
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    auto *kernel = sparse ? mla_combine_kernel<true, true> : tree ? mla_combine_kernel<true, false> : mla_combine_kernel<false, false>;
+    auto *kernel = sparse ? mla_combine_kernel<true, true>
+                   : tree ? mla_combine_kernel<true, false>
+                          : mla_combine_kernel<false, false>;
     return cudaLaunchKernelEx(&cfg, kernel,
                               static_cast<const uint8_t *>(ws), static_cast<__nv_bfloat16 *>(o_latent), lse, batch,
                               s_q, max_pages, num_units);

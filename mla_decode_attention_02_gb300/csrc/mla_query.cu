@@ -295,7 +295,8 @@ __global__ void __launch_bounds__(kQueryThreads, 1) mla_query_kernel(const __gri
             gh[j] = P.rope_table[pair0 + j];
             gl[j] = P.rope_table[kPairs + pair0 + j];
         }
-        const int64_t units = kSparse ? (int64_t)tiles * kTile * 4 : (int64_t)P.tokens * 4, warps = (int64_t)gridDim.x * kRopeWarps;
+        const int64_t units = (kSparse ? (int64_t)tiles * kTile : (int64_t)P.tokens) * 4;
+        const int64_t warps = (int64_t)gridDim.x * kRopeWarps;
         const int64_t w = (int64_t)blockIdx.x * kRopeWarps + warp - 1 - kEpiWarps;
         for (int64_t u = units * w / warps, end = units * (w + 1) / warps; u < end; ++u) {
             int tok = (int)(u >> 2);

@@ -81,7 +81,8 @@ def check_exact(c, out, lse, heads=HEADS):
     o, l, spread = oracle(c, heads)
     n, d = c["n"], 24e-6 * reach_of(c, heads)
     o, l, spread, d, got = o[:n], l[:n], spread[:n], d[:n], out[:n, heads].double()
-    bound = (torch.exp(2 * d) - 1 + 2 * FP + 1e-6)[..., None] * spread + BF * o.abs() + 512 * 2.0 ** -24 * value_sums(c, heads) + 2.0 ** -25
+    value = 512 * 2.0 ** -24 * value_sums(c, heads) + 2.0 ** -25
+    bound = (torch.exp(2 * d) - 1 + 2 * FP + 1e-6)[..., None] * spread + BF * o.abs() + value
     assert ((got - o).abs() <= bound).all(), ((got - o).abs() - bound).max()
     assert ((lse[:n, heads].double() - l).abs() <= d + 1e-5).all()
     return o, got, bound

@@ -216,20 +216,22 @@ def chunk_plan(seq_lens, token_offsets, *, tokens: int, max_pages_per_seq: int, 
     ordered, and it may be dropped once the last is enqueued.
     """
     import torch
-    tokens, max_pages_per_seq = _int(tokens, "tokens"), _int(max_pages_per_seq, "max_pages_per_seq")
-    kv_tokens = None if kv_tokens is None else _int(kv_tokens, "kv_tokens", 62)
+    if not (0 < tokens < 1 << 31 and 0 < max_pages_per_seq < 1 << 31 and (kv_tokens is None or 0 < kv_tokens < 1 << 62)):
+        _int(tokens, "tokens")               # (what the fields hold is refused by the C ABI)
+        _int(max_pages_per_seq, "max_pages_per_seq")
+        _int(kv_tokens or 0, "kv_tokens", 62)
     index = _index_of(seq_lens, "seq_lens", 1, torch.int32)
     n = seq_lens.shape[0]
     if kv_tokens is None:
-        kv_tokens = n * max_pages_per_seq * PAGE_SIZE
-    kv_tokens = -(-kv_tokens // PAGE_SIZE) * PAGE_SIZE
+        kv_tokens = n * int(max_pages_per_seq) * PAGE_SIZE
+    kv_tokens = -(-int(kv_tokens) // PAGE_SIZE) * PAGE_SIZE
     if stream is None:
         r = (B._host or B._native()).chunk_plan(seq_lens, token_offsets, tokens, max_pages_per_seq, kv_tokens, workspace)
         if r is not None:
             return ChunkPlan(n, tokens, max_pages_per_seq, kv_tokens, B._made(r, "mla_chunk_plan"))
     sl = _dense(seq_lens, "seq_lens", torch.int32, (n,), index, 4)
     off = _dense(token_offsets, "token_offsets", torch.int32, (n + 1,), index, 4)
-    p = ChunkPlan(n, tokens, max_pages_per_seq, kv_tokens, workspace)
+    p = ChunkPlan(n, int(tokens), int(max_pages_per_seq), kv_tokens, workspace)
     prob, lib = p.problem(), load_library()
     with _launch_on(index, stream, seq_lens, token_offsets, workspace):
         if workspace is None:

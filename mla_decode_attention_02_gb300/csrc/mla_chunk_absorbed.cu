@@ -96,9 +96,8 @@ ChunkForm chunk_form(const mla_chunk *p, int32_t units) {
     if (tokens <= kQuerySmall) return most < kWholeFixed + least ? ChunkForm::kAbsorbed : ChunkForm::kWhole;
     if (tokens <= kChunkTile && most < (kWholeFixed + least) * 3 / 4) return ChunkForm::kAbsorbed;
     if ((least + slots) * 3 / 4 < 2 * kAbsorbedFixed) return ChunkForm::kWhole;
-    return kWholeFixed + least < kMixedLeast && absorbed_gain((tokens + batch - 1) / batch, keys / batch, units) <= 0
-               ? ChunkForm::kWhole
-               : ChunkForm::kMixed;
+    const int64_t even = batch * absorbed_gain((tokens + batch - 1) / batch, keys / batch, units);
+    return kWholeFixed + least < kMixedLeast && even <= kAbsorbedFixed ? ChunkForm::kWhole : ChunkForm::kMixed;
 }
 
 size_t absorbed_workspace_bytes(const mla_chunk *p, int32_t units) { return zeros_at(p, units) + zeros_bytes(p); }

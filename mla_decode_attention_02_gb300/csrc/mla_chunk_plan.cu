@@ -67,6 +67,8 @@ __device__ __forceinline__ int find(const int32_t *sum, int n, int32_t i) {
     return lo;
 }
 
+// kMixed: of a mixed step (with forms).
+template <bool kMixed>
 __global__ void __launch_bounds__(kPlanThreads)
 mla_chunk_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__restrict__ off, uint8_t *ws, int32_t batch,
                       int32_t tokens, int32_t max_pages, int64_t kv_tokens, uint8_t *forms, int32_t units) {
@@ -91,7 +93,7 @@ mla_chunk_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__res
     };
     bool take = false;   // whether any request is in the absorbed form
     auto leave = [&](Request &r) {
-        r.absorbed = take && r.gain(units) > 0;
+        r.absorbed = kMixed && take && r.gain(units) > 0;
         if (r.absorbed) r.np = r.nt = 0;
     };
     auto request = [&](int32_t b) {
@@ -117,7 +119,7 @@ mla_chunk_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__res
         bad_off |= b < batch && (own.begin < 0 || own.n < 0);
         bad_len |= !own.ok;
         mine += own.np;
-        if (forms) {
+        if constexpr (kMixed) {
             const int64_t g = own.gain(units);
             if (g > 0) gain += g;
             keeps |= own.nt > 0 && g <= 0;
@@ -125,7 +127,7 @@ mla_chunk_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__res
     }
     bad_off = __syncthreads_or(bad_off);
     bad_len = __syncthreads_or(bad_len);
-    if (forms) {
+    if constexpr (kMixed) {
         // (in whole nanoseconds, so that the sum does not depend on its order)
         if (gain) atomicAdd(&all_gain, (unsigned long long)gain);
         keeps = __syncthreads_or(keeps);
@@ -271,7 +273,8 @@ extern "C" mla_status mla_chunk_plan(const mla_chunk *prob, const int32_t *seq_l
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, mla_chunk_plan_kernel, seq_lens, token_offsets, ws, prob->batch, prob->tokens,
+    auto *kernel = forms ? mla_chunk_plan_kernel<true> : mla_chunk_plan_kernel<false>;
+    if (cudaLaunchKernelEx(&cfg, kernel, seq_lens, token_offsets, ws, prob->batch, prob->tokens,
                            prob->max_pages_per_seq, prob->kv_tokens, forms, units) != cudaSuccess)
         return MLA_ERR_CUDA;
     return forms ? absorbed_plan(prob, seq_lens, token_offsets, forms, ws + mixed_tree(prob), units, s) : MLA_OK;

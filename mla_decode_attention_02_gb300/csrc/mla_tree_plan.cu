@@ -148,8 +148,8 @@ __device__ int64_t block_scan(int64_t v, int64_t *warp_sums) {
 template <bool kChunk>
 __global__ void __launch_bounds__(kTreeThreads, 1)
 mla_tree_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__restrict__ offsets,
-                     const uint64_t *__restrict__ masks, const uint8_t *__restrict__ forms, int32_t *__restrict__ zeros,
-                     uint8_t *__restrict__ ws, int32_t batch, int32_t tokens, int32_t max_pages, int32_t num_units) {
+                     const uint64_t *__restrict__ masks, const uint8_t *forms, int32_t *zeros, uint8_t *__restrict__ ws,
+                     int32_t batch, int32_t tokens, int32_t max_pages, int32_t num_units) {
     __shared__ int64_t warp_sums[kTreeThreads / 32], warp_most[kTreeThreads / 32];
     __shared__ int64_t carry, carry_parts;
     __shared__ __align__(16) uint32_t unit_key[kMaxUnits];
@@ -187,7 +187,7 @@ mla_tree_plan_kernel(const int32_t *__restrict__ seq_lens, const int32_t *__rest
     // the main kernel may start its prologue now; it waits for this grid before it reads the schedule
     ptx::pdl_launch_dependents();
 
-    if (kChunk && forms) {   // (none: no request, and so with bad offsets)
+    if (kChunk && forms) {   // (none: no request, and so with bad offsets; the chunks' planner has just written them)
         bool any = false;
         for (int32_t b = tid; b < batch; b += kTreeThreads) any |= forms[b] != 0;
         if (!__syncthreads_or(any)) {

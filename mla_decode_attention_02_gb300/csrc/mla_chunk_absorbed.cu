@@ -77,8 +77,8 @@ size_t zeros_bytes(const mla_chunk *p) { return align_up(4 * ((size_t)p->tokens 
 // 14.0 absorbed; 2048 tokens beside 15 single ones over 32768 keys each: 15.4 and, a form for each request, 0.43).  So a step
 // is mixed, the plan takes a form for each request, but where one is sound for the whole step whatever the spread:
 //  - one request;
-//  - up to kQuerySmall tokens: absorbed if that is no slower even with all of them at the longest context that kv_tokens and
-//    the table allow;
+//  - up to kQuerySmall tokens: absorbed if an even spread saves a quarter and no spread is slower, not with all tokens at the
+//    longest context that kv_tokens and the table allow;
 //  - up to a tile of tokens: absorbed if it saves a quarter even so;
 //  - few keys: the absorbed form could save no more than twice its fixed part.
 // The launches of a form that no request takes cost some 10 us (15 over an fp8 cache), so steps of less than kMixedLeast are
@@ -87,13 +87,15 @@ constexpr int64_t kMixedLeast = 300000;
 ChunkForm chunk_form(const mla_chunk *p, int32_t units) {
     if (!tree_plan_fits(p->tokens, units)) return ChunkForm::kWhole;
     const int64_t tokens = p->tokens, keys = p->kv_tokens, batch = p->batch, some = batch < tokens ? batch : tokens;
-    if (batch == 1)
-        return absorbed_gain(tokens, keys, units) > kAbsorbedFixed - kWholeFixed * 3 / 4 ? ChunkForm::kAbsorbed
-                                                                                          : ChunkForm::kWhole;
+    const int64_t pays = kAbsorbedFixed - kWholeFixed * 3 / 4;
+    if (batch == 1) return absorbed_gain(tokens, keys, units) > pays ? ChunkForm::kAbsorbed : ChunkForm::kWhole;
     const int64_t width = (int64_t)p->max_pages_per_seq * kPage, longest = keys < width ? keys : width;
     const int64_t most = kAbsorbedFixed + absorbed_ns(tokens, longest, units);
     const int64_t least = whole_ns(1, keys, units), slots = (some - 1) * whole_ns(1, 0, units);
-    if (tokens <= kQuerySmall) return most < kWholeFixed + least ? ChunkForm::kAbsorbed : ChunkForm::kWhole;
+    if (tokens <= kQuerySmall)
+        return most < kWholeFixed + least && some * absorbed_gain((tokens + some - 1) / some, keys / some, units) > pays
+                   ? ChunkForm::kAbsorbed
+                   : ChunkForm::kWhole;
     if (tokens <= kChunkTile && most < (kWholeFixed + least) * 3 / 4) return ChunkForm::kAbsorbed;
     if ((least + slots) * 3 / 4 < 2 * kAbsorbedFixed) return ChunkForm::kWhole;
     const int64_t even = batch * absorbed_gain((tokens + batch - 1) / batch, keys / batch, units);
